@@ -164,7 +164,7 @@ def _run_scan(s):
     h_last[:, seq[end]] = h[:, end]
     out = {"h": h.to(dt), "h_last": h_last}
     if train:
-        lam = s["dh"].float()
+        lam = s["dh"].to(torch.float32, copy=True)
         lam[:, end] += s["d_last"][:, seq[end]]
         a_next = torch.cat([ar[:, 1:], ar[:, :1] * 0], 1)
         lam = _linear_scan(a_next.flip(1), lam.flip(1)).flip(1)
