@@ -1,6 +1,6 @@
-"""Build libpararnn.so (HIP, gfx950 only) in-tree with hipcc.
+"""Build libpararnn.so and libpararnn_lm.so (HIP, gfx950 only) in-tree with hipcc.
 
-    python -m nonlinear_rnn_solve_amd.build            # build the library and its look-back stress variant
+    python -m nonlinear_rnn_solve_amd.build            # build the libraries and their look-back stress variants
     python -m nonlinear_rnn_solve_amd.build --asm      # also keep the gfx950 assembly for inspection
 
 Flags: -O3, --offload-arch=gfx950, the packed-fp32 instructions disabled
@@ -13,6 +13,9 @@ computation inlined into two kernels rounds the same way in both.
 libpararnn_stress.so is the same source with -DPR_LB_STRESS=1: tiles pause for
 pseudo-random times before publishing look-back words, so that scans walk far
 back.  Only the tests load it; its results must equal libpararnn.so's bit for bit.
+
+libpararnn_lm.so holds the language-model operators of include/pararnn_lm.h, one source file each, compiled in
+parallel and linked.
 """
 from __future__ import annotations
 
@@ -26,6 +29,8 @@ SRC = os.path.join(HERE, "csrc", "pararnn.hip")
 INC = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpararnn.so")
 STRESS_LIB = os.path.join(HERE, "libpararnn_stress.so")
+LM_SRCS = [os.path.join(HERE, "csrc", f) for f in ("lm_scan.hip", "lm_norm.hip", "lm_logp.hip")]
+LM_LIB = os.path.join(HERE, "libpararnn_lm.so")
 ARCH = "gfx950"
 
 
@@ -35,10 +40,12 @@ def hipcc() -> str:
     return p if os.path.exists(p) else "hipcc"
 
 
+FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-ffp-contract=on",
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-Wall", "-Wno-unused-function", "-I", INC]
+
+
 def _command(out: str, stress: bool, asm: bool) -> list:
-    cmd = [hipcc(), "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-shared", "-ffp-contract=on",
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-           "-Wall", "-Wno-unused-function", "-I", INC, SRC, "-o", out]
+    cmd = [hipcc()] + FLAGS + ["-shared", SRC, "-o", out]
     if stress:
         cmd.insert(1, "-DPR_LB_STRESS=1")
     if asm:
@@ -47,7 +54,8 @@ def _command(out: str, stress: bool, asm: bool) -> list:
 
 
 def build(asm: bool = False, verbose: bool = True, stress: bool = True) -> str:
-    """Compile libpararnn.so (and, with stress, libpararnn_stress.so in parallel); returns the library path."""
+    """Compile libpararnn.so, libpararnn_lm.so (and, with stress, the stress variants), all in parallel;
+    returns the path of libpararnn.so."""
     jobs = [(LIB, False)] + ([(STRESS_LIB, True)] if stress else [])
     if asm:
         os.makedirs(os.path.join(ROOT, "_build"), exist_ok=True)
@@ -55,11 +63,44 @@ def build(asm: bool = False, verbose: bool = True, stress: bool = True) -> str:
     for lib, st in jobs:
         tmp = lib + ".tmp%d" % os.getpid()
         cmd = _command(tmp, st, asm and not st)
-        if verbose:
-            print("[build]", " ".join(cmd), flush=True)
-        p = subprocess.Popen(cmd, cwd=os.path.join(ROOT, "_build") if (asm and not st) else HERE,
-                             stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-        procs.append((p, tmp, lib))
+        procs.append((_start(cmd, verbose, os.path.join(ROOT, "_build") if (asm and not st) else HERE), tmp, lib))
+    lm = _start_lm(verbose)
+    failed = _finish(procs, verbose)
+    failed += _finish_lm(lm, LM_LIB, verbose)
+    if failed:
+        raise RuntimeError("hipcc failed: %s" % failed)
+    return LIB
+
+
+def _start(cmd, verbose, cwd=HERE):
+    if verbose:
+        print("[build]", " ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, cwd=cwd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _start_lm(verbose, defines=()):
+    """Start compiling the language-model operators' sources; objects beside the library until it is linked."""
+    jobs = []
+    for src in LM_SRCS:
+        obj = os.path.join(HERE, "%s%s.tmp%d.o" % (os.path.basename(src)[:-4], "_".join(defines), os.getpid()))
+        jobs.append((_start([hipcc()] + FLAGS + ["-D" + d for d in defines] + ["-c", src, "-o", obj], verbose), obj, obj))
+    return jobs
+
+
+def _finish_lm(jobs, lib, verbose):
+    failed = _finish(jobs, verbose)
+    objs = [obj for _, _, obj in jobs]
+    if not failed:
+        tmp = lib + ".tmp%d" % os.getpid()
+        link = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC"] + objs + ["-o", tmp]
+        failed = _finish([(_start(link, verbose), tmp, lib)], verbose)
+    for obj in objs:
+        if os.path.exists(obj):
+            os.remove(obj)
+    return failed
+
+
+def _finish(procs, verbose):
     failed = []
     for p, tmp, lib in procs:
         out, _ = p.communicate()
@@ -68,11 +109,9 @@ def build(asm: bool = False, verbose: bool = True, stress: bool = True) -> str:
             print(out)
         if p.returncode != 0:
             failed.append((lib, p.returncode))
-        else:
+        elif tmp != lib:
             os.replace(tmp, lib)
-    if failed:
-        raise RuntimeError("hipcc failed: %s" % failed)
-    return LIB
+    return failed
 
 
 if __name__ == "__main__":

@@ -1,0 +1,344 @@
+"""The gated linear recurrence and its gradients (include/pararnn_lm.h) against the plain 64-bit recurrence.
+
+Tolerances.  A step rounds a, m u and the fma: at most 3 units in the last place of values up to H = max |h|, of either
+sign, and the recurrence remembers M = min(T, 1 / min(1 - a)) steps, so independent roundings add to about
+3 sqrt(M) u H; 8 sqrt(M) + 16 units are allowed (u = 2^-24; 16 for the gates' own roundings).  The adjoint obeys the same
+recurrence and multiplies two such values: twice that, relative to the largest entry of its output.  A sum of terms is
+allowed its terms' relative error times the sum of their magnitudes."""
+import math
+
+import pytest
+import torch
+
+import lm_plain as plain
+from lm_plain import U32, close, f64, rounded
+from nonlinear_rnn_solve_amd import lm
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def make(B, T, D, dtype, seed, n=0, layout="slices", state=True, grads=True):
+    g = torch.Generator().manual_seed(seed)
+    proj = torch.randn(B, T, 3 * D, generator=g).to(dtype)
+    if layout == "slices":
+        x, r, i = proj.cuda().split(D, -1) if D else [proj.cuda()[..., :0]] * 3
+    elif layout == "time-major":
+        x, r, i = (p.transpose(0, 1).contiguous().cuda().transpose(0, 1) for p in proj.split(D, -1))
+    else:
+        x, r, i = (p.contiguous().cuda() for p in proj.split(D, -1))
+    a = torch.rand(D, generator=g, dtype=torch.float64) * 0.099 + 0.9
+    lam = torch.log(torch.expm1(-torch.log(a) / 8)).float().cuda()
+    shape = (B, n, D) if n else (B, D)
+    h0 = torch.randn(shape, generator=g).cuda() if state else None
+    dh = torch.randn(B, T, D, generator=g).to(dtype).cuda() if grads else None
+    dl = torch.randn(shape, generator=g).cuda() if grads and state else None
+    return x, r, i, lam, h0, dh, dl
+
+
+def cuda_cu(cu):
+    return None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+
+def reference(x, r, i, lam, h0, dh, dl, c=8.0, cu=None):
+    leaves = [None if t is None else f64(t).requires_grad_() for t in (x, r, i, lam, h0)]
+    h, last = plain.scan(*leaves, c=c, cu=cu)
+    out = {"h": h.detach(), "h_last": last.detach()}
+    if dh is not None:
+        loss = (h * f64(dh)).sum() + (0.0 if dl is None else (last * f64(dl).reshape(last.shape)).sum())
+        if not (loss.requires_grad):
+            loss = loss + 0 * sum(t.sum() for t in leaves if t is not None)
+        want = [t for t in leaves if t is not None]
+        gs = torch.autograd.grad(loss, want, allow_unused=True)
+        gs = [torch.zeros_like(t) if q is None else q for t, q in zip(want, gs)]
+        out.update(zip(("d_x", "d_r", "d_i", "d_lam", "d_h0"), gs))
+    M = min(max(1, x.shape[1]), 1 / max(plain.scan_decays(f64(r), f64(lam), c), 1e-7))
+    return out, (16 + 8 * math.sqrt(M)) * U32
+
+
+def check(args, c=8.0, cu=None, seqs=None):
+    x, r, i, lam, h0, dh, dl = args
+    ref, unit = reference(x, r, i, lam, h0, dh, dl, c, cu)
+    dt, dcu = x.dtype, cuda_cu(cu)
+    h, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, c=c, cu_seqlens=dcu, want_carry=True)
+    H = max(1.0, float(ref["h"].abs().max()) if ref["h"].numel() else 1.0,
+            float(ref["h_last"].abs().max()) if ref["h_last"].numel() else 1.0)
+    close(h, ref["h"], rounded(ref["h"], unit * H, dt), "h")
+    close(last.reshape(ref["h_last"].shape), ref["h_last"], unit * H, "h_last")
+    if dh is None:
+        return
+    got = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl, c=c, cu_seqlens=dcu)
+    for k in ("d_x", "d_r", "d_i"):
+        tol = 2 * unit * max(1.0, float(ref[k].abs().max()) if ref[k].numel() else 1.0)
+        close(got[k], ref[k], rounded(ref[k], tol, dt), k)
+    if h0 is not None:
+        close(got["d_h0"], ref["d_h0"], 2 * unit * max(1.0, float(ref["d_h0"].abs().max()) if ref["d_h0"].numel() else 1.0), "d_h0")
+    # d_lam = sum of terms: each as exact as d_r, whose terms carry the same factors
+    rate = c * torch.nn.functional.softplus(f64(lam), threshold=700.0)
+    s = torch.sigmoid(f64(r))
+    terms = (ref["d_r"] / (rate * (1 - s)).clamp(min=1e-30)).abs().sum((0, 1)) * c * torch.sigmoid(f64(lam))
+    close(got["d_lam"], ref["d_lam"], 4 * unit * (terms + 1e-6), "d_lam")
+
+
+SHAPES = [(1, 1, 1), (2, 1, 64), (5, 1, 1030), (3, 5, 7), (1, 16, 130), (2, 17, 33), (1, 127, 64), (1, 128, 65), (2, 129, 66),
+          (1, 300, 1), (2, 256, 128), (2, 1000, 48), (1, 4099, 20), (3, 640, 200)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_scan_and_gradients(shape, dtype):
+    check(make(*shape, dtype, seed=sum(shape)))
+
+
+@pytest.mark.parametrize("layout", ["slices", "dense", "time-major"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(3, 150, 96), (3, 150, 95), (2, 3, 10)])
+def test_layouts(shape, dtype, layout):
+    check(make(*shape, dtype, seed=3, layout=layout))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_no_state(dtype):
+    check(make(2, 200, 40, dtype, seed=4, state=False))
+
+
+PACKED = [(300, [0, 1, 2, 150, 300]), (300, [0, 0, 128, 128, 129, 256, 300, 300]), (300, [0, 300]), (5, [0, 0, 2, 2, 5]),
+          (1, [0, 0, 1, 1]), (512, [0, 127, 128, 255, 256, 257, 512]), (700, [0] + list(range(1, 700, 7)) + [700]),
+          (16, [0, 16, 16]), (1500, [0, 1490, 1500]), (1500, [0, 3, 1500])]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,cu", PACKED)
+def test_packed_sequences(T, cu, dtype):
+    check(make(2, T, 70, dtype, seed=T + len(cu), n=len(cu) - 1), cu=cu)
+
+
+def test_packed_ends_are_read_as_0_and_T():
+    x, r, i, lam, h0, dh, dl = make(1, 200, 32, F32, seed=6, n=3)
+    a = lm.gated_scan(x, r, i, lam, h0=h0, cu_seqlens=cuda_cu([0, 50, 120, 200]))[0]
+    b = lm.gated_scan(x, r, i, lam, h0=h0, cu_seqlens=cuda_cu([7, 50, 120, 130]))[0]
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [10, 400])
+def test_packed_without_states(T):
+    args = make(2, T, 33, F32, seed=7, n=3)
+    check(args[:4] + (None, args[5], None), cu=[0, 4, T // 2, T])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("T,cut", [(12, 5), (400, 130), (400, 256)])
+def test_nothing_leaks_between_sequences(T, cut, bad):
+    x, r, i, lam, h0, dh, dl = make(2, T, 40, F32, seed=8, n=3, layout="dense")
+    cu = cuda_cu([0, cut, cut + 3, T])
+    clean = lm.gated_scan(x, r, i, lam, h0=h0, cu_seqlens=cu, want_carry=True)
+    gclean = lm.gated_scan_vjp(x, r, i, lam, clean[2], dh, h0=h0, d_last=dl, cu_seqlens=cu)
+    x2, dh2 = x.clone(), dh.clone()
+    x2[:, cut:cut + 3] = bad          # the middle sequence is spoilt, in both directions
+    dh2[:, cut:cut + 3] = bad
+    h, last, carry = lm.gated_scan(x2, r, i, lam, h0=h0, cu_seqlens=cu, want_carry=True)
+    g = lm.gated_scan_vjp(x2, r, i, lam, carry, dh2, h0=h0, d_last=dl, cu_seqlens=cu)
+    keep = [t for t in range(T) if not cut <= t < cut + 3]
+    assert torch.equal(h[:, keep], clean[0][:, keep]) and torch.equal(last[:, [0, 2]], clean[1][:, [0, 2]])
+    for k in ("d_x", "d_r", "d_i"):
+        assert torch.equal(g[k][:, keep], gclean[k][:, keep]), k
+    assert torch.equal(g["d_h0"][:, [0, 2]], gclean["d_h0"][:, [0, 2]])
+    assert not torch.isfinite(h[:, cut:cut + 3]).any()
+
+
+def test_gates_at_their_limits():
+    # closed decay gate: a = 1, the state is held; wide open input; saturated values: finite everywhere
+    B, T, D = 2, 300, 16
+    x, r, i, lam, h0, dh, dl = make(B, T, D, F32, seed=9, layout="dense")
+    r[:, ::3], r[:, 1::3], i[:, ::2], i[:, 1::5] = -float("inf"), 80.0, 90.0, -float("inf")
+    h, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)
+    want, wlast = plain.scan(*(f64(t) for t in (x, r, i, lam, h0)))
+    close(h, want, 1e-4, "h")
+    assert torch.equal(h[:, 0], h0)                   # a = 1, m = 0 exactly
+    g = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl)
+    for k, v in g.items():
+        assert torch.isfinite(v).all(), k
+    assert (g["d_r"][:, ::3] == 0).all() and (g["d_x"][:, ::3] == 0).all()
+
+
+@pytest.mark.parametrize("value", [-90.0, -30.0, -9.0, 0.0, 20.0, 100.0])
+def test_decay_parameter_range(value):
+    x, r, i, _, h0, dh, dl = make(1, 200, 8, F32, seed=10)
+    check((x, r, i, torch.full((8,), value, device="cuda"), h0, dh, dl) if value > -80 else
+          (x, r, i, torch.full((8,), value, device="cuda"), h0, None, None))
+
+
+@pytest.mark.parametrize("c", [0.5, 30.0])
+def test_decay_scale(c):
+    check(make(2, 140, 24, F32, seed=11), c=c)
+
+
+@pytest.mark.parametrize("shape", [(0, 5, 4), (2, 0, 4), (2, 5, 0)])
+def test_empty(shape):
+    B, T, D = shape
+    x = torch.zeros(shape, device="cuda")
+    lam, h0 = torch.zeros(D, device="cuda"), torch.randn(B, D, device="cuda")
+    h, last, carry = lm.gated_scan(x, x, x, lam, h0=h0, want_carry=True)
+    assert h.shape == shape and (T > 0 or torch.equal(last, h0))
+    dl = torch.randn(B, D, device="cuda")
+    g = lm.gated_scan_vjp(x, x, x, lam, carry, x, h0=h0, d_last=dl)
+    assert (g["d_lam"] == 0).all() and (T > 0 or torch.equal(g["d_h0"], dl))
+
+
+def test_token_by_token_equals_the_whole():
+    # a decoder that keeps its state in place gives the bits of one call over all steps of up to 16
+    x, r, i, lam, h0, _, _ = make(4, 16, 100, BF, seed=12)
+    want, last, _ = lm.gated_scan(x, r, i, lam, h0=h0)
+    state = h0.clone()
+    for t in range(16):
+        h, s, _ = lm.gated_scan(x[:, t:t + 1], r[:, t:t + 1], i[:, t:t + 1], lam, h0=state, h_last=state)
+        assert s.data_ptr() == state.data_ptr() and torch.equal(h, want[:, t:t + 1])
+    assert torch.equal(state, last)
+
+
+@pytest.mark.parametrize("T,cu", [(500, None), (500, [0, 200, 200, 500])])
+def test_state_in_place_over_long_inputs(T, cu):
+    x, r, i, lam, h0, _, _ = make(2, T, 64, BF, seed=13, n=3 if cu else 0)
+    h, last, _ = lm.gated_scan(x, r, i, lam, h0=h0, cu_seqlens=cuda_cu(cu))
+    state = h0.clone()
+    h2, _, _ = lm.gated_scan(x, r, i, lam, h0=state, h_last=state, cu_seqlens=cuda_cu(cu))
+    assert torch.equal(h, h2) and torch.equal(state, last)
+
+
+def test_split_row_equals_whole_row():
+    # the state handed from one call to the next, and its gradient handed back
+    x, r, i, lam, h0, dh, dl = make(2, 700, 40, F32, seed=14)
+    whole, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)
+    gw = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl)
+    a, b = slice(0, 333), slice(333, 700)
+    h1, s1, c1 = lm.gated_scan(x[:, a], r[:, a], i[:, a], lam, h0=h0, want_carry=True)
+    h2, s2, c2 = lm.gated_scan(x[:, b], r[:, b], i[:, b], lam, h0=s1, want_carry=True)
+    g2 = lm.gated_scan_vjp(x[:, b], r[:, b], i[:, b], lam, c2, dh[:, b], h0=s1, d_last=dl)
+    g1 = lm.gated_scan_vjp(x[:, a], r[:, a], i[:, a], lam, c1, dh[:, a], h0=h0, d_last=g2["d_h0"])
+    unit = (16 + 8 * math.sqrt(700)) * U32
+    close(torch.cat([h1, h2], 1), whole, unit * float(whole.abs().max()), "h")
+    close(g1["d_h0"], gw["d_h0"], 2 * unit * float(gw["d_h0"].abs().max()), "d_h0")
+    close(torch.cat([g1["d_r"], g2["d_r"]], 1), gw["d_r"], 2 * unit * float(gw["d_r"].abs().max()), "d_r")
+
+
+def test_gradients_against_differences():
+    args = make(2, 150, 6, F32, seed=15)
+    x, r, i, lam, h0, dh, dl = args
+    carry = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)[2]
+    g = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl)
+    gen = torch.Generator().manual_seed(1)
+    base = [f64(t) for t in (x, r, i, lam, h0)]
+
+    def loss(ts):
+        h, last = plain.scan(*ts)
+        return float((h * f64(dh)).sum() + (last * f64(dl)[:, None]).sum())
+
+    for k, name in enumerate(("d_x", "d_r", "d_i", "d_lam", "d_h0")):
+        v = torch.randn(base[k].shape, generator=gen, dtype=torch.float64)
+        step = 1e-5
+        up, down = list(base), list(base)
+        up[k], down[k] = base[k] + step * v, base[k] - step * v
+        want = (loss(up) - loss(down)) / (2 * step)
+        got = float((f64(g[name]) * v).sum())
+        # the difference is exact to ~step^2; float32 gradients to their own tolerance on the terms' magnitudes
+        assert abs(got - want) <= 1e-5 * float((f64(g[name]) * v).abs().sum()) + 1e-6, (name, got, want)
+
+
+def test_gradient_slices_of_one_array():
+    x, r, i, lam, h0, dh, dl = make(2, 260, 48, BF, seed=16)
+    carry = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)[2]
+    want = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl)
+    buf = torch.full((2, 260, 3 * 48 + 5), 7.0, dtype=BF, device="cuda")
+    out = [buf[..., 48 * k:48 * (k + 1)] for k in range(3)]
+    got = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl, out=out)
+    for k in ("d_x", "d_r", "d_i", "d_lam", "d_h0"):
+        assert torch.equal(got[k], want[k]), k
+    assert (buf[..., 144:] == 7).all()
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_broadcast_planes(T):
+    # one gate for all rows (stride 0 over b): the gradient is that of each row's use of it
+    x, r, i, lam, h0, dh, dl = make(3, T, 20, F32, seed=17)
+    r = r[:1].expand(3, -1, -1)
+    check((x, r, i, lam, h0, dh, dl))
+
+
+def test_offsets_beyond_32_bits():
+    # rows over 2^32 elements apart, steps 2^25 apart: most offsets need 64 bits
+    T, D = 130, 64
+    x, r, i, lam, h0, _, _ = make(2, T, D, BF, seed=18, grads=False)
+    want, last, _ = lm.gated_scan(x, r, i, lam, h0=h0)
+    row = 200 << 25
+    buf = torch.empty(row + T * (1 << 25) + D, dtype=BF, device="cuda")
+    far = buf.as_strided((2, T, D), (row, 1 << 25, 1))
+    far.copy_(x)
+    got, glast, _ = lm.gated_scan(far, r, i, lam, h0=h0)
+    assert torch.equal(got, want) and torch.equal(glast, last)
+    outbuf = buf.as_strided((2, T, D), (row, 1 << 25, 1), 64)
+    lm.gated_scan(x, r, i, lam, h0=h0, out=outbuf)
+    assert torch.equal(outbuf, want)
+
+
+def test_same_bits_in_every_run_and_on_another_stream():
+    args = make(2, 2000, 130, BF, seed=19)
+    x, r, i, lam, h0, dh, dl = args
+
+    def run():
+        h, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)
+        return [h, last, *lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl).values()]
+
+    want = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run()
+    side.synchronize()
+    for a, b, c in zip(want, got, run()):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_graph_replays():
+    x, r, i, lam, h0, dh, dl = make(2, 700, 64, BF, seed=20, layout="dense")
+    new = make(2, 700, 64, BF, seed=21, layout="dense")
+
+    def run():
+        h, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)
+        return [h, last, *lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl).values()]
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = run()
+    torch.cuda.synchronize()
+    old = x.clone()
+    for src in (old, new[0], old, new[0]):
+        x.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        for a, b in zip(got, run()):
+            assert torch.equal(a, b)
+        torch.cuda.synchronize()
+
+
+def test_refusals():
+    x, r, i, lam, h0, dh, dl = make(2, 20, 16, F32, seed=22, layout="dense")
+    ok = lambda **k: lm.gated_scan(*(k.get(n, v) for n, v in zip("xril", (x, r, i, lam))), h0=k.get("h0"),  # noqa: E731
+                                   c=k.get("c", 8.0), cu_seqlens=k.get("cu"), out=k.get("out"), h_last=k.get("h_last"))
+    ok()
+    for bad in (dict(x=x.cpu()), dict(r=r.bfloat16()), dict(x=x.half(), r=r.half(), i=i.half()), dict(i=i[:, :5]), dict(x=x[0]),
+                dict(r=r.transpose(1, 2).contiguous().transpose(1, 2)), dict(l=lam.double()), dict(l=lam[:3]), dict(h0=h0[:1]),
+                dict(h0=h0.bfloat16()), dict(cu=torch.tensor([0, 20], device="cuda")), dict(cu=cuda_cu([0])),
+                dict(cu=cuda_cu([0, 5, 20]), h0=h0), dict(out=torch.empty_like(x, dtype=BF)), dict(h_last=h0[:1])):
+        with pytest.raises(ValueError):
+            ok(**bad)
+    for c in (0.0, -1.0, float("nan")):
+        with pytest.raises(lm.PararnnError) as e:
+            ok(c=c)
+        assert e.value.status == -1
+    with pytest.raises(ValueError, match="carry"):
+        lm.gated_scan_vjp(x, r, i, lam, None, dh)
