@@ -39,6 +39,18 @@ template <typename T> DEV T from_f32(float x);
 template <> DEV float from_f32<float>(float x) { return x; }
 template <> DEV bf16 from_f32<bf16>(float x) { return bf16{bf16_bits(x)}; }
 
+// V consecutive elements as one load or store of 2 to 16 bytes, and their values
+template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
+  T e[V];
+};
+template <typename T, int V> DEV Vec<T, V> load_vec(const T* p) { return *reinterpret_cast<const Vec<T, V>*>(p); }
+template <typename T, int V> DEV void store_vec(T* p, const float (&x)[V]) {
+  Vec<T, V> v;
+#pragma unroll
+  for (int k = 0; k < V; ++k) v.e[k] = from_f32<T>(x[k]);
+  *reinterpret_cast<Vec<T, V>*>(p) = v;
+}
+
 // ---------------- host: argument checks ----------------
 inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 inline bool dtype_ok(int dt) { return dt == PARARNN_F32 || dt == PARARNN_BF16; }

@@ -2,6 +2,9 @@
 //
 //   a_t = exp(k sig(r_t)), k = -c softplus(lam);  h_t = a_t h_{t-1} + m_t u_t,  m = sqrt(1 - a^2), u = sig(i) x
 
+#include <algorithm>
+#include <type_traits>
+
 #include "lm_common.h"
 
 namespace lm {
@@ -76,7 +79,11 @@ DEV int32_t sequence_of(const int32_t* cu, int32_t n, int64_t t) {
   return lo;
 }
 
-// one channel of one row, all steps in order
+// ------------------------------------------------------------------------------------------------
+// Few steps (kSerial or fewer, one generated token for instance): one channel of one row a thread, all steps
+// in order, no shared memory, one launch.
+// ------------------------------------------------------------------------------------------------
+constexpr int64_t kSerial = 16;
 template <typename T>
 __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
   const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x, b = blockIdx.y;
@@ -86,14 +93,14 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
   const T* r = static_cast<const T*>(p.r) + b * p.sr[0] + d;
   const T* i = static_cast<const T*>(p.i) + b * p.si[0] + d;
   T* out = static_cast<T*>(p.h) + b * p.sh[0] + d;
-  const int64_t state = b * p.n * p.D + d, chunks = (p.T + CT - 1) / CT;
+  const int64_t state = b * p.n * p.D + d;
   int64_t t = 0;
   for (int32_t j = 0; j < p.n; ++j) {
     float h = p.h0 ? p.h0[state + j * p.D] : 0.0f;
     int64_t end = j + 1 < p.n ? p.cu[j + 1] : p.T;
     if (end > p.T) end = p.T;
     for (; t < end; ++t) {
-      if (p.carry && t % CT == 0) p.carry[(b * chunks + t / CT) * p.D + d] = h;
+      if (p.carry && t == 0) p.carry[b * p.D + d] = h;
       const Gate g = gate(to_f32(r[t * p.sr[1]]), to_f32(i[t * p.si[1]]), k);
       h = fmaf(g.a, h, root(g.w) * (g.si * to_f32(x[t * p.sx[1]])));
       out[t * p.sh[1]] = from_f32<T>(h);
@@ -102,72 +109,456 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
   }
 }
 
-// the gradients of one channel of one row: chunk by chunk from the end, h rebuilt into the chunk's workspace
-// rows [B][CT][D] first
-template <typename T>
-__global__ __launch_bounds__(64) void k_scan_grad_serial(const GradArgs p, float* rows) {
-  const ScanArgs& f = p.f;
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x, b = blockIdx.y;
-  if (d >= f.D) return;
-  const float k = -f.c * softplus(f.lam[d]);
-  const T* x = static_cast<const T*>(f.x) + b * f.sx[0] + d;
-  const T* r = static_cast<const T*>(f.r) + b * f.sr[0] + d;
-  const T* i = static_cast<const T*>(f.i) + b * f.si[0] + d;
-  const T* dh = static_cast<const T*>(p.dh) + b * p.sdh[0] + d;
-  T* dx = static_cast<T*>(p.dx) + b * p.sdx[0] + d;
-  T* dr = static_cast<T*>(p.dr) + b * p.sdr[0] + d;
-  T* di = static_cast<T*>(p.di) + b * p.sdi[0] + d;
-  const int64_t state = b * f.n * f.D + d, chunks = (f.T + CT - 1) / CT;
-  float* row = rows + b * CT * f.D + d;
-  int32_t j = f.n;               // sequences j .. n-1 have been entered from their end
-  float mu = 0.0f;               // gradient that reaches the state after step t
-  for (int64_t ch = chunks - 1; ch >= 0; --ch) {
-    const int64_t t0 = ch * CT, t1 = t0 + CT < f.T ? t0 + CT : f.T;
-    float h = f.carry[(b * chunks + ch) * f.D + d], sum = 0.0f;
-    int32_t s = f.cu ? sequence_of(f.cu, f.n, t0) : 0;
-    for (int64_t t = t0; t < t1; ++t) {
-      if (t > t0)
-        while (s + 1 < f.n && f.cu[s + 1] <= t) h = f.h0 ? f.h0[state + ++s * f.D] : (++s, 0.0f);
-      row[(t - t0) * f.D] = h;
-      const Gate g = gate(to_f32(r[t * f.sr[1]]), to_f32(i[t * f.si[1]]), k);
-      h = fmaf(g.a, h, root(g.w) * (g.si * to_f32(x[t * f.sx[1]])));
+// ------------------------------------------------------------------------------------------------
+// The parallel scan.  A tile is one workgroup: CT steps of TW channels of one row.  A lane holds V channels of
+// L = 16 / V consecutive steps; the lanes of a wave cover TW channels V times over, as V time slices.  A tile's steps are
+// NSEG segments of SL, whatever V is, so that alignment changes no bit.  Each lane composes its segments' maps
+// h -> a h + b, one wave joins the segments (a lane a channel), takes the state entering the tile from the tiles
+// before it, and gives every segment its own entering state; the lanes then walk their steps from it.  Inputs are
+// read once.
+//
+// Between tiles a 64-bit word for each (tile, channel) carries either the tile's map or, once known, the state leaving
+// it.  a is in [0, 1], so the sign bit of A marks a word as written: zero = nothing yet, (A | sign, B) = the map,
+// (~0, h) = the state.  A tile reads the words of the W tiles before it at once and applies the maps after the nearest
+// state, in order: the result is the sequential chain of maps, whichever words had come, so every run gives the same
+// bits.  Words are relaxed device-scope atomics and carry their own validity: no fences.  Tiles take their place from
+// an atomic ticket, so those a tile waits for have been started before it.
+// ------------------------------------------------------------------------------------------------
+constexpr int NW = 8, TW = WAVE, NTH = NW * WAVE, W = 8;
+static_assert(NW * 16 == CT, "16 elements a lane");
+constexpr int SL = 4, NSEG = CT / SL;
+template <int V> struct Shape { static constexpr int L = 16 / V, Q = L / SL; };   // steps and segments of a lane
+
+struct Grid {
+  uint64_t* words;      // [chunks][chains][TW]
+  uint32_t* ticket;     // null: one chunk, the tile is the block
+  int64_t chunks;
+  int32_t chains, ctiles;   // chains = B ctiles: channel tiles of all rows
+};
+
+struct Aff { float A, B; };
+// the map of `later` after `earlier`; with packed sequences A = 0 is a cut, which nothing crosses, not even a NaN
+template <bool SEG> DEV float apply(const Aff& f, float h) { return SEG && f.A == 0.0f ? f.B : fmaf(f.A, h, f.B); }
+template <bool SEG> DEV Aff compose(const Aff& later, const Aff& earlier) {
+  return {later.A * earlier.A, apply<SEG>(later, earlier.B)};
+}
+
+DEV uint64_t ld_word(const uint64_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+DEV void st_word(uint64_t* p, uint32_t hi, float lo) {
+  __hip_atomic_store(p, (static_cast<uint64_t>(hi) << 32) | __float_as_uint(lo), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+constexpr uint32_t kState = 0xffffffffu, kSign = 0x80000000u;
+DEV uint32_t map_bits(float A) { return A != A ? 0xffc00000u : (__float_as_uint(A) | kSign); }
+
+// the state entering position `pos` (> 0) of a chain, for this lane's channel
+template <bool SEG>
+DEV float lookback(const Grid& g, int64_t pos, int32_t chain, int lane) {
+  const int64_t step = static_cast<int64_t>(g.chains) * TW;
+  const uint64_t* w0 = g.words + (pos - 1) * step + static_cast<int64_t>(chain) * TW + lane;
+  while (true) {
+    uint64_t w[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = ld_word(w0 - (k < pos ? k : pos - 1) * step);
+    int at = -1;          // the nearest state, if every word before it is there
+    bool there = true;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const uint32_t hi = static_cast<uint32_t>(w[k] >> 32);
+      if (there && at < 0 && hi == kState) at = k;
+      there = there && hi != 0;
     }
-    for (int64_t t = t1 - 1; t >= t0; --t) {
-      // every sequence that begins after t has ended: their states' gradients are out, and the next one enters
-      while (j > 0 && (j == f.n ? f.T : static_cast<int64_t>(f.cu[j])) > t) {
-        if (j < f.n && p.d_h0) p.d_h0[state + j * f.D] = mu;
-        --j;
-        mu = p.d_last ? p.d_last[state + j * f.D] : 0.0f;
+    if (at >= 0) {
+      float h = 0.0f;
+#pragma unroll
+      for (int k = W - 1; k >= 0; --k) {
+        const float lo = __uint_as_float(static_cast<uint32_t>(w[k]));
+        const Aff f{__uint_as_float(static_cast<uint32_t>(w[k] >> 32) & ~kSign), lo};
+        if (k == at) h = lo;
+        else if (k < at) h = apply<SEG>(f, h);
       }
-      const float l = to_f32(dh[t * p.sdh[1]]) + mu, xv = to_f32(x[t * f.sx[1]]);
-      const Gate g = gate(to_f32(r[t * f.sr[1]]), to_f32(i[t * f.si[1]]), k);
-      const float m = root(g.w), u = g.si * xv, im = g.w > 0.0f ? hw_rcp(m) : 0.0f;
-      const float e = l * (g.a * row[(t - t0) * f.D] - u * (g.a * g.a * im));
-      sum = fmaf(e, g.sr, sum);
-      dr[t * p.sdr[1]] = from_f32<T>(e * k * (g.sr * (1.0f - g.sr)));
-      di[t * p.sdi[1]] = from_f32<T>(l * m * (u * (1.0f - g.si)));
-      dx[t * p.sdx[1]] = from_f32<T>(l * m * g.si);
-      mu = g.a * l;
+      return h;
     }
-    if (p.part) p.part[(b * chunks + ch) * f.D + d] = sum;
+    __builtin_amdgcn_s_sleep(1);
   }
-  if (p.d_h0) {
-    // the first sequence with a step, then the empty ones before it (all of them, when T = 0)
-    for (; j >= 0; --j) {
-      if (j < f.n) p.d_h0[state + j * f.D] = mu;
-      if (j > 0) mu = p.d_last ? p.d_last[state + (j - 1) * f.D] : 0.0f;
+}
+
+// where a tile and its lanes are
+template <int V>
+struct Tile {
+  int64_t pos, chunk, b, t0, t, d, c0;   // place in scan order; chunk; row; the tile's and the lane's first step; the lane's
+                                         // first channel; the tile's first channel
+  int32_t chain;
+  int seg, ch, lane, wave;               // the lane's first segment and first channel within the tile
+  bool active;
+  int valid;                             // steps of the lane below T
+  DEV Tile(const Grid& g, const ScanArgs& p, uint32_t ticket, bool reverse) {
+    constexpr int L = Shape<V>::L;
+    lane = threadIdx.x % WAVE;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    pos = ticket / static_cast<uint32_t>(g.chains);
+    chain = static_cast<int32_t>(ticket % static_cast<uint32_t>(g.chains));
+    chunk = reverse ? g.chunks - 1 - pos : pos;
+    b = chain / g.ctiles;
+    c0 = static_cast<int64_t>(chain % g.ctiles) * TW;
+    t0 = chunk * CT;
+    seg = (wave * V + lane / (WAVE / V)) * Shape<V>::Q;
+    ch = (lane % (WAVE / V)) * V;
+    t = t0 + seg * SL;
+    active = c0 + ch < p.D;
+    d = active ? c0 + ch : 0;
+    const int64_t left = p.T - t;
+    valid = static_cast<int>(left < 0 ? 0 : left > L ? L : left);
+  }
+};
+
+DEV uint32_t take_ticket(const Grid& g, uint32_t& sh) {
+  if (!g.ticket) return blockIdx.x;
+  if (threadIdx.x == 0) sh = __hip_atomic_fetch_add(g.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(sh);
+}
+
+// one plane's L steps of V channels; steps past the end repeat the last one (their values are not used)
+template <typename T, int V, int L>
+DEV void load_steps(const void* base, const int64_t (&s)[2], const Tile<V>& tl, int64_t steps, Vec<T, V> (&v)[L]) {
+  const T* p = static_cast<const T*>(base) + tl.b * s[0] + tl.d;
+  if (tl.t0 + CT <= steps) {   // uniform
+    p += tl.t * s[1];
+#pragma unroll
+    for (int l = 0; l < L; ++l) v[l] = load_vec<T, V>(p + l * s[1]);
+  } else {
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+      const int64_t t = tl.t + l < steps ? tl.t + l : steps - 1;
+      v[l] = load_vec<T, V>(p + t * s[1]);
     }
   }
 }
 
-// d_lam = -c sig(lam) times the sum of the chunks' parts, rows in ascending order
-__global__ __launch_bounds__(64) void k_scan_dlam(const float* part, int64_t rows, int64_t D, const float* lam, float c,
-                                                  float* d_lam) {
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-  if (d >= D) return;
+// packed sequences: which of the lane's steps begin and which end one (the row's first and last step included)
+template <int V>
+DEV void boundaries(const ScanArgs& p, const Tile<V>& tl, uint32_t& starts, uint32_t& ends) {
+  starts = ends = 0;
+  if (tl.valid <= 0) return;
+  int32_t j = sequence_of(p.cu, p.n, tl.t);
+  if (tl.t == 0 || (j > 0 && p.cu[j] == tl.t)) starts = 1;
+  for (int l = 0; l < tl.valid; ++l) {
+    const int64_t t = tl.t + l + 1;
+    bool next = t == p.T;
+    while (j + 1 < p.n && p.cu[j + 1] <= t) {
+      ++j;
+      next = true;
+    }
+    if (next) {
+      ends |= 1u << l;
+      if (l + 1 < tl.valid) starts |= 2u << l;
+    }
+  }
+}
+
+template <typename T, int V, bool SEG>
+__global__ __launch_bounds__(NTH) void k_scan(const ScanArgs p, const Grid g) {
+  constexpr int L = Shape<V>::L, Q = Shape<V>::Q;
+  __shared__ uint32_t sh_ticket;
+  __shared__ Aff sh_map[NSEG][TW];
+  __shared__ float sh_enter[NSEG][TW];
+  const Tile<V> tl(g, p, take_ticket(g, sh_ticket), false);
+
+  float a[L][V], b[L][V];
+  uint32_t starts = 0, ends = 0;
+  {
+    Vec<T, V> x[L], r[L], i[L];
+    load_steps(p.r, p.sr, tl, p.T, r);
+    load_steps(p.i, p.si, tl, p.T, i);
+    load_steps(p.x, p.sx, tl, p.T, x);
+    if (SEG) boundaries(p, tl, starts, ends);
+    float k[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) k[v] = -p.c * softplus(p.lam[tl.d + v]);
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Gate q = gate(to_f32(r[l].e[v]), to_f32(i[l].e[v]), k[v]);
+        const bool in = l < tl.valid;
+        a[l][v] = in ? q.a : 1.0f;
+        b[l][v] = in ? root(q.w) * (q.si * to_f32(x[l].e[v])) : 0.0f;
+      }
+  }
+  if (SEG && starts) {
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+      if (starts >> l & 1) {
+        const int64_t state = (tl.b * p.n + sequence_of(p.cu, p.n, tl.t + l)) * p.D + tl.d;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (p.h0) b[l][v] = fmaf(a[l][v], p.h0[state + v], b[l][v]);
+          a[l][v] = 0.0f;
+        }
+      }
+  }
+#pragma unroll
+  for (int s = 0; s < Q; ++s)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      Aff f{a[s * SL][v], b[s * SL][v]};
+#pragma unroll
+      for (int l = s * SL + 1; l < (s + 1) * SL; ++l) f = compose<SEG>(Aff{a[l][v], b[l][v]}, f);
+      sh_map[tl.seg + s][tl.ch + v] = f;
+    }
+  __syncthreads();
+  if (tl.wave == 0) {
+    const int64_t d = tl.c0 + tl.lane;
+    const bool on = d < p.D;
+    uint64_t* word = g.words + (tl.pos * g.chains + tl.chain) * TW + tl.lane;
+    float h = 0.0f;
+    if (on) {
+      Aff f = sh_map[0][tl.lane];
+#pragma unroll 8
+      for (int s = 1; s < NSEG; ++s) f = compose<SEG>(sh_map[s][tl.lane], f);
+      if (tl.pos > 0) {
+        if (tl.pos + 1 < g.chunks) st_word(word, map_bits(f.A), f.B);
+        h = lookback<SEG>(g, tl.pos, tl.chain, tl.lane);
+      } else if (!SEG) {
+        h = p.h0 ? p.h0[tl.b * p.D + d] : 0.0f;
+      }
+      if (tl.pos + 1 < g.chunks) st_word(word, kState, apply<SEG>(f, h));
+      if (p.carry) {
+        float in = h;
+        if (SEG) {
+          const int32_t j = sequence_of(p.cu, p.n, tl.t0);
+          if (tl.t0 == 0 || (j > 0 && p.cu[j] == tl.t0)) in = p.h0 ? p.h0[(tl.b * p.n + j) * p.D + d] : 0.0f;
+        }
+        p.carry[(tl.b * g.chunks + tl.chunk) * p.D + d] = in;
+      }
+#pragma unroll 8
+      for (int s = 0; s < NSEG; ++s) {
+        sh_enter[s][tl.lane] = h;
+        h = apply<SEG>(sh_map[s][tl.lane], h);
+      }
+    }
+  }
+  __syncthreads();
+  if (!tl.active) return;
+  float h[V];
+  T* out = static_cast<T*>(p.h) + tl.b * p.sh[0] + tl.t * p.sh[1] + tl.d;
+#pragma unroll
+  for (int l = 0; l < L; ++l) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (l % SL == 0) h[v] = sh_enter[tl.seg + l / SL][tl.ch + v];
+      h[v] = apply<SEG>(Aff{a[l][v], b[l][v]}, h[v]);
+    }
+    if (l < tl.valid) store_vec<T, V>(out + l * p.sh[1], h);
+    const bool end = SEG ? ends >> l & 1 : tl.t + l == p.T - 1;
+    if (end && p.h_last) {
+      const int32_t j = SEG ? sequence_of(p.cu, p.n, tl.t + l) : 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.h_last[(tl.b * p.n + j) * p.D + tl.d + v] = h[v];
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// The gradients: the same tiles from the last chunk to the first.  A lane holds its steps' gates; the state entering
+// the tile (carry) gives h_{t-1} by the forward walk, and the adjoint mu_t = a_t l_t, l_t = dh_t + mu_{t+1}, is the same
+// kind of scan (map mu -> a (dh + mu)) run backwards, whose maps share the products of a with the forward one.
+// ------------------------------------------------------------------------------------------------
+template <typename T, int V, bool SEG>
+__global__ __launch_bounds__(NTH) void k_scan_grad(const GradArgs q, const Grid g) {
+  constexpr int L = Shape<V>::L, Q = Shape<V>::Q;
+  const ScanArgs& p = q.f;
+  __shared__ uint32_t sh_ticket;
+  __shared__ Aff sh_fwd[NSEG][TW], sh_rev[NSEG][TW];
+  __shared__ float sh_h[NSEG][TW], sh_mu[NSEG][TW];
+  const Tile<V> tl(g, p, take_ticket(g, sh_ticket), true);
+
+  Vec<T, V> x[L], dh[L];
+  float a[L][V], w[L][V], sr[L][V], si[L][V], k[V];
+  uint32_t starts = 0, ends = 0;
+  {
+    Vec<T, V> r[L], i[L];
+    load_steps(p.r, p.sr, tl, p.T, r);
+    load_steps(p.i, p.si, tl, p.T, i);
+    load_steps(p.x, p.sx, tl, p.T, x);
+    load_steps(q.dh, q.sdh, tl, p.T, dh);
+    if (SEG) boundaries(p, tl, starts, ends);
+#pragma unroll
+    for (int v = 0; v < V; ++v) k[v] = -p.c * softplus(p.lam[tl.d + v]);
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Gate t = gate(to_f32(r[l].e[v]), to_f32(i[l].e[v]), k[v]);
+        const bool in = l < tl.valid;
+        a[l][v] = in ? t.a : 1.0f;
+        w[l][v] = in ? t.w : 0.0f;
+        sr[l][v] = t.sr;
+        si[l][v] = t.si;
+        if (!in) x[l].e[v] = dh[l].e[v] = from_f32<T>(0.0f);
+      }
+  }
+  // what enters at a boundary: h0 at a sequence's first step, d_last at its last
+  const auto at = [&](const float* base, int l, int v) {
+    return base ? base[(tl.b * p.n + sequence_of(p.cu, p.n, tl.t + l)) * p.D + tl.d + v] : 0.0f;
+  };
+  const auto input = [&](int l, int v) { return root(w[l][v]) * (si[l][v] * to_f32(x[l].e[v])); };
+#pragma unroll
+  for (int s = 0; s < Q; ++s)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      Aff f{1.0f, 0.0f}, r{1.0f, 0.0f};
+#pragma unroll
+      for (int l = s * SL; l < (s + 1) * SL; ++l) {
+        Aff e{a[l][v], input(l, v)};
+        if (SEG && starts >> l & 1) e = Aff{0.0f, fmaf(e.A, at(p.h0, l, v), e.B)};
+        f = l % SL ? compose<SEG>(e, f) : e;
+      }
+#pragma unroll
+      for (int l = (s + 1) * SL - 1; l >= s * SL; --l) {
+        float in = r.B, A = a[l][v] * r.A;
+        if (SEG && ends >> l & 1) {
+          in = at(q.d_last, l, v);
+          A = 0.0f;
+        }
+        r = Aff{A, a[l][v] * (to_f32(dh[l].e[v]) + in)};
+      }
+      sh_fwd[tl.seg + s][tl.ch + v] = f;
+      sh_rev[tl.seg + s][tl.ch + v] = r;
+    }
+  __syncthreads();
+  const int64_t dl = tl.c0 + tl.lane;
+  if (tl.wave == 0 && dl < p.D) {
+    uint64_t* word = g.words + (tl.pos * g.chains + tl.chain) * TW + tl.lane;
+    Aff f = sh_rev[NSEG - 1][tl.lane];
+#pragma unroll 8
+    for (int s = NSEG - 2; s >= 0; --s) f = compose<SEG>(sh_rev[s][tl.lane], f);
+    float mu = 0.0f;
+    if (tl.pos > 0) {
+      if (tl.pos + 1 < g.chunks) st_word(word, map_bits(f.A), f.B);
+      mu = lookback<SEG>(g, tl.pos, tl.chain, tl.lane);
+    } else if (!SEG) {
+      mu = q.d_last ? q.d_last[tl.b * p.D + dl] : 0.0f;
+    }
+    if (tl.pos + 1 < g.chunks) st_word(word, kState, apply<SEG>(f, mu));
+#pragma unroll 8
+    for (int s = NSEG - 1; s >= 0; --s) {
+      sh_mu[s][tl.lane] = mu;
+      mu = apply<SEG>(sh_rev[s][tl.lane], mu);
+    }
+  }
+  if (tl.wave == 1 && dl < p.D) {
+    float h = p.carry[(tl.b * g.chunks + tl.chunk) * p.D + dl];
+#pragma unroll 8
+    for (int s = 0; s < NSEG; ++s) {
+      sh_h[s][tl.lane] = h;
+      h = apply<SEG>(sh_fwd[s][tl.lane], h);
+    }
+  }
+  __syncthreads();
+  float sum[Q][V];
+#pragma unroll
+  for (int s = 0; s < Q; ++s)
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum[s][v] = 0.0f;
+  if (tl.active) {
+    float hp[L][V], mu[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float h = 0.0f;
+#pragma unroll
+      for (int l = 0; l < L; ++l) {
+        if (l % SL == 0) h = sh_h[tl.seg + l / SL][tl.ch + v];
+        if (SEG && starts >> l & 1) h = at(p.h0, l, v);
+        hp[l][v] = h;
+        h = fmaf(a[l][v], h, input(l, v));
+      }
+    }
+    T* dx = static_cast<T*>(q.dx) + tl.b * q.sdx[0] + tl.t * q.sdx[1] + tl.d;
+    T* dr = static_cast<T*>(q.dr) + tl.b * q.sdr[0] + tl.t * q.sdr[1] + tl.d;
+    T* di = static_cast<T*>(q.di) + tl.b * q.sdi[0] + tl.t * q.sdi[1] + tl.d;
+#pragma unroll
+    for (int l = L - 1; l >= 0; --l) {
+      float ox[V], orr[V], oi[V];
+      const bool start = SEG ? starts >> l & 1 : tl.t + l == 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (l % SL == SL - 1) mu[v] = sh_mu[tl.seg + l / SL][tl.ch + v];
+        if (SEG && ends >> l & 1) mu[v] = at(q.d_last, l, v);
+        const float lam = to_f32(dh[l].e[v]) + mu[v], xv = to_f32(x[l].e[v]);
+        const float im = w[l][v] > 0.0f ? hw_rsq(w[l][v]) : 0.0f, m = w[l][v] * im, u = si[l][v] * xv;
+        const float e = lam * a[l][v] * (hp[l][v] - u * a[l][v] * im);
+        sum[l / SL][v] = fmaf(e, l < tl.valid ? sr[l][v] : 0.0f, sum[l / SL][v]);
+        const float lm_ = lam * m;
+        orr[v] = e * k[v] * (sr[l][v] * (1.0f - sr[l][v]));
+        oi[v] = lm_ * (u * (1.0f - si[l][v]));
+        ox[v] = lm_ * si[l][v];
+        mu[v] = a[l][v] * lam;
+        if (start && l < tl.valid && q.d_h0)
+          q.d_h0[(tl.b * p.n + (SEG ? sequence_of(p.cu, p.n, tl.t + l) : 0)) * p.D + tl.d + v] = mu[v];
+      }
+      if (l < tl.valid) {
+        store_vec<T, V>(dx + l * q.sdx[1], ox);
+        store_vec<T, V>(dr + l * q.sdr[1], orr);
+        store_vec<T, V>(di + l * q.sdi[1], oi);
+      }
+    }
+  }
+  if (!q.part) return;
+  // the segments' sums in order: sh_h is free once every lane has read it
+  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < Q; ++s)
+#pragma unroll
+    for (int v = 0; v < V; ++v) sh_h[tl.seg + s][tl.ch + v] = sum[s][v];
+  __syncthreads();
+  if (tl.wave == 0 && dl < p.D) {
+    float s = 0.0f;
+#pragma unroll 8
+    for (int n = 0; n < NSEG; ++n) s += sh_h[n][tl.lane];
+    q.part[(tl.b * g.chunks + tl.chunk) * p.D + dl] = s;
+  }
+}
+
+// before a scan: the words and the ticket are cleared, and sequences without a step pass their state on (from `in`, zeros
+// when null, to `out`)
+__global__ __launch_bounds__(256) void k_scan_prepare(uint4* clear, int64_t n16, const int32_t* cu, int32_t n, int64_t B,
+                                                      int64_t T, int64_t D, const float* in, float* out) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 256, first = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  for (int64_t k = first; k < n16; k += stride) clear[k] = make_uint4(0u, 0u, 0u, 0u);
+  if (!out) return;
+  for (int64_t k = first; k < B * n * D; k += stride) {
+    const int32_t j = static_cast<int32_t>(k / D % n);
+    int64_t t0 = j > 0 ? cu[j] : 0, t1 = j + 1 < n ? cu[j + 1] : T;
+    if (t0 > T) t0 = T;
+    if (t1 > T) t1 = T;
+    if (t0 >= t1) out[k] = in ? in[k] : 0.0f;
+  }
+}
+
+// d_lam = -c sig(lam) times the sum of the chunks' parts: a wave sums every 16th row, eight loads at a time, the waves'
+// sums are added in order
+__global__ __launch_bounds__(1024) void k_scan_dlam(const float* part, int64_t rows, int64_t D, const float* lam, float c,
+                                                    float* d_lam) {
+  __shared__ float sh[16][WAVE];
+  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  const int64_t d = static_cast<int64_t>(blockIdx.x) * WAVE + lane, dc = d < D ? d : D - 1;
   float s = 0.0f;
-  for (int64_t n = 0; n < rows; ++n) s += part[n * D + d];
-  d_lam[d] = -c * sigmoid(lam[d]) * s;
+  for (int64_t n = wave; n < rows; n += 16 * 8) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = n + u * 16 < rows ? part[(n + u * 16) * D + dc] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += v[u];
+  }
+  sh[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && d < D) {
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s += sh[w][lane];
+    d_lam[d] = -c * sigmoid(lam[d]) * s;
+  }
 }
 
 // ---------------- host ----------------
@@ -200,6 +591,52 @@ static ScanArgs scan_args(const pararnn_lm_scan* p) {
   return a;
 }
 
+// the workspace: [ticket, 256 bytes][words][parts]
+struct Layout {
+  int64_t chunks, ctiles, tiles, words, parts, total;   // the last three in bytes
+};
+static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
+  if (!sizes_fit(B, T, D) || !sizes_fit(B, D + TW, CT)) return false;
+  o.chunks = T <= 0 ? 0 : ceil_div(T, CT);
+  o.ctiles = ceil_div(D, TW);
+  o.tiles = B * o.ctiles * o.chunks;
+  o.words = o.chunks > 1 ? o.tiles * TW * 8 : 0;
+  o.parts = B * o.chunks * D * 4;
+  o.total = 256 + o.words + o.parts;
+  return true;
+}
+
+// V consecutive elements from every row and step of a plane are one aligned access
+static bool wide(const void* p, const int64_t (&s)[2], size_t es, int V, int64_t B, int64_t T) {
+  return aligned(p, es * V) && (B <= 1 || s[0] % V == 0) && (T <= 1 || s[1] % V == 0);
+}
+
+template <class F>
+static void pick(int dtype, bool vec, bool seg, F f) {
+  const auto types = [&](auto t) {
+    using T = decltype(t);
+    if (vec) seg ? f(T{}, std::integral_constant<int, 4>{}, std::true_type{}) : f(T{}, std::integral_constant<int, 4>{}, std::false_type{});
+    else seg ? f(T{}, std::integral_constant<int, 1>{}, std::true_type{}) : f(T{}, std::integral_constant<int, 1>{}, std::false_type{});
+  };
+  if (dtype == PARARNN_BF16) types(bf16{});
+  else types(float{});
+}
+
+// clears the words where there is more than one chunk, and hands states through empty sequences
+static void prepare(const Layout& l, void* ws, const ScanArgs& a, const float* in, float* out, hipStream_t st) {
+  const bool empty = out && (a.cu || a.T == 0);
+  const int64_t n16 = l.chunks > 1 ? (256 + l.words) / 16 : 0;
+  if (!n16 && !empty) return;
+  const int64_t work = empty ? std::max(n16, a.B * a.n * a.D) : n16;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(ceil_div(work, 256), 2048));
+  k_scan_prepare<<<grid, 256, 0, st>>>(static_cast<uint4*>(ws), n16, a.cu, a.n, a.B, a.T, a.D, in, empty ? out : nullptr);
+}
+static Grid grid_of(const Layout& l, void* ws, int64_t B) {
+  char* w = static_cast<char*>(ws);
+  return Grid{reinterpret_cast<uint64_t*>(w + 256), l.chunks > 1 ? reinterpret_cast<uint32_t*>(w) : nullptr, l.chunks,
+              static_cast<int32_t>(B * l.ctiles), static_cast<int32_t>(l.ctiles)};
+}
+
 }  // namespace lm
 
 using namespace lm;
@@ -207,8 +644,8 @@ using namespace lm;
 extern "C" int64_t pararnn_lm_scan_chunks(int64_t T) { return T <= 0 ? 0 : ceil_div(T, CT); }
 
 extern "C" size_t pararnn_lm_scan_workspace_bytes(int64_t B, int64_t T, int64_t D) {
-  if (!sizes_fit(B, T, D) || !sizes_fit(B, D, CT)) return 0;
-  return static_cast<size_t>(B * D * (pararnn_lm_scan_chunks(T) + CT)) * 4 + 256;
+  Layout l;
+  return layout(B, T, D, l) ? static_cast<size_t>(l.total) : 0;
 }
 
 extern "C" pararnn_status pararnn_lm_gated_scan(const pararnn_lm_scan* prob, void* h, const int64_t sh[2], float* h_last,
@@ -216,15 +653,29 @@ extern "C" pararnn_status pararnn_lm_gated_scan(const pararnn_lm_scan* prob, voi
   if (const pararnn_status st = check_scan(prob)) return st;
   if (!sh || !ptr_ok(h_last, 4, false) || !ptr_ok(carry, 4, false)) return PARARNN_ERR_INVALID_ARG;
   if (prob->B == 0 || prob->D == 0) return PARARNN_OK;
-  if (prob->T > 0 && (!ptr_ok(h, dtype_size(prob->dtype)) || !plane_ok(prob->B, sh[0]) || !plane_ok(prob->T, sh[1])))
+  const size_t es = dtype_size(prob->dtype);
+  if (prob->T > 0 && (!ptr_ok(h, es) || !plane_ok(prob->B, sh[0]) || !plane_ok(prob->T, sh[1])))
     return PARARNN_ERR_INVALID_ARG;
-  if (!ptr_ok(ws, 256) || ws_bytes < pararnn_lm_scan_workspace_bytes(prob->B, prob->T, prob->D)) return PARARNN_ERR_WORKSPACE;
+  Layout l;
+  if (!layout(prob->B, prob->T, prob->D, l)) return PARARNN_ERR_INVALID_ARG;
+  if (l.tiles > kMaxGrid || ceil_div(prob->D, 64) > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
+  if (!ptr_ok(ws, 256) || ws_bytes < static_cast<size_t>(l.total)) return PARARNN_ERR_WORKSPACE;
   ScanArgs a = scan_args(prob);
   a.h = h; a.sh[0] = sh[0]; a.sh[1] = sh[1]; a.h_last = h_last; a.carry = carry;
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.D, 64)), static_cast<unsigned>(a.B));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (prob->dtype == PARARNN_BF16) k_scan_serial<bf16><<<grid, 64, 0, st>>>(a);
-  else k_scan_serial<float><<<grid, 64, 0, st>>>(a);
+  if (a.T <= kSerial) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.D, 64)), static_cast<unsigned>(a.B));
+    if (prob->dtype == PARARNN_BF16) k_scan_serial<bf16><<<grid, 64, 0, st>>>(a);
+    else k_scan_serial<float><<<grid, 64, 0, st>>>(a);
+    return launched();
+  }
+  prepare(l, ws, a, a.h0, a.h_last, st);
+  const bool vec = a.D % 4 == 0 && wide(a.x, a.sx, es, 4, a.B, a.T) && wide(a.r, a.sr, es, 4, a.B, a.T) &&
+                   wide(a.i, a.si, es, 4, a.B, a.T) && wide(h, a.sh, es, 4, a.B, a.T);
+  const Grid g = grid_of(l, ws, a.B);
+  pick(prob->dtype, vec, a.cu != nullptr, [&](auto t, auto v, auto seg) {
+    k_scan<decltype(t), decltype(v)::value, decltype(seg)::value><<<static_cast<unsigned>(l.tiles), NTH, 0, st>>>(a, g);
+  });
   return launched();
 }
 
@@ -243,25 +694,33 @@ extern "C" pararnn_status pararnn_lm_gated_scan_vjp(const pararnn_lm_scan* prob,
     for (const int64_t* q : s)
       if (!plane_ok(prob->B, q[0]) || !plane_ok(prob->T, q[1])) return PARARNN_ERR_INVALID_ARG;
   }
-  if (!ptr_ok(ws, 256) || ws_bytes < pararnn_lm_scan_workspace_bytes(prob->B, prob->T, prob->D)) return PARARNN_ERR_WORKSPACE;
-  GradArgs a{};
-  a.f = scan_args(prob);
-  a.f.carry = const_cast<float*>(gr->carry);
-  a.dh = gr->dh; a.d_last = gr->d_last; a.dx = gr->d_x; a.dr = gr->d_r; a.di = gr->d_i; a.d_h0 = gr->d_h0;
+  Layout l;
+  if (!layout(prob->B, prob->T, prob->D, l)) return PARARNN_ERR_INVALID_ARG;
+  if (l.tiles > kMaxGrid || l.ctiles > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
+  if (!ptr_ok(ws, 256) || ws_bytes < static_cast<size_t>(l.total)) return PARARNN_ERR_WORKSPACE;
+  GradArgs q{};
+  q.f = scan_args(prob);
+  q.f.carry = const_cast<float*>(gr->carry);
+  q.dh = gr->dh; q.d_last = gr->d_last; q.dx = gr->d_x; q.dr = gr->d_r; q.di = gr->d_i; q.d_h0 = gr->d_h0;
   for (int k = 0; k < 2; ++k) {
-    a.sdh[k] = gr->sdh[k]; a.sdx[k] = gr->sdx[k]; a.sdr[k] = gr->sdr[k]; a.sdi[k] = gr->sdi[k];
+    q.sdh[k] = gr->sdh[k]; q.sdx[k] = gr->sdx[k]; q.sdr[k] = gr->sdr[k]; q.sdi[k] = gr->sdi[k];
   }
-  const int64_t rows = prob->B * pararnn_lm_scan_chunks(prob->T);
-  a.part = gr->d_lam ? static_cast<float*>(ws) : nullptr;
-  float* hrows = static_cast<float*>(ws) + rows * prob->D;
+  q.part = gr->d_lam ? reinterpret_cast<float*>(static_cast<char*>(ws) + 256 + l.words) : nullptr;
+  const ScanArgs& a = q.f;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const unsigned gd = static_cast<unsigned>(ceil_div(prob->D, 64));
-  if (prob->B > 0) {
-    const dim3 grid(gd, static_cast<unsigned>(prob->B));
-    if (prob->dtype == PARARNN_BF16) k_scan_grad_serial<bf16><<<grid, 64, 0, st>>>(a, hrows);
-    else k_scan_grad_serial<float><<<grid, 64, 0, st>>>(a, hrows);
+  if (a.B > 0) prepare(l, ws, a, q.d_last, q.d_h0, st);
+  if (l.tiles > 0) {
+    const bool vec = a.D % 4 == 0 && wide(a.x, a.sx, es, 4, a.B, a.T) && wide(a.r, a.sr, es, 4, a.B, a.T) &&
+                     wide(a.i, a.si, es, 4, a.B, a.T) && wide(q.dh, q.sdh, es, 4, a.B, a.T) &&
+                     wide(q.dx, q.sdx, es, 4, a.B, a.T) && wide(q.dr, q.sdr, es, 4, a.B, a.T) &&
+                     wide(q.di, q.sdi, es, 4, a.B, a.T);
+    const Grid g = grid_of(l, ws, a.B);
+    pick(prob->dtype, vec, a.cu != nullptr, [&](auto t, auto v, auto seg) {
+      k_scan_grad<decltype(t), decltype(v)::value, decltype(seg)::value><<<static_cast<unsigned>(l.tiles), NTH, 0, st>>>(q, g);
+    });
   }
-  if (gr->d_lam) k_scan_dlam<<<gd, 64, 0, st>>>(a.part, rows, prob->D, prob->lam, prob->c, gr->d_lam);
+  if (gr->d_lam)
+    k_scan_dlam<<<static_cast<unsigned>(l.ctiles), 1024, 0, st>>>(q.part, a.B * l.chunks, a.D, a.lam, a.c, gr->d_lam);
   return launched();
 }
 
