@@ -36,7 +36,7 @@ extern "C" {
  * T = 1).
  * ---------------------------------------------------------------------------------------------- */
 /* steps of one chunk of the scan (the state entering each is what the gradient rebuilds h from) */
-#define PARARNN_LM_SCAN_CHUNK 128
+#define PARARNN_LM_SCAN_CHUNK 64
 
 typedef struct {
   int32_t dtype;             /* of x, r, i, h and, in the gradient, dh, d_x, d_r, d_i                   */

@@ -39,16 +39,49 @@ template <typename T> DEV T from_f32(float x);
 template <> DEV float from_f32<float>(float x) { return x; }
 template <> DEV bf16 from_f32<bf16>(float x) { return bf16{bf16_bits(x)}; }
 
-// V consecutive elements as one load or store of 2 to 16 bytes, and their values
-template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
-  T e[V];
+// V consecutive elements in their storage type, loaded as one access of 2 to 16 bytes and kept as 32-bit words (two
+// bf16 a word: element by element the compiler would spend a register on each)
+template <typename T, int V> struct Vec {
+  static constexpr int N = V * sizeof(T) < 4 ? 1 : V * static_cast<int>(sizeof(T)) / 4;
+  uint32_t w[N];
+  DEV float get(int v) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[v]);
+    else if constexpr (V == 1) return __uint_as_float(w[0] << 16);
+    else return __uint_as_float(v % 2 ? w[v / 2] & 0xffff0000u : w[v / 2] << 16);
+  }
 };
-template <typename T, int V> DEV Vec<T, V> load_vec(const T* p) { return *reinterpret_cast<const Vec<T, V>*>(p); }
-template <typename T, int V> DEV void store_vec(T* p, const float (&x)[V]) {
-  Vec<T, V> v;
+template <int N> struct alignas(4 * N) Words { uint32_t w[N]; };
+template <typename T, int V> DEV Vec<T, V> load_vec(const T* p) {
+  Vec<T, V> r;
+  if constexpr (sizeof(T) * V == 2) {
+    r.w[0] = p->u;
+  } else {
+    const auto q = *reinterpret_cast<const Words<Vec<T, V>::N>*>(p);
 #pragma unroll
-  for (int k = 0; k < V; ++k) v.e[k] = from_f32<T>(x[k]);
-  *reinterpret_cast<Vec<T, V>*>(p) = v;
+    for (int k = 0; k < Vec<T, V>::N; ++k) r.w[k] = q.w[k];
+  }
+  return r;
+}
+template <typename T, int V> DEV Vec<T, V> pack_vec(const float (&x)[V]) {
+  Vec<T, V> r;
+#pragma unroll
+  for (int k = 0; k < Vec<T, V>::N; ++k) {
+    if constexpr (sizeof(T) == 4) r.w[k] = __float_as_uint(x[k]);
+    else if constexpr (V == 1) r.w[k] = bf16_bits(x[0]);
+    else r.w[k] = bf16_bits(x[2 * k]) | static_cast<uint32_t>(bf16_bits(x[2 * k + 1])) << 16;
+  }
+  return r;
+}
+template <typename T, int V> DEV void store_vec(T* p, const float (&x)[V]) {
+  if constexpr (V == 1) {
+    *p = from_f32<T>(x[0]);
+  } else {
+    const Vec<T, V> r = pack_vec<T, V>(x);
+    Words<Vec<T, V>::N> q;
+#pragma unroll
+    for (int k = 0; k < Vec<T, V>::N; ++k) q.w[k] = r.w[k];
+    *reinterpret_cast<Words<Vec<T, V>::N>*>(p) = q;
+  }
 }
 
 // ---------------- host: argument checks ----------------

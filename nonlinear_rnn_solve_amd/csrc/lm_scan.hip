@@ -3,6 +3,7 @@
 //   a_t = exp(k sig(r_t)), k = -c softplus(lam);  h_t = a_t h_{t-1} + m_t u_t,  m = sqrt(1 - a^2), u = sig(i) x
 
 #include <algorithm>
+#include <numeric>
 #include <type_traits>
 
 #include "lm_common.h"
@@ -41,29 +42,35 @@ struct GradArgs {
 DEV float softplus(float x) {
   const float e = hw_exp2(-kLog2e * fabsf(x));
   const float w = 1.0f + e;
-  const float l = w == 1.0f ? e : kLn2 * hw_log2(w) * e / (w - 1.0f);
+  const float l = w == 1.0f ? e : kLn2 * hw_log2(w) * e * hw_rcp(w - 1.0f);
   return fmaxf(x, 0.0f) + l;
 }
 
 // The gates of one element.  For small |log a| q = 1 - a comes first, from the Taylor series of expm1, so that
 // a = 1 - q is rounded to nearest and m^2 = 1 - a^2 = q (2 - q) has full relative accuracy (1 - exp() would lose
 // it all where a is near 1, which is where these recurrences live); for large |log a| a itself comes first.
+// |log a| < |k|: FAR = false is for a k of at most kNear in size, which needs no exponential for a.
 struct Gate {
   float a, w, sr, si;   // decay, 1 - a^2, sig(r), sig(i)
 };
+constexpr float kNear = 0.25f;
+template <bool FAR>
 DEV Gate gate(float r, float i, float k) {
   Gate g;
   g.sr = sigmoid(r);
   g.si = sigmoid(i);
   const float z = k * g.sr;
   // -expm1(z), |z| <= 1/4: the first term left out is z^6 / 5040 of the sum, 5e-8
-  const float small = -z * fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 720.0f, 1.0f / 120.0f), 1.0f / 24.0f),
-                                                 1.0f / 6.0f), 0.5f), 1.0f);
-  const float big = hw_exp2(kLog2e * z);
-  const bool far = z < -0.25f;
-  const float q = far ? 1.0f - big : small;
-  g.a = far ? big : 1.0f - q;
-  g.w = q * (2.0f - q);
+  float q = -z * fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 720.0f, 1.0f / 120.0f), 1.0f / 24.0f), 1.0f / 6.0f),
+                              0.5f), 1.0f);
+  g.a = 1.0f - q;
+  if constexpr (FAR) {
+    const float big = hw_exp2(kLog2e * z);
+    const bool far = z < -kNear;
+    q = far ? 1.0f - big : q;
+    g.a = far ? big : g.a;
+  }
+  g.w = fmaf(q, g.a, q);   // 1 - a^2 = q (1 + a)
   return g;
 }
 DEV float root(float w) { return __builtin_amdgcn_sqrtf(w); }
@@ -101,7 +108,7 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
     if (end > p.T) end = p.T;
     for (; t < end; ++t) {
       if (p.carry && t == 0) p.carry[b * p.D + d] = h;
-      const Gate g = gate(to_f32(r[t * p.sr[1]]), to_f32(i[t * p.si[1]]), k);
+      const Gate g = gate<true>(to_f32(r[t * p.sr[1]]), to_f32(i[t * p.si[1]]), k);
       h = fmaf(g.a, h, root(g.w) * (g.si * to_f32(x[t * p.sx[1]])));
       out[t * p.sh[1]] = from_f32<T>(h);
     }
@@ -113,28 +120,39 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
 // The parallel scan.  A tile is one workgroup: CT steps of TW channels of one row.  A lane holds V channels of
 // L = 16 / V consecutive steps; the lanes of a wave cover TW channels V times over, as V time slices.  A tile's steps are
 // NSEG segments of SL, whatever V is, so that alignment changes no bit.  Each lane composes its segments' maps
-// h -> a h + b, one wave joins the segments (a lane a channel), takes the state entering the tile from the tiles
-// before it, and gives every segment its own entering state; the lanes then walk their steps from it.  Inputs are
-// read once.
+// h -> a h + b; each wave, now a lane a channel, joins its own segments; one wave joins the waves', takes the state
+// entering the tile from the tiles before it and gives every wave its entering state, from which each wave finds its
+// segments' and the lanes walk their steps.  Inputs are read once.
 //
 // Between tiles a 64-bit word for each (tile, channel) carries either the tile's map or, once known, the state leaving
 // it.  a is in [0, 1], so the sign bit of A marks a word as written: zero = nothing yet, (A | sign, B) = the map,
 // (~0, h) = the state.  A tile reads the words of the W tiles before it at once and applies the maps after the nearest
 // state, in order: the result is the sequential chain of maps, whichever words had come, so every run gives the same
-// bits.  Words are relaxed device-scope atomics and carry their own validity: no fences.  Tiles take their place from
-// an atomic ticket, so those a tile waits for have been started before it.
+// bits.  Words are relaxed device-scope atomics and carry their own validity: no fences.
+//
+// A tile takes its place from a ticket counter, so those it waits for have been started before it.  One counter hands
+// out a ticket in 13 ns, which bounded the whole scan; the chains therefore form `groups` groups with a counter each
+// (groups divides the number of chains, so all groups have as many tiles).  A workgroup starts with a group that is no
+// function of its XCD (the block number modulo 8): chains bound to an XCD cost 25% at T = 131072, D = 1024.
+//
+// 64 steps a tile (4 waves) against 128 (8 waves), bf16: the gradient at B = 2, T = 4096, D = 4096 118 against 151 us,
+// since its 150 registers leave 12 waves on a CU in workgroups of 4 and 8 in workgroups of 8; the forward scan there 65.6
+// against 72 us; at T = 131072, D = 1024, where the chain of tiles is long, 457 against 575 and 299 against 268 us.
+// W = 8 words at a time against 4 and 16: 299, 418, 296 us at T = 131072 and 65.6, 63.7, 78 us at T = 4096.
 // ------------------------------------------------------------------------------------------------
-constexpr int NW = 8, TW = WAVE, NTH = NW * WAVE, W = 8;
-static_assert(NW * 16 == CT, "16 elements a lane");
-constexpr int SL = 4, NSEG = CT / SL;
+constexpr int NW = CT / 16, TW = WAVE, NTH = NW * WAVE, W = 8;
+static_assert(NW * 16 == CT && NW >= 2, "16 elements a lane");
+constexpr int SL = 4, NSEG = CT / SL, SW = NSEG / NW;   // steps of a segment, segments of a tile and of a wave
 template <int V> struct Shape { static constexpr int L = 16 / V, Q = L / SL; };   // steps and segments of a lane
 
 struct Grid {
   uint64_t* words;      // [chunks][chains][TW]
-  uint32_t* ticket;     // null: one chunk, the tile is the block
+  uint32_t* tickets;    // a counter for each chain, kTicket words apart; null: one chunk, the tile is the block
   int64_t chunks;
-  int32_t chains, ctiles;   // chains = B ctiles: channel tiles of all rows
+  int32_t chains, ctiles, groups;   // chains = B ctiles: channel tiles of all rows; groups divides it
 };
+
+constexpr int kTicket = 32;   // 128 bytes: counters of different chains share no cache line
 
 struct Aff { float A, B; };
 // the map of `later` after `earlier`; with packed sequences A = 0 is a cut, which nothing crosses, not even a NaN
@@ -154,11 +172,11 @@ DEV uint32_t map_bits(float A) { return A != A ? 0xffc00000u : (__float_as_uint(
 template <bool SEG>
 DEV float lookback(const Grid& g, int64_t pos, int32_t chain, int lane) {
   const int64_t step = static_cast<int64_t>(g.chains) * TW;
-  const uint64_t* w0 = g.words + (pos - 1) * step + static_cast<int64_t>(chain) * TW + lane;
+  const uint64_t* w0 = g.words + (pos - 1) * step + static_cast<int64_t>(chain) * TW;   // uniform
   while (true) {
     uint64_t w[W];
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k] = ld_word(w0 - (k < pos ? k : pos - 1) * step);
+    for (int k = 0; k < W; ++k) w[k] = ld_word(w0 - (k < pos ? k : pos - 1) * step + lane);
     int at = -1;          // the nearest state, if every word before it is there
     bool there = true;
 #pragma unroll
@@ -182,57 +200,168 @@ DEV float lookback(const Grid& g, int64_t pos, int32_t chain, int lane) {
   }
 }
 
+// what the lanes of a wave wrote to shared memory is there for its other lanes (a wave's accesses are in order; this keeps
+// the compiler from moving them)
+DEV void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+// the maps of N consecutive pieces (a lane's column of them) as one, in scan order
+template <bool SEG, bool REV, int N> DEV Aff join(const Aff (*m)[TW], int lane) {
+  Aff f = m[REV ? N - 1 : 0][lane];
+#pragma unroll
+  for (int k = 1; k < N; ++k) f = compose<SEG>(m[REV ? N - 1 - k : k][lane], f);
+  return f;
+}
+// the states entering them, from the one entering the first.  The maps are read again: held since join() they would cost
+// the registers of a wave a SIMD.
+template <bool SEG, bool REV, int N> DEV void spread(const Aff (*m)[TW], float (*enter)[TW], int lane, float h) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int s = REV ? N - 1 - k : k;
+    enter[s][lane] = h;
+    if (k + 1 < N) h = apply<SEG>(m[s][lane], h);
+  }
+}
+// publishes the tile's map and the state leaving it; returns the state entering it (`first` where it is the chain's first)
+template <bool SEG> DEV float enter_tile(const Grid& g, uint32_t pos, int32_t chain, int lane, const Aff& f, float first) {
+  uint64_t* word = g.words + (static_cast<int64_t>(pos) * g.chains + chain) * TW;
+  const bool publish = pos + 1 < g.chunks;
+  float h = first;
+  if (pos > 0) {
+    if (publish) st_word(word + lane, map_bits(f.A), f.B);
+    h = lookback<SEG>(g, pos, chain, lane);
+  }
+  if (publish) st_word(word + lane, kState, apply<SEG>(f, h));
+  return h;
+}
+
+// the tile's place: pos gets its position in the chain
+DEV void take_ticket(const Grid& g, uint32_t (&sh)[2], uint32_t& pos, uint32_t& chain) {
+  const uint32_t G = static_cast<uint32_t>(g.groups), per = static_cast<uint32_t>(g.chains) / G;   // chains of a group
+  if (!g.tickets) {
+    pos = 0;
+    chain = blockIdx.x;
+    return;
+  }
+  if (threadIdx.x == 0) {
+    uint32_t n = (blockIdx.x >> 3) % G, t;
+    while ((t = __hip_atomic_fetch_add(g.tickets + n * kTicket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) >=
+           per * static_cast<uint32_t>(g.chunks))
+      n = n + 1 < G ? n + 1 : 0;
+    sh[0] = t;
+    sh[1] = n;
+  }
+  __syncthreads();
+  const uint32_t t = __builtin_amdgcn_readfirstlane(sh[0]), n = __builtin_amdgcn_readfirstlane(sh[1]);
+  pos = t / per;
+  chain = (t - pos * per) * G + n;
+}
+
 // where a tile and its lanes are
 template <int V>
 struct Tile {
-  int64_t pos, chunk, b, t0, t, d, c0;   // place in scan order; chunk; row; the tile's and the lane's first step; the lane's
-                                         // first channel; the tile's first channel
+  int64_t b, t0, c0, t;   // row, the tile's first step and channel; the lane's first step
+  uint32_t pos, chunk;    // place in scan order, chunk
   int32_t chain;
-  int seg, ch, lane, wave;               // the lane's first segment and first channel within the tile
-  bool active;
-  int valid;                             // steps of the lane below T
-  DEV Tile(const Grid& g, const ScanArgs& p, uint32_t ticket, bool reverse) {
-    constexpr int L = Shape<V>::L;
+  int seg, ch, lane, wave, slice;   // the lane's first segment and first channel within the tile
+  bool active, full;      // the lane's channels exist; all the tile's steps do
+  int valid;              // steps of the lane below T
+  DEV Tile(const Grid& g, const ScanArgs& p, uint32_t (&sh)[2], bool reverse) {
+    constexpr int L = Shape<V>::L, Q = Shape<V>::Q;
     lane = threadIdx.x % WAVE;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    pos = ticket / static_cast<uint32_t>(g.chains);
-    chain = static_cast<int32_t>(ticket % static_cast<uint32_t>(g.chains));
-    chunk = reverse ? g.chunks - 1 - pos : pos;
-    b = chain / g.ctiles;
-    c0 = static_cast<int64_t>(chain % g.ctiles) * TW;
-    t0 = chunk * CT;
-    seg = (wave * V + lane / (WAVE / V)) * Shape<V>::Q;
+    uint32_t c;
+    take_ticket(g, sh, pos, c);
+    chain = static_cast<int32_t>(c);
+    chunk = reverse ? static_cast<uint32_t>(g.chunks) - 1 - pos : pos;
+    const uint32_t row = static_cast<uint32_t>(chain) / static_cast<uint32_t>(g.ctiles);
+    b = row;
+    c0 = static_cast<int64_t>(static_cast<uint32_t>(chain) - row * static_cast<uint32_t>(g.ctiles)) * TW;
+    t0 = static_cast<int64_t>(chunk) * CT;
+    slice = lane / (WAVE / V);
+    seg = (wave * V + slice) * Q;
     ch = (lane % (WAVE / V)) * V;
     t = t0 + seg * SL;
     active = c0 + ch < p.D;
-    d = active ? c0 + ch : 0;
-    const int64_t left = p.T - t;
-    valid = static_cast<int>(left < 0 ? 0 : left > L ? L : left);
+    full = t0 + CT <= p.T;
+    valid = L;
+    if (!full) {
+      const int64_t left = p.T - t;
+      valid = static_cast<int>(left < 0 ? 0 : left > L ? L : left);
+    }
   }
 };
 
-DEV uint32_t take_ticket(const Grid& g, uint32_t& sh) {
-  if (!g.ticket) return blockIdx.x;
-  if (threadIdx.x == 0) sh = __hip_atomic_fetch_add(g.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  return __builtin_amdgcn_readfirstlane(sh);
+// A plane as a wave sees it: for each of its lanes' steps l a buffer descriptor that begins at the wave's step l and ends
+// with the row's last step, so that loads past the end return zero and stores there do nothing, without a branch or an
+// address computation of the lane's own.  The lane's byte offset (its slice's steps and its channels) fits 32 bits: the
+// host takes V = 1, one slice a wave, where V slices would not.  Lanes without channels are out of range.
+template <typename T, int V>
+struct Plane {
+  static constexpr int L = Shape<V>::L;
+  char* base;
+  int64_t st;      // bytes from step to step
+  int32_t steps;   // of the wave, below T
+  uint32_t width, off;
+  DEV Plane(const void* p, const int64_t (&s)[2], const Tile<V>& tl, const ScanArgs& a) {
+    const int64_t t = tl.t0 + tl.wave * (V * L), left = a.T - t, cols = a.D - tl.c0;
+    st = s[1] * static_cast<int64_t>(sizeof(T));
+    base = static_cast<char*>(const_cast<void*>(p)) + (tl.b * s[0] + t * s[1] + tl.c0) * static_cast<int64_t>(sizeof(T));
+    steps = static_cast<int32_t>(left < 0 ? 0 : left > V * L ? V * L : left);
+    width = static_cast<uint32_t>(cols > TW ? TW : cols) * static_cast<uint32_t>(sizeof(T));
+    off = static_cast<uint32_t>(tl.slice * L) * static_cast<uint32_t>(st) + static_cast<uint32_t>(tl.ch * sizeof(T));
+    if (!tl.active) off = 0xf0000000u;
+  }
+  DEV __amdgpu_buffer_rsrc_t at(int l) const {
+    const int32_t left = V == 1 ? (l < steps ? 1 : 0) : steps - l;   // V = 1: no lane looks past step l
+    const uint32_t bytes = left > 0 ? static_cast<uint32_t>(left - 1) * static_cast<uint32_t>(st) + width : 0u;
+    return __builtin_amdgcn_make_buffer_rsrc(base + l * st, static_cast<short>(0), static_cast<int>(bytes), 0x00020000);
+  }
+  DEV Vec<T, V> load(int l) const {
+    Vec<T, V> r;
+    if constexpr (V * sizeof(T) == 2) {
+      r.w[0] = __builtin_amdgcn_raw_buffer_load_b16(at(l), off, 0, 0);
+    } else if constexpr (V * sizeof(T) == 4) {
+      r.w[0] = __builtin_amdgcn_raw_buffer_load_b32(at(l), off, 0, 0);
+    } else if constexpr (V * sizeof(T) == 8) {
+      const auto q = __builtin_amdgcn_raw_buffer_load_b64(at(l), off, 0, 0);
+      r.w[0] = q[0], r.w[1] = q[1];
+    } else {
+      const auto q = __builtin_amdgcn_raw_buffer_load_b128(at(l), off, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r.w[k] = q[k];
+    }
+    return r;
+  }
+  DEV void store(int l, const float (&x)[V]) const {
+    const Vec<T, V> r = pack_vec<T, V>(x);
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    if constexpr (V * sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(r.w[0]), at(l), off, 0, 0);
+    else if constexpr (V * sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(r.w[0], at(l), off, 0, 0);
+    else if constexpr (V * sizeof(T) == 8) __builtin_amdgcn_raw_buffer_store_b64(u32x2{r.w[0], r.w[1]}, at(l), off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b128(u32x4{r.w[0], r.w[1], r.w[2], r.w[3]}, at(l), off, 0, 0);
+  }
+};
+
+// one plane's L steps of V channels
+template <typename T, int V, int L>
+DEV void load_steps(const void* p, const int64_t (&s)[2], const Tile<V>& tl, const ScanArgs& a, Vec<T, V> (&v)[L]) {
+  const Plane<T, V> pl(p, s, tl, a);
+#pragma unroll
+  for (int l = 0; l < L; ++l) v[l] = pl.load(l);
 }
 
-// one plane's L steps of V channels; steps past the end repeat the last one (their values are not used)
-template <typename T, int V, int L>
-DEV void load_steps(const void* base, const int64_t (&s)[2], const Tile<V>& tl, int64_t steps, Vec<T, V> (&v)[L]) {
-  const T* p = static_cast<const T*>(base) + tl.b * s[0] + tl.d;
-  if (tl.t0 + CT <= steps) {   // uniform
-    p += tl.t * s[1];
+// k = -c softplus(lam) of the lane's channels: a lane evaluates one channel of the tile, the others fetch it; `far`: some
+// channel of the tile is beyond kNear
+template <int V>
+DEV bool rates(const ScanArgs& p, const Tile<V>& tl, float (&k)[V]) {
+  const int64_t d = tl.c0 + tl.lane < p.D ? tl.c0 + tl.lane : p.D - 1;
+  const float own = -p.c * softplus(p.lam[d]);
 #pragma unroll
-    for (int l = 0; l < L; ++l) v[l] = load_vec<T, V>(p + l * s[1]);
-  } else {
-#pragma unroll
-    for (int l = 0; l < L; ++l) {
-      const int64_t t = tl.t + l < steps ? tl.t + l : steps - 1;
-      v[l] = load_vec<T, V>(p + t * s[1]);
-    }
-  }
+  for (int v = 0; v < V; ++v) k[v] = V == 1 ? own : __shfl(own, tl.ch + v, WAVE);
+  return __any(!(own >= -kNear));
 }
 
 // packed sequences: which of the lane's steps begin and which end one (the row's first and last step included)
@@ -257,39 +386,46 @@ DEV void boundaries(const ScanArgs& p, const Tile<V>& tl, uint32_t& starts, uint
 }
 
 template <typename T, int V, bool SEG>
-__global__ __launch_bounds__(NTH) void k_scan(const ScanArgs p, const Grid g) {
+__global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k_scan(const ScanArgs p, const Grid g) {
   constexpr int L = Shape<V>::L, Q = Shape<V>::Q;
-  __shared__ uint32_t sh_ticket;
-  __shared__ Aff sh_map[NSEG][TW];
-  __shared__ float sh_enter[NSEG][TW];
-  const Tile<V> tl(g, p, take_ticket(g, sh_ticket), false);
+  __shared__ uint32_t sh_ticket[2];
+  __shared__ Aff sh_map[NSEG][TW], sh_wave[NW][TW];
+  __shared__ float sh_enter[NSEG][TW], sh_in[NW][TW];
+  const Tile<V> tl(g, p, sh_ticket, false);
 
   float a[L][V], b[L][V];
   uint32_t starts = 0, ends = 0;
   {
     Vec<T, V> x[L], r[L], i[L];
-    load_steps(p.r, p.sr, tl, p.T, r);
-    load_steps(p.i, p.si, tl, p.T, i);
-    load_steps(p.x, p.sx, tl, p.T, x);
+    load_steps(p.r, p.sr, tl, p, r);
+    load_steps(p.i, p.si, tl, p, i);
+    load_steps(p.x, p.sx, tl, p, x);
     if (SEG) boundaries(p, tl, starts, ends);
     float k[V];
+    const auto gates = [&](auto far) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) k[v] = -p.c * softplus(p.lam[tl.d + v]);
+      for (int l = 0; l < L; ++l)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const Gate q = gate<decltype(far)::value>(r[l].get(v), i[l].get(v), k[v]);
+          a[l][v] = q.a;
+          b[l][v] = root(q.w) * (q.si * x[l].get(v));
+        }
+    };
+    if (rates(p, tl, k)) gates(std::true_type{});
+    else gates(std::false_type{});
+  }
+  if (!tl.full) {   // steps past the end change nothing (x = 0 there)
 #pragma unroll
     for (int l = 0; l < L; ++l)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Gate q = gate(to_f32(r[l].e[v]), to_f32(i[l].e[v]), k[v]);
-        const bool in = l < tl.valid;
-        a[l][v] = in ? q.a : 1.0f;
-        b[l][v] = in ? root(q.w) * (q.si * to_f32(x[l].e[v])) : 0.0f;
-      }
+      for (int v = 0; v < V; ++v) a[l][v] = l < tl.valid ? a[l][v] : 1.0f;
   }
   if (SEG && starts) {
 #pragma unroll
     for (int l = 0; l < L; ++l)
       if (starts >> l & 1) {
-        const int64_t state = (tl.b * p.n + sequence_of(p.cu, p.n, tl.t + l)) * p.D + tl.d;
+        const int64_t state = (tl.b * p.n + sequence_of(p.cu, p.n, tl.t + l)) * p.D + tl.c0 + (tl.active ? tl.ch : 0);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           if (p.h0) b[l][v] = fmaf(a[l][v], p.h0[state + v], b[l][v]);
@@ -306,23 +442,15 @@ __global__ __launch_bounds__(NTH) void k_scan(const ScanArgs p, const Grid g) {
       for (int l = s * SL + 1; l < (s + 1) * SL; ++l) f = compose<SEG>(Aff{a[l][v], b[l][v]}, f);
       sh_map[tl.seg + s][tl.ch + v] = f;
     }
+  wave_sync();
+  sh_wave[tl.wave][tl.lane] = join<SEG, false, SW>(sh_map + tl.wave * SW, tl.lane);
   __syncthreads();
   if (tl.wave == 0) {
     const int64_t d = tl.c0 + tl.lane;
-    const bool on = d < p.D;
-    uint64_t* word = g.words + (tl.pos * g.chains + tl.chain) * TW + tl.lane;
     float h = 0.0f;
-    if (on) {
-      Aff f = sh_map[0][tl.lane];
-#pragma unroll 8
-      for (int s = 1; s < NSEG; ++s) f = compose<SEG>(sh_map[s][tl.lane], f);
-      if (tl.pos > 0) {
-        if (tl.pos + 1 < g.chunks) st_word(word, map_bits(f.A), f.B);
-        h = lookback<SEG>(g, tl.pos, tl.chain, tl.lane);
-      } else if (!SEG) {
-        h = p.h0 ? p.h0[tl.b * p.D + d] : 0.0f;
-      }
-      if (tl.pos + 1 < g.chunks) st_word(word, kState, apply<SEG>(f, h));
+    if (d < p.D) {
+      if (!SEG && tl.pos == 0) h = p.h0 ? p.h0[tl.b * p.D + d] : 0.0f;
+      h = enter_tile<SEG>(g, tl.pos, tl.chain, tl.lane, join<SEG, false, NW>(sh_wave, tl.lane), h);
       if (p.carry) {
         float in = h;
         if (SEG) {
@@ -331,17 +459,16 @@ __global__ __launch_bounds__(NTH) void k_scan(const ScanArgs p, const Grid g) {
         }
         p.carry[(tl.b * g.chunks + tl.chunk) * p.D + d] = in;
       }
-#pragma unroll 8
-      for (int s = 0; s < NSEG; ++s) {
-        sh_enter[s][tl.lane] = h;
-        h = apply<SEG>(sh_map[s][tl.lane], h);
-      }
     }
+    spread<SEG, false, NW>(sh_wave, sh_in, tl.lane, h);
   }
   __syncthreads();
-  if (!tl.active) return;
+  spread<SEG, false, SW>(sh_map + tl.wave * SW, sh_enter + tl.wave * SW, tl.lane, sh_in[tl.wave][tl.lane]);
+  wave_sync();
   float h[V];
-  T* out = static_cast<T*>(p.h) + tl.b * p.sh[0] + tl.t * p.sh[1] + tl.d;
+  const Plane<T, V> out(p.h, p.sh, tl, p);
+  // the step (of the lane) that ends the row
+  const int last = !SEG && tl.chunk + 1 == g.chunks && p.h_last ? static_cast<int>(p.T - 1 - tl.t) : -1;
 #pragma unroll
   for (int l = 0; l < L; ++l) {
 #pragma unroll
@@ -349,12 +476,11 @@ __global__ __launch_bounds__(NTH) void k_scan(const ScanArgs p, const Grid g) {
       if (l % SL == 0) h[v] = sh_enter[tl.seg + l / SL][tl.ch + v];
       h[v] = apply<SEG>(Aff{a[l][v], b[l][v]}, h[v]);
     }
-    if (l < tl.valid) store_vec<T, V>(out + l * p.sh[1], h);
-    const bool end = SEG ? ends >> l & 1 : tl.t + l == p.T - 1;
-    if (end && p.h_last) {
+    out.store(l, h);
+    if ((SEG ? (ends >> l & 1) && p.h_last : l == last) && tl.active) {
       const int32_t j = SEG ? sequence_of(p.cu, p.n, tl.t + l) : 0;
 #pragma unroll
-      for (int v = 0; v < V; ++v) p.h_last[(tl.b * p.n + j) * p.D + tl.d + v] = h[v];
+      for (int v = 0; v < V; ++v) p.h_last[(tl.b * p.n + j) * p.D + tl.c0 + tl.ch + v] = h[v];
     }
   }
 }
@@ -365,44 +491,55 @@ __global__ __launch_bounds__(NTH) void k_scan(const ScanArgs p, const Grid g) {
 // kind of scan (map mu -> a (dh + mu)) run backwards, whose maps share the products of a with the forward one.
 // ------------------------------------------------------------------------------------------------
 template <typename T, int V, bool SEG>
-__global__ __launch_bounds__(NTH) void k_scan_grad(const GradArgs q, const Grid g) {
+__global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k_scan_grad(const GradArgs q, const Grid g) {
   constexpr int L = Shape<V>::L, Q = Shape<V>::Q;
   const ScanArgs& p = q.f;
-  __shared__ uint32_t sh_ticket;
-  __shared__ Aff sh_fwd[NSEG][TW], sh_rev[NSEG][TW];
-  __shared__ float sh_h[NSEG][TW], sh_mu[NSEG][TW];
-  const Tile<V> tl(g, p, take_ticket(g, sh_ticket), true);
+  __shared__ uint32_t sh_ticket[2];
+  __shared__ Aff sh_fwd[NSEG][TW], sh_rev[NSEG][TW], sh_wfwd[NW][TW], sh_wrev[NW][TW];
+  __shared__ float sh_h[NSEG][TW], sh_mu[NSEG][TW], sh_wh[NW][TW], sh_wmu[NW][TW];
+  const Tile<V> tl(g, p, sh_ticket, true);
 
-  Vec<T, V> x[L], dh[L];
-  float a[L][V], w[L][V], sr[L][V], si[L][V], k[V];
+  // kept of each element: a, m, the input m u, sig(r), sig(i); dh in its storage type
+  Vec<T, V> dh[L];
+  float a[L][V], in[L][V], m[L][V], sr[L][V], si[L][V], k[V];
   uint32_t starts = 0, ends = 0;
   {
-    Vec<T, V> r[L], i[L];
-    load_steps(p.r, p.sr, tl, p.T, r);
-    load_steps(p.i, p.si, tl, p.T, i);
-    load_steps(p.x, p.sx, tl, p.T, x);
-    load_steps(q.dh, q.sdh, tl, p.T, dh);
+    Vec<T, V> x[L], r[L], i[L];
+    load_steps(p.r, p.sr, tl, p, r);
+    load_steps(p.i, p.si, tl, p, i);
+    load_steps(p.x, p.sx, tl, p, x);
+    load_steps(q.dh, q.sdh, tl, p, dh);
     if (SEG) boundaries(p, tl, starts, ends);
+    const auto gates = [&](auto far) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) k[v] = -p.c * softplus(p.lam[tl.d + v]);
+      for (int l = 0; l < L; ++l)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const Gate t = gate<decltype(far)::value>(r[l].get(v), i[l].get(v), k[v]);
+          a[l][v] = t.a;
+          sr[l][v] = t.sr;
+          si[l][v] = t.si;
+          m[l][v] = root(t.w);
+          in[l][v] = m[l][v] * (t.si * x[l].get(v));
+        }
+    };
+    if (rates(p, tl, k)) gates(std::true_type{});
+    else gates(std::false_type{});
+  }
+  if (!tl.full) {   // steps past the end change nothing (x = dh = 0 there) and add nothing
 #pragma unroll
     for (int l = 0; l < L; ++l)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Gate t = gate(to_f32(r[l].e[v]), to_f32(i[l].e[v]), k[v]);
-        const bool in = l < tl.valid;
-        a[l][v] = in ? t.a : 1.0f;
-        w[l][v] = in ? t.w : 0.0f;
-        sr[l][v] = t.sr;
-        si[l][v] = t.si;
-        if (!in) x[l].e[v] = dh[l].e[v] = from_f32<T>(0.0f);
+        a[l][v] = l < tl.valid ? a[l][v] : 1.0f;
+        sr[l][v] = l < tl.valid ? sr[l][v] : 0.0f;
       }
   }
   // what enters at a boundary: h0 at a sequence's first step, d_last at its last
+  const int64_t dc = tl.c0 + (tl.active ? tl.ch : 0);
   const auto at = [&](const float* base, int l, int v) {
-    return base ? base[(tl.b * p.n + sequence_of(p.cu, p.n, tl.t + l)) * p.D + tl.d + v] : 0.0f;
+    return base ? base[(tl.b * p.n + sequence_of(p.cu, p.n, tl.t + l)) * p.D + dc + v] : 0.0f;
   };
-  const auto input = [&](int l, int v) { return root(w[l][v]) * (si[l][v] * to_f32(x[l].e[v])); };
 #pragma unroll
   for (int s = 0; s < Q; ++s)
 #pragma unroll
@@ -410,59 +547,49 @@ __global__ __launch_bounds__(NTH) void k_scan_grad(const GradArgs q, const Grid 
       Aff f{1.0f, 0.0f}, r{1.0f, 0.0f};
 #pragma unroll
       for (int l = s * SL; l < (s + 1) * SL; ++l) {
-        Aff e{a[l][v], input(l, v)};
+        Aff e{a[l][v], in[l][v]};
         if (SEG && starts >> l & 1) e = Aff{0.0f, fmaf(e.A, at(p.h0, l, v), e.B)};
         f = l % SL ? compose<SEG>(e, f) : e;
       }
 #pragma unroll
       for (int l = (s + 1) * SL - 1; l >= s * SL; --l) {
-        float in = r.B, A = a[l][v] * r.A;
+        const bool first = l % SL == SL - 1;   // in scan order
+        float mu = r.B, A = first ? a[l][v] : a[l][v] * r.A;
         if (SEG && ends >> l & 1) {
-          in = at(q.d_last, l, v);
+          mu = at(q.d_last, l, v);
           A = 0.0f;
         }
-        r = Aff{A, a[l][v] * (to_f32(dh[l].e[v]) + in)};
+        r = Aff{A, a[l][v] * (first && !SEG ? dh[l].get(v) : dh[l].get(v) + mu)};
       }
       sh_fwd[tl.seg + s][tl.ch + v] = f;
       sh_rev[tl.seg + s][tl.ch + v] = r;
     }
+  wave_sync();
+  sh_wfwd[tl.wave][tl.lane] = join<SEG, false, SW>(sh_fwd + tl.wave * SW, tl.lane);
+  sh_wrev[tl.wave][tl.lane] = join<SEG, true, SW>(sh_rev + tl.wave * SW, tl.lane);
   __syncthreads();
   const int64_t dl = tl.c0 + tl.lane;
-  if (tl.wave == 0 && dl < p.D) {
-    uint64_t* word = g.words + (tl.pos * g.chains + tl.chain) * TW + tl.lane;
-    Aff f = sh_rev[NSEG - 1][tl.lane];
-#pragma unroll 8
-    for (int s = NSEG - 2; s >= 0; --s) f = compose<SEG>(sh_rev[s][tl.lane], f);
+  if (tl.wave == 0) {
     float mu = 0.0f;
-    if (tl.pos > 0) {
-      if (tl.pos + 1 < g.chunks) st_word(word, map_bits(f.A), f.B);
-      mu = lookback<SEG>(g, tl.pos, tl.chain, tl.lane);
-    } else if (!SEG) {
-      mu = q.d_last ? q.d_last[tl.b * p.D + dl] : 0.0f;
+    if (dl < p.D) {
+      if (!SEG && tl.pos == 0) mu = q.d_last ? q.d_last[tl.b * p.D + dl] : 0.0f;
+      mu = enter_tile<SEG>(g, tl.pos, tl.chain, tl.lane, join<SEG, true, NW>(sh_wrev, tl.lane), mu);
     }
-    if (tl.pos + 1 < g.chunks) st_word(word, kState, apply<SEG>(f, mu));
-#pragma unroll 8
-    for (int s = NSEG - 1; s >= 0; --s) {
-      sh_mu[s][tl.lane] = mu;
-      mu = apply<SEG>(sh_rev[s][tl.lane], mu);
-    }
+    spread<SEG, true, NW>(sh_wrev, sh_wmu, tl.lane, mu);
   }
-  if (tl.wave == 1 && dl < p.D) {
-    float h = p.carry[(tl.b * g.chunks + tl.chunk) * p.D + dl];
-#pragma unroll 8
-    for (int s = 0; s < NSEG; ++s) {
-      sh_h[s][tl.lane] = h;
-      h = apply<SEG>(sh_fwd[s][tl.lane], h);
-    }
-  }
+  if (tl.wave == 1)
+    spread<SEG, false, NW>(sh_wfwd, sh_wh, tl.lane, dl < p.D ? p.carry[(tl.b * g.chunks + tl.chunk) * p.D + dl] : 0.0f);
   __syncthreads();
+  spread<SEG, false, SW>(sh_fwd + tl.wave * SW, sh_h + tl.wave * SW, tl.lane, sh_wh[tl.wave][tl.lane]);
+  spread<SEG, true, SW>(sh_rev + tl.wave * SW, sh_mu + tl.wave * SW, tl.lane, sh_wmu[tl.wave][tl.lane]);
+  wave_sync();
   float sum[Q][V];
 #pragma unroll
   for (int s = 0; s < Q; ++s)
 #pragma unroll
     for (int v = 0; v < V; ++v) sum[s][v] = 0.0f;
-  if (tl.active) {
-    float hp[L][V], mu[V];
+  {
+    float mu[V], hq[L][V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float h = 0.0f;
@@ -470,52 +597,56 @@ __global__ __launch_bounds__(NTH) void k_scan_grad(const GradArgs q, const Grid 
       for (int l = 0; l < L; ++l) {
         if (l % SL == 0) h = sh_h[tl.seg + l / SL][tl.ch + v];
         if (SEG && starts >> l & 1) h = at(p.h0, l, v);
-        hp[l][v] = h;
-        h = fmaf(a[l][v], h, input(l, v));
+        // hq = e / (l a sig(r)) = h_{t-1} - u a / m, where u = in / m
+        const float im = m[l][v] > 0.0f ? hw_rcp(m[l][v]) : 0.0f;
+        hq[l][v] = fmaf(-in[l][v] * im, a[l][v] * im, h);
+        h = fmaf(a[l][v], h, in[l][v]);
       }
     }
-    T* dx = static_cast<T*>(q.dx) + tl.b * q.sdx[0] + tl.t * q.sdx[1] + tl.d;
-    T* dr = static_cast<T*>(q.dr) + tl.b * q.sdr[0] + tl.t * q.sdr[1] + tl.d;
-    T* di = static_cast<T*>(q.di) + tl.b * q.sdi[0] + tl.t * q.sdi[1] + tl.d;
+    const Plane<T, V> dx(q.dx, q.sdx, tl, p), dr(q.dr, q.sdr, tl, p), di(q.di, q.sdi, tl, p);
+    const bool first = !SEG && tl.t == 0 && q.d_h0 && tl.active;
 #pragma unroll
     for (int l = L - 1; l >= 0; --l) {
-      float ox[V], orr[V], oi[V];
-      const bool start = SEG ? starts >> l & 1 : tl.t + l == 0;
+      float ox[V], og[V], oi[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (l % SL == SL - 1) mu[v] = sh_mu[tl.seg + l / SL][tl.ch + v];
         if (SEG && ends >> l & 1) mu[v] = at(q.d_last, l, v);
-        const float lam = to_f32(dh[l].e[v]) + mu[v], xv = to_f32(x[l].e[v]);
-        const float im = w[l][v] > 0.0f ? hw_rsq(w[l][v]) : 0.0f, m = w[l][v] * im, u = si[l][v] * xv;
-        const float e = lam * a[l][v] * (hp[l][v] - u * a[l][v] * im);
-        sum[l / SL][v] = fmaf(e, l < tl.valid ? sr[l][v] : 0.0f, sum[l / SL][v]);
-        const float lm_ = lam * m;
-        orr[v] = e * k[v] * (sr[l][v] * (1.0f - sr[l][v]));
-        oi[v] = lm_ * (u * (1.0f - si[l][v]));
-        ox[v] = lm_ * si[l][v];
+        const float lam = dh[l].get(v) + mu[v];
         mu[v] = a[l][v] * lam;
-        if (start && l < tl.valid && q.d_h0)
-          q.d_h0[(tl.b * p.n + (SEG ? sequence_of(p.cu, p.n, tl.t + l) : 0)) * p.D + tl.d + v] = mu[v];
+        const float e = mu[v] * hq[l][v] * sr[l][v];
+        sum[l / SL][v] += e;
+        og[v] = e * k[v] * (1.0f - sr[l][v]);
+        oi[v] = lam * in[l][v] * (1.0f - si[l][v]);
+        ox[v] = lam * m[l][v] * si[l][v];
       }
-      if (l < tl.valid) {
-        store_vec<T, V>(dx + l * q.sdx[1], ox);
-        store_vec<T, V>(dr + l * q.sdr[1], orr);
-        store_vec<T, V>(di + l * q.sdi[1], oi);
+      dx.store(l, ox);
+      dr.store(l, og);
+      di.store(l, oi);
+      if (SEG ? (starts >> l & 1) && q.d_h0 && tl.active : l == 0 && first) {
+        const int32_t j = SEG ? sequence_of(p.cu, p.n, tl.t + l) : 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) q.d_h0[(tl.b * p.n + j) * p.D + dc + v] = mu[v];
       }
     }
   }
   if (!q.part) return;
-  // the segments' sums in order: sh_h is free once every lane has read it
-  __syncthreads();
+  // the segments' sums in order, a wave's first (its rows of sh_h are free again), then the waves'
+  wave_sync();
 #pragma unroll
   for (int s = 0; s < Q; ++s)
 #pragma unroll
     for (int v = 0; v < V; ++v) sh_h[tl.seg + s][tl.ch + v] = sum[s][v];
+  wave_sync();
+  float s = 0.0f;
+#pragma unroll
+  for (int n = 0; n < SW; ++n) s += sh_h[tl.wave * SW + n][tl.lane];
+  sh_wh[tl.wave][tl.lane] = s;
   __syncthreads();
   if (tl.wave == 0 && dl < p.D) {
-    float s = 0.0f;
-#pragma unroll 8
-    for (int n = 0; n < NSEG; ++n) s += sh_h[n][tl.lane];
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) s += sh_wh[w][tl.lane];
     q.part[(tl.b * g.chunks + tl.chunk) * p.D + dl] = s;
   }
 }
@@ -591,9 +722,9 @@ static ScanArgs scan_args(const pararnn_lm_scan* p) {
   return a;
 }
 
-// the workspace: [ticket, 256 bytes][words][parts]
+// the workspace: [tickets][words][parts]
 struct Layout {
-  int64_t chunks, ctiles, tiles, words, parts, total;   // the last three in bytes
+  int64_t chunks, ctiles, tiles, tickets, words, parts, total;   // the last four in bytes
 };
 static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
   if (!sizes_fit(B, T, D) || !sizes_fit(B, D + TW, CT)) return false;
@@ -601,14 +732,16 @@ static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
   o.ctiles = ceil_div(D, TW);
   o.tiles = B * o.ctiles * o.chunks;
   o.words = o.chunks > 1 ? o.tiles * TW * 8 : 0;
+  o.tickets = o.chunks > 1 ? B * o.ctiles * kTicket * 4 : 0;
   o.parts = B * o.chunks * D * 4;
-  o.total = 256 + o.words + o.parts;
+  o.total = 256 + o.tickets + o.words + o.parts;
   return true;
 }
 
-// V consecutive elements from every row and step of a plane are one aligned access
+// V consecutive elements from every row and step of a plane are one aligned access, and V slices of a wave lie within
+// 32-bit byte offsets
 static bool wide(const void* p, const int64_t (&s)[2], size_t es, int V, int64_t B, int64_t T) {
-  return aligned(p, es * V) && (B <= 1 || s[0] % V == 0) && (T <= 1 || s[1] % V == 0);
+  return aligned(p, es * V) && (B <= 1 || s[0] % V == 0) && (T <= 1 || s[1] % V == 0) && s[1] < (INT64_C(1) << 31) / 64;
 }
 
 template <class F>
@@ -625,7 +758,7 @@ static void pick(int dtype, bool vec, bool seg, F f) {
 // clears the words where there is more than one chunk, and hands states through empty sequences
 static void prepare(const Layout& l, void* ws, const ScanArgs& a, const float* in, float* out, hipStream_t st) {
   const bool empty = out && (a.cu || a.T == 0);
-  const int64_t n16 = l.chunks > 1 ? (256 + l.words) / 16 : 0;
+  const int64_t n16 = (l.tickets + l.words) / 16;
   if (!n16 && !empty) return;
   const int64_t work = empty ? std::max(n16, a.B * a.n * a.D) : n16;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(ceil_div(work, 256), 2048));
@@ -633,8 +766,8 @@ static void prepare(const Layout& l, void* ws, const ScanArgs& a, const float* i
 }
 static Grid grid_of(const Layout& l, void* ws, int64_t B) {
   char* w = static_cast<char*>(ws);
-  return Grid{reinterpret_cast<uint64_t*>(w + 256), l.chunks > 1 ? reinterpret_cast<uint32_t*>(w) : nullptr, l.chunks,
-              static_cast<int32_t>(B * l.ctiles), static_cast<int32_t>(l.ctiles)};
+  return Grid{reinterpret_cast<uint64_t*>(w + l.tickets), l.chunks > 1 ? reinterpret_cast<uint32_t*>(w) : nullptr, l.chunks,
+              static_cast<int32_t>(B * l.ctiles), static_cast<int32_t>(l.ctiles), std::gcd(static_cast<int32_t>(B * l.ctiles), 8)};
 }
 
 }  // namespace lm
@@ -705,7 +838,7 @@ extern "C" pararnn_status pararnn_lm_gated_scan_vjp(const pararnn_lm_scan* prob,
   for (int k = 0; k < 2; ++k) {
     q.sdh[k] = gr->sdh[k]; q.sdx[k] = gr->sdx[k]; q.sdr[k] = gr->sdr[k]; q.sdi[k] = gr->sdi[k];
   }
-  q.part = gr->d_lam ? reinterpret_cast<float*>(static_cast<char*>(ws) + 256 + l.words) : nullptr;
+  q.part = gr->d_lam ? reinterpret_cast<float*>(static_cast<char*>(ws) + l.tickets + l.words) : nullptr;
   const ScanArgs& a = q.f;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.B > 0) prepare(l, ws, a, q.d_last, q.d_h0, st);

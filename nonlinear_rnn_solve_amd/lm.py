@@ -20,7 +20,7 @@ from .api import PararnnError
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpararnn_lm.so")
 ABI_VERSION = 1
-SCAN_CHUNK = 128          # PARARNN_LM_SCAN_CHUNK
+SCAN_CHUNK = 64           # PARARNN_LM_SCAN_CHUNK
 NORM_MAX_D = 16384        # PARARNN_LM_NORM_MAX_D
 MAX_TOP = 32              # PARARNN_LM_MAX_TOP
 

@@ -80,7 +80,7 @@ def check(args, c=8.0, cu=None, seqs=None):
     close(got["d_lam"], ref["d_lam"], 4 * unit * (terms + 1e-6), "d_lam")
 
 
-SHAPES = [(1, 1, 1), (2, 1, 64), (5, 1, 1030), (3, 5, 7), (1, 16, 130), (2, 17, 33), (1, 127, 64), (1, 128, 65), (2, 129, 66),
+SHAPES = [(1, 1, 1), (2, 1, 64), (5, 1, 1030), (3, 5, 7), (1, 16, 130), (2, 17, 33), (2, 63, 65), (1, 64, 32), (2, 65, 70), (1, 127, 64), (1, 128, 65), (2, 129, 66),
           (1, 300, 1), (2, 256, 128), (2, 1000, 48), (1, 4099, 20), (3, 640, 200)]
 
 
@@ -102,7 +102,7 @@ def test_no_state(dtype):
     check(make(2, 200, 40, dtype, seed=4, state=False))
 
 
-PACKED = [(300, [0, 1, 2, 150, 300]), (300, [0, 0, 128, 128, 129, 256, 300, 300]), (300, [0, 300]), (5, [0, 0, 2, 2, 5]),
+PACKED = [(300, [0, 1, 2, 150, 300]), (200, [0, 63, 64, 65, 128, 200]), (300, [0, 0, 128, 128, 129, 256, 300, 300]), (300, [0, 300]), (5, [0, 0, 2, 2, 5]),
           (1, [0, 0, 1, 1]), (512, [0, 127, 128, 255, 256, 257, 512]), (700, [0] + list(range(1, 700, 7)) + [700]),
           (16, [0, 16, 16]), (1500, [0, 1490, 1500]), (1500, [0, 3, 1500])]
 

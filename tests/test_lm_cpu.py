@@ -80,7 +80,7 @@ def test_scan_validation(lib):
     assert lib.pararnn_lm_gated_scan(scan_problem(), P, None, None, None, WS, BIG, None) == -1
     assert lib.pararnn_lm_scan_workspace_bytes(2, 300, 64) > 0
     assert lib.pararnn_lm_scan_workspace_bytes(-1, 300, 64) == 0
-    assert [lib.pararnn_lm_scan_chunks(t) for t in (0, 1, 128, 129)] == [0, 1, 1, 2]
+    assert [lib.pararnn_lm_scan_chunks(t) for t in (0, 1, lm.SCAN_CHUNK, lm.SCAN_CHUNK + 1)] == [0, 1, 1, 2]
 
 
 def test_scan_gradient_validation(lib):
