@@ -50,18 +50,6 @@ template <typename T, int V> struct Vec {
     else return __uint_as_float(v % 2 ? w[v / 2] & 0xffff0000u : w[v / 2] << 16);
   }
 };
-template <int N> struct alignas(4 * N) Words { uint32_t w[N]; };
-template <typename T, int V> DEV Vec<T, V> load_vec(const T* p) {
-  Vec<T, V> r;
-  if constexpr (sizeof(T) * V == 2) {
-    r.w[0] = p->u;
-  } else {
-    const auto q = *reinterpret_cast<const Words<Vec<T, V>::N>*>(p);
-#pragma unroll
-    for (int k = 0; k < Vec<T, V>::N; ++k) r.w[k] = q.w[k];
-  }
-  return r;
-}
 template <typename T, int V> DEV Vec<T, V> pack_vec(const float (&x)[V]) {
   Vec<T, V> r;
 #pragma unroll
@@ -72,16 +60,59 @@ template <typename T, int V> DEV Vec<T, V> pack_vec(const float (&x)[V]) {
   }
   return r;
 }
-template <typename T, int V> DEV void store_vec(T* p, const float (&x)[V]) {
-  if constexpr (V == 1) {
-    *p = from_f32<T>(x[0]);
+
+// The first `n` of V elements at p (all of them where n >= V), as one access at any alignment of the element: the GPU
+// runs in unaligned access mode, so odd row lengths need no narrower loads.  The elements past n are `fill`.
+template <typename T, int V> struct __attribute__((packed, aligned(sizeof(T)))) Loose { uint32_t w[Vec<T, V>::N]; };
+template <typename T, int V> DEV Vec<T, V> load_row(const T* p, int64_t n, T fill) {
+  static_assert(V * sizeof(T) >= 4, "whole words");
+  Vec<T, V> r;
+  if (n >= V) {
+    const auto q = *reinterpret_cast<const Loose<T, V>*>(p);
+#pragma unroll
+    for (int k = 0; k < Vec<T, V>::N; ++k) r.w[k] = q.w[k];
   } else {
-    const Vec<T, V> r = pack_vec<T, V>(x);
-    Words<Vec<T, V>::N> q;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const T e = v < n ? p[v] : fill;
+      if constexpr (sizeof(T) == 4) r.w[v] = __float_as_uint(e);
+      else r.w[v / 2] = v % 2 ? r.w[v / 2] | static_cast<uint32_t>(e.u) << 16 : e.u;
+    }
+  }
+  return r;
+}
+template <typename T, int V> DEV void store_row(T* p, int64_t n, const float (&x)[V]) {
+  const Vec<T, V> r = pack_vec<T, V>(x);
+  if (n >= V) {
+    Loose<T, V> q;
 #pragma unroll
     for (int k = 0; k < Vec<T, V>::N; ++k) q.w[k] = r.w[k];
-    *reinterpret_cast<Words<Vec<T, V>::N>*>(p) = q;
+    *reinterpret_cast<Loose<T, V>*>(p) = q;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v < n) p[v] = from_f32<T>(x[v]);
   }
+}
+
+// Sums over 16 consecutive lanes (a DPP row), over a wave: the same value for every lane, in a fixed order.
+template <int CTRL> DEV float dpp(float v) {
+  return __uint_as_float(static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), CTRL, 0xf, 0xf, true)));
+}
+DEV float row_sum(float v) {
+  v += dpp<0xb1>(v);    // quad_perm [1,0,3,2]
+  v += dpp<0x4e>(v);    // quad_perm [2,3,0,1]
+  v += dpp<0x141>(v);   // row_half_mirror
+  v += dpp<0x140>(v);   // row_mirror
+  return v;
+}
+DEV float read_lane(float v, int lane) {
+  return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(v)), lane)));
+}
+DEV float wave_sum(float v) {
+  v = row_sum(v);
+  return (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
 }
 
 // ---------------- host: argument checks ----------------

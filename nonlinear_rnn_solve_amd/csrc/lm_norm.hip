@@ -1,22 +1,50 @@
 // lm_norm.hip -- layer normalisation of pararnn_lm.h and its gradients.
+//
+// Both directions are bound by memory: a row is read once into registers (up to 16 columns a lane), reduced there and
+// written.  The mean comes first and the variance is summed about it, since the row is at hand.
+
+#include <algorithm>
+#include <type_traits>
 
 #include "lm_common.h"
 
 namespace lm {
 
-constexpr int NT = 256;
+// A row is held by LPR lanes (16, 64, 256 or 1024) of CPL columns each (8 or 16), in vectors of 16 bytes: vector k of lane l
+// is columns (k LPR + l) V and on.
+template <typename T, int LPR_, int CPL_> struct Shape {
+  static constexpr int LPR = LPR_, CPL = CPL_, V = 16 / sizeof(T), NV = CPL / V;
+};
 
-// the workgroup's sum of v, the same for every thread: lanes by a butterfly, then the waves in order
-DEV float block_sum(float v, float (&sh)[NT / WAVE]) {
+// Sums of K values over the LPR lanes of a row, the same for each of them: lanes, then (LPR > 64) waves in order through
+// shared memory, which alternates between two sets so that one barrier a call is enough.  Every thread of the workgroup
+// calls it.
+template <int LPR, int K, int NT> struct RowSum {
+  static constexpr int WPR = LPR > WAVE ? LPR / WAVE : 1;
+  float sh[LPR > WAVE ? 2 : 1][K][LPR > WAVE ? NT / WAVE : 1];
+};
+template <int LPR, int K, int NT> DEV void row_sums(float (&v)[K], RowSum<LPR, K, NT>& s, int& turn) {
+  if constexpr (LPR == 16) {
 #pragma unroll
-  for (int o = WAVE / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, WAVE);
-  __syncthreads();
-  if (threadIdx.x % WAVE == 0) sh[threadIdx.x / WAVE] = v;
-  __syncthreads();
-  float s = 0.0f;
+    for (int k = 0; k < K; ++k) v[k] = row_sum(v[k]);
+  } else {
 #pragma unroll
-  for (int w = 0; w < NT / WAVE; ++w) s += sh[w];
-  return s;
+    for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
+    if constexpr (LPR > WAVE) {
+      const int wave = threadIdx.x / WAVE, first = wave / s.WPR * s.WPR;
+      if (threadIdx.x % WAVE == 0)
+#pragma unroll
+        for (int k = 0; k < K; ++k) s.sh[turn][k][wave] = v[k];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        v[k] = s.sh[turn][k][first];
+#pragma unroll
+        for (int w = 1; w < s.WPR; ++w) v[k] += s.sh[turn][k][first + w];
+      }
+      turn ^= 1;
+    }
+  }
 }
 
 struct NormArgs {
@@ -24,40 +52,73 @@ struct NormArgs {
   const float *weight, *bias;
   void *y, *sum;
   float* stats;
-  int64_t sx, sres, sy, ssum, D;
+  int64_t sx, sres, sy, ssum, N, D;
   float eps;
 };
 
-// one row a workgroup: the row is read once for the mean, once for the variance about it, once to write
-template <typename T>
+template <typename T, class S, int NT>
 __global__ __launch_bounds__(NT) void k_norm(const NormArgs p) {
-  __shared__ float sh[NT / WAVE];
-  const int64_t n = blockIdx.x;
-  const T* x = static_cast<const T*>(p.x) + n * p.sx;
-  const T* res = p.res ? static_cast<const T*>(p.res) + n * p.sres : nullptr;
-  T* y = static_cast<T*>(p.y) + n * p.sy;
-  T* sum = p.sum ? static_cast<T*>(p.sum) + n * p.ssum : nullptr;
-  float s = 0.0f;
-  for (int64_t d = threadIdx.x; d < p.D; d += NT) {
-    float v = to_f32(x[d]);
-    if (res) {
-      const T t = from_f32<T>(v + to_f32(res[d]));
-      sum[d] = t;
-      v = to_f32(t);
+  constexpr int LPR = S::LPR, V = S::V, NV = S::NV;
+  __shared__ RowSum<LPR, 1, NT> sh;
+  int turn = 0;
+  const int lane = threadIdx.x % LPR;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * (NT / LPR) + threadIdx.x / LPR;
+  const bool on = n < p.N;
+  const T* x = static_cast<const T*>(p.x) + (on ? n : 0) * p.sx;
+  const T* res = p.res ? static_cast<const T*>(p.res) + (on ? n : 0) * p.sres : nullptr;
+  float v[NV][V];
+  {
+    Vec<T, V> a[NV], b[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = static_cast<int64_t>(k * LPR + lane) * V;
+      a[k] = load_row<T, V>(x + c, p.D - c, T{});
+      if (res) b[k] = load_row<T, V>(res + c, p.D - c, T{});
     }
-    s += v;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = static_cast<int64_t>(k * LPR + lane) * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[k][e] = a[k].get(e);
+      if (res) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[k][e] = to_f32(from_f32<T>(v[k][e] + b[k].get(e)));
+        if (on) store_row<T, V>(static_cast<T*>(p.sum) + n * p.ssum + c, p.D - c, v[k]);
+      }
+    }
   }
-  const T* in = res ? sum : x;   // each thread reads back what it wrote itself
-  const float mean = block_sum(s, sh) / static_cast<float>(p.D);
-  s = 0.0f;
-  for (int64_t d = threadIdx.x; d < p.D; d += NT) {
-    const float v = to_f32(in[d]) - mean;
-    s = fmaf(v, v, s);
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[0] += v[k][e];   // columns past D are 0
+  row_sums(s, sh, turn);
+  const float mean = s[0] / static_cast<float>(p.D);
+  s[0] = 0.0f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      v[k][e] = (k * LPR + lane) * V + e < p.D ? v[k][e] - mean : 0.0f;
+      s[0] = fmaf(v[k][e], v[k][e], s[0]);
+    }
+  row_sums(s, sh, turn);
+  if (!on) return;
+  const float rstd = 1.0f / sqrtf(s[0] / static_cast<float>(p.D) + p.eps);
+  T* y = static_cast<T*>(p.y) + n * p.sy;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int64_t c = static_cast<int64_t>(k * LPR + lane) * V;
+    if (c >= p.D) break;
+    float o[V];
+    const Vec<float, V> w = load_row<float, V>(p.weight + c, p.D - c, 0.0f);
+    Vec<float, V> b{};
+    if (p.bias) b = load_row<float, V>(p.bias + c, p.D - c, 0.0f);
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = fmaf(v[k][e] * rstd, w.get(e), b.get(e));
+    store_row<T, V>(y + c, p.D - c, o);
   }
-  const float rstd = 1.0f / sqrtf(block_sum(s, sh) / static_cast<float>(p.D) + p.eps);
-  for (int64_t d = threadIdx.x; d < p.D; d += NT)
-    y[d] = from_f32<T>(fmaf((to_f32(in[d]) - mean) * rstd, p.weight[d], p.bias ? p.bias[d] : 0.0f));
-  if (p.stats && threadIdx.x == 0) {
+  if (p.stats && lane == 0) {
     p.stats[2 * n] = mean;
     p.stats[2 * n + 1] = rstd;
   }
@@ -68,49 +129,147 @@ struct NormGradArgs {
   const float *weight, *stats;
   void* dx;
   int64_t sdy, ss, sdsum, sdx, N, D;
-  float *dweight, *dbias;
+  float* part;   // [workgroups][2][D] sums of dy n and of dy over a workgroup's rows, or null
 };
 
-template <typename T>
-__global__ __launch_bounds__(NT) void k_norm_dx(const NormGradArgs p) {
-  __shared__ float sh[NT / WAVE];
-  const int64_t n = blockIdx.x;
-  const T* dy = static_cast<const T*>(p.dy) + n * p.sdy;
-  const T* s = static_cast<const T*>(p.s) + n * p.ss;
-  const T* dsum = p.dsum ? static_cast<const T*>(p.dsum) + n * p.sdsum : nullptr;
-  T* dx = static_cast<T*>(p.dx) + n * p.sdx;
-  const float mean = p.stats[2 * n], rstd = p.stats[2 * n + 1];
-  float c1 = 0.0f, c2 = 0.0f;
-  for (int64_t d = threadIdx.x; d < p.D; d += NT) {
-    const float g = to_f32(dy[d]) * p.weight[d];
-    c1 += g;
-    c2 = fmaf(g, (to_f32(s[d]) - mean) * rstd, c2);
+// A workgroup takes NT / LPR rows at a time, kGradGroups workgroups in turn, and keeps the parameter sums of its lanes'
+// columns in registers; its row groups add theirs up in order through shared memory at the end.
+constexpr int kGradThreads = 1024, kGradGroups = 256;
+template <typename T, class S>
+__global__ __launch_bounds__(kGradThreads) void k_norm_grad(const NormGradArgs p) {
+  constexpr int LPR = S::LPR, V = S::V, NV = S::NV, NT = kGradThreads, RG = NT / LPR;
+  __shared__ RowSum<LPR, 2, NT> sh;
+  __shared__ float sh_p[RG > 1 ? 2 : 1][RG > 1 ? LPR * S::CPL : 1];
+  int turn = 0;
+  const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
+  const float inv = 1.0f / static_cast<float>(p.D);
+  float sw[NV][V], sb[NV][V];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e) sw[k][e] = sb[k][e] = 0.0f;
+  for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * RG; n0 < p.N; n0 += static_cast<int64_t>(gridDim.x) * RG) {
+    const int64_t n = n0 + group < p.N ? n0 + group : p.N - 1;
+    const bool on = n0 + group < p.N;
+    const T* dy = static_cast<const T*>(p.dy) + n * p.sdy;
+    const T* s = static_cast<const T*>(p.s) + n * p.ss;
+    const T* dsum = p.dsum ? static_cast<const T*>(p.dsum) + n * p.sdsum : nullptr;
+    Vec<T, V> a[NV], g[NV], ds[NV];
+    Vec<float, V> w[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = static_cast<int64_t>(k * LPR + lane) * V;
+      a[k] = load_row<T, V>(s + c, p.D - c, T{});
+      g[k] = load_row<T, V>(dy + c, p.D - c, T{});
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = static_cast<int64_t>(k * LPR + lane) * V;
+      if (dsum) ds[k] = load_row<T, V>(dsum + c, p.D - c, T{});
+      w[k] = load_row<float, V>(p.weight + c, p.D - c, 0.0f);
+    }
+    const float mean = p.stats[2 * n], rstd = p.stats[2 * n + 1];
+    float c12[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = g[k].get(e), xn = (a[k].get(e) - mean) * rstd, t = d * w[k].get(e);   // past D: d = 0
+        c12[0] += t;
+        c12[1] = fmaf(t, xn, c12[1]);
+        if (on) {
+          sw[k][e] = fmaf(d, xn, sw[k][e]);
+          sb[k][e] += d;
+        }
+      }
+    row_sums(c12, sh, turn);
+    const float c1 = c12[0] * inv, c2 = c12[1] * inv;
+    if (on) {
+      T* dx = static_cast<T*>(p.dx) + n * p.sdx;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int64_t c = static_cast<int64_t>(k * LPR + lane) * V;
+        float o[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float xn = (a[k].get(e) - mean) * rstd;
+          o[e] = rstd * (fmaf(g[k].get(e), w[k].get(e), -c1) - xn * c2);
+          if (dsum) o[e] += ds[k].get(e);
+        }
+        store_row<T, V>(dx + c, p.D - c, o);
+      }
+    }
   }
-  c1 = block_sum(c1, sh) / static_cast<float>(p.D);
-  c2 = block_sum(c2, sh) / static_cast<float>(p.D);
-  for (int64_t d = threadIdx.x; d < p.D; d += NT) {
-    const float g = to_f32(dy[d]) * p.weight[d], xn = (to_f32(s[d]) - mean) * rstd;
-    float v = rstd * (g - c1 - xn * c2);
-    if (dsum) v += to_f32(dsum[d]);
-    dx[d] = from_f32<T>(v);
+  if (!p.part) return;
+  if constexpr (RG > 1) {
+    for (int r = 0; r < RG; ++r) {
+      __syncthreads();
+      if (group == r)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const int c = (k * LPR + lane) * V + e;
+            sh_p[0][c] = (r ? sh_p[0][c] : 0.0f) + sw[k][e];
+            sh_p[1][c] = (r ? sh_p[1][c] : 0.0f) + sb[k][e];
+          }
+    }
+    __syncthreads();
+    float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
+    for (int64_t c = threadIdx.x; c < p.D; c += NT) {
+      out[c] = sh_p[0][c];
+      out[p.D + c] = sh_p[1][c];
+    }
+  } else {
+    float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = static_cast<int64_t>(k * LPR + lane) * V;
+      store_row<float, V>(out + c, p.D - c, sw[k]);
+      store_row<float, V>(out + p.D + c, p.D - c, sb[k]);
+    }
   }
 }
 
-// parameter sums, a column a thread, rows in ascending order (launched before k_norm_dx, which may write over dy)
-template <typename T>
-__global__ __launch_bounds__(WAVE) void k_norm_params(const NormGradArgs p) {
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * WAVE + threadIdx.x;
-  if (d >= p.D) return;
-  float sw = 0.0f, sb = 0.0f;
-  for (int64_t n = 0; n < p.N; ++n) {
-    const float dy = to_f32(static_cast<const T*>(p.dy)[n * p.sdy + d]);
-    const float xn = (to_f32(static_cast<const T*>(p.s)[n * p.ss + d]) - p.stats[2 * n]) * p.stats[2 * n + 1];
-    sw = fmaf(dy, xn, sw);
-    sb += dy;
+// the workgroups' parts [rows][2][D] as d_weight and d_bias: a wave sums every 16th row, eight loads at a time, the
+// waves' sums are added in order
+__global__ __launch_bounds__(1024) void k_norm_params(const float* part, int64_t rows, int64_t D, float* dweight, float* dbias) {
+  __shared__ float sh[16][WAVE];
+  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * WAVE + lane, cc = c < 2 * D ? c : 0;
+  float s = 0.0f;
+  for (int64_t n = wave; n < rows; n += 16 * 8) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = n + u * 16 < rows ? part[(n + u * 16) * 2 * D + cc] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += v[u];
   }
-  if (p.dweight) p.dweight[d] = sw;
-  if (p.dbias) p.dbias[d] = sb;
+  sh[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || c >= 2 * D) return;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += sh[w][lane];
+  float* out = c < D ? dweight : dbias;
+  if (out) out[c < D ? c : c - D] = s;
 }
+
+// calls f with the shape that holds D columns
+template <typename T, class F> static void shape_of(int64_t D, F f) {
+  const auto lanes = [&](auto lpr) {
+    constexpr int L = decltype(lpr)::value;
+    if (D <= L * 8) f(Shape<T, L, 8>{});
+    else f(Shape<T, L, 16>{});
+  };
+  if (D <= 256) lanes(std::integral_constant<int, 16>{});
+  else if (D <= 1024) lanes(std::integral_constant<int, 64>{});
+  else if (D <= 4096) lanes(std::integral_constant<int, 256>{});
+  else lanes(std::integral_constant<int, 1024>{});
+}
+
+static int64_t grad_rows(int64_t D) { return D <= 256 ? 64 : D <= 1024 ? 16 : D <= 4096 ? 4 : 1; }
+static int64_t grad_groups(int64_t N, int64_t D) { return std::min<int64_t>(ceil_div(N, grad_rows(D)), kGradGroups); }
 
 }  // namespace lm
 
@@ -130,15 +289,24 @@ extern "C" pararnn_status pararnn_lm_layer_norm(int dtype, int64_t N, int64_t D,
   if (!plane_ok(N, x_stride) || !plane_ok(N, y_stride) || (residual && (!plane_ok(N, residual_stride) || !plane_ok(N, sum_stride))))
     return PARARNN_ERR_INVALID_ARG;
   if (D > PARARNN_LM_NORM_MAX_D || N > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
-  const NormArgs a{x, residual, weight, bias, y, sum, stats, x_stride, residual_stride, y_stride, sum_stride, D, eps};
+  const NormArgs a{x, residual, weight, bias, y, sum, stats, x_stride, residual_stride, y_stride, sum_stride, N, D, eps};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (dtype == PARARNN_BF16) k_norm<bf16><<<static_cast<unsigned>(N), NT, 0, st>>>(a);
-  else k_norm<float><<<static_cast<unsigned>(N), NT, 0, st>>>(a);
+  const auto run = [&](auto t) {
+    using T = decltype(t);
+    shape_of<T>(D, [&](auto s) {
+      using S = decltype(s);
+      constexpr int NT = S::LPR > 256 ? S::LPR : 256;
+      k_norm<T, S, NT><<<static_cast<unsigned>(ceil_div(N, NT / S::LPR)), NT, 0, st>>>(a);
+    });
+  };
+  if (dtype == PARARNN_BF16) run(bf16{});
+  else run(float{});
   return launched();
 }
 
 extern "C" size_t pararnn_lm_layer_norm_vjp_workspace_bytes(int64_t N, int64_t D) {
-  return sizes_fit(N, D) ? 256 : 0;
+  if (!sizes_fit(N, D) || !sizes_fit(2 * kGradGroups, D)) return 0;
+  return static_cast<size_t>(grad_groups(N, D) * 2 * D * 4 + 256);
 }
 
 extern "C" pararnn_status pararnn_lm_layer_norm_vjp(int dtype, int64_t N, int64_t D, const void* dy, int64_t dy_stride,
@@ -157,16 +325,20 @@ extern "C" pararnn_status pararnn_lm_layer_norm_vjp(int dtype, int64_t N, int64_
     return PARARNN_ERR_INVALID_ARG;
   if (D > PARARNN_LM_NORM_MAX_D || N > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
   if (!ptr_ok(ws, 256) || ws_bytes < pararnn_lm_layer_norm_vjp_workspace_bytes(N, D)) return PARARNN_ERR_WORKSPACE;
-  const NormGradArgs a{dy, s, d_sum, weight, stats, d_x, dy_stride, s_stride, d_sum_stride, d_x_stride, N, D, d_weight, d_bias};
+  const bool params = d_weight || d_bias;
+  const int64_t groups = grad_groups(N, D);
+  const NormGradArgs a{dy, s, d_sum, weight, stats, d_x, dy_stride, s_stride, d_sum_stride, d_x_stride, N, D,
+                       params ? static_cast<float*>(ws) : nullptr};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (d_weight || d_bias) {
-    const unsigned g = static_cast<unsigned>(ceil_div(D, WAVE));
-    if (dtype == PARARNN_BF16) k_norm_params<bf16><<<g, WAVE, 0, st>>>(a);
-    else k_norm_params<float><<<g, WAVE, 0, st>>>(a);
-  }
+  const auto run = [&](auto t) {
+    using T = decltype(t);
+    shape_of<T>(D, [&](auto sh) { k_norm_grad<T, decltype(sh)><<<static_cast<unsigned>(groups), kGradThreads, 0, st>>>(a); });
+  };
   if (N > 0) {
-    if (dtype == PARARNN_BF16) k_norm_dx<bf16><<<static_cast<unsigned>(N), NT, 0, st>>>(a);
-    else k_norm_dx<float><<<static_cast<unsigned>(N), NT, 0, st>>>(a);
+    if (dtype == PARARNN_BF16) run(bf16{});
+    else run(float{});
   }
+  if (params)
+    k_norm_params<<<static_cast<unsigned>(ceil_div(2 * D, WAVE)), 1024, 0, st>>>(a.part, groups, D, d_weight, d_bias);
   return launched();
 }
