@@ -1,24 +1,10 @@
 // lm_logp.hip -- log probabilities of given tokens, entropy and top alternatives of pararnn_lm.h, and their gradient.
 
+#include <type_traits>
+
 #include "lm_common.h"
 
 namespace lm {
-
-constexpr int NT = 256;
-
-// combines v over the workgroup with f, the same result for every thread
-template <class V, class F>
-DEV V block_fold(V v, V (&sh)[NT / WAVE], F f) {
-#pragma unroll
-  for (int o = WAVE / 2; o > 0; o >>= 1) v = f(v, __shfl_xor(v, o, WAVE));
-  __syncthreads();
-  if (threadIdx.x % WAVE == 0) sh[threadIdx.x / WAVE] = v;
-  __syncthreads();
-  v = sh[0];
-#pragma unroll
-  for (int w = 1; w < NT / WAVE; ++w) v = f(v, sh[w]);
-  return v;
-}
 
 // A logit and its index as one whole number that orders by (value descending, index ascending) as a larger number
 // first: the value's bits in the order of the values (-0 counts as 0, NaN as -infinity), the index complemented.
@@ -35,84 +21,254 @@ DEV int64_t target_of(const void* t, int bytes, int64_t n) {
 
 struct LogpArgs {
   const void* z;
-  int64_t stride, V;
+  int64_t stride, N, V;
   const void* targets;
   int tbytes, top;
   float *lse, *logp, *entropy, *top_logp;
   int64_t* top_ids;
 };
 
-// one row a workgroup: the maximum, then sum e^{z-m} and sum e^{z-m}(z-m), then one pass for each alternative
-template <typename T>
-__global__ __launch_bounds__(NT) void k_logp(const LogpArgs p) {
-  __shared__ float sh[NT / WAVE];
-  __shared__ uint64_t shk[NT / WAVE];
-  const int64_t n = blockIdx.x;
-  const T* z = static_cast<const T*>(p.z) + n * p.stride;
-  float m = -INFINITY;
-  for (int64_t j = threadIdx.x; j < p.V; j += NT) m = fmaxf(m, to_f32(z[j]));
-  m = block_fold(m, sh, [](float a, float b) { return fmaxf(a, b); });
-  const float base = m == -INFINITY ? 0.0f : m;   // nothing left: every term is 0
-  float s = 0.0f, e = 0.0f;
-  for (int64_t j = threadIdx.x; j < p.V; j += NT) {
-    const float t = to_f32(z[j]) - base, w = hw_exp2(kLog2e * t);
-    s += w;
-    e = fmaf(w, fmaxf(t, -1e30f), e);             // a ruled out token adds 0, not 0 * infinity
+// Running statistics of some logits: their maximum m, z = sum e^{x-m} and s = sum e^{x-m} (x-m), so that
+// ln sum e^x = m + ln z and the entropy is ln z - s / z.  m = -infinity: no token (left) among them, z = s = 0.
+struct Stat { float m, z, s; };
+// t = x - m of a ruled out token is -infinity and its e^t 0: the product is 0, not NaN
+DEV float weighted(float w, float t, float add) { return fmaf(w, fmaxf(t, -1e30f), add); }
+// the same sums about a maximum `to` >= m
+DEV void rebase(Stat& a, float to) {
+  const float d = a.m - (to == -INFINITY ? 0.0f : to), f = hw_exp2(kLog2e * d);
+  a.s = f * weighted(a.z, d, a.s);
+  a.z *= f;
+  a.m = to;
+}
+
+// the statistics of the LPR lanes of a row, joined in a fixed order, for each of them
+template <int LPR> DEV void join(Stat& a, float (&sh)[3][LPR > WAVE ? LPR / WAVE : 1]) {
+  float m = LPR == 16 ? row_max(a.m) : wave_max(a.m);
+  if constexpr (LPR > WAVE) {
+    if (threadIdx.x % WAVE == 0) sh[0][threadIdx.x / WAVE] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < LPR / WAVE; ++w) m = fmaxf(m, sh[0][w]);
   }
-  const auto add = [](float a, float b) { return a + b; };
-  s = block_fold(s, sh, add);
-  e = block_fold(e, sh, add);
-  const bool none = s == 0.0f;
-  const float ls = kLn2 * hw_log2(s);
-  if (threadIdx.x == 0) {
-    if (p.lse) p.lse[n] = none ? -INFINITY : m + ls;
-    if (p.entropy) p.entropy[n] = none ? 0.0f : ls - e / s;
-    if (p.logp) {
-      const int64_t t = target_of(p.targets, p.tbytes, n);
-      p.logp[n] = t < 0 ? 0.0f : t >= p.V ? NAN : none ? -INFINITY : (to_f32(z[t]) - m) - ls;
+  rebase(a, m);
+  a.z = LPR == 16 ? row_sum(a.z) : wave_sum(a.z);
+  a.s = LPR == 16 ? row_sum(a.s) : wave_sum(a.s);
+  if constexpr (LPR > WAVE) {
+    if (threadIdx.x % WAVE == 0) {
+      sh[1][threadIdx.x / WAVE] = a.z;
+      sh[2][threadIdx.x / WAVE] = a.s;
+    }
+    __syncthreads();
+    a.z = sh[1][0];
+    a.s = sh[2][0];
+#pragma unroll
+    for (int w = 1; w < LPR / WAVE; ++w) {
+      a.z += sh[1][w];
+      a.s += sh[2][w];
     }
   }
+}
+
+// Top alternatives.  While the row streams by, each lane remembers its best chunk (16 bytes of logits): the first with
+// its largest value.  With chunks ranked as (value, chunk) keys, the lanes' bests are folded into 64 columns (lane modulo
+// 64); the k-th largest of the 64 is a key that at least k logits of the row reach, so the k alternatives are among the
+// logits whose (value, chunk) reaches it, and those lie with the lanes whose own best does: a few dozen lanes, whose
+// chunks the workgroup reads again.  What passes goes to a list; its entries' ranks are counted and the first k written.
+constexpr int kCols = 64, kList = 512;
+template <int LPR> struct TopShared {
+  uint64_t best[LPR / WAVE][WAVE];
+  uint64_t list[kList];
+  uint64_t bar;
+  uint32_t lanes[LPR];
+  uint32_t n_lanes, n;
+};
+
+template <typename T, int LPR>
+DEV void top_of(const LogpArgs& p, const T* z, int64_t n, uint64_t best, float m, float ls, bool none, TopShared<LPR>& sh) {
+  constexpr int V = 16 / sizeof(T);
+  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  sh.best[wave][lane] = best;
+  if (threadIdx.x == 0) sh.n_lanes = sh.n = 0;
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int w = 1; w < LPR / WAVE; ++w) best = max(best, sh.best[w][lane]);
+    // 0: a lane without a logit.  Keys are unique otherwise (every chunk has one lane).
+    int rank = 0;
+    for (int j = 0; j < kCols; ++j) {
+      const uint64_t o = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(best >> 32), j)) << 32 |
+                         static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(best), j));
+      rank += o > best;
+    }
+    const uint64_t kth = __ballot(rank == p.top - 1 && best != 0);   // one lane, or none: fewer than k columns have a logit
+    const int at = kth ? __ffsll(static_cast<unsigned long long>(kth)) - 1 : 0;
+    const uint64_t bar = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(best >> 32), at)) << 32 |
+                         static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(best), at));
+    if (lane == 0) sh.bar = kth ? bar : 0;
+  }
+  __syncthreads();
+  const uint64_t bar = sh.bar;
+  if (sh.best[wave][lane] >= bar && sh.best[wave][lane] != 0) sh.lanes[atomicAdd(&sh.n_lanes, 1u)] = threadIdx.x;
+  __syncthreads();
+  const int64_t chunks = (p.V + V - 1) / V, rounds = (chunks + LPR - 1) / LPR;
+  for (int64_t w = threadIdx.x; w < rounds * sh.n_lanes; w += LPR) {
+    const int64_t c = w / sh.n_lanes * LPR + sh.lanes[w % sh.n_lanes];
+    if (c >= chunks) continue;
+    const Vec<T, V> x = load_row<T, V>(z + c * V, p.V - c * V, T{});
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (c * V + e >= p.V || rank_key(x.get(e), static_cast<uint32_t>(c)) < bar) continue;
+      const uint32_t at = atomicAdd(&sh.n, 1u);
+      if (at < kList) sh.list[at] = rank_key(x.get(e), static_cast<uint32_t>(c * V + e));
+    }
+  }
+  __syncthreads();
+  const auto put = [&](int k, uint64_t key) {
+    const int64_t j = static_cast<uint32_t>(~static_cast<uint32_t>(key));
+    p.top_ids[n * p.top + k] = j;
+    p.top_logp[n * p.top + k] = none ? -INFINITY : (to_f32(z[j]) - m) - ls;
+  };
+  const uint32_t count = sh.n;
+  if (count <= kList) {
+    for (uint32_t i = threadIdx.x; i < count; i += LPR) {
+      const uint64_t key = sh.list[i];
+      int rank = 0;
+      for (uint32_t j = 0; j < count; ++j) rank += sh.list[j] > key;
+      if (rank < p.top) put(rank, key);
+    }
+    return;
+  }
+  // a row whose large logits fill fewer than k columns overflows the list: a pass over the row for each alternative
   uint64_t last = ~UINT64_C(0);
   for (int k = 0; k < p.top; ++k) {
-    uint64_t best = 0;
-    for (int64_t j = threadIdx.x; j < p.V; j += NT) {
+    uint64_t next = 0;
+    for (int64_t j = threadIdx.x; j < p.V; j += LPR) {
       const uint64_t key = rank_key(to_f32(z[j]), static_cast<uint32_t>(j));
-      if (key < last && key > best) best = key;
+      if (key < last && key > next) next = key;
     }
-    last = block_fold(best, shk, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-    if (threadIdx.x == 0) {
-      const int64_t j = static_cast<uint32_t>(~static_cast<uint32_t>(last));
-      p.top_ids[n * p.top + k] = j;
-      p.top_logp[n * p.top + k] = none ? -INFINITY : (to_f32(z[j]) - m) - ls;
+    __syncthreads();
+#pragma unroll
+    for (int o = WAVE / 2; o > 0; o >>= 1) next = max(next, static_cast<uint64_t>(__shfl_xor(static_cast<unsigned long long>(next), o, WAVE)));
+    if (lane == 0) sh.best[wave][0] = next;
+    __syncthreads();
+    last = sh.best[0][0];
+#pragma unroll
+    for (int w = 1; w < LPR / WAVE; ++w) last = max(last, sh.best[w][0]);
+    if (threadIdx.x == 0) put(k, last);
+  }
+}
+
+// A row is read once by LPR lanes, chunk by chunk, kAhead chunks of a lane at a time.
+constexpr int kAhead = 4;
+template <typename T, int LPR, bool TOP>
+__global__ __launch_bounds__(LPR > WAVE ? LPR : WAVE) void k_logp(const LogpArgs p) {
+  constexpr int V = 16 / sizeof(T), NT = LPR > WAVE ? LPR : WAVE;
+  __shared__ float sh[3][LPR > WAVE ? LPR / WAVE : 1];
+  const int lane = threadIdx.x % LPR;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * (NT / LPR) + threadIdx.x / LPR;
+  const bool on = NT == LPR || n < p.N;
+  const T* z = static_cast<const T*>(p.z) + (on ? n : 0) * p.stride;
+  Stat a{-INFINITY, 0.0f, 0.0f};
+  uint32_t best = 0;
+  bool any = false;
+  for (int64_t c0 = lane; c0 * V < p.V; c0 += LPR * kAhead) {
+    Vec<T, V> x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t c = c0 + u * LPR;
+      if (c * V < p.V) x[u] = load_row<T, V>(z + c * V, p.V - c * V, from_f32<T>(-INFINITY));
+      else
+#pragma unroll
+        for (int k = 0; k < Vec<T, V>::N; ++k) x[u].w[k] = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
     }
+    float m = a.m;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float cm = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < V; ++e) cm = fmaxf(cm, x[u].get(e));
+      if (TOP) {
+        if (cm > m || !any) best = static_cast<uint32_t>(c0 + u * LPR);
+        any = true;
+      }
+      m = fmaxf(m, cm);
+    }
+    if (m > a.m) rebase(a, m);
+    const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float t = x[u].get(e) - base, w = hw_exp2(kLog2e * t);
+        a.z += w;
+        a.s = weighted(w, t, a.s);
+      }
+  }
+  const float own = a.m;
+  join<LPR>(a, sh);
+  const bool none = a.z == 0.0f;
+  const float ls = kLn2 * hw_log2(a.z);
+  if (lane == 0 && on) {
+    if (p.lse) p.lse[n] = none ? -INFINITY : a.m + ls;
+    if (p.entropy) p.entropy[n] = none ? 0.0f : ls - a.s / a.z;
+    if (p.logp) {
+      const int64_t t = target_of(p.targets, p.tbytes, n);
+      p.logp[n] = t < 0 ? 0.0f : t >= p.V ? NAN : none ? -INFINITY : (to_f32(z[t]) - a.m) - ls;
+    }
+  }
+  if constexpr (TOP) {
+    __shared__ TopShared<LPR> top;
+    top_of<T, LPR>(p, z, n, any ? rank_key(own, best) : 0, a.m, ls, none, top);
   }
 }
 
 struct LogpGradArgs {
   const void* z;
-  int64_t stride, V;
+  int64_t stride, N, V;
   const void* targets;
   int tbytes;
   const float *lse, *entropy, *g_logp, *g_entropy;
   void* dz;
-  int64_t dstride;
+  int64_t dstride, segments;
 };
 
-template <typename T>
-__global__ __launch_bounds__(NT) void k_logp_grad(const LogpGradArgs p) {
-  const int64_t n = blockIdx.x;
+// LPR lanes of one row write a segment of kAhead chunks each
+constexpr int kGradThreads = 256;
+template <typename T, int LPR>
+__global__ __launch_bounds__(kGradThreads) void k_logp_grad(const LogpGradArgs p) {
+  constexpr int V = 16 / sizeof(T), RG = kGradThreads / LPR;
+  const int lane = threadIdx.x % LPR;
+  const int64_t block = blockIdx.x, rows = block / p.segments, seg = block - rows * p.segments;
+  const int64_t n = rows * RG + threadIdx.x / LPR;
+  if (n >= p.N) return;
   const T* z = static_cast<const T*>(p.z) + n * p.stride;
   T* dz = static_cast<T*>(p.dz) + n * p.dstride;
+  Vec<T, V> x[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int64_t j = ((seg * kAhead + u) * LPR + lane) * V;
+    if (j < p.V) x[u] = load_row<T, V>(z + j, p.V - j, T{});
+  }
   const int64_t t = p.targets ? target_of(p.targets, p.tbytes, n) : -1;
   const float lse = p.lse[n], g = t < 0 ? 0.0f : t >= p.V ? NAN : p.g_logp[n];
   const float ge = p.g_entropy ? p.g_entropy[n] : 0.0f, h = p.g_entropy ? p.entropy[n] : 0.0f;
   const bool none = lse == -INFINITY;
-  for (int64_t j = threadIdx.x; j < p.V; j += NT) {
-    const float l = none ? -INFINITY : to_f32(z[j]) - lse;
-    const float q = hw_exp2(kLog2e * l);
-    float v = -q * fmaf(ge, fmaxf(l, -1e30f) + h, g);
-    if (j == t && !none) v += g;
-    dz[j] = from_f32<T>(v);
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int64_t j = ((seg * kAhead + u) * LPR + lane) * V;
+    if (j >= p.V) break;
+    float o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float l = none ? -INFINITY : x[u].get(e) - lse, q = hw_exp2(kLog2e * l);
+      o[e] = -q * fmaf(ge, fmaxf(l, -1e30f) + h, g);
+    }
+    const int64_t at = t - j;
+    if (at >= 0 && at < V && !none)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e == at) o[e] += g;
+    store_row<T, V>(dz + j, p.V - j, o);
   }
 }
 
@@ -147,10 +303,24 @@ extern "C" pararnn_status pararnn_lm_token_logprobs(int dtype, int64_t N, int64_
       !ptr_ok(top_logp, 4, top > 0) || !ptr_ok(top_ids, 8, top > 0))
     return PARARNN_ERR_INVALID_ARG;
   if (!ptr_ok(ws, 256) || ws_bytes < pararnn_lm_token_logprobs_workspace_bytes(N, V, top)) return PARARNN_ERR_WORKSPACE;
-  const LogpArgs a{logits, stride, V, targets, target_bytes, top, lse, logp, entropy, top_logp, top_ids};
+  const LogpArgs a{logits, stride, N, V, targets, target_bytes, top, lse, logp, entropy, top_logp, top_ids};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (dtype == PARARNN_BF16) k_logp<bf16><<<static_cast<unsigned>(N), NT, 0, st>>>(a);
-  else k_logp<float><<<static_cast<unsigned>(N), NT, 0, st>>>(a);
+  const auto run = [&](auto t, auto lanes, auto alt) {
+    constexpr int LPR = decltype(lanes)::value, NT = LPR > WAVE ? LPR : WAVE;
+    k_logp<decltype(t), LPR, decltype(alt)::value><<<static_cast<unsigned>(ceil_div(N, NT / LPR)), NT, 0, st>>>(a);
+  };
+  const auto sized = [&](auto t) {
+    const auto alt = [&](auto lanes) {
+      if (top) run(t, lanes, std::true_type{});
+      else run(t, lanes, std::false_type{});
+    };
+    if (V <= 512 && !top) run(t, std::integral_constant<int, 16>{}, std::false_type{});
+    else if (V <= 4096) alt(std::integral_constant<int, 64>{});
+    else if (V <= 32768) alt(std::integral_constant<int, 256>{});
+    else alt(std::integral_constant<int, 1024>{});
+  };
+  if (dtype == PARARNN_BF16) sized(bf16{});
+  else sized(float{});
   return launched();
 }
 
@@ -163,9 +333,22 @@ extern "C" pararnn_status pararnn_lm_token_logprobs_vjp(int dtype, int64_t N, in
   if (!ptr_ok(lse, 4) || !ptr_ok(g_logp, 4, targets != nullptr) || !ptr_ok(g_entropy, 4, false) ||
       !ptr_ok(entropy, 4, g_entropy != nullptr) || !ptr_ok(d_logits, dtype_size(dtype)) || !plane_ok(N, d_stride))
     return PARARNN_ERR_INVALID_ARG;
-  const LogpGradArgs a{logits, stride, V, targets, target_bytes, lse, entropy, g_logp, g_entropy, d_logits, d_stride};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (dtype == PARARNN_BF16) k_logp_grad<bf16><<<static_cast<unsigned>(N), NT, 0, st>>>(a);
-  else k_logp_grad<float><<<static_cast<unsigned>(N), NT, 0, st>>>(a);
-  return launched();
+  const auto run = [&](auto t, auto lanes) {
+    using T = decltype(t);
+    constexpr int LPR = decltype(lanes)::value;
+    const int64_t segments = ceil_div(V, LPR * kAhead * 16 / static_cast<int64_t>(sizeof(T)));
+    const int64_t blocks = ceil_div(N, kGradThreads / LPR) * segments;
+    if (blocks > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
+    const LogpGradArgs a{logits, stride, N, V, targets, target_bytes, lse, entropy, g_logp, g_entropy, d_logits, d_stride, segments};
+    k_logp_grad<T, LPR><<<static_cast<unsigned>(blocks), kGradThreads, 0, st>>>(a);
+    return launched();
+  };
+  const auto sized = [&](auto t) {
+    const int64_t chunks = ceil_div(V, 16 / static_cast<int64_t>(sizeof(t)));
+    if (chunks <= 16 * kAhead) return run(t, std::integral_constant<int, 16>{});
+    if (chunks <= 64 * kAhead) return run(t, std::integral_constant<int, 64>{});
+    return run(t, std::integral_constant<int, 256>{});
+  };
+  return dtype == PARARNN_BF16 ? sized(bf16{}) : sized(float{});
 }

@@ -103,6 +103,20 @@ def test_ties_and_orders(V, dtype):
     assert torch.equal(res.top_ids.cpu(), plain.top(f64(rows), 32))
 
 
+@pytest.mark.parametrize("V", [3000, 30000, 66000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("top", [1, 31, 32])
+def test_large_logits_in_few_columns(V, dtype, top):
+    # the large logits fill only some of the positions modulo the stride in which a row is read
+    j = torch.arange(V)
+    rows = []
+    for per in (4, 8, 16):
+        for cols in (1, 31, 40):
+            rows.append(torch.where((j // per) % 64 < cols, 10 + j / V, -j / V))
+    z = torch.stack(rows).to(dtype).cuda()
+    assert torch.equal(lm.token_logprobs(z, None, top=top).top_ids.cpu(), plain.top(f64(z), top))
+
+
 def test_rows_with_nothing_left():
     for V in (5, 700, 9000, 70000):
         z, t, g, ge = make(6, V, F32, seed=V)
