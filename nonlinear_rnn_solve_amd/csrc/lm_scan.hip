@@ -140,13 +140,14 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
 // against 72 us; at T = 131072, D = 1024, where the chain of tiles is long, 457 against 575 and 299 against 268 us.
 // W = 8 words at a time against 4 and 16: 299, 418, 296 us at T = 131072 and 65.6, 63.7, 78 us at T = 4096.
 // ------------------------------------------------------------------------------------------------
-constexpr int NW = CT / 16, TW = WAVE, NTH = NW * WAVE, W = 8;
+constexpr int NW = CT / 16, TW = WAVE, NTH = NW * WAVE, W = 8, GS = 8;
 static_assert(NW * 16 == CT && NW >= 2, "16 elements a lane");
 constexpr int SL = 4, NSEG = CT / SL, SW = NSEG / NW;   // steps of a segment, segments of a tile and of a wave
 template <int V> struct Shape { static constexpr int L = 16 / V, Q = L / SL; };   // steps and segments of a lane
 
 struct Grid {
-  uint64_t* words;      // [chunks][chains][TW]
+  uint64_t* words;      // [chunks][chains][TW]: the tiles' maps
+  uint64_t* gwords;     // [chunks / GS][chains][TW]: the groups' maps, then the states leaving them
   uint32_t* tickets;    // a counter for each chain, kTicket words apart; null: one chunk, the tile is the block
   int64_t chunks;
   int32_t chains, ctiles, groups;   // chains = B ctiles: channel tiles of all rows; groups divides it
@@ -168,36 +169,78 @@ DEV void st_word(uint64_t* p, uint32_t hi, float lo) {
 constexpr uint32_t kState = 0xffffffffu, kSign = 0x80000000u;
 DEV uint32_t map_bits(float A) { return A != A ? 0xffc00000u : (__float_as_uint(A) | kSign); }
 
-// the state entering position `pos` (> 0) of a chain, for this lane's channel
-template <bool SEG>
-DEV float lookback(const Grid& g, int64_t pos, int32_t chain, int lane) {
-  const int64_t step = static_cast<int64_t>(g.chains) * TW;
-  const uint64_t* w0 = g.words + (pos - 1) * step + static_cast<int64_t>(chain) * TW;   // uniform
-  while (true) {
-    uint64_t w[W];
+// N words of one channel at `word` - k step for k = 0 .. N-1, those with k >= have not read
+template <int N> DEV void ld_words(const uint64_t* word, int64_t step, int have, uint64_t (&w)[N]) {
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k] = ld_word(w0 - (k < pos ? k : pos - 1) * step + lane);
+  for (int k = 0; k < N; ++k) w[k] = k < have ? ld_word(word - k * step) : 0;   // uniform
+}
+DEV uint32_t hi(uint64_t w) { return static_cast<uint32_t>(w >> 32); }
+DEV float lo(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w)); }
+DEV Aff map_of(uint64_t w) { return {__uint_as_float(hi(w) & ~kSign), lo(w)}; }
+
+// The state entering group `j` > 0 of a chain, for this lane's channel: the nearest state among the N groups before it,
+// advanced by the maps of the groups between, in order.
+template <bool SEG, int N>
+DEV float group_state(const Grid& g, uint32_t j, int32_t chain, int lane) {
+  const int64_t step = static_cast<int64_t>(g.chains) * TW;
+  const uint64_t* word = g.gwords + static_cast<int64_t>(j - 1) * step + static_cast<int64_t>(chain) * TW + lane;
+  while (true) {
+    uint64_t w[N];
+    ld_words(word, step, j < N ? static_cast<int>(j) : N, w);
     int at = -1;          // the nearest state, if every word before it is there
     bool there = true;
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const uint32_t hi = static_cast<uint32_t>(w[k] >> 32);
-      if (there && at < 0 && hi == kState) at = k;
-      there = there && hi != 0;
+    for (int k = 0; k < N; ++k) {
+      if (there && at < 0 && hi(w[k]) == kState) at = k;
+      there = there && hi(w[k]) != 0;
     }
     if (at >= 0) {
       float h = 0.0f;
 #pragma unroll
-      for (int k = W - 1; k >= 0; --k) {
-        const float lo = __uint_as_float(static_cast<uint32_t>(w[k]));
-        const Aff f{__uint_as_float(static_cast<uint32_t>(w[k] >> 32) & ~kSign), lo};
-        if (k == at) h = lo;
-        else if (k < at) h = apply<SEG>(f, h);
+      for (int k = N - 1; k >= 0; --k) {
+        if (k == at) h = lo(w[k]);
+        else if (k < at) h = apply<SEG>(map_of(w[k]), h);
       }
       return h;
     }
     __builtin_amdgcn_s_sleep(1);
   }
+}
+
+// The state entering the tile at `pos`, whose own map is f, for this lane's channel; `first` is the one entering the chain.
+template <bool SEG> DEV float enter_tile(const Grid& g, uint32_t pos, int32_t chain, int lane, const Aff& f, float first) {
+  const int64_t step = static_cast<int64_t>(g.chains) * TW, col = static_cast<int64_t>(chain) * TW + lane;
+  const uint32_t j = pos / GS;
+  const int i = static_cast<int>(pos % GS);
+  const bool more = pos + 1 < g.chunks;
+  uint64_t* own = g.words + pos * step + col;
+  if (more && i + 1 < GS) st_word(own, map_bits(f.A), f.B);
+  uint64_t w[GS - 1];   // the maps of the group's tiles before this one, the nearest first
+  while (true) {
+    ld_words(own - step, step, i, w);
+    bool there = true;
+#pragma unroll
+    for (int k = 0; k < GS - 1; ++k) there = there && (k >= i || hi(w[k]) != 0);
+    if (there) break;
+    __builtin_amdgcn_s_sleep(1);
+  }
+  float h;
+  if (more && i + 1 == GS) {   // the group's last tile: publishes the group's map, then the state leaving it
+    Aff m = map_of(w[GS - 2]);
+#pragma unroll
+    for (int k = GS - 3; k >= 0; --k) m = compose<SEG>(map_of(w[k]), m);
+    m = compose<SEG>(f, m);
+    uint64_t* group = g.gwords + j * step + col;
+    if (j > 0) st_word(group, map_bits(m.A), m.B);
+    h = j > 0 ? group_state<SEG, W>(g, j, chain, lane) : first;
+    st_word(group, kState, apply<SEG>(m, h));
+  } else {
+    h = j > 0 ? group_state<SEG, 4>(g, j, chain, lane) : first;
+  }
+#pragma unroll
+  for (int k = GS - 2; k >= 0; --k)
+    if (k < i) h = apply<SEG>(map_of(w[k]), h);
+  return h;
 }
 
 // what the lanes of a wave wrote to shared memory is there for its other lanes (a wave's accesses are in order; this keeps
@@ -223,19 +266,6 @@ template <bool SEG, bool REV, int N> DEV void spread(const Aff (*m)[TW], float (
     if (k + 1 < N) h = apply<SEG>(m[s][lane], h);
   }
 }
-// publishes the tile's map and the state leaving it; returns the state entering it (`first` where it is the chain's first)
-template <bool SEG> DEV float enter_tile(const Grid& g, uint32_t pos, int32_t chain, int lane, const Aff& f, float first) {
-  uint64_t* word = g.words + (static_cast<int64_t>(pos) * g.chains + chain) * TW;
-  const bool publish = pos + 1 < g.chunks;
-  float h = first;
-  if (pos > 0) {
-    if (publish) st_word(word + lane, map_bits(f.A), f.B);
-    h = lookback<SEG>(g, pos, chain, lane);
-  }
-  if (publish) st_word(word + lane, kState, apply<SEG>(f, h));
-  return h;
-}
-
 // the tile's place: pos gets its position in the chain
 DEV void take_ticket(const Grid& g, uint32_t (&sh)[2], uint32_t& pos, uint32_t& chain) {
   const uint32_t G = static_cast<uint32_t>(g.groups), per = static_cast<uint32_t>(g.chains) / G;   // chains of a group
@@ -364,25 +394,27 @@ DEV bool rates(const ScanArgs& p, const Tile<V>& tl, float (&k)[V]) {
   return __any(!(own >= -kNear));
 }
 
-// packed sequences: which of the lane's steps begin and which end one (the row's first and last step included)
+// Packed sequences: which of the lane's steps begin and which end one (the row's first and last step included).  The
+// offsets are searched for the wave's 16 steps together, with scalar loads, which do not wait for the planes'.
 template <int V>
 DEV void boundaries(const ScanArgs& p, const Tile<V>& tl, uint32_t& starts, uint32_t& ends) {
+  constexpr int S = V * Shape<V>::L;
+  static_assert(S == 16, "steps of a wave");
+  const int64_t t = tl.t0 + tl.wave * S;
   starts = ends = 0;
-  if (tl.valid <= 0) return;
-  int32_t j = sequence_of(p.cu, p.n, tl.t);
-  if (tl.t == 0 || (j > 0 && p.cu[j] == tl.t)) starts = 1;
-  for (int l = 0; l < tl.valid; ++l) {
-    const int64_t t = tl.t + l + 1;
-    bool next = t == p.T;
-    while (j + 1 < p.n && p.cu[j + 1] <= t) {
-      ++j;
-      next = true;
-    }
-    if (next) {
-      ends |= 1u << l;
-      if (l + 1 < tl.valid) starts |= 2u << l;
-    }
+  if (t >= p.T) return;
+  const int left = static_cast<int>(p.T - t < S ? p.T - t : S);
+  int32_t j = sequence_of(p.cu, p.n, t);
+  if (t == 0 || (j > 0 && p.cu[j] == t)) starts = 1;
+  for (++j; j < p.n; ++j) {   // the sequences that begin after step t
+    const int64_t at = p.cu[j] - t;
+    if (at > left || at < 1) break;   // at < 1: offsets out of order
+    ends |= 1u << (at - 1);
+    if (at < left) starts |= 1u << at;
   }
+  if (t + left == p.T) ends |= 1u << (left - 1);
+  starts = starts >> (tl.slice * Shape<V>::L) & ((1u << Shape<V>::L) - 1);
+  ends = ends >> (tl.slice * Shape<V>::L) & ((1u << Shape<V>::L) - 1);
 }
 
 template <typename T, int V, bool SEG>
@@ -449,7 +481,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
     const int64_t d = tl.c0 + tl.lane;
     float h = 0.0f;
     if (d < p.D) {
-      if (!SEG && tl.pos == 0) h = p.h0 ? p.h0[tl.b * p.D + d] : 0.0f;
+      if (!SEG && tl.pos < GS) h = p.h0 ? p.h0[tl.b * p.D + d] : 0.0f;
       h = enter_tile<SEG>(g, tl.pos, tl.chain, tl.lane, join<SEG, false, NW>(sh_wave, tl.lane), h);
       if (p.carry) {
         float in = h;
@@ -572,7 +604,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
   if (tl.wave == 0) {
     float mu = 0.0f;
     if (dl < p.D) {
-      if (!SEG && tl.pos == 0) mu = q.d_last ? q.d_last[tl.b * p.D + dl] : 0.0f;
+      if (!SEG && tl.pos < GS) mu = q.d_last ? q.d_last[tl.b * p.D + dl] : 0.0f;
       mu = enter_tile<SEG>(g, tl.pos, tl.chain, tl.lane, join<SEG, true, NW>(sh_wrev, tl.lane), mu);
     }
     spread<SEG, true, NW>(sh_wrev, sh_wmu, tl.lane, mu);
@@ -722,9 +754,9 @@ static ScanArgs scan_args(const pararnn_lm_scan* p) {
   return a;
 }
 
-// the workspace: [tickets][words][parts]
+// the workspace: [tickets][words][group words][parts]
 struct Layout {
-  int64_t chunks, ctiles, tiles, tickets, words, parts, total;   // the last four in bytes
+  int64_t chunks, ctiles, tiles, tickets, words, gwords, parts, total;   // the last five in bytes
 };
 static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
   if (!sizes_fit(B, T, D) || !sizes_fit(B, D + TW, CT)) return false;
@@ -733,8 +765,9 @@ static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
   o.tiles = B * o.ctiles * o.chunks;
   o.words = o.chunks > 1 ? o.tiles * TW * 8 : 0;
   o.tickets = o.chunks > 1 ? B * o.ctiles * kTicket * 4 : 0;
+  o.gwords = B * o.ctiles * (o.chunks / GS) * TW * 8;
   o.parts = B * o.chunks * D * 4;
-  o.total = 256 + o.tickets + o.words + o.parts;
+  o.total = 256 + o.tickets + o.words + o.gwords + o.parts;
   return true;
 }
 
@@ -758,7 +791,7 @@ static void pick(int dtype, bool vec, bool seg, F f) {
 // clears the words where there is more than one chunk, and hands states through empty sequences
 static void prepare(const Layout& l, void* ws, const ScanArgs& a, const float* in, float* out, hipStream_t st) {
   const bool empty = out && (a.cu || a.T == 0);
-  const int64_t n16 = (l.tickets + l.words) / 16;
+  const int64_t n16 = (l.tickets + l.words + l.gwords) / 16;
   if (!n16 && !empty) return;
   const int64_t work = empty ? std::max(n16, a.B * a.n * a.D) : n16;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(ceil_div(work, 256), 2048));
@@ -766,7 +799,7 @@ static void prepare(const Layout& l, void* ws, const ScanArgs& a, const float* i
 }
 static Grid grid_of(const Layout& l, void* ws, int64_t B) {
   char* w = static_cast<char*>(ws);
-  return Grid{reinterpret_cast<uint64_t*>(w + l.tickets), l.chunks > 1 ? reinterpret_cast<uint32_t*>(w) : nullptr, l.chunks,
+  return Grid{reinterpret_cast<uint64_t*>(w + l.tickets), reinterpret_cast<uint64_t*>(w + l.tickets + l.words), l.chunks > 1 ? reinterpret_cast<uint32_t*>(w) : nullptr, l.chunks,
               static_cast<int32_t>(B * l.ctiles), static_cast<int32_t>(l.ctiles), std::gcd(static_cast<int32_t>(B * l.ctiles), 8)};
 }
 
@@ -838,7 +871,7 @@ extern "C" pararnn_status pararnn_lm_gated_scan_vjp(const pararnn_lm_scan* prob,
   for (int k = 0; k < 2; ++k) {
     q.sdh[k] = gr->sdh[k]; q.sdx[k] = gr->sdx[k]; q.sdr[k] = gr->sdr[k]; q.sdi[k] = gr->sdi[k];
   }
-  q.part = gr->d_lam ? reinterpret_cast<float*>(static_cast<char*>(ws) + l.tickets + l.words) : nullptr;
+  q.part = gr->d_lam ? reinterpret_cast<float*>(static_cast<char*>(ws) + l.tickets + l.words + l.gwords) : nullptr;
   const ScanArgs& a = q.f;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.B > 0) prepare(l, ws, a, q.d_last, q.d_h0, st);
