@@ -124,42 +124,48 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
 // entering the tile from the tiles before it and gives every wave its entering state, from which each wave finds its
 // segments' and the lanes walk their steps.  Inputs are read once.
 //
-// Between tiles a 64-bit word for each (tile, channel) carries either the tile's map or, once known, the state leaving
-// it.  a is in [0, 1], so the sign bit of A marks a word as written: zero = nothing yet, (A | sign, B) = the map,
-// (~0, h) = the state.  A tile reads the words of the W tiles before it at once and applies the maps after the nearest
-// state, in order: the result is the sequential chain of maps, whichever words had come, so every run gives the same
-// bits.  Words are relaxed device-scope atomics and carry their own validity: no fences.
+// Between tiles.  Each tile publishes its map for each channel as a 64-bit word; GS tiles of a chain form a group, whose
+// last tile joins their maps to the group's and publishes that, then finds the state entering the group -- the nearest
+// state among the W groups before it, advanced by the maps of those between -- and replaces the group's map by the state
+// leaving it.  Every tile's entering state is its group's, advanced by the maps of the group's tiles before it.  So a
+// state travels 64 tiles in one round trip through memory, and what is composed with what is fixed: every run gives the
+// same bits.  a is in [0, 1], so the sign bit of A marks a word as written: zero = nothing yet, (A | sign, B) = a map,
+// (~0, h) = a state.  Words are relaxed device-scope atomics and carry their own validity: no fences.
 //
 // A tile takes its place from a ticket counter, so those it waits for have been started before it.  One counter hands
-// out a ticket in 13 ns, which bounded the whole scan; the chains therefore form `groups` groups with a counter each
-// (groups divides the number of chains, so all groups have as many tiles).  A workgroup starts with a group that is no
-// function of its XCD (the block number modulo 8): chains bound to an XCD cost 25% at T = 131072, D = 1024.
+// out a ticket in 13 ns, which bounded the whole scan; the chains therefore form up to 8 classes with a counter each
+// (their number divides the chains', so all have as many tiles).  A workgroup starts with a class that is no function of
+// its XCD (the block number modulo 8): chains bound to an XCD cost 25% at T = 131072, D = 1024.
 //
-// 64 steps a tile (4 waves) against 128 (8 waves), bf16: the gradient at B = 2, T = 4096, D = 4096 118 against 151 us,
-// since its 150 registers leave 12 waves on a CU in workgroups of 4 and 8 in workgroups of 8; the forward scan there 65.6
-// against 72 us; at T = 131072, D = 1024, where the chain of tiles is long, 457 against 575 and 299 against 268 us.
-// W = 8 words at a time against 4 and 16: 299, 418, 296 us at T = 131072 and 65.6, 63.7, 78 us at T = 4096.
+// Bound by memory for float32, by memory and vector instructions about equally for bfloat16 (56% and 54% of the issue
+// slots in the forward and the gradient kernel).  Measured, bf16 (wide: B = 2, T = 4096, D = 4096; long: B = 1, T = 131072,
+// D = 1024): forward 62.6 and 251 us (4.3 TB/s), gradient 111 and 446 us (4.2 TB/s); a copy runs at 5.1 TB/s.
+//  - 64 steps a tile (4 waves) against 128 (8 waves): gradient 118 against 151 us (wide), since its 150 registers leave
+//    12 waves on a CU in workgroups of 4 and 8 in workgroups of 8; forward 66 against 72.  32 elements a lane: 66 and 124.
+//  - groups against a look-back over the W tiles before: forward 257 against 297 us (long).  Groups of 16: 325.
+//  - stores that do not stay in the caches: float32 B = 8, T = 2048, D = 1000 forward 69 against 81 us; wide 62.6 against 64.0.
 // ------------------------------------------------------------------------------------------------
-constexpr int NW = CT / 16, TW = WAVE, NTH = NW * WAVE, W = 8, GS = 8;
-static_assert(NW * 16 == CT && NW >= 2, "16 elements a lane");
+constexpr int EPL = 16, NW = CT / EPL, TW = WAVE, NTH = NW * WAVE, W = 8, GS = 8;
+static_assert(NW * EPL == CT && NW >= 2, "EPL elements a lane");
+constexpr int kStream = 2;   // cache policy of a buffer store: non-temporal
 constexpr int SL = 4, NSEG = CT / SL, SW = NSEG / NW;   // steps of a segment, segments of a tile and of a wave
-template <int V> struct Shape { static constexpr int L = 16 / V, Q = L / SL; };   // steps and segments of a lane
+template <int V> struct Shape { static constexpr int L = EPL / V, Q = L / SL; };   // steps and segments of a lane
 
 struct Grid {
   uint64_t* words;      // [chunks][chains][TW]: the tiles' maps
   uint64_t* gwords;     // [chunks / GS][chains][TW]: the groups' maps, then the states leaving them
-  uint32_t* tickets;    // a counter for each chain, kTicket words apart; null: one chunk, the tile is the block
+  uint32_t* tickets;    // a counter for each class of chains, kTicket words apart; null: one chunk, the tile is the block
   int64_t chunks;
-  int32_t chains, ctiles, groups;   // chains = B ctiles: channel tiles of all rows; groups divides it
+  int32_t chains, ctiles, classes;   // chains = B ctiles: channel tiles of all rows; chain c is of class c modulo classes
 };
 
-constexpr int kTicket = 32;   // 128 bytes: counters of different chains share no cache line
+constexpr int kTicket = 32, kClasses = 8;   // 128 bytes: counters share no cache line
 
 struct Aff { float A, B; };
 // the map of `later` after `earlier`; with packed sequences A = 0 is a cut, which nothing crosses, not even a NaN
 template <bool SEG> DEV float apply(const Aff& f, float h) { return SEG && f.A == 0.0f ? f.B : fmaf(f.A, h, f.B); }
 template <bool SEG> DEV Aff compose(const Aff& later, const Aff& earlier) {
-  return {later.A * earlier.A, apply<SEG>(later, earlier.B)};
+  return {SEG && later.A == 0.0f ? 0.0f : later.A * earlier.A, apply<SEG>(later, earlier.B)};
 }
 
 DEV uint64_t ld_word(const uint64_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
@@ -268,7 +274,7 @@ template <bool SEG, bool REV, int N> DEV void spread(const Aff (*m)[TW], float (
 }
 // the tile's place: pos gets its position in the chain
 DEV void take_ticket(const Grid& g, uint32_t (&sh)[2], uint32_t& pos, uint32_t& chain) {
-  const uint32_t G = static_cast<uint32_t>(g.groups), per = static_cast<uint32_t>(g.chains) / G;   // chains of a group
+  const uint32_t G = static_cast<uint32_t>(g.classes), per = static_cast<uint32_t>(g.chains) / G;   // chains of a class
   if (!g.tickets) {
     pos = 0;
     chain = blockIdx.x;
@@ -368,10 +374,10 @@ struct Plane {
     const Vec<T, V> r = pack_vec<T, V>(x);
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    if constexpr (V * sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(r.w[0]), at(l), off, 0, 0);
-    else if constexpr (V * sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(r.w[0], at(l), off, 0, 0);
-    else if constexpr (V * sizeof(T) == 8) __builtin_amdgcn_raw_buffer_store_b64(u32x2{r.w[0], r.w[1]}, at(l), off, 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b128(u32x4{r.w[0], r.w[1], r.w[2], r.w[3]}, at(l), off, 0, 0);
+    if constexpr (V * sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(r.w[0]), at(l), off, 0, kStream);
+    else if constexpr (V * sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(r.w[0], at(l), off, 0, kStream);
+    else if constexpr (V * sizeof(T) == 8) __builtin_amdgcn_raw_buffer_store_b64(u32x2{r.w[0], r.w[1]}, at(l), off, 0, kStream);
+    else __builtin_amdgcn_raw_buffer_store_b128(u32x4{r.w[0], r.w[1], r.w[2], r.w[3]}, at(l), off, 0, kStream);
   }
 };
 
@@ -399,7 +405,7 @@ DEV bool rates(const ScanArgs& p, const Tile<V>& tl, float (&k)[V]) {
 template <int V>
 DEV void boundaries(const ScanArgs& p, const Tile<V>& tl, uint32_t& starts, uint32_t& ends) {
   constexpr int S = V * Shape<V>::L;
-  static_assert(S == 16, "steps of a wave");
+  static_assert(S == EPL && S <= 32, "the steps of a wave are bits of a word");
   const int64_t t = tl.t0 + tl.wave * S;
   starts = ends = 0;
   if (t >= p.T) return;
@@ -413,8 +419,8 @@ DEV void boundaries(const ScanArgs& p, const Tile<V>& tl, uint32_t& starts, uint
     if (at < left) starts |= 1u << at;
   }
   if (t + left == p.T) ends |= 1u << (left - 1);
-  starts = starts >> (tl.slice * Shape<V>::L) & ((1u << Shape<V>::L) - 1);
-  ends = ends >> (tl.slice * Shape<V>::L) & ((1u << Shape<V>::L) - 1);
+  starts = starts >> (tl.slice * Shape<V>::L) & (~0u >> (32 - Shape<V>::L));
+  ends = ends >> (tl.slice * Shape<V>::L) & (~0u >> (32 - Shape<V>::L));
 }
 
 template <typename T, int V, bool SEG>
@@ -764,7 +770,7 @@ static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
   o.ctiles = ceil_div(D, TW);
   o.tiles = B * o.ctiles * o.chunks;
   o.words = o.chunks > 1 ? o.tiles * TW * 8 : 0;
-  o.tickets = o.chunks > 1 ? B * o.ctiles * kTicket * 4 : 0;
+  o.tickets = o.chunks > 1 ? kClasses * kTicket * 4 : 0;
   o.gwords = B * o.ctiles * (o.chunks / GS) * TW * 8;
   o.parts = B * o.chunks * D * 4;
   o.total = 256 + o.tickets + o.words + o.gwords + o.parts;
@@ -774,7 +780,7 @@ static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
 // V consecutive elements from every row and step of a plane are one aligned access, and V slices of a wave lie within
 // 32-bit byte offsets
 static bool wide(const void* p, const int64_t (&s)[2], size_t es, int V, int64_t B, int64_t T) {
-  return aligned(p, es * V) && (B <= 1 || s[0] % V == 0) && (T <= 1 || s[1] % V == 0) && s[1] < (INT64_C(1) << 31) / 64;
+  return aligned(p, es * V) && (B <= 1 || s[0] % V == 0) && (T <= 1 || s[1] % V == 0) && s[1] < (INT64_C(1) << 31) / (EPL * 4);
 }
 
 template <class F>
@@ -800,7 +806,7 @@ static void prepare(const Layout& l, void* ws, const ScanArgs& a, const float* i
 static Grid grid_of(const Layout& l, void* ws, int64_t B) {
   char* w = static_cast<char*>(ws);
   return Grid{reinterpret_cast<uint64_t*>(w + l.tickets), reinterpret_cast<uint64_t*>(w + l.tickets + l.words), l.chunks > 1 ? reinterpret_cast<uint32_t*>(w) : nullptr, l.chunks,
-              static_cast<int32_t>(B * l.ctiles), static_cast<int32_t>(l.ctiles), std::gcd(static_cast<int32_t>(B * l.ctiles), 8)};
+              static_cast<int32_t>(B * l.ctiles), static_cast<int32_t>(l.ctiles), std::gcd(static_cast<int32_t>(B * l.ctiles), kClasses)};
 }
 
 }  // namespace lm

@@ -146,6 +146,25 @@ def test_nothing_leaks_between_sequences(T, cut, bad):
     assert not torch.isfinite(h[:, cut:cut + 3]).any()
 
 
+@pytest.mark.parametrize("T,cut", [(12, 5), (400, 130), (400, 256), (3000, 1500)])
+def test_a_spoilt_decay_gate_stays_in_its_sequence(T, cut):
+    # NaN decays: the products of decays across a boundary are NaN, and must not count there
+    x, r, i, lam, h0, dh, dl = make(2, T, 40, F32, seed=23, n=3, layout="dense")
+    cu = cuda_cu([0, cut, cut + 3, T])
+    clean = lm.gated_scan(x, r, i, lam, h0=h0, cu_seqlens=cu, want_carry=True)
+    gclean = lm.gated_scan_vjp(x, r, i, lam, clean[2], dh, h0=h0, d_last=dl, cu_seqlens=cu)
+    r2 = r.clone()
+    r2[:, cut:cut + 3] = float("nan")
+    h, last, carry = lm.gated_scan(x, r2, i, lam, h0=h0, cu_seqlens=cu, want_carry=True)
+    g = lm.gated_scan_vjp(x, r2, i, lam, carry, dh, h0=h0, d_last=dl, cu_seqlens=cu)
+    keep = [t for t in range(T) if not cut <= t < cut + 3]
+    assert torch.equal(h[:, keep], clean[0][:, keep]) and torch.equal(last[:, [0, 2]], clean[1][:, [0, 2]])
+    for k in ("d_x", "d_r", "d_i"):
+        assert torch.equal(g[k][:, keep], gclean[k][:, keep]), k
+    assert torch.equal(g["d_h0"][:, [0, 2]], gclean["d_h0"][:, [0, 2]])
+    assert torch.isnan(h[:, cut:cut + 3]).all() and torch.isnan(g["d_lam"]).all()
+
+
 def test_gates_at_their_limits():
     # closed decay gate: a = 1, the state is held; wide open input; saturated values: finite everywhere
     B, T, D = 2, 300, 16
