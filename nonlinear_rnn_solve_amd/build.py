@@ -15,13 +15,14 @@ pseudo-random times before publishing look-back words, so that scans walk far
 back.  Only the tests load it; its results must equal libpararnn.so's bit for bit.
 
 libpararnn_lm.so holds the language-model operators of include/pararnn_lm.h, one source file each, compiled in
-parallel and linked.
+parallel and linked; _lm_binding.so is its Python binding (host C++ against torch's headers).
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -31,6 +32,8 @@ LIB = os.path.join(HERE, "libpararnn.so")
 STRESS_LIB = os.path.join(HERE, "libpararnn_stress.so")
 LM_SRCS = [os.path.join(HERE, "csrc", f) for f in ("lm_scan.hip", "lm_norm.hip", "lm_logp.hip")]
 LM_LIB = os.path.join(HERE, "libpararnn_lm.so")
+LM_BINDING_SRC = os.path.join(HERE, "csrc", "lm_binding.cpp")
+LM_BINDING = os.path.join(HERE, "_lm_binding.so")
 ARCH = "gfx950"
 
 
@@ -64,9 +67,10 @@ def build(asm: bool = False, verbose: bool = True, stress: bool = True) -> str:
         tmp = lib + ".tmp%d" % os.getpid()
         cmd = _command(tmp, st, asm and not st)
         procs.append((_start(cmd, verbose, os.path.join(ROOT, "_build") if (asm and not st) else HERE), tmp, lib))
-    lm = _start_lm(verbose)
+    lm, binding = _start_lm(verbose), _start_binding(verbose)
     failed = _finish(procs, verbose)
     failed += _finish_lm(lm, LM_LIB, verbose)
+    failed += _finish_binding(binding, verbose, not failed)
     if failed:
         raise RuntimeError("hipcc failed: %s" % failed)
     return LIB
@@ -97,6 +101,30 @@ def _finish_lm(jobs, lib, verbose):
     for obj in objs:
         if os.path.exists(obj):
             os.remove(obj)
+    return failed
+
+
+def _start_binding(verbose):
+    """Start compiling the binding; its object beside it until it is linked against libpararnn_lm.so."""
+    from torch.utils.cpp_extension import include_paths
+    obj = os.path.join(HERE, "lm_binding.tmp%d.o" % os.getpid())
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-I", INC]
+    for p in include_paths() + [os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", p]
+    return [(_start(cmd + ["-c", LM_BINDING_SRC, "-o", obj], verbose), obj, obj)]
+
+
+def _finish_binding(jobs, verbose, link):
+    import torch
+    failed = _finish(jobs, verbose)
+    obj, tmp = jobs[0][1], LM_BINDING + ".tmp%d" % os.getpid()
+    if link and not failed:
+        cmd = ["g++", "-shared", obj, "-L", HERE, "-lpararnn_lm", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+               "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-o", tmp]
+        failed = _finish([(_start(cmd, verbose), tmp, LM_BINDING)], verbose)
+    if os.path.exists(obj):
+        os.remove(obj)
     return failed
 
 

@@ -7,6 +7,7 @@ import subprocess
 import pytest
 import torch
 
+import lm_abi
 import lm_plain as plain
 from nonlinear_rnn_solve_amd import build, lm
 
@@ -20,7 +21,7 @@ WS, BIG = 1 << 24, 1 << 50
 def lib():
     if not os.path.exists(lm.LIB_PATH):
         build.build(verbose=False)
-    return lm.load_library()
+    return lm_abi.load(lm.LIB_PATH)
 
 
 def declared():
@@ -50,16 +51,16 @@ def test_constants_and_struct_layouts_match_the_header(tmp_path):
     exe = tmp_path / "layout"
     subprocess.check_call(["gcc", "-I", os.path.dirname(HEADER), str(src), "-o", str(exe)])
     got = [int(v) for v in subprocess.check_output([str(exe)]).split()]
-    assert got == [lm._SCAN.size, 4, 8, 32, 56, 104, 112, 120, 128, lm._SCAN_GRAD.size, 8, 16, 24, 48, 64, 96, 112, 120,
+    assert got == [lm_abi.SCAN.size, 4, 8, 32, 56, 104, 112, 120, 128, lm_abi.SCAN_GRAD.size, 8, 16, 24, 48, 64, 96, 112, 120,
                    lm.SCAN_CHUNK, lm.NORM_MAX_D, lm.MAX_TOP, lm.ABI_VERSION]
 
 
 def scan_problem(dtype=0, c=8.0, B=2, T=300, D=64, x=P, r=P, i=P, st=(64, 64), lam=P, h0=0, cu=0, n=1):
-    return lm._SCAN.pack(dtype, c, B, T, D, x, r, i, *(st * 3), lam, h0, cu, n)
+    return lm_abi.SCAN.pack(dtype, c, B, T, D, x, r, i, *(st * 3), lam, h0, cu, n)
 
 
 def test_scan_validation(lib):
-    sh = lm._PAIR.pack(300 * 64, 64)
+    sh = lm_abi.PAIR.pack(300 * 64, 64)
     run = lambda prob, h=P, last=None, carry=None, ws=WS, n=BIG: lib.pararnn_lm_gated_scan(  # noqa: E731
         prob, h, sh, last, carry, ws, n, None)
     assert run(None) == -1
@@ -85,7 +86,7 @@ def test_scan_validation(lib):
 
 def test_scan_gradient_validation(lib):
     def grad(carry=P, dh=P, dl=0, dx=P, dr=P, di=P, st=64, dlam=0, dh0=0):
-        return lm._SCAN_GRAD.pack(carry, dh, dl, dx, dr, di, *([st] * 8), dlam, dh0)
+        return lm_abi.SCAN_GRAD.pack(carry, dh, dl, dx, dr, di, *([st] * 8), dlam, dh0)
 
     run = lambda prob, g, ws=WS, n=BIG: lib.pararnn_lm_gated_scan_vjp(prob, g, ws, n, None)  # noqa: E731
     assert run(scan_problem(), None) == -1
@@ -141,6 +142,12 @@ def test_logprobs_validation(lib):
                 dict(ds=-1), dict(ge=P + 2), dict(t=P + 2), dict(tb=3)):
         assert bwd(**bad) == -1, bad
     assert bwd(N=0) == 0 and bwd(V=0) == 0
+
+
+def test_binding_is_built_for_the_library(lib):
+    b = lm.load_library()
+    assert (b.ABI_VERSION, b.SCAN_CHUNK, b.NORM_MAX_D, b.MAX_TOP) == (lm.ABI_VERSION, lm.SCAN_CHUNK, lm.NORM_MAX_D, lm.MAX_TOP)
+    assert lib.pararnn_lm_abi_version() == lm.ABI_VERSION
 
 
 def test_binding_refuses_cpu_tensors(lib):
