@@ -15,6 +15,12 @@ DEV uint64_t rank_key(float z, uint32_t index) {
   return (static_cast<uint64_t>(o) << 32) | static_cast<uint32_t>(~index);
 }
 
+// the value in a key
+DEV float key_value(uint64_t key) {
+  const uint32_t o = static_cast<uint32_t>(key >> 32);
+  return __uint_as_float(o ^ (o & 0x80000000u ? 0x80000000u : 0xffffffffu));
+}
+
 DEV int64_t target_of(const void* t, int bytes, int64_t n) {
   return bytes == 8 ? static_cast<const int64_t*>(t)[n] : static_cast<const int32_t*>(t)[n];
 }
@@ -95,6 +101,7 @@ DEV void top_of(const LogpArgs& p, const T* z, int64_t n, uint64_t best, float m
     for (int w = 1; w < LPR / WAVE; ++w) best = max(best, sh.best[w][lane]);
     // 0: a lane without a logit.  Keys are unique otherwise (every chunk has one lane).
     int rank = 0;
+#pragma unroll
     for (int j = 0; j < kCols; ++j) {
       const uint64_t o = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(best >> 32), j)) << 32 |
                          static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(best), j));
@@ -110,9 +117,11 @@ DEV void top_of(const LogpArgs& p, const T* z, int64_t n, uint64_t best, float m
   const uint64_t bar = sh.bar;
   if (sh.best[wave][lane] >= bar && sh.best[wave][lane] != 0) sh.lanes[atomicAdd(&sh.n_lanes, 1u)] = threadIdx.x;
   __syncthreads();
-  const int64_t chunks = (p.V + V - 1) / V, rounds = (chunks + LPR - 1) / LPR;
-  for (int64_t w = threadIdx.x; w < rounds * sh.n_lanes; w += LPR) {
-    const int64_t c = w / sh.n_lanes * LPR + sh.lanes[w % sh.n_lanes];
+  // below 2^31 logits: 32-bit indices throughout
+  const uint32_t chunks = static_cast<uint32_t>((p.V + V - 1) / V), rounds = (chunks + LPR - 1) / LPR, lanes = sh.n_lanes;
+  for (uint32_t w = threadIdx.x; w < rounds * lanes; w += LPR) {
+    const uint32_t q = w / lanes;
+    const int64_t c = static_cast<int64_t>(q) * LPR + sh.lanes[w - q * lanes];
     if (c >= chunks) continue;
     const Vec<T, V> x = load_row<T, V>(z + c * V, p.V - c * V, T{});
 #pragma unroll
@@ -124,16 +133,21 @@ DEV void top_of(const LogpArgs& p, const T* z, int64_t n, uint64_t best, float m
   }
   __syncthreads();
   const auto put = [&](int k, uint64_t key) {
-    const int64_t j = static_cast<uint32_t>(~static_cast<uint32_t>(key));
-    p.top_ids[n * p.top + k] = j;
-    p.top_logp[n * p.top + k] = none ? -INFINITY : (to_f32(z[j]) - m) - ls;
+    p.top_ids[n * p.top + k] = static_cast<uint32_t>(~static_cast<uint32_t>(key));
+    p.top_logp[n * p.top + k] = none ? -INFINITY : (key_value(key) - m) - ls;   // a row with a NaN has a NaN ls
   };
   const uint32_t count = sh.n;
   if (count <= kList) {
     for (uint32_t i = threadIdx.x; i < count; i += LPR) {
       const uint64_t key = sh.list[i];
       int rank = 0;
-      for (uint32_t j = 0; j < count; ++j) rank += sh.list[j] > key;
+      for (uint32_t j = 0; j < count; j += 8) {
+        uint64_t o[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) o[u] = sh.list[j + u];   // kList is a multiple of 8
+#pragma unroll
+        for (int u = 0; u < 8; ++u) rank += j + u < count && o[u] > key;
+      }
       if (rank < p.top) put(rank, key);
     }
     return;
@@ -314,9 +328,13 @@ extern "C" pararnn_status pararnn_lm_token_logprobs(int dtype, int64_t N, int64_
       if (top) run(t, lanes, std::true_type{});
       else run(t, lanes, std::false_type{});
     };
+    // Lanes of a row.  Few rows leave CUs idle, so theirs are read by more lanes: 32 rows, 20 alternatives, bf16: V = 3000
+    // 8.2 us with 64 lanes and 6.7 with 256; V = 24000 9.9 with 256 and 8.8 with 1024 (float32 11.7 and 9.4).  Many rows fill
+    // the chip either way and waste less of a row's end: 4096 rows: V = 3000 16.5 and 19.7; V = 24000 50 and 79.
+    const bool few = N <= 512;
     if (V <= 512 && !top) run(t, std::integral_constant<int, 16>{}, std::false_type{});
-    else if (V <= 4096) alt(std::integral_constant<int, 64>{});
-    else if (V <= 32768) alt(std::integral_constant<int, 256>{});
+    else if (V <= (few ? 2048 : 4096)) alt(std::integral_constant<int, 64>{});
+    else if (V <= (few ? 16384 : 32768)) alt(std::integral_constant<int, 256>{});
     else alt(std::integral_constant<int, 1024>{});
   };
   if (dtype == PARARNN_BF16) sized(bf16{});

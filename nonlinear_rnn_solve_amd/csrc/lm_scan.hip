@@ -90,7 +90,7 @@ DEV int32_t sequence_of(const int32_t* cu, int32_t n, int64_t t) {
 // Few steps (kSerial or fewer, one generated token for instance): one channel of one row a thread, all steps
 // in order, no shared memory, one launch.
 // ------------------------------------------------------------------------------------------------
-constexpr int64_t kSerial = 16;
+constexpr int64_t kSerial = 16;   // T = 8, 16, 32: 5.1, 9.9, 16.6 us against the scan's 13.4, 13.8, 14.2 (B = 32, D = 4096, bf16)
 template <typename T>
 __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
   const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x, b = blockIdx.y;
