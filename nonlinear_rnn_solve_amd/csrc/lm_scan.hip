@@ -127,7 +127,7 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
 // Between tiles.  Each tile publishes its map for each channel as a 64-bit word; GS tiles of a chain form a group, whose
 // last tile joins their maps to the group's and publishes that, then finds the state entering the group -- the nearest
 // state among the W groups before it, advanced by the maps of those between -- and replaces the group's map by the state
-// leaving it.  Every tile's entering state is its group's, advanced by the maps of the group's tiles before it.  So a
+// leaving it.  Every tile's entering state is its group's, advanced by the joint map of the group's tiles before it.  So a
 // state travels 64 tiles in one round trip through memory, and what is composed with what is fixed: every run gives the
 // same bits.  a is in [0, 1], so the sign bit of A marks a word as written: zero = nothing yet, (A | sign, B) = a map,
 // (~0, h) = a state.  Words are relaxed device-scope atomics and carry their own validity: no fences.
@@ -221,32 +221,32 @@ template <bool SEG> DEV float enter_tile(const Grid& g, uint32_t pos, int32_t ch
   const bool more = pos + 1 < g.chunks;
   uint64_t* own = g.words + pos * step + col;
   if (more && i + 1 < GS) st_word(own, map_bits(f.A), f.B);
-  uint64_t w[GS - 1];   // the maps of the group's tiles before this one, the nearest first
-  while (true) {
-    ld_words(own - step, step, i, w);
-    bool there = true;
+  Aff m{1.0f, 0.0f};   // the group's tiles before this one
+  if (i > 0) {
+    uint64_t w[GS - 1];
+    while (true) {
+      ld_words(own - step, step, i, w);
+      bool there = true;
 #pragma unroll
-    for (int k = 0; k < GS - 1; ++k) there = there && (k >= i || hi(w[k]) != 0);
-    if (there) break;
-    __builtin_amdgcn_s_sleep(1);
+      for (int k = 0; k < GS - 1; ++k) there = there && (k >= i || hi(w[k]) != 0);
+      if (there) break;
+      __builtin_amdgcn_s_sleep(1);
+    }
+#pragma unroll
+    for (int k = GS - 2; k >= 0; --k)
+      if (k < i) m = k == i - 1 ? map_of(w[k]) : compose<SEG>(map_of(w[k]), m);
   }
   float h;
   if (more && i + 1 == GS) {   // the group's last tile: publishes the group's map, then the state leaving it
-    Aff m = map_of(w[GS - 2]);
-#pragma unroll
-    for (int k = GS - 3; k >= 0; --k) m = compose<SEG>(map_of(w[k]), m);
-    m = compose<SEG>(f, m);
+    const Aff all = compose<SEG>(f, m);
     uint64_t* group = g.gwords + j * step + col;
-    if (j > 0) st_word(group, map_bits(m.A), m.B);
+    if (j > 0) st_word(group, map_bits(all.A), all.B);
     h = j > 0 ? group_state<SEG, W>(g, j, chain, lane) : first;
-    st_word(group, kState, apply<SEG>(m, h));
+    st_word(group, kState, apply<SEG>(all, h));
   } else {
     h = j > 0 ? group_state<SEG, 4>(g, j, chain, lane) : first;
   }
-#pragma unroll
-  for (int k = GS - 2; k >= 0; --k)
-    if (k < i) h = apply<SEG>(map_of(w[k]), h);
-  return h;
+  return i > 0 ? apply<SEG>(m, h) : h;
 }
 
 // what the lanes of a wave wrote to shared memory is there for its other lanes (a wave's accesses are in order; this keeps
