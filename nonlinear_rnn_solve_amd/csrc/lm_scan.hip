@@ -3,7 +3,6 @@
 //   a_t = exp(k sig(r_t)), k = -c softplus(lam);  h_t = a_t h_{t-1} + m_t u_t,  m = sqrt(1 - a^2), u = sig(i) x
 
 #include <algorithm>
-#include <numeric>
 #include <type_traits>
 
 #include "lm_common.h"
@@ -133,9 +132,9 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
 // (~0, h) = a state.  Words are relaxed device-scope atomics and carry their own validity: no fences.
 //
 // A tile takes its place from a ticket counter, so those it waits for have been started before it.  One counter hands
-// out a ticket in 13 ns, which bounded the whole scan; the chains therefore form up to 8 classes with a counter each
-// (their number divides the chains', so all have as many tiles).  A workgroup starts with a class that is no function of
-// its XCD (the block number modulo 8): chains bound to an XCD cost 25% at T = 131072, D = 1024.
+// out a ticket in 13 ns, which bounded the whole scan; the chains therefore form up to 8 classes with a counter each.  A
+// workgroup starts with a class that is no function of its XCD (the block number modulo 8): chains bound to an XCD cost
+// 25% at T = 131072, D = 1024.
 //
 // Bound by memory for float32, by memory and vector instructions about equally for bfloat16 (56% and 54% of the issue
 // slots in the forward and the gradient kernel).  Measured, bf16 (wide: B = 2, T = 4096, D = 4096; long: B = 1, T = 131072,
@@ -156,10 +155,10 @@ struct Grid {
   uint64_t* gwords;     // [chunks / GS][chains][TW]: the groups' maps, then the states leaving them
   uint32_t* tickets;    // a counter for each class of chains, kTicket words apart; null: one chunk, the tile is the block
   int64_t chunks;
-  int32_t chains, ctiles, classes;   // chains = B ctiles: channel tiles of all rows; chain c is of class c modulo classes
+  int32_t chains, ctiles, log_classes;   // chains = B ctiles: channel tiles of all rows
 };
 
-constexpr int kTicket = 32, kClasses = 8;   // 128 bytes: counters share no cache line
+constexpr int kTicket = 32, kLogClasses = 3;   // 128 bytes: counters share no cache line
 
 struct Aff { float A, B; };
 // the map of `later` after `earlier`; with packed sequences A = 0 is a cut, which nothing crosses, not even a NaN
@@ -272,26 +271,30 @@ template <bool SEG, bool REV, int N> DEV void spread(const Aff (*m)[TW], float (
     if (k + 1 < N) h = apply<SEG>(m[s][lane], h);
   }
 }
-// the tile's place: pos gets its position in the chain
+// the tile's place: its position in its chain.  Chain c is of class c modulo 2^log_classes; a workgroup whose class has no
+// ticket left goes on to the next (there are as many workgroups as tiles).
 DEV void take_ticket(const Grid& g, uint32_t (&sh)[2], uint32_t& pos, uint32_t& chain) {
-  const uint32_t G = static_cast<uint32_t>(g.classes), per = static_cast<uint32_t>(g.chains) / G;   // chains of a class
+  const uint32_t mask = (1u << g.log_classes) - 1, chains = static_cast<uint32_t>(g.chains);
+  const auto size = [&](uint32_t n) { return (chains + mask - n) >> g.log_classes; };   // chains of class n
   if (!g.tickets) {
     pos = 0;
     chain = blockIdx.x;
     return;
   }
   if (threadIdx.x == 0) {
-    uint32_t n = (blockIdx.x >> 3) % G, t;
+    uint32_t n = (blockIdx.x >> 3) & mask, t;
     while ((t = __hip_atomic_fetch_add(g.tickets + n * kTicket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) >=
-           per * static_cast<uint32_t>(g.chunks))
-      n = n + 1 < G ? n + 1 : 0;
+           size(n) * static_cast<uint32_t>(g.chunks))
+      n = (n + 1) & mask;
     sh[0] = t;
     sh[1] = n;
   }
   __syncthreads();
   const uint32_t t = __builtin_amdgcn_readfirstlane(sh[0]), n = __builtin_amdgcn_readfirstlane(sh[1]);
-  pos = t / per;
-  chain = (t - pos * per) * G + n;
+  const uint32_t per = size(n);
+  // scalar registers for what every address is made of (else in vector registers: 44 bytes spilled, 92 against 63 us)
+  pos = __builtin_amdgcn_readfirstlane(t / per);
+  chain = __builtin_amdgcn_readfirstlane(((t - pos * per) << g.log_classes) + n);
 }
 
 // where a tile and its lanes are
@@ -770,7 +773,7 @@ static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
   o.ctiles = ceil_div(D, TW);
   o.tiles = B * o.ctiles * o.chunks;
   o.words = o.chunks > 1 ? o.tiles * TW * 8 : 0;
-  o.tickets = o.chunks > 1 ? kClasses * kTicket * 4 : 0;
+  o.tickets = o.chunks > 1 ? (kTicket * 4 << kLogClasses) : 0;
   o.gwords = B * o.ctiles * (o.chunks / GS) * TW * 8;
   o.parts = B * o.chunks * D * 4;
   o.total = 256 + o.tickets + o.words + o.gwords + o.parts;
@@ -804,9 +807,11 @@ static void prepare(const Layout& l, void* ws, const ScanArgs& a, const float* i
   k_scan_prepare<<<grid, 256, 0, st>>>(static_cast<uint4*>(ws), n16, a.cu, a.n, a.B, a.T, a.D, in, empty ? out : nullptr);
 }
 static Grid grid_of(const Layout& l, void* ws, int64_t B) {
+  int32_t log = 0;
+  while (log < kLogClasses && B * l.ctiles >> (log + 1)) ++log;
   char* w = static_cast<char*>(ws);
   return Grid{reinterpret_cast<uint64_t*>(w + l.tickets), reinterpret_cast<uint64_t*>(w + l.tickets + l.words), l.chunks > 1 ? reinterpret_cast<uint32_t*>(w) : nullptr, l.chunks,
-              static_cast<int32_t>(B * l.ctiles), static_cast<int32_t>(l.ctiles), std::gcd(static_cast<int32_t>(B * l.ctiles), kClasses)};
+              static_cast<int32_t>(B * l.ctiles), static_cast<int32_t>(l.ctiles), log};
 }
 
 }  // namespace lm
