@@ -263,7 +263,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logp_grad(const LogpGradArgs p
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) {
     const int64_t j = ((seg * kAhead + u) * LPR + lane) * V;
-    if (j < p.V) x[u] = load_row<T, V>(z + j, p.V - j, T{});
+    if (j < p.V) x[u] = load_row<T, V, true>(z + j, p.V - j, T{});
   }
   const int64_t t = p.targets ? target_of(p.targets, p.tbytes, n) : -1;
   const float lse = p.lse[n], g = t < 0 ? 0.0f : t >= p.V ? NAN : p.g_logp[n];
