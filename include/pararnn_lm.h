@@ -33,7 +33,7 @@ extern "C" {
  *     a_t = exp(-c softplus(lam) sig(r_t)),     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sig(i_t) x_t
  * (sig(r) opens the decay, sig(i) the input; the square root keeps the state's variance).  It is solved by a
  * parallel scan along time, whatever T is; T <= 16 runs without one, in a single launch (one generated token is
- * T = 1).
+ * T = 1).  UNSUPPORTED: 2^24 or more tiles of 64 channels by PARARNN_LM_SCAN_CHUNK steps.
  * ---------------------------------------------------------------------------------------------- */
 /* steps of one chunk of the scan (the state entering each is what the gradient rebuilds h from) */
 #define PARARNN_LM_SCAN_CHUNK 64
@@ -88,7 +88,8 @@ pararnn_status pararnn_lm_gated_scan_vjp(const pararnn_lm_scan* prob, const para
                                          size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------------------
- * Layer normalisation of N rows of D channels (D <= PARARNN_LM_NORM_MAX_D, else UNSUPPORTED):
+ * Layer normalisation of N rows of D channels (D <= PARARNN_LM_NORM_MAX_D, else UNSUPPORTED; so
+ * is N of 2^28 or more, 2^26 where D > 256, 2^24 where D > 1024, 2^22 where D > 4096):
  *     s = x + residual (rounded to dtype; s = x without one),  mean and variance of each row of s,
  *     y = (s - mean) / sqrt(var + eps) * weight + bias
  *   x, residual (or NULL), y, sum  [N][D] of dtype with row strides; weight [D], bias [D] or NULL float32
@@ -121,6 +122,7 @@ pararnn_status pararnn_lm_layer_norm_vjp(int dtype, int64_t N, int64_t D, const 
  *           One at or above V gives logp = NaN.
  *   lse, logp, entropy [N] float32 (entropy, or logp with targets, may be NULL);
  *   top_logp [N][top] float32, top_ids [N][top] int64 (NULL when top = 0)
+ * UNSUPPORTED: N of 2^26 or more, 2^24 where V > 4096, 2^22 where V > 32768.
  * Logits of -infinity are tokens ruled out.  A row with nothing left has lse = -infinity, logp = -infinity,
  * entropy = 0 and a gradient of zeros.  A NaN or +infinity makes its row's numbers NaN; a NaN ranks as -infinity.
  * ---------------------------------------------------------------------------------------------- */

@@ -15,7 +15,8 @@ pseudo-random times before publishing look-back words, so that scans walk far
 back.  Only the tests load it; its results must equal libpararnn.so's bit for bit.
 
 libpararnn_lm.so holds the language-model operators of include/pararnn_lm.h, one source file each, compiled in
-parallel and linked; _lm_binding.so is its Python binding (host C++ against torch's headers).
+parallel and linked; _lm_binding.so is its Python binding (host C++ against torch's headers), and
+libpararnn_lm_stress.so its look-back stress variant.
 """
 from __future__ import annotations
 
@@ -32,6 +33,7 @@ LIB = os.path.join(HERE, "libpararnn.so")
 STRESS_LIB = os.path.join(HERE, "libpararnn_stress.so")
 LM_SRCS = [os.path.join(HERE, "csrc", f) for f in ("lm_scan.hip", "lm_norm.hip", "lm_logp.hip")]
 LM_LIB = os.path.join(HERE, "libpararnn_lm.so")
+LM_STRESS_LIB = os.path.join(HERE, "libpararnn_lm_stress.so")
 LM_BINDING_SRC = os.path.join(HERE, "csrc", "lm_binding.cpp")
 LM_BINDING = os.path.join(HERE, "_lm_binding.so")
 ARCH = "gfx950"
@@ -68,8 +70,11 @@ def build(asm: bool = False, verbose: bool = True, stress: bool = True) -> str:
         cmd = _command(tmp, st, asm and not st)
         procs.append((_start(cmd, verbose, os.path.join(ROOT, "_build") if (asm and not st) else HERE), tmp, lib))
     lm, binding = _start_lm(verbose), _start_binding(verbose)
+    lm_stress = _start_lm(verbose, LM_SRCS[:1], "PR_LB_STRESS=1") if stress else []
     failed = _finish(procs, verbose)
     failed += _finish_lm(lm, LM_LIB, verbose)
+    if stress:
+        failed += _finish_lm(lm_stress, LM_STRESS_LIB, verbose)
     failed += _finish_binding(binding, verbose, not failed)
     if failed:
         raise RuntimeError("hipcc failed: %s" % failed)
@@ -82,12 +87,13 @@ def _start(cmd, verbose, cwd=HERE):
     return subprocess.Popen(cmd, cwd=cwd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
 
 
-def _start_lm(verbose, defines=()):
+def _start_lm(verbose, srcs=LM_SRCS, define=None):
     """Start compiling the language-model operators' sources; objects beside the library until it is linked."""
     jobs = []
-    for src in LM_SRCS:
-        obj = os.path.join(HERE, "%s%s.tmp%d.o" % (os.path.basename(src)[:-4], "_".join(defines), os.getpid()))
-        jobs.append((_start([hipcc()] + FLAGS + ["-D" + d for d in defines] + ["-c", src, "-o", obj], verbose), obj, obj))
+    for src in srcs:
+        obj = os.path.join(HERE, "%s%s.tmp%d.o" % (os.path.basename(src)[:-4], "_stress" if define else "", os.getpid()))
+        cmd = [hipcc()] + FLAGS + (["-D" + define] if define else []) + ["-c", src, "-o", obj]
+        jobs.append((_start(cmd, verbose), obj, obj))
     return jobs
 
 

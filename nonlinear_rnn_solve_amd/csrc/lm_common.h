@@ -153,7 +153,8 @@ inline bool sizes_fit(int64_t a, int64_t b, int64_t c = 1) {
 inline bool plane_ok(int64_t n, int64_t s) { return s >= 0 && (n <= 1 || s <= INT64_MAX / 16 / (n - 1)); }
 inline pararnn_status launched() { return hipGetLastError() == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-constexpr int64_t kMaxGrid = INT64_C(0x7fffffff);
+// a launch has fewer than 2^32 threads
+inline bool grid_ok(int64_t blocks, int64_t threads) { return blocks <= INT64_C(0xffffffff) / threads; }
 
 }  // namespace lm
 #endif

@@ -304,7 +304,7 @@ static pararnn_status check_logp(int dtype, int64_t N, int64_t V, const void* lo
   if (targets && !aligned(targets, static_cast<size_t>(target_bytes))) return PARARNN_ERR_INVALID_ARG;
   if (N > 0 && V > 0 && !ptr_ok(logits, dtype_size(dtype))) return PARARNN_ERR_INVALID_ARG;
   if (!plane_ok(N, stride)) return PARARNN_ERR_INVALID_ARG;
-  if (N > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
+  if (!grid_ok(N, V <= 4096 ? 64 : V <= 32768 ? 256 : 1024)) return PARARNN_ERR_UNSUPPORTED;   // the lanes of a row
   return PARARNN_OK;
 }
 
@@ -359,7 +359,7 @@ extern "C" pararnn_status pararnn_lm_token_logprobs_vjp(int dtype, int64_t N, in
     constexpr int LPR = decltype(lanes)::value;
     const int64_t segments = ceil_div(V, LPR * kAhead * 16 / static_cast<int64_t>(sizeof(T)));
     const int64_t blocks = ceil_div(N, kGradThreads / LPR) * segments;
-    if (blocks > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
+    if (!grid_ok(blocks, kGradThreads)) return PARARNN_ERR_UNSUPPORTED;
     const LogpGradArgs a{logits, stride, N, V, targets, target_bytes, lse, entropy, g_logp, g_entropy, d_logits, d_stride, segments};
     k_logp_grad<T, LPR><<<static_cast<unsigned>(blocks), kGradThreads, 0, st>>>(a);
     return launched();

@@ -268,7 +268,9 @@ template <typename T, class F> static void shape_of(int64_t D, F f) {
   else lanes(std::integral_constant<int, 1024>{});
 }
 
-static int64_t grad_rows(int64_t D) { return D <= 256 ? 64 : D <= 1024 ? 16 : D <= 4096 ? 4 : 1; }
+// threads that a row of k_norm takes at most
+static int64_t norm_threads(int64_t D) { return D <= 256 ? 16 : D <= 1024 ? 64 : D <= 4096 ? 256 : 1024; }
+static int64_t grad_rows(int64_t D) { return kGradThreads / norm_threads(D); }
 static int64_t grad_groups(int64_t N, int64_t D) { return std::min<int64_t>(ceil_div(N, grad_rows(D)), kGradGroups); }
 
 }  // namespace lm
@@ -288,7 +290,7 @@ extern "C" pararnn_status pararnn_lm_layer_norm(int dtype, int64_t N, int64_t D,
     return PARARNN_ERR_INVALID_ARG;
   if (!plane_ok(N, x_stride) || !plane_ok(N, y_stride) || (residual && (!plane_ok(N, residual_stride) || !plane_ok(N, sum_stride))))
     return PARARNN_ERR_INVALID_ARG;
-  if (D > PARARNN_LM_NORM_MAX_D || N > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
+  if (D > PARARNN_LM_NORM_MAX_D || !grid_ok(N, norm_threads(D))) return PARARNN_ERR_UNSUPPORTED;
   const NormArgs a{x, residual, weight, bias, y, sum, stats, x_stride, residual_stride, y_stride, sum_stride, N, D, eps};
   hipStream_t st = static_cast<hipStream_t>(stream);
   const auto run = [&](auto t) {
@@ -323,7 +325,7 @@ extern "C" pararnn_status pararnn_lm_layer_norm_vjp(int dtype, int64_t N, int64_
     return PARARNN_ERR_INVALID_ARG;
   if (!plane_ok(N, dy_stride) || !plane_ok(N, s_stride) || !plane_ok(N, d_x_stride) || (d_sum && !plane_ok(N, d_sum_stride)))
     return PARARNN_ERR_INVALID_ARG;
-  if (D > PARARNN_LM_NORM_MAX_D || N > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
+  if (D > PARARNN_LM_NORM_MAX_D || !grid_ok(N, norm_threads(D))) return PARARNN_ERR_UNSUPPORTED;
   if (!ptr_ok(ws, 256) || ws_bytes < pararnn_lm_layer_norm_vjp_workspace_bytes(N, D)) return PARARNN_ERR_WORKSPACE;
   const bool params = d_weight || d_bias;
   const int64_t groups = grad_groups(N, D);

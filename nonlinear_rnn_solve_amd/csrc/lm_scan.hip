@@ -91,8 +91,8 @@ DEV int32_t sequence_of(const int32_t* cu, int32_t n, int64_t t) {
 // ------------------------------------------------------------------------------------------------
 constexpr int64_t kSerial = 16;   // T = 8, 16, 32: 5.1, 9.9, 16.6 us against the scan's 13.4, 13.8, 14.2 (B = 32, D = 4096, bf16)
 template <typename T>
-__global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p) {
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x, b = blockIdx.y;
+__global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p, uint32_t ctiles) {
+  const int64_t b = blockIdx.x / ctiles, d = static_cast<int64_t>(blockIdx.x - b * ctiles) * 64 + threadIdx.x;
   if (d >= p.D) return;
   const float k = -p.c * softplus(p.lam[d]);
   const T* x = static_cast<const T*>(p.x) + b * p.sx[0] + d;
@@ -174,6 +174,23 @@ DEV void st_word(uint64_t* p, uint32_t hi, float lo) {
 constexpr uint32_t kState = 0xffffffffu, kSign = 0x80000000u;
 DEV uint32_t map_bits(float A) { return A != A ? 0xffc00000u : (__float_as_uint(A) | kSign); }
 
+// The stress build (-DPR_LB_STRESS=1) pauses a quarter of the tiles for a bounded, pseudo-random time before they publish a
+// word, so that words come in a scrambled order; its results must be the plain library's, bit for bit.
+#ifndef PR_LB_STRESS
+#define PR_LB_STRESS 0
+#endif
+DEV void stress_pause(uint32_t pos, int32_t chain, uint32_t site) {
+  if constexpr (PR_LB_STRESS) {
+    uint32_t h = pos * 0x85EBCA77u ^ static_cast<uint32_t>(chain) * 0xC2B2AE3Du ^ site * 0x27D4EB2Fu ^
+                 static_cast<uint32_t>(__builtin_readcyclecounter() >> 8) * 0x9E3779B1u;
+    h ^= h >> 15;
+    h *= 0x2C1B3C6Du;
+    h ^= h >> 12;
+    const int n = (h & 3) == 0 ? static_cast<int>((h >> 8) & 31) : 0;   // up to ~100 us
+    for (int i = 0; i < n; ++i) __builtin_amdgcn_s_sleep(127);
+  }
+}
+
 // N words of one channel at `word` - k step for k = 0 .. N-1, those with k >= have not read
 template <int N> DEV void ld_words(const uint64_t* word, int64_t step, int have, uint64_t (&w)[N]) {
 #pragma unroll
@@ -219,6 +236,7 @@ template <bool SEG> DEV float enter_tile(const Grid& g, uint32_t pos, int32_t ch
   const int i = static_cast<int>(pos % GS);
   const bool more = pos + 1 < g.chunks;
   uint64_t* own = g.words + pos * step + col;
+  stress_pause(pos, chain, 0);
   if (more && i + 1 < GS) st_word(own, map_bits(f.A), f.B);
   Aff m{1.0f, 0.0f};   // the group's tiles before this one
   if (i > 0) {
@@ -239,8 +257,10 @@ template <bool SEG> DEV float enter_tile(const Grid& g, uint32_t pos, int32_t ch
   if (more && i + 1 == GS) {   // the group's last tile: publishes the group's map, then the state leaving it
     const Aff all = compose<SEG>(f, m);
     uint64_t* group = g.gwords + j * step + col;
+    stress_pause(pos, chain, 1);
     if (j > 0) st_word(group, map_bits(all.A), all.B);
     h = j > 0 ? group_state<SEG, W>(g, j, chain, lane) : first;
+    stress_pause(pos, chain, 2);
     st_word(group, kState, apply<SEG>(all, h));
   } else {
     h = j > 0 ? group_state<SEG, 4>(g, j, chain, lane) : first;
@@ -254,6 +274,8 @@ DEV void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
+// a loaded value is there: what the wave stores from here on cannot overtake the load
+DEV void arrived(float& v) { asm volatile("" : "+v"(v) : : "memory"); }
 // the maps of N consecutive pieces (a lane's column of them) as one, in scan order
 template <bool SEG, bool REV, int N> DEV Aff join(const Aff (*m)[TW], int lane) {
   Aff f = m[REV ? N - 1 : 0][lane];
@@ -490,16 +512,19 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
     const int64_t d = tl.c0 + tl.lane;
     float h = 0.0f;
     if (d < p.D) {
-      if (!SEG && tl.pos < GS) h = p.h0 ? p.h0[tl.b * p.D + d] : 0.0f;
-      h = enter_tile<SEG>(g, tl.pos, tl.chain, tl.lane, join<SEG, false, NW>(sh_wave, tl.lane), h);
-      if (p.carry) {
-        float in = h;
-        if (SEG) {
-          const int32_t j = sequence_of(p.cu, p.n, tl.t0);
-          if (tl.t0 == 0 || (j > 0 && p.cu[j] == tl.t0)) in = p.h0 ? p.h0[(tl.b * p.n + j) * p.D + d] : 0.0f;
-        }
-        p.carry[(tl.b * g.chunks + tl.chunk) * p.D + d] = in;
+      // h0 before anything is published: h_last may be the same array, and a tile that waits for this one's map may write it
+      float begin = 0.0f;      // the state of a sequence that begins with the tile
+      bool begins = false;
+      if (SEG) {
+        const int32_t j = sequence_of(p.cu, p.n, tl.t0);
+        begins = tl.t0 == 0 || (j > 0 && p.cu[j] == tl.t0);
+        if (begins && p.h0 && p.carry) begin = p.h0[(tl.b * p.n + j) * p.D + d];
+      } else if (tl.pos < GS && p.h0) {
+        begin = p.h0[tl.b * p.D + d];
       }
+      arrived(begin);
+      h = enter_tile<SEG>(g, tl.pos, tl.chain, tl.lane, join<SEG, false, NW>(sh_wave, tl.lane), SEG ? 0.0f : begin);
+      if (p.carry) p.carry[(tl.b * g.chunks + tl.chunk) * p.D + d] = SEG && begins ? begin : h;
     }
     spread<SEG, false, NW>(sh_wave, sh_in, tl.lane, h);
   }
@@ -702,8 +727,8 @@ __global__ __launch_bounds__(256) void k_scan_prepare(uint4* clear, int64_t n16,
   for (int64_t k = first; k < B * n * D; k += stride) {
     const int32_t j = static_cast<int32_t>(k / D % n);
     int64_t t0 = j > 0 ? cu[j] : 0, t1 = j + 1 < n ? cu[j + 1] : T;
-    if (t0 > T) t0 = T;
-    if (t1 > T) t1 = T;
+    t0 = t0 < 0 ? 0 : t0 > T ? T : t0;
+    t1 = t1 < 0 ? 0 : t1 > T ? T : t1;
     if (t0 >= t1) out[k] = in ? in[k] : 0.0f;
   }
 }
@@ -742,14 +767,14 @@ static pararnn_status check_scan(const pararnn_lm_scan* p) {
     return PARARNN_ERR_INVALID_ARG;
   if (p->cu_seqlens && !sizes_fit(p->B, p->n_seqs, p->D)) return PARARNN_ERR_INVALID_ARG;
   if (!ptr_ok(p->h0, 4, false)) return PARARNN_ERR_INVALID_ARG;
-  if (p->B == 0 || p->D == 0) return PARARNN_OK;
+  if (p->D == 0) return PARARNN_OK;
   if (!ptr_ok(p->lam, 4)) return PARARNN_ERR_INVALID_ARG;
+  if (p->B == 0) return PARARNN_OK;
   const size_t es = dtype_size(p->dtype);
   if (p->T > 0 && (!ptr_ok(p->x, es) || !ptr_ok(p->r, es) || !ptr_ok(p->i, es))) return PARARNN_ERR_INVALID_ARG;
   const int64_t* s[3] = {p->sx, p->sr, p->si};
   for (const int64_t* q : s)
     if (!plane_ok(p->B, q[0]) || !plane_ok(p->T, q[1])) return PARARNN_ERR_INVALID_ARG;
-  if (p->B > 65535) return PARARNN_ERR_UNSUPPORTED;
   return PARARNN_OK;
 }
 
@@ -835,15 +860,15 @@ extern "C" pararnn_status pararnn_lm_gated_scan(const pararnn_lm_scan* prob, voi
     return PARARNN_ERR_INVALID_ARG;
   Layout l;
   if (!layout(prob->B, prob->T, prob->D, l)) return PARARNN_ERR_INVALID_ARG;
-  if (l.tiles > kMaxGrid || ceil_div(prob->D, 64) > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
+  if (!grid_ok(l.tiles, NTH) || !grid_ok(prob->B * l.ctiles, NTH)) return PARARNN_ERR_UNSUPPORTED;
   if (!ptr_ok(ws, 256) || ws_bytes < static_cast<size_t>(l.total)) return PARARNN_ERR_WORKSPACE;
   ScanArgs a = scan_args(prob);
   a.h = h; a.sh[0] = sh[0]; a.sh[1] = sh[1]; a.h_last = h_last; a.carry = carry;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.T <= kSerial) {
-    const dim3 grid(static_cast<unsigned>(ceil_div(a.D, 64)), static_cast<unsigned>(a.B));
-    if (prob->dtype == PARARNN_BF16) k_scan_serial<bf16><<<grid, 64, 0, st>>>(a);
-    else k_scan_serial<float><<<grid, 64, 0, st>>>(a);
+    const uint32_t ctiles = static_cast<uint32_t>(l.ctiles), grid = static_cast<uint32_t>(a.B) * ctiles;
+    if (prob->dtype == PARARNN_BF16) k_scan_serial<bf16><<<grid, 64, 0, st>>>(a, ctiles);
+    else k_scan_serial<float><<<grid, 64, 0, st>>>(a, ctiles);
     return launched();
   }
   prepare(l, ws, a, a.h0, a.h_last, st);
@@ -873,7 +898,7 @@ extern "C" pararnn_status pararnn_lm_gated_scan_vjp(const pararnn_lm_scan* prob,
   }
   Layout l;
   if (!layout(prob->B, prob->T, prob->D, l)) return PARARNN_ERR_INVALID_ARG;
-  if (l.tiles > kMaxGrid || l.ctiles > kMaxGrid) return PARARNN_ERR_UNSUPPORTED;
+  if (!grid_ok(l.tiles, NTH) || !grid_ok(prob->B * l.ctiles, NTH)) return PARARNN_ERR_UNSUPPORTED;
   if (!ptr_ok(ws, 256) || ws_bytes < static_cast<size_t>(l.total)) return PARARNN_ERR_WORKSPACE;
   GradArgs q{};
   q.f = scan_args(prob);

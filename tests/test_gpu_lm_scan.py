@@ -218,10 +218,10 @@ def test_token_by_token_equals_the_whole():
 @pytest.mark.parametrize("T,cu", [(500, None), (500, [0, 200, 200, 500])])
 def test_state_in_place_over_long_inputs(T, cu):
     x, r, i, lam, h0, _, _ = make(2, T, 64, BF, seed=13, n=3 if cu else 0)
-    h, last, _ = lm.gated_scan(x, r, i, lam, h0=h0, cu_seqlens=cuda_cu(cu))
+    h, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, cu_seqlens=cuda_cu(cu), want_carry=True)
     state = h0.clone()
-    h2, _, _ = lm.gated_scan(x, r, i, lam, h0=state, h_last=state, cu_seqlens=cuda_cu(cu))
-    assert torch.equal(h, h2) and torch.equal(state, last)
+    h2, _, carry2 = lm.gated_scan(x, r, i, lam, h0=state, h_last=state, cu_seqlens=cuda_cu(cu), want_carry=True)
+    assert torch.equal(h, h2) and torch.equal(state, last) and torch.equal(carry, carry2)
 
 
 def test_split_row_equals_whole_row():

@@ -69,7 +69,8 @@ def test_scan_validation(lib):
                 dict(lam=P + 1), dict(h0=P + 2), dict(cu=P + 2), dict(cu=P, n=0), dict(cu=P, n=-1), dict(cu=P, T=1 << 31),
                 dict(st=(-1, 64)), dict(st=(1 << 62, 64), B=64), dict(st=(64, 1 << 61))):
         assert run(scan_problem(**bad)) == -1, bad
-    assert run(scan_problem(dtype=1, x=P + 2, r=P + 2, i=P + 2, B=70000, D=1)) == -2      # element alignment is enough
+    assert run(scan_problem(dtype=1, x=P + 2, r=P + 2, i=P + 2, B=1 << 31, D=1)) == -2    # element alignment is enough
+    assert run(scan_problem(B=1 << 31, T=1)) == -2
     assert run(scan_problem(), h=0) == -1
     assert run(scan_problem(), h=P + 1) == -1
     assert run(scan_problem(), last=P + 2) == -1
@@ -94,6 +95,7 @@ def test_scan_gradient_validation(lib):
     for bad in (dict(carry=0), dict(dh=0), dict(dx=0), dict(dr=0), dict(di=0), dict(dh=P + 2), dict(dl=P + 2), dict(dlam=P + 2),
                 dict(dh0=P + 1), dict(st=-1), dict(st=1 << 61)):
         assert run(scan_problem(), grad(**bad)) == -1, bad
+    assert run(scan_problem(B=0, lam=0), grad(dlam=P)) == -1      # d_lam needs lam, rows or not
     assert run(scan_problem(), grad(), n=16) == -3
     assert run(scan_problem(), grad(), ws=None) == -3
 
@@ -107,7 +109,7 @@ def test_norm_validation(lib):
                 dict(res=P, s=P, rs=-1), dict(res=P, s=P, ss=-1), dict(stats=P + 2), dict(N=1 << 40, D=1 << 40), dict(xs=1 << 61)):
         assert fwd(**bad) == -1, bad
     assert fwd(D=lm.NORM_MAX_D + 1) == -2
-    assert fwd(N=1 << 31, D=1, xs=1, ys=1) == -2
+    assert fwd(N=1 << 31, D=1, xs=1, ys=1) == -2 and fwd(N=1 << 22, D=5000) == -2
     assert fwd(N=0) == 0 and fwd(D=0) == 0
 
     def bwd(dtype=0, N=4, D=64, dy=P, s=P, w=P, stats=P, ds=None, dx=P, st=64, dw=None, db=None, ws=WS, n=BIG):
@@ -131,6 +133,7 @@ def test_logprobs_validation(lib):
                 dict(top=5, V=4, tl=P, ti=P), dict(top=3, tl=P), dict(top=3, ti=P), dict(top=3, tl=P, ti=P + 4), dict(st=1 << 61)):
         assert fwd(**bad) == -1, bad
     assert fwd(n=16) == -3 and fwd(ws=None) == -3 and fwd(ws=WS + 16) == -3
+    assert fwd(N=1 << 26, V=5, st=5) == -2 and fwd(N=1 << 22, V=40000) == -2
     assert fwd(N=0) == 0
     assert lib.pararnn_lm_token_logprobs_workspace_bytes(4, 100, 33) == 0
     assert lib.pararnn_lm_token_logprobs_workspace_bytes(4, 100, 32) > 0
