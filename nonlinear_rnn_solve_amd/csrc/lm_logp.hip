@@ -115,6 +115,7 @@ DEV void top_of(const LogpArgs& p, const T* z, int64_t n, uint64_t best, float m
   }
   __syncthreads();
   const uint64_t bar = sh.bar;
+  const float reach = bar ? key_value(bar) : -INFINITY;
   if (sh.best[wave][lane] >= bar && sh.best[wave][lane] != 0) sh.lanes[atomicAdd(&sh.n_lanes, 1u)] = threadIdx.x;
   __syncthreads();
   // below 2^31 logits: 32-bit indices throughout
@@ -123,7 +124,11 @@ DEV void top_of(const LogpArgs& p, const T* z, int64_t n, uint64_t best, float m
     const uint32_t q = w / lanes;
     const int64_t c = static_cast<int64_t>(q) * LPR + sh.lanes[w - q * lanes];
     if (c >= chunks) continue;
-    const Vec<T, V> x = load_row<T, V>(z + c * V, p.V - c * V, T{});
+    const Vec<T, V> x = load_row<T, V>(z + c * V, p.V - c * V, from_f32<T>(-INFINITY));
+    float most = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < V; ++e) most = fmaxf(most, x.get(e));
+    if (most < reach) continue;   // most chunks of these lanes
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if (c * V + e >= p.V || rank_key(x.get(e), static_cast<uint32_t>(c)) < bar) continue;
@@ -185,8 +190,7 @@ void k_logp(const LogpArgs p) {
   const bool on = NT == LPR || n < p.N;
   const T* z = static_cast<const T*>(p.z) + (on ? n : 0) * p.stride;
   Stat a{-INFINITY, 0.0f, 0.0f};
-  uint32_t best = 0;
-  bool any = false;
+  uint32_t best = static_cast<uint32_t>(lane);   // the first of the lane's chunks, where it has any
   for (int64_t c0 = 0; c0 * V < p.V; c0 += LPR * kAhead) {   // uniform, as is whether any lane has a chunk
     Vec<T, V> x[kAhead];
 #pragma unroll
@@ -201,11 +205,7 @@ void k_logp(const LogpArgs p) {
         float cm = -INFINITY;
 #pragma unroll
         for (int e = 0; e < V; ++e) cm = fmaxf(cm, x[u].get(e));
-        if (TOP) {
-          const int64_t c = c0 + u * LPR + lane;
-          if (c * V < p.V && (cm > m || !any)) best = static_cast<uint32_t>(c);
-          any = any || c * V < p.V;
-        }
+        if (TOP) best = cm > m ? static_cast<uint32_t>(c0) + u * LPR + lane : best;
         m = fmaxf(m, cm);
       }
     if (m > a.m) rebase(a, m);
@@ -234,7 +234,7 @@ void k_logp(const LogpArgs p) {
   }
   if constexpr (TOP) {
     __shared__ TopShared<LPR> top;
-    top_of<T, LPR>(p, z, n, any ? rank_key(own, best) : 0, a.m, ls, none, top);
+    top_of<T, LPR>(p, z, n, static_cast<int64_t>(lane) * V < p.V ? rank_key(own, best) : 0, a.m, ls, none, top);
   }
 }
 
