@@ -1,4 +1,9 @@
 // lm_logp.hip -- log probabilities of given tokens, entropy and top alternatives of pararnn_lm.h, and their gradient.
+//
+// One pass over the logits each way.  The forward kernel is bound by vector instructions in bfloat16 (11 an element, two of
+// them conversions and one an exponential; 97% of the issue slots at 4096 x 131072 with 5 alternatives, 192 us, 5.6 TB/s),
+// by memory in float32 (4096 x 32000: 93 us, 5.6 TB/s), by one CU's instructions for few rows (32 x 50001 with 20
+// alternatives: 11 us).  The gradient is bound by memory (4096 x 32000 float32: 168 us for 1.05 GB, 6.2 TB/s).
 
 #include <type_traits>
 

@@ -1,7 +1,9 @@
 // lm_norm.hip -- layer normalisation of pararnn_lm.h and its gradients.
 //
 // Both directions are bound by memory: a row is read once into registers (up to 16 columns a lane), reduced there and
-// written.  The mean comes first and the variance is summed about it, since the row is at hand.
+// written.  The mean comes first and the variance is summed about it, since the row is at hand.  Measured, bf16 8192 x 4096
+// with residual: forward 51.6 us (268 MB, 5.2 TB/s), gradient 60 us (268 MB and 8 MB of parts, 4.6 TB/s) and 4.7 us for the
+// parameter sums; float32 5001 x 2047 15, 23.7 and 4.2 us.  A copy runs at 5.1 TB/s.
 
 #include <algorithm>
 #include <type_traits>
