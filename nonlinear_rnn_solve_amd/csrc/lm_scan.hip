@@ -138,7 +138,7 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p, uint32_t c
 //
 // Bound by memory for float32, by memory and vector instructions about equally for bfloat16 (56% and 54% of the issue
 // slots in the forward and the gradient kernel).  Measured, bf16 (wide: B = 2, T = 4096, D = 4096; long: B = 1, T = 131072,
-// D = 1024): forward 62.6 and 251 us (4.3 TB/s), gradient 111 and 446 us (4.2 TB/s); a copy runs at 5.1 TB/s.
+// D = 1024): forward 64 and 257 us (4.2 TB/s), gradient 112 and 449 us (4.2 TB/s); a copy runs at 5.1 TB/s.
 //  - 64 steps a tile (4 waves) against 128 (8 waves): gradient 118 against 151 us (wide), since its 150 registers leave
 //    12 waves on a CU in workgroups of 4 and 8 in workgroups of 8; forward 66 against 72.  32 elements a lane: 66 and 124.
 //  - groups against a look-back over the W tiles before: forward 257 against 297 us (long).  Groups of 16: 325.
@@ -161,10 +161,13 @@ struct Grid {
 constexpr int kTicket = 32, kLogClasses = 3;   // 128 bytes: counters share no cache line
 
 struct Aff { float A, B; };
-// the map of `later` after `earlier`; with packed sequences A = 0 is a cut, which nothing crosses, not even a NaN
-template <bool SEG> DEV float apply(const Aff& f, float h) { return SEG && f.A == 0.0f ? f.B : fmaf(f.A, h, f.B); }
+// The map of `later` after `earlier`.  With packed sequences A = NaN is a cut: nothing crosses it, not even a NaN, and the
+// product keeps it without a select.  (A = 0 would not do: strong decays have products of zero, which a NaN crosses.)  A map
+// whose own decay is NaN has B = NaN too, so that nothing is lost by reading it as a cut.
+constexpr float kCut = __builtin_nanf("");
+template <bool SEG> DEV float apply(const Aff& f, float h) { return SEG && f.A != f.A ? f.B : fmaf(f.A, h, f.B); }
 template <bool SEG> DEV Aff compose(const Aff& later, const Aff& earlier) {
-  return {SEG && later.A == 0.0f ? 0.0f : later.A * earlier.A, apply<SEG>(later, earlier.B)};
+  return {later.A * earlier.A, apply<SEG>(later, earlier.B)};
 }
 
 DEV uint64_t ld_word(const uint64_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
@@ -492,7 +495,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           if (p.h0) b[l][v] = fmaf(a[l][v], p.h0[state + v], b[l][v]);
-          a[l][v] = 0.0f;
+          a[l][v] = kCut;
         }
       }
   }
@@ -614,7 +617,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
 #pragma unroll
       for (int l = s * SL; l < (s + 1) * SL; ++l) {
         Aff e{a[l][v], in[l][v]};
-        if (SEG && starts >> l & 1) e = Aff{0.0f, fmaf(e.A, at(p.h0, l, v), e.B)};
+        if (SEG && starts >> l & 1) e = Aff{kCut, fmaf(e.A, at(p.h0, l, v), e.B)};
         f = l % SL ? compose<SEG>(e, f) : e;
       }
 #pragma unroll
@@ -623,7 +626,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
         float mu = r.B, A = first ? a[l][v] : a[l][v] * r.A;
         if (SEG && ends >> l & 1) {
           mu = at(q.d_last, l, v);
-          A = 0.0f;
+          A = kCut;
         }
         r = Aff{A, a[l][v] * (first && !SEG ? dh[l].get(v) : dh[l].get(v) + mu)};
       }

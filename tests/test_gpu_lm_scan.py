@@ -165,6 +165,28 @@ def test_a_spoilt_decay_gate_stays_in_its_sequence(T, cut):
     assert torch.isnan(h[:, cut:cut + 3]).all() and torch.isnan(g["d_lam"]).all()
 
 
+@pytest.mark.parametrize("lam_value", [3.0, 30.0])
+@pytest.mark.parametrize("T,at", [(14, 2), (400, 3), (1500, 200)])
+def test_a_spoilt_value_stays_to_the_end_of_its_sequence(T, at, lam_value):
+    # strong decays: their products (lam = 3: of some 10 steps, lam = 30: each one) are zero in float32, which is no cut
+    x, r, i, _, h0, dh, dl = make(2, T, 40, F32, seed=29, n=3, layout="dense")
+    r = r.abs() + 3
+    lam = torch.full((40,), lam_value, device="cuda")
+    end, nan = T - 5, float("nan")
+    cu = cuda_cu([0, 1, end, T])
+    x2, dh2 = x.clone(), dh.clone()
+    x2[:, at] = nan
+    h, last, carry = lm.gated_scan(x2, r, i, lam, h0=h0, cu_seqlens=cu, want_carry=True)
+    assert torch.isnan(h[:, at:end]).all() and torch.isnan(last[:, 1]).all()
+    assert torch.isfinite(h[:, :at]).all() and torch.isfinite(h[:, end:]).all() and torch.isfinite(last[:, [0, 2]]).all()
+    h, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, cu_seqlens=cu, want_carry=True)
+    dh2[:, end - 1 - at] = nan
+    g = lm.gated_scan_vjp(x, r, i, lam, carry, dh2, h0=h0, d_last=dl, cu_seqlens=cu)
+    assert torch.isnan(g["d_x"][:, 1:end - at]).all() and torch.isnan(g["d_h0"][:, 1]).all()
+    keep = [0] + list(range(end - at, T))
+    assert torch.isfinite(g["d_x"][:, keep]).all() and torch.isfinite(g["d_h0"][:, [0, 2]]).all()
+
+
 def test_gates_at_their_limits():
     # closed decay gate: a = 1, the state is held; wide open input; saturated values: finite everywhere
     B, T, D = 2, 300, 16
