@@ -282,7 +282,8 @@ __global__ __launch_bounds__(kGradThreads) void k_logp_grad(const LogpGradArgs p
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float l = none ? -INFINITY : x[u].get(e) - lse, q = hw_exp2(kLog2e * l);
-      o[e] = -q * fmaf(ge, fmaxf(l, -1e30f) + h, g);
+      // below -104 q is 0, and ge l stays finite up to ge = 1e34
+      o[e] = -q * fmaf(ge, fmaxf(l, -1e4f) + h, g);
     }
     const int64_t at = t - j;
     if (at >= 0 && at < V && !none)

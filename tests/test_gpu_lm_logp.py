@@ -85,6 +85,16 @@ def test_ruled_out_tokens(N, V, dtype):
     check(z, t, g, ge, top=20)
 
 
+@pytest.mark.parametrize("V", [300, 5001])
+def test_large_entropy_gradient_with_ruled_out_tokens(V):
+    # a power of two scales every product exactly; ln p of a ruled out token is -infinity
+    z, t, g, ge = make(5, V, F32, seed=V, banned=0.3)
+    res = lm.token_logprobs(z)
+    one = lm.token_logprobs_vjp(z, None, res.lse, res.entropy, None, ge)
+    large = lm.token_logprobs_vjp(z, None, res.lse, res.entropy, None, ge * 2.0 ** 108)
+    assert torch.equal(large, one * 2.0 ** 108) and torch.isfinite(large).all()
+
+
 @pytest.mark.parametrize("top", [0, 1, 2, 5, 31, 32])
 def test_alternative_counts(top):
     for V in (40, 3000, 20011):
