@@ -89,20 +89,28 @@ Tensor output(const Maybe& given, const char* name, const Tensor& like) {
 Tensor new_floats(at::IntArrayRef sizes, const Tensor& like) { return at::empty(sizes, like.options().dtype(at::kFloat)); }
 
 // One call of the C ABI: its device is current, its stream that of the device, its workspace that of the stream (calls on
-// different streams may overlap, calls on one stream follow each other), grown on demand.
+// different streams may overlap, calls on one stream follow each other), grown on demand.  A call that is being captured
+// into a graph takes a workspace of its own, which the graph's memory pool keeps: the stream's may be outgrown and
+// given back while the graph is still replayed, and two graphs captured on one stream may replay on two.
 struct Call {
   c10::DeviceGuard guard;
   c10::DeviceIndex index;
+  hipStream_t hip;
   void* stream;
   explicit Call(c10::Device device)
-      : guard(device), index(device.index()), stream(c10::hip::getCurrentHIPStream(device.index()).stream()) {}
-  Tensor& workspace(size_t bytes) const {
+      : guard(device), index(device.index()), hip(c10::hip::getCurrentHIPStream(device.index()).stream()), stream(hip) {}
+  Tensor workspace(size_t bytes) const {
+    const auto fresh = [&](size_t n) {
+      return at::empty({static_cast<int64_t>(n)},
+                       at::TensorOptions().dtype(at::kByte).device(c10::Device(c10::DeviceType::CUDA, index)));
+    };
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    if (hip && hipStreamIsCapturing(hip, &capture) == hipSuccess && capture == hipStreamCaptureStatusActive)
+      return fresh(bytes);
     // never destroyed: at exit the GPU runtime may be gone before a static's turn
     static auto* cache = new std::map<std::pair<int, void*>, Tensor>;
     Tensor& ws = (*cache)[{index, stream}];
-    if (!ws.defined() || static_cast<size_t>(ws.numel()) < bytes)
-      ws = at::empty({static_cast<int64_t>(std::max<size_t>(bytes, 1 << 16))},
-                     at::TensorOptions().dtype(at::kByte).device(c10::Device(c10::DeviceType::CUDA, index)));
+    if (!ws.defined() || static_cast<size_t>(ws.numel()) < bytes) ws = fresh(std::max<size_t>(bytes, 1 << 16));
     return ws;
   }
 };
@@ -162,7 +170,7 @@ std::tuple<Tensor, Tensor, Maybe> gated_scan(const Tensor& x, const Tensor& r, c
   Maybe carry;
   if (want_carry) carry = new_floats({s.p.B, pararnn_lm_scan_chunks(s.p.T), s.p.D}, x);
   const int64_t sh[2] = {h.stride(0), h.stride(1)};
-  Tensor& ws = call.workspace(pararnn_lm_scan_workspace_bytes(s.p.B, s.p.T, s.p.D));
+  const Tensor ws = call.workspace(pararnn_lm_scan_workspace_bytes(s.p.B, s.p.T, s.p.D));
   check(pararnn_lm_gated_scan(&s.p, h.data_ptr(), sh, pl, carry ? static_cast<float*>(carry->data_ptr()) : nullptr,
                               ws.data_ptr(), static_cast<size_t>(ws.numel()), call.stream),
         "pararnn_lm_gated_scan");
@@ -198,7 +206,7 @@ py::dict gated_scan_vjp(const Tensor& x, const Tensor& r, const Tensor& i, const
     g.d_h0 = static_cast<float*>(d_h0.data_ptr());
     res["d_h0"] = d_h0;
   }
-  Tensor& ws = call.workspace(pararnn_lm_scan_workspace_bytes(s.p.B, s.p.T, s.p.D));
+  const Tensor ws = call.workspace(pararnn_lm_scan_workspace_bytes(s.p.B, s.p.T, s.p.D));
   check(pararnn_lm_gated_scan_vjp(&s.p, &g, ws.data_ptr(), static_cast<size_t>(ws.numel()), call.stream),
         "pararnn_lm_gated_scan_vjp");
   return res;
@@ -258,7 +266,7 @@ py::dict layer_norm_vjp(const Tensor& dy, const Tensor& s, const Tensor& weight,
     pw = static_cast<float*>(dw.data_ptr()), pb = static_cast<float*>(db.data_ptr());
     res["d_weight"] = dw, res["d_bias"] = db;
   }
-  Tensor& ws = call.workspace(pararnn_lm_layer_norm_vjp_workspace_bytes(N, D));
+  const Tensor ws = call.workspace(pararnn_lm_layer_norm_vjp_workspace_bytes(N, D));
   check(pararnn_lm_layer_norm_vjp(dt, N, D, dy.data_ptr(), rows(dy, "dy").second, s.data_ptr(), ss,
                                   floats(weight, "weight", D, dev), floats(stats, "stats", 2 * N, dev),
                                   d_sum ? d_sum->data_ptr() : nullptr, ps, dx.data_ptr(), rows(dx, "out").second, pw, pb,
@@ -297,7 +305,7 @@ std::tuple<Maybe, Tensor, Tensor, Maybe, Maybe> token_logprobs(const Tensor& log
     top_logp = new_floats(lead, logits);
     top_ids = at::empty(lead, logits.options().dtype(at::kLong));
   }
-  Tensor& ws = call.workspace(pararnn_lm_token_logprobs_workspace_bytes(N, V, static_cast<int>(top)));
+  const Tensor ws = call.workspace(pararnn_lm_token_logprobs_workspace_bytes(N, V, static_cast<int>(top)));
   check(pararnn_lm_token_logprobs(dt, N, V, logits.data_ptr(), stride, tp, tb, static_cast<float*>(lse.data_ptr()),
                                   logp ? static_cast<float*>(logp->data_ptr()) : nullptr,
                                   static_cast<float*>(entropy.data_ptr()), static_cast<int>(top),

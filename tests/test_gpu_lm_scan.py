@@ -366,6 +366,37 @@ def test_graph_replays():
         torch.cuda.synchronize()
 
 
+def test_a_graph_keeps_its_workspace():
+    # a later, larger call on the stream that the graph was captured on, then other tensors where a workspace could have been
+    args = make(2, 700, 64, BF, seed=30, layout="dense")
+    big = make(2, 40000, 64, BF, seed=31, layout="dense")
+
+    def run(x, r, i, lam, h0, dh, dl):
+        h, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)
+        return [h, last, *lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl).values()]
+
+    want, want_big = run(*args), run(*big)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run(*args)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = run(*args)
+        got_big = run(*big)
+        side.synchronize()
+        others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in (1 << 12, 1 << 16, 1 << 18, 1 << 20, 1 << 22) * 3]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for o in out:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all((o == 7).all() for o in others)
+        assert all(torch.equal(a, b) for a, b in zip(out, want)) and all(torch.equal(a, b) for a, b in zip(got_big, want_big))
+
+
 def test_refusals():
     x, r, i, lam, h0, dh, dl = make(2, 20, 16, F32, seed=22, layout="dense")
     ok = lambda **k: lm.gated_scan(*(k.get(n, v) for n, v in zip("xril", (x, r, i, lam))), h0=k.get("h0"),  # noqa: E731
