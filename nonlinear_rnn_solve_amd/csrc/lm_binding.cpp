@@ -84,6 +84,8 @@ std::pair<int64_t, int64_t> rows(const Tensor& t, const char* name) {
 Tensor output(const Maybe& given, const char* name, const Tensor& like) {
   if (!given) return at::empty(like.sizes(), like.options());
   plane(*given, name, like);
+  for (int64_t k = 0; k < given->dim(); ++k)
+    if (given->size(k) > 1 && given->stride(k) == 0) refuse(std::string(name) + " must not be a broadcast view: it is written");
   return *given;
 }
 Tensor new_floats(at::IntArrayRef sizes, const Tensor& like) { return at::empty(sizes, like.options().dtype(at::kFloat)); }

@@ -405,7 +405,7 @@ def test_refusals():
     for bad in (dict(x=x.cpu()), dict(r=r.bfloat16()), dict(x=x.half(), r=r.half(), i=i.half()), dict(i=i[:, :5]), dict(x=x[0]),
                 dict(r=r.transpose(1, 2).contiguous().transpose(1, 2)), dict(l=lam.double()), dict(l=lam[:3]), dict(h0=h0[:1]),
                 dict(h0=h0.bfloat16()), dict(cu=torch.tensor([0, 20], device="cuda")), dict(cu=cuda_cu([0])),
-                dict(cu=cuda_cu([0, 5, 20]), h0=h0), dict(out=torch.empty_like(x, dtype=BF)), dict(h_last=h0[:1])):
+                dict(cu=cuda_cu([0, 5, 20]), h0=h0), dict(out=torch.empty_like(x, dtype=BF)), dict(out=x[:1].clone().expand(2, -1, -1)), dict(h_last=h0[:1])):
         with pytest.raises(ValueError):
             ok(**bad)
     for c in (0.0, -1.0, float("nan")):
