@@ -481,7 +481,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
     if (rates(p, tl, k)) gates(std::true_type{});
     else gates(std::false_type{});
   }
-  if (!tl.full) {   // steps past the end change nothing (x = 0 there)
+  if (!tl.full) {   // steps past the end change nothing that is used: no step before them depends on their b
 #pragma unroll
     for (int l = 0; l < L; ++l)
 #pragma unroll
@@ -595,14 +595,18 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
     if (rates(p, tl, k)) gates(std::true_type{});
     else gates(std::false_type{});
   }
-  if (!tl.full) {   // steps past the end change nothing (x = dh = 0 there) and add nothing
+  if (!tl.full) {   // steps past the end change nothing and add nothing, whatever a plane of overlapping steps has there
 #pragma unroll
-    for (int l = 0; l < L; ++l)
+    for (int l = 0; l < L; ++l) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         a[l][v] = l < tl.valid ? a[l][v] : 1.0f;
+        in[l][v] = l < tl.valid ? in[l][v] : 0.0f;
         sr[l][v] = l < tl.valid ? sr[l][v] : 0.0f;
       }
+#pragma unroll
+      for (int n = 0; n < Vec<T, V>::N; ++n) dh[l].w[n] = l < tl.valid ? dh[l].w[n] : 0u;
+    }
   }
   // what enters at a boundary: h0 at a sequence's first step, d_last at its last
   const int64_t dc = tl.c0 + (tl.active ? tl.ch : 0);

@@ -305,6 +305,21 @@ def test_broadcast_planes(T):
     check((x, r, i, lam, h0, dh, dl))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,cu", [(7, None), (40, None), (108, None), (333, None), (333, [0, 20, 300, 333])])
+def test_planes_broadcast_over_time_or_overlapping(T, cu, dtype):
+    # stride 0 over t (the gradient of a mean over time, for instance), steps closer than a row
+    n = len(cu) - 1 if cu else 0
+    x, r, i, lam, h0, dh, dl = make(2, T, 36, dtype, seed=32, n=n, layout="dense")
+    same = lambda p: p[:, T // 2:T // 2 + 1].expand(-1, T, -1)  # noqa: E731
+    over = lambda p: p.reshape(-1).as_strided((2, T, 36), (16 * T, 8, 1))  # noqa: E731
+    check((x, r, i, lam, h0, same(dh), dl), cu=cu)
+    check((same(x), same(r), same(i), lam, h0, dh, dl), cu=cu)
+    check((over(x), over(r), over(i), lam, h0, over(dh), dl), cu=cu)
+    check((x[..., :33], r[..., :33], i[..., :33], lam[:33], h0[..., :33].contiguous(), same(dh)[..., :33],
+           dl[..., :33].contiguous()), cu=cu)
+
+
 def test_offsets_beyond_32_bits():
     # rows over 2^32 elements apart, steps 2^25 apart: most offsets need 64 bits
     T, D = 130, 64
