@@ -357,10 +357,11 @@ struct Tile {
   }
 };
 
-// A plane as a wave sees it: for each of its lanes' steps l a buffer descriptor that begins at the wave's step l and ends
-// with the row's last step, so that loads past the end return zero and stores there do nothing, without a branch or an
-// address computation of the lane's own.  The lane's byte offset (its slice's steps and its channels) fits 32 bits: the
-// host takes V = 1, one slice a wave, where V slices would not.  Lanes without channels are out of range.
+// A plane as a wave sees it: a buffer descriptor that begins at the wave's first step and ends with the row's last step, so
+// that no access leaves the row and stores past its end do nothing, without a branch (loads past the end return zero, or a
+// step's values where steps overlap); the lane's byte offsets from it are 32 bits.  Lanes without channels are out of range.
+// Steps too far apart for that (kFar bytes) go one by one with 64-bit addresses, V = 1 only.
+constexpr int64_t kFar = (INT64_C(1) << 31) / EPL;
 template <typename T, int V>
 struct Plane {
   static constexpr int L = Shape<V>::L;
@@ -368,6 +369,7 @@ struct Plane {
   int64_t st;      // bytes from step to step
   int32_t steps;   // of the wave, below T
   uint32_t width, off;
+  bool far;
   DEV Plane(const void* p, const int64_t (&s)[2], const Tile<V>& tl, const ScanArgs& a) {
     const int64_t t = tl.t0 + tl.wave * (V * L), left = a.T - t, cols = a.D - tl.c0;
     st = s[1] * static_cast<int64_t>(sizeof(T));
@@ -375,24 +377,27 @@ struct Plane {
     steps = static_cast<int32_t>(left < 0 ? 0 : left > V * L ? V * L : left);
     width = static_cast<uint32_t>(cols > TW ? TW : cols) * static_cast<uint32_t>(sizeof(T));
     off = static_cast<uint32_t>(tl.slice * L) * static_cast<uint32_t>(st) + static_cast<uint32_t>(tl.ch * sizeof(T));
-    if (!tl.active) off = 0xf0000000u;
+    if (!tl.active) off = 0x80000000u;   // + 15 steps: still past any end, and no wrap
+    far = V == 1 && st > kFar;
   }
-  DEV __amdgpu_buffer_rsrc_t at(int l) const {
-    const int32_t left = V == 1 ? (l < steps ? 1 : 0) : steps - l;   // V = 1: no lane looks past step l
-    const uint32_t bytes = left > 0 ? static_cast<uint32_t>(left - 1) * static_cast<uint32_t>(st) + width : 0u;
-    return __builtin_amdgcn_make_buffer_rsrc(base + l * st, static_cast<short>(0), static_cast<int>(bytes), 0x00020000);
+  DEV __amdgpu_buffer_rsrc_t all() const {
+    const uint32_t bytes = steps > 0 ? static_cast<uint32_t>(steps - 1) * static_cast<uint32_t>(st) + width : 0u;
+    return __builtin_amdgcn_make_buffer_rsrc(base, static_cast<short>(0), static_cast<int>(bytes), 0x00020000);
   }
+  DEV uint32_t at(int l) const { return off + static_cast<uint32_t>(l) * static_cast<uint32_t>(st); }
+  DEV bool has(int l) const { return l < steps && off < width; }   // far, V = 1
+  DEV T* element(int l) const { return reinterpret_cast<T*>(base + l * st + off); }
   DEV Vec<T, V> load(int l) const {
     Vec<T, V> r;
     if constexpr (V * sizeof(T) == 2) {
-      r.w[0] = __builtin_amdgcn_raw_buffer_load_b16(at(l), off, 0, 0);
+      r.w[0] = __builtin_amdgcn_raw_buffer_load_b16(all(), at(l), 0, 0);
     } else if constexpr (V * sizeof(T) == 4) {
-      r.w[0] = __builtin_amdgcn_raw_buffer_load_b32(at(l), off, 0, 0);
+      r.w[0] = __builtin_amdgcn_raw_buffer_load_b32(all(), at(l), 0, 0);
     } else if constexpr (V * sizeof(T) == 8) {
-      const auto q = __builtin_amdgcn_raw_buffer_load_b64(at(l), off, 0, 0);
+      const auto q = __builtin_amdgcn_raw_buffer_load_b64(all(), at(l), 0, 0);
       r.w[0] = q[0], r.w[1] = q[1];
     } else {
-      const auto q = __builtin_amdgcn_raw_buffer_load_b128(at(l), off, 0, 0);
+      const auto q = __builtin_amdgcn_raw_buffer_load_b128(all(), at(l), 0, 0);
 #pragma unroll
       for (int k = 0; k < 4; ++k) r.w[k] = q[k];
     }
@@ -402,10 +407,13 @@ struct Plane {
     const Vec<T, V> r = pack_vec<T, V>(x);
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    if constexpr (V * sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(r.w[0]), at(l), off, 0, kStream);
-    else if constexpr (V * sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(r.w[0], at(l), off, 0, kStream);
-    else if constexpr (V * sizeof(T) == 8) __builtin_amdgcn_raw_buffer_store_b64(u32x2{r.w[0], r.w[1]}, at(l), off, 0, kStream);
-    else __builtin_amdgcn_raw_buffer_store_b128(u32x4{r.w[0], r.w[1], r.w[2], r.w[3]}, at(l), off, 0, kStream);
+    if (far) {   // uniform
+      if (has(l)) *element(l) = from_f32<T>(x[0]);
+    }
+    else if constexpr (V * sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(r.w[0]), all(), at(l), 0, kStream);
+    else if constexpr (V * sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(r.w[0], all(), at(l), 0, kStream);
+    else if constexpr (V * sizeof(T) == 8) __builtin_amdgcn_raw_buffer_store_b64(u32x2{r.w[0], r.w[1]}, all(), at(l), 0, kStream);
+    else __builtin_amdgcn_raw_buffer_store_b128(u32x4{r.w[0], r.w[1], r.w[2], r.w[3]}, all(), at(l), 0, kStream);
   }
 };
 
@@ -413,6 +421,18 @@ struct Plane {
 template <typename T, int V, int L>
 DEV void load_steps(const void* p, const int64_t (&s)[2], const Tile<V>& tl, const ScanArgs& a, Vec<T, V> (&v)[L]) {
   const Plane<T, V> pl(p, s, tl, a);
+  if (pl.far) {   // uniform
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+      v[l].w[0] = 0;
+      if (pl.has(l)) {
+        const T e = *pl.element(l);
+        if constexpr (sizeof(T) == 4) v[l].w[0] = __float_as_uint(e);
+        else v[l].w[0] = e.u;
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int l = 0; l < L; ++l) v[l] = pl.load(l);
 }
@@ -785,10 +805,17 @@ static pararnn_status check_scan(const pararnn_lm_scan* p) {
   return PARARNN_OK;
 }
 
+// the strides of a plane of T steps of D channels; that of a single step means nothing, and is made one that a Plane can use
+static void strides(int64_t (&to)[2], const int64_t (&from)[2], int64_t T, int64_t D) {
+  to[0] = from[0];
+  to[1] = T > 1 ? from[1] : D;
+}
 static ScanArgs scan_args(const pararnn_lm_scan* p) {
   ScanArgs a{};
   a.x = p->x; a.r = p->r; a.i = p->i;
-  for (int k = 0; k < 2; ++k) { a.sx[k] = p->sx[k]; a.sr[k] = p->sr[k]; a.si[k] = p->si[k]; }
+  strides(a.sx, p->sx, p->T, p->D);
+  strides(a.sr, p->sr, p->T, p->D);
+  strides(a.si, p->si, p->T, p->D);
   a.lam = p->lam; a.h0 = p->h0; a.cu = p->cu_seqlens;
   a.n = p->cu_seqlens ? static_cast<int32_t>(p->n_seqs) : 1;
   a.c = p->c; a.B = p->B; a.T = p->T; a.D = p->D;
@@ -814,8 +841,8 @@ static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
 
 // V consecutive elements from every row and step of a plane are one aligned access, and V slices of a wave lie within
 // 32-bit byte offsets
-static bool wide(const void* p, const int64_t (&s)[2], size_t es, int V, int64_t B, int64_t T) {
-  return aligned(p, es * V) && (B <= 1 || s[0] % V == 0) && (T <= 1 || s[1] % V == 0) && s[1] < (INT64_C(1) << 31) / (EPL * 4);
+static bool wide(const void* p, const int64_t (&s)[2], size_t es, int V, int64_t B) {
+  return aligned(p, es * V) && (B <= 1 || s[0] % V == 0) && s[1] % V == 0 && s[1] <= kFar / static_cast<int64_t>(es);
 }
 
 template <class F>
@@ -870,7 +897,8 @@ extern "C" pararnn_status pararnn_lm_gated_scan(const pararnn_lm_scan* prob, voi
   if (!grid_ok(l.tiles, NTH) || !grid_ok(prob->B * l.ctiles, NTH)) return PARARNN_ERR_UNSUPPORTED;
   if (!ptr_ok(ws, 256) || ws_bytes < static_cast<size_t>(l.total)) return PARARNN_ERR_WORKSPACE;
   ScanArgs a = scan_args(prob);
-  a.h = h; a.sh[0] = sh[0]; a.sh[1] = sh[1]; a.h_last = h_last; a.carry = carry;
+  a.h = h; a.h_last = h_last; a.carry = carry;
+  a.sh[0] = sh[0]; a.sh[1] = a.T > 1 ? sh[1] : a.D;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.T <= kSerial) {
     const uint32_t ctiles = static_cast<uint32_t>(l.ctiles), grid = static_cast<uint32_t>(a.B) * ctiles;
@@ -879,8 +907,8 @@ extern "C" pararnn_status pararnn_lm_gated_scan(const pararnn_lm_scan* prob, voi
     return launched();
   }
   prepare(l, ws, a, a.h0, a.h_last, st);
-  const bool vec = a.D % 4 == 0 && wide(a.x, a.sx, es, 4, a.B, a.T) && wide(a.r, a.sr, es, 4, a.B, a.T) &&
-                   wide(a.i, a.si, es, 4, a.B, a.T) && wide(h, a.sh, es, 4, a.B, a.T);
+  const bool vec = a.D % 4 == 0 && wide(a.x, a.sx, es, 4, a.B) && wide(a.r, a.sr, es, 4, a.B) &&
+                   wide(a.i, a.si, es, 4, a.B) && wide(h, a.sh, es, 4, a.B);
   const Grid g = grid_of(l, ws, a.B);
   pick(prob->dtype, vec, a.cu != nullptr, [&](auto t, auto v, auto seg) {
     k_scan<decltype(t), decltype(v)::value, decltype(seg)::value><<<static_cast<unsigned>(l.tiles), NTH, 0, st>>>(a, g);
@@ -911,18 +939,19 @@ extern "C" pararnn_status pararnn_lm_gated_scan_vjp(const pararnn_lm_scan* prob,
   q.f = scan_args(prob);
   q.f.carry = const_cast<float*>(gr->carry);
   q.dh = gr->dh; q.d_last = gr->d_last; q.dx = gr->d_x; q.dr = gr->d_r; q.di = gr->d_i; q.d_h0 = gr->d_h0;
-  for (int k = 0; k < 2; ++k) {
-    q.sdh[k] = gr->sdh[k]; q.sdx[k] = gr->sdx[k]; q.sdr[k] = gr->sdr[k]; q.sdi[k] = gr->sdi[k];
-  }
+  strides(q.sdh, gr->sdh, prob->T, prob->D);
+  strides(q.sdx, gr->sdx, prob->T, prob->D);
+  strides(q.sdr, gr->sdr, prob->T, prob->D);
+  strides(q.sdi, gr->sdi, prob->T, prob->D);
   q.part = gr->d_lam ? reinterpret_cast<float*>(static_cast<char*>(ws) + l.tickets + l.words + l.gwords) : nullptr;
   const ScanArgs& a = q.f;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.B > 0) prepare(l, ws, a, q.d_last, q.d_h0, st);
   if (l.tiles > 0) {
-    const bool vec = a.D % 4 == 0 && wide(a.x, a.sx, es, 4, a.B, a.T) && wide(a.r, a.sr, es, 4, a.B, a.T) &&
-                     wide(a.i, a.si, es, 4, a.B, a.T) && wide(q.dh, q.sdh, es, 4, a.B, a.T) &&
-                     wide(q.dx, q.sdx, es, 4, a.B, a.T) && wide(q.dr, q.sdr, es, 4, a.B, a.T) &&
-                     wide(q.di, q.sdi, es, 4, a.B, a.T);
+    const bool vec = a.D % 4 == 0 && wide(a.x, a.sx, es, 4, a.B) && wide(a.r, a.sr, es, 4, a.B) &&
+                     wide(a.i, a.si, es, 4, a.B) && wide(q.dh, q.sdh, es, 4, a.B) &&
+                     wide(q.dx, q.sdx, es, 4, a.B) && wide(q.dr, q.sdr, es, 4, a.B) &&
+                     wide(q.di, q.sdi, es, 4, a.B);
     const Grid g = grid_of(l, ws, a.B);
     pick(prob->dtype, vec, a.cu != nullptr, [&](auto t, auto v, auto seg) {
       k_scan_grad<decltype(t), decltype(v)::value, decltype(seg)::value><<<static_cast<unsigned>(l.tiles), NTH, 0, st>>>(q, g);

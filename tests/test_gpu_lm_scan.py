@@ -336,6 +336,43 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(outbuf, want)
 
 
+@pytest.mark.parametrize("D", [64, 50])
+def test_steps_too_far_apart_for_32_bits_in_a_tile(D):
+    # steps over 2^27 bytes apart, every plane and output of both passes in one array
+    T, step = 40, (1 << 26) + 8
+    x, r, i, lam, h0, dh, dl = make(2, T, D, BF, seed=33, layout="dense")
+    buf = torch.empty(2 * T * step, dtype=BF, device="cuda")
+    planes = [buf.as_strided((2, T, D), (T * step, step, 1), 64 * k) for k in range(9)]
+    guards = buf.as_strided((2, T, 64), (T * step, step, 1), 64 * 9)
+    for p, src in zip(planes, (x, r, i, dh)):
+        p.copy_(src)
+    guards.fill_(7)
+    h, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)
+    g = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl)
+    far = planes[:3]
+    fh, flast, fcarry = lm.gated_scan(*far, lam, h0=h0, want_carry=True, out=planes[4])
+    fg = lm.gated_scan_vjp(*far, lam, fcarry, planes[3], h0=h0, d_last=dl, out=planes[5:8])
+    assert torch.equal(fh, h) and torch.equal(flast, last) and torch.equal(fcarry, carry)
+    assert set(g) == set(fg) and all(torch.equal(fg[k], g[k]) for k in g)
+    assert (guards == 7).all()
+    lm.gated_scan(*(p[:, :5] for p in far), lam, h0=h0, out=planes[8][:, :5])
+    assert torch.equal(planes[8][:, :5], h[:, :5])
+
+
+def test_a_single_step_of_any_stride():
+    # the stride of a dimension of one entry means nothing
+    x, r, i, lam, h0, dh, dl = make(2, 1, 33, BF, seed=34, layout="dense")
+    want = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)
+    g = lm.gated_scan_vjp(x, r, i, lam, want[2], dh, h0=h0, d_last=dl)
+    for stride in (0, 1, 3, 64, 1 << 40, (1 << 62) + 1):
+        view = lambda t: t.as_strided((2, 1, 33), (33, stride, 1))  # noqa: E731
+        out = [torch.empty(66, dtype=BF, device="cuda") for _ in range(4)]
+        got = lm.gated_scan(view(x), view(r), view(i), lam, h0=h0, want_carry=True, out=view(out[0]))
+        gg = lm.gated_scan_vjp(view(x), view(r), view(i), lam, got[2], view(dh), h0=h0, d_last=dl, out=[view(o) for o in out[1:]])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(gg[k], g[k]) for k in g)
+
+
 def test_same_bits_in_every_run_and_on_another_stream():
     args = make(2, 2000, 130, BF, seed=19)
     x, r, i, lam, h0, dh, dl = args
