@@ -2,8 +2,8 @@
 //
 // Both directions are bound by memory: a row is read once into registers (up to 16 columns a lane), reduced there and
 // written.  The mean comes first and the variance is summed about it, since the row is at hand.  Measured, bf16 8192 x 4096
-// with residual: forward 51.6 us (268 MB, 5.2 TB/s), gradient 60 us (268 MB and 8 MB of parts, 4.6 TB/s) and 4.7 us for the
-// parameter sums; float32 5001 x 2047 15, 23.7 and 4.2 us.  A copy runs at 5.1 TB/s.
+// with residual: forward 51.6 us (268 MB, 5.2 TB/s), gradient 53.6 us (268 MB and 17 MB of parts, 5.3 TB/s) and 4.7 us for the
+// parameter sums; float32 5001 x 2047 15, 22.7 and 4.2 us.  A copy runs at 5.1 TB/s.
 
 #include <algorithm>
 #include <type_traits>
@@ -134,14 +134,20 @@ struct NormGradArgs {
   float* part;   // [workgroups][2][D] sums of dy n and of dy over a workgroup's rows, or null
 };
 
-// A workgroup takes NT / LPR rows at a time, kGradGroups workgroups in turn, and keeps the parameter sums of its lanes'
-// columns in registers; its row groups add theirs up in order through shared memory at the end.
-constexpr int kGradThreads = 1024, kGradGroups = 256;
+// A workgroup takes NT / LPR rows at a time, as many workgroups as the chip holds at once in turn, and keeps the parameter sums of its lanes'
+// columns in registers; in the end its row groups' are added up in order, those of a wave by lane exchanges, then the
+// PG waves (or groups of waves) of different rows through shared memory, kStage columns a lane at a time.
+// 512 threads and 512 workgroups against 1024 and 256: bf16 8192 x 4096 53.6 and 54.6 us, 20000 x 700 33.8 and 34.4, 3 x 552
+// 4.3 and 5.2; 256 threads 55.6 and 35.0, and twice the time for their sums.  What a lane keeps over a row's reduction are
+// the normalised values and dy weight, in the registers of what was loaded: nothing spills (60 us where it did).
+constexpr int kGradAll = 1 << 18, kStage = 4;
+constexpr int grad_threads(int64_t lpr) { return lpr > 512 ? 1024 : 512; }
 template <typename T, class S>
-__global__ __launch_bounds__(kGradThreads) void k_norm_grad(const NormGradArgs p) {
-  constexpr int LPR = S::LPR, V = S::V, NV = S::NV, NT = kGradThreads, RG = NT / LPR;
+__global__ __launch_bounds__(grad_threads(S::LPR)) void k_norm_grad(const NormGradArgs p) {
+  constexpr int LPR = S::LPR, V = S::V, NV = S::NV, NT = grad_threads(S::LPR), RG = NT / LPR;
+  constexpr int PL = LPR < WAVE ? WAVE : LPR, PG = NT / PL;
   __shared__ RowSum<LPR, 2, NT> sh;
-  __shared__ float sh_p[RG > 1 ? 2 : 1][RG > 1 ? LPR * S::CPL : 1];
+  __shared__ float sh_p[PG > 1 ? PG : 1][2][PG > 1 ? LPR * kStage : 1];
   int turn = 0;
   const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
   const float inv = 1.0f / static_cast<float>(p.D);
@@ -172,15 +178,18 @@ __global__ __launch_bounds__(kGradThreads) void k_norm_grad(const NormGradArgs p
     }
     const float mean = p.stats[2 * n], rstd = p.stats[2 * n + 1];
     float c12[2] = {0.0f, 0.0f};
+    float xn[NV][V], t[NV][V];   // in the registers of s, dy and the weights
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float d = g[k].get(e), xn = (a[k].get(e) - mean) * rstd, t = d * w[k].get(e);   // past D: d = 0
-        c12[0] += t;
-        c12[1] = fmaf(t, xn, c12[1]);
+        const float d = g[k].get(e);   // past D: 0
+        xn[k][e] = (a[k].get(e) - mean) * rstd;
+        t[k][e] = d * w[k].get(e);
+        c12[0] += t[k][e];
+        c12[1] = fmaf(t[k][e], xn[k][e], c12[1]);
         if (on) {
-          sw[k][e] = fmaf(d, xn, sw[k][e]);
+          sw[k][e] = fmaf(d, xn[k][e], sw[k][e]);
           sb[k][e] += d;
         }
       }
@@ -194,8 +203,7 @@ __global__ __launch_bounds__(kGradThreads) void k_norm_grad(const NormGradArgs p
         float o[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float xn = (a[k].get(e) - mean) * rstd;
-          o[e] = rstd * (fmaf(g[k].get(e), w[k].get(e), -c1) - xn * c2);
+          o[e] = rstd * ((t[k][e] - c1) - xn[k][e] * c2);
           if (dsum) o[e] += ds[k].get(e);
         }
         store_row<T, V>(dx + c, p.D - c, o);
@@ -203,25 +211,37 @@ __global__ __launch_bounds__(kGradThreads) void k_norm_grad(const NormGradArgs p
     }
   }
   if (!p.part) return;
-  if constexpr (RG > 1) {
-    for (int r = 0; r < RG; ++r) {
-      __syncthreads();
-      if (group == r)
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const int c = (k * LPR + lane) * V + e;
-            sh_p[0][c] = (r ? sh_p[0][c] : 0.0f) + sw[k][e];
-            sh_p[1][c] = (r ? sh_p[1][c] : 0.0f) + sb[k][e];
-          }
-    }
-    __syncthreads();
+  if constexpr (PG > 1) {
+    const int place = threadIdx.x / PL;
     float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
-    for (int64_t c = threadIdx.x; c < p.D; c += NT) {
-      out[c] = sh_p[0][c];
-      out[p.D + c] = sh_p[1][c];
-    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int e0 = 0; e0 < V; e0 += kStage) {
+#pragma unroll
+        for (int e = 0; e < kStage; ++e) {
+          float w = sw[k][e0 + e], b = sb[k][e0 + e];
+#pragma unroll
+          for (int o = LPR; o < WAVE; o <<= 1) {
+            w += __shfl_xor(w, o, WAVE);
+            b += __shfl_xor(b, o, WAVE);
+          }
+          if (threadIdx.x % PL < LPR) {
+            sh_p[place][0][lane * kStage + e] = w;
+            sh_p[place][1][lane * kStage + e] = b;
+          }
+        }
+        __syncthreads();
+        for (int at = threadIdx.x; at < 2 * LPR * kStage; at += NT) {
+          const int which = at / (LPR * kStage), c = at % (LPR * kStage);
+          float t = sh_p[0][which][c];
+#pragma unroll
+          for (int g = 1; g < PG; ++g) t += sh_p[g][which][c];
+          const int64_t col = static_cast<int64_t>(k * LPR + c / kStage) * V + e0 + c % kStage;
+          if (col < p.D) out[which * p.D + col] = t;
+        }
+        __syncthreads();
+      }
   } else {
     float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
 #pragma unroll
@@ -272,8 +292,10 @@ template <typename T, class F> static void shape_of(int64_t D, F f) {
 
 // threads that a row of k_norm takes at most
 static int64_t norm_threads(int64_t D) { return D <= 256 ? 16 : D <= 1024 ? 64 : D <= 4096 ? 256 : 1024; }
-static int64_t grad_rows(int64_t D) { return kGradThreads / norm_threads(D); }
-static int64_t grad_groups(int64_t N, int64_t D) { return std::min<int64_t>(ceil_div(N, grad_rows(D)), kGradGroups); }
+static int64_t grad_groups(int64_t N, int64_t D) {
+  const int64_t lanes = norm_threads(D), threads = grad_threads(lanes);
+  return std::min<int64_t>(ceil_div(N, threads / lanes), kGradAll / threads);
+}
 
 }  // namespace lm
 
@@ -309,7 +331,7 @@ extern "C" pararnn_status pararnn_lm_layer_norm(int dtype, int64_t N, int64_t D,
 }
 
 extern "C" size_t pararnn_lm_layer_norm_vjp_workspace_bytes(int64_t N, int64_t D) {
-  if (!sizes_fit(N, D) || !sizes_fit(2 * kGradGroups, D)) return 0;
+  if (!sizes_fit(N, D) || !sizes_fit(1024, D)) return 0;
   return static_cast<size_t>(grad_groups(N, D) * 2 * D * 4 + 256);
 }
 
@@ -336,7 +358,7 @@ extern "C" pararnn_status pararnn_lm_layer_norm_vjp(int dtype, int64_t N, int64_
   hipStream_t st = static_cast<hipStream_t>(stream);
   const auto run = [&](auto t) {
     using T = decltype(t);
-    shape_of<T>(D, [&](auto sh) { k_norm_grad<T, decltype(sh)><<<static_cast<unsigned>(groups), kGradThreads, 0, st>>>(a); });
+    shape_of<T>(D, [&](auto sh) { k_norm_grad<T, decltype(sh)><<<static_cast<unsigned>(groups), grad_threads(decltype(sh)::LPR), 0, st>>>(a); });
   };
   if (N > 0) {
     if (dtype == PARARNN_BF16) run(bf16{});
