@@ -14,7 +14,7 @@
  *    statistics, parameters and their gradients are float32; an output in bfloat16 is rounded once, to the
  *    nearest even.
  *  - Sizes of any value are accepted (odd ones included); pointers need the alignment of their element type
- *    only.  Wider alignment is used where base and strides have it.
+ *    only.
  *  - Every result is a fixed sequence of operations on its inputs: it is the same bits in every run.
  */
 #ifndef PARARNN_LM_H

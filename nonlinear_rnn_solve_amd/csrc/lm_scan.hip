@@ -118,7 +118,7 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p, uint32_t c
 // ------------------------------------------------------------------------------------------------
 // The parallel scan.  A tile is one workgroup: CT steps of TW channels of one row.  A lane holds V channels of
 // L = 16 / V consecutive steps; the lanes of a wave cover TW channels V times over, as V time slices.  A tile's steps are
-// NSEG segments of SL, whatever V is, so that alignment changes no bit.  Each lane composes its segments' maps
+// NSEG segments of SL, whatever V is, so that strides and widths change no bit.  Each lane composes its segments' maps
 // h -> a h + b; each wave, now a lane a channel, joins its own segments; one wave joins the waves', takes the state
 // entering the tile from the tiles before it and gives every wave its entering state, from which each wave finds its
 // segments' and the lanes walk their steps.  Inputs are read once.
@@ -136,9 +136,17 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p, uint32_t c
 // workgroup starts with a class that is no function of its XCD (the block number modulo 8): chains bound to an XCD cost
 // 25% at T = 131072, D = 1024.
 //
+// V = 4, with accesses of 8 or 16 bytes at any alignment of the element; where four does not divide the width the last lane's
+// channels overlap the lane's before (two lanes then store the same values).  One element a lane (V = 1) costs 50.8 against
+// 46.1 us in the gradient of bf16 B = 2, T = 10301, D = 345 and 11 against 8 us where one tile is all of time; it stays
+// for fewer than four channels and for steps too far apart for 32-bit offsets.
+//
+// Packed sequences: a wave finds its steps' sequences once and keeps them in shared memory (searched for at each boundary
+// by its lane: bf16 B = 4, T = 4096, D = 1000, 9 sequences 108 against 93 us in the gradient, 61 against 51 forward).
+//
 // Bound by memory for float32, by memory and vector instructions about equally for bfloat16 (56% and 54% of the issue
 // slots in the forward and the gradient kernel).  Measured, bf16 (wide: B = 2, T = 4096, D = 4096; long: B = 1, T = 131072,
-// D = 1024): forward 64 and 257 us (4.2 TB/s), gradient 112 and 449 us (4.2 TB/s); a copy runs at 5.1 TB/s.
+// D = 1024): forward 62 and 260 us (4.2 TB/s), gradient 103 and 440 us (4.3 TB/s); a copy runs at 5.1 TB/s.
 //  - 64 steps a tile (4 waves) against 128 (8 waves): gradient 118 against 151 us (wide), since its 150 registers leave
 //    12 waves on a CU in workgroups of 4 and 8 in workgroups of 8; forward 66 against 72.  32 elements a lane: 66 and 124.
 //  - groups against a look-back over the W tiles before: forward 257 against 297 us (long).  Groups of 16: 325.
@@ -329,6 +337,7 @@ struct Tile {
   uint32_t pos, chunk;    // place in scan order, chunk
   int32_t chain;
   int seg, ch, lane, wave, slice;   // the lane's first segment and first channel within the tile
+  int cols;               // the tile's channels
   bool active, full;      // the lane's channels exist; all the tile's steps do
   int valid;              // steps of the lane below T
   DEV Tile(const Grid& g, const ScanArgs& p, uint32_t (&sh)[2], bool reverse) {
@@ -341,13 +350,23 @@ struct Tile {
     chunk = reverse ? static_cast<uint32_t>(g.chunks) - 1 - pos : pos;
     const uint32_t row = static_cast<uint32_t>(chain) / static_cast<uint32_t>(g.ctiles);
     b = row;
-    c0 = static_cast<int64_t>(static_cast<uint32_t>(chain) - row * static_cast<uint32_t>(g.ctiles)) * TW;
+    const int32_t column = chain - static_cast<int32_t>(row) * g.ctiles;
+    c0 = static_cast<int64_t>(column) * TW;
+    cols = p.D - c0 < TW ? static_cast<int>(p.D - c0) : TW;
+    if (V > 1) {   // a last tile of fewer than V channels takes V of the one before
+      const int rest = static_cast<int>(p.D % TW);
+      if (rest > 0 && rest < V) {
+        if (column == g.ctiles - 1) c0 -= V, cols += V;
+        if (column == g.ctiles - 2) cols -= V;
+      }
+    }
     t0 = static_cast<int64_t>(chunk) * CT;
     slice = lane / (WAVE / V);
     seg = (wave * V + slice) * Q;
     ch = (lane % (WAVE / V)) * V;
+    active = ch < cols;
+    if (active && ch > cols - V) ch = cols - V;   // the last V channels, some of them with the lane before: the same values
     t = t0 + seg * SL;
-    active = c0 + ch < p.D;
     full = t0 + CT <= p.T;
     valid = L;
     if (!full) {
@@ -371,11 +390,11 @@ struct Plane {
   uint32_t width, off;
   bool far;
   DEV Plane(const void* p, const int64_t (&s)[2], const Tile<V>& tl, const ScanArgs& a) {
-    const int64_t t = tl.t0 + tl.wave * (V * L), left = a.T - t, cols = a.D - tl.c0;
+    const int64_t t = tl.t0 + tl.wave * (V * L), left = a.T - t;
     st = s[1] * static_cast<int64_t>(sizeof(T));
     base = static_cast<char*>(const_cast<void*>(p)) + (tl.b * s[0] + t * s[1] + tl.c0) * static_cast<int64_t>(sizeof(T));
     steps = static_cast<int32_t>(left < 0 ? 0 : left > V * L ? V * L : left);
-    width = static_cast<uint32_t>(cols > TW ? TW : cols) * static_cast<uint32_t>(sizeof(T));
+    width = static_cast<uint32_t>(tl.cols) * static_cast<uint32_t>(sizeof(T));
     off = static_cast<uint32_t>(tl.slice * L) * static_cast<uint32_t>(st) + static_cast<uint32_t>(tl.ch * sizeof(T));
     if (!tl.active) off = 0x80000000u;   // + 15 steps: still past any end, and no wrap
     far = V == 1 && st > kFar;
@@ -448,24 +467,28 @@ DEV bool rates(const ScanArgs& p, const Tile<V>& tl, float (&k)[V]) {
   return __any(!(own >= -kNear));
 }
 
-// Packed sequences: which of the lane's steps begin and which end one (the row's first and last step included).  The
-// offsets are searched for the wave's 16 steps together, with scalar loads, which do not wait for the planes'.
+// Packed sequences: which of the lane's steps begin and which end one (the row's first and last step included), and the
+// sequence of each of the wave's steps in `seq`.  The offsets are searched once for the wave's steps together, with scalar
+// loads, which do not wait for the planes'.
 template <int V>
-DEV void boundaries(const ScanArgs& p, const Tile<V>& tl, uint32_t& starts, uint32_t& ends) {
+DEV void boundaries(const ScanArgs& p, const Tile<V>& tl, uint32_t& starts, uint32_t& ends, int32_t (&seq)[EPL]) {
   constexpr int S = V * Shape<V>::L;
   static_assert(S == EPL && S <= 32, "the steps of a wave are bits of a word");
   const int64_t t = tl.t0 + tl.wave * S;
   starts = ends = 0;
   if (t >= p.T) return;
   const int left = static_cast<int>(p.T - t < S ? p.T - t : S);
-  int32_t j = sequence_of(p.cu, p.n, t);
+  int32_t j = sequence_of(p.cu, p.n, t), mine = j;   // mine: of step number `lane`
   if (t == 0 || (j > 0 && p.cu[j] == t)) starts = 1;
   for (++j; j < p.n; ++j) {   // the sequences that begin after step t
     const int64_t at = p.cu[j] - t;
     if (at > left || at < 1) break;   // at < 1: offsets out of order
     ends |= 1u << (at - 1);
     if (at < left) starts |= 1u << at;
+    if (tl.lane >= at) mine = j;
   }
+  if (tl.lane < S) seq[tl.lane] = mine;
+  wave_sync();
   if (t + left == p.T) ends |= 1u << (left - 1);
   starts = starts >> (tl.slice * Shape<V>::L) & (~0u >> (32 - Shape<V>::L));
   ends = ends >> (tl.slice * Shape<V>::L) & (~0u >> (32 - Shape<V>::L));
@@ -475,6 +498,7 @@ template <typename T, int V, bool SEG>
 __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k_scan(const ScanArgs p, const Grid g) {
   constexpr int L = Shape<V>::L, Q = Shape<V>::Q;
   __shared__ uint32_t sh_ticket[2];
+  __shared__ int32_t sh_seq[SEG ? NW : 1][EPL];
   __shared__ Aff sh_map[NSEG][TW], sh_wave[NW][TW];
   __shared__ float sh_enter[NSEG][TW], sh_in[NW][TW];
   const Tile<V> tl(g, p, sh_ticket, false);
@@ -486,7 +510,6 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
     load_steps(p.r, p.sr, tl, p, r);
     load_steps(p.i, p.si, tl, p, i);
     load_steps(p.x, p.sx, tl, p, x);
-    if (SEG) boundaries(p, tl, starts, ends);
     float k[V];
     const auto gates = [&](auto far) {
 #pragma unroll
@@ -501,6 +524,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
     if (rates(p, tl, k)) gates(std::true_type{});
     else gates(std::false_type{});
   }
+  if (SEG) boundaries(p, tl, starts, ends, sh_seq[tl.wave]);
   if (!tl.full) {   // steps past the end change nothing that is used: no step before them depends on their b
 #pragma unroll
     for (int l = 0; l < L; ++l)
@@ -511,7 +535,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
 #pragma unroll
     for (int l = 0; l < L; ++l)
       if (starts >> l & 1) {
-        const int64_t state = (tl.b * p.n + sequence_of(p.cu, p.n, tl.t + l)) * p.D + tl.c0 + (tl.active ? tl.ch : 0);
+        const int64_t state = (tl.b * p.n + sh_seq[tl.wave][tl.slice * L + l]) * p.D + tl.c0 + (tl.active ? tl.ch : 0);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           if (p.h0) b[l][v] = fmaf(a[l][v], p.h0[state + v], b[l][v]);
@@ -534,12 +558,12 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
   if (tl.wave == 0) {
     const int64_t d = tl.c0 + tl.lane;
     float h = 0.0f;
-    if (d < p.D) {
+    if (tl.lane < tl.cols) {
       // h0 before anything is published: h_last may be the same array, and a tile that waits for this one's map may write it
       float begin = 0.0f;      // the state of a sequence that begins with the tile
       bool begins = false;
       if (SEG) {
-        const int32_t j = sequence_of(p.cu, p.n, tl.t0);
+        const int32_t j = sh_seq[0][0];
         begins = tl.t0 == 0 || (j > 0 && p.cu[j] == tl.t0);
         if (begins && p.h0 && p.carry) begin = p.h0[(tl.b * p.n + j) * p.D + d];
       } else if (tl.pos < GS && p.h0) {
@@ -567,7 +591,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
     }
     out.store(l, h);
     if ((SEG ? (ends >> l & 1) && p.h_last : l == last) && tl.active) {
-      const int32_t j = SEG ? sequence_of(p.cu, p.n, tl.t + l) : 0;
+      const int32_t j = SEG ? sh_seq[tl.wave][tl.slice * L + l] : 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) p.h_last[(tl.b * p.n + j) * p.D + tl.c0 + tl.ch + v] = h[v];
     }
@@ -584,6 +608,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
   constexpr int L = Shape<V>::L, Q = Shape<V>::Q;
   const ScanArgs& p = q.f;
   __shared__ uint32_t sh_ticket[2];
+  __shared__ int32_t sh_seq[SEG ? NW : 1][EPL];
   __shared__ Aff sh_fwd[NSEG][TW], sh_rev[NSEG][TW], sh_wfwd[NW][TW], sh_wrev[NW][TW];
   __shared__ float sh_h[NSEG][TW], sh_mu[NSEG][TW], sh_wh[NW][TW], sh_wmu[NW][TW];
   const Tile<V> tl(g, p, sh_ticket, true);
@@ -598,7 +623,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
     load_steps(p.i, p.si, tl, p, i);
     load_steps(p.x, p.sx, tl, p, x);
     load_steps(q.dh, q.sdh, tl, p, dh);
-    if (SEG) boundaries(p, tl, starts, ends);
+    if (SEG) boundaries(p, tl, starts, ends, sh_seq[tl.wave]);
     const auto gates = [&](auto far) {
 #pragma unroll
       for (int l = 0; l < L; ++l)
@@ -631,7 +656,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
   // what enters at a boundary: h0 at a sequence's first step, d_last at its last
   const int64_t dc = tl.c0 + (tl.active ? tl.ch : 0);
   const auto at = [&](const float* base, int l, int v) {
-    return base ? base[(tl.b * p.n + sequence_of(p.cu, p.n, tl.t + l)) * p.D + dc + v] : 0.0f;
+    return base ? base[(tl.b * p.n + sh_seq[tl.wave][tl.slice * L + l]) * p.D + dc + v] : 0.0f;
   };
 #pragma unroll
   for (int s = 0; s < Q; ++s)
@@ -664,14 +689,14 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
   const int64_t dl = tl.c0 + tl.lane;
   if (tl.wave == 0) {
     float mu = 0.0f;
-    if (dl < p.D) {
+    if (tl.lane < tl.cols) {
       if (!SEG && tl.pos < GS) mu = q.d_last ? q.d_last[tl.b * p.D + dl] : 0.0f;
       mu = enter_tile<SEG>(g, tl.pos, tl.chain, tl.lane, join<SEG, true, NW>(sh_wrev, tl.lane), mu);
     }
     spread<SEG, true, NW>(sh_wrev, sh_wmu, tl.lane, mu);
   }
   if (tl.wave == 1)
-    spread<SEG, false, NW>(sh_wfwd, sh_wh, tl.lane, dl < p.D ? p.carry[(tl.b * g.chunks + tl.chunk) * p.D + dl] : 0.0f);
+    spread<SEG, false, NW>(sh_wfwd, sh_wh, tl.lane, tl.lane < tl.cols ? p.carry[(tl.b * g.chunks + tl.chunk) * p.D + dl] : 0.0f);
   __syncthreads();
   spread<SEG, false, SW>(sh_fwd + tl.wave * SW, sh_h + tl.wave * SW, tl.lane, sh_wh[tl.wave][tl.lane]);
   spread<SEG, true, SW>(sh_rev + tl.wave * SW, sh_mu + tl.wave * SW, tl.lane, sh_wmu[tl.wave][tl.lane]);
@@ -717,7 +742,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
       dr.store(l, og);
       di.store(l, oi);
       if (SEG ? (starts >> l & 1) && q.d_h0 && tl.active : l == 0 && first) {
-        const int32_t j = SEG ? sequence_of(p.cu, p.n, tl.t + l) : 0;
+        const int32_t j = SEG ? sh_seq[tl.wave][tl.slice * L + l] : 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) q.d_h0[(tl.b * p.n + j) * p.D + dc + v] = mu[v];
       }
@@ -736,7 +761,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
   for (int n = 0; n < SW; ++n) s += sh_h[tl.wave * SW + n][tl.lane];
   sh_wh[tl.wave][tl.lane] = s;
   __syncthreads();
-  if (tl.wave == 0 && dl < p.D) {
+  if (tl.wave == 0 && tl.lane < tl.cols) {
     s = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) s += sh_wh[w][tl.lane];
@@ -845,11 +870,8 @@ static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
   return true;
 }
 
-// V consecutive elements from every row and step of a plane are one aligned access, and V slices of a wave lie within
-// 32-bit byte offsets
-static bool wide(const void* p, const int64_t (&s)[2], size_t es, int V, int64_t B) {
-  return aligned(p, es * V) && (B <= 1 || s[0] % V == 0) && s[1] % V == 0 && s[1] <= kFar / static_cast<int64_t>(es);
-}
+// a wave's steps of a plane lie within 32-bit byte offsets
+static bool near(const int64_t (&s)[2], size_t es) { return s[1] <= kFar / static_cast<int64_t>(es); }
 
 template <class F>
 static void pick(int dtype, bool vec, bool seg, F f) {
@@ -913,8 +935,7 @@ extern "C" pararnn_status pararnn_lm_gated_scan(const pararnn_lm_scan* prob, voi
     return launched();
   }
   prepare(l, ws, a, a.h0, a.h_last, st);
-  const bool vec = a.D % 4 == 0 && wide(a.x, a.sx, es, 4, a.B) && wide(a.r, a.sr, es, 4, a.B) &&
-                   wide(a.i, a.si, es, 4, a.B) && wide(h, a.sh, es, 4, a.B);
+  const bool vec = a.D >= 4 && near(a.sx, es) && near(a.sr, es) && near(a.si, es) && near(a.sh, es);
   const Grid g = grid_of(l, ws, a.B);
   pick(prob->dtype, vec, a.cu != nullptr, [&](auto t, auto v, auto seg) {
     k_scan<decltype(t), decltype(v)::value, decltype(seg)::value><<<static_cast<unsigned>(l.tiles), NTH, 0, st>>>(a, g);
@@ -954,10 +975,8 @@ extern "C" pararnn_status pararnn_lm_gated_scan_vjp(const pararnn_lm_scan* prob,
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.B > 0) prepare(l, ws, a, q.d_last, q.d_h0, st);
   if (l.tiles > 0) {
-    const bool vec = a.D % 4 == 0 && wide(a.x, a.sx, es, 4, a.B) && wide(a.r, a.sr, es, 4, a.B) &&
-                     wide(a.i, a.si, es, 4, a.B) && wide(q.dh, q.sdh, es, 4, a.B) &&
-                     wide(q.dx, q.sdx, es, 4, a.B) && wide(q.dr, q.sdr, es, 4, a.B) &&
-                     wide(q.di, q.sdi, es, 4, a.B);
+    const bool vec = a.D >= 4 && near(a.sx, es) && near(a.sr, es) && near(a.si, es) && near(q.sdh, es) && near(q.sdx, es) &&
+                     near(q.sdr, es) && near(q.sdi, es);
     const Grid g = grid_of(l, ws, a.B);
     pick(prob->dtype, vec, a.cu != nullptr, [&](auto t, auto v, auto seg) {
       k_scan_grad<decltype(t), decltype(v)::value, decltype(seg)::value><<<static_cast<unsigned>(l.tiles), NTH, 0, st>>>(q, g);

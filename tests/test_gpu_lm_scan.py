@@ -306,6 +306,33 @@ def test_broadcast_planes(T):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [0, 4])
+def test_a_channel_is_the_same_in_any_width(n, dtype):
+    # the channels are independent: a problem's first D are those of a wider one, whatever tiles and lanes they fall to
+    T, most = 203, 256
+    cu = cuda_cu([0, 60, 60, 133, T]) if n else None
+
+    def run(D, layout):
+        x, r, i, lam, h0, dh, dl = make(2, T, most, dtype, seed=35, n=n, layout="dense")
+        proj = torch.cat([p[..., :D] for p in (x, r, i)], -1)
+        x, r, i = proj.chunk(3, -1) if layout == "slices" else (p.contiguous() for p in proj.chunk(3, -1))
+        cut = lambda t: t[..., :D].contiguous()  # noqa: E731
+        h0, dl, lam, dh = cut(h0), cut(dl), cut(lam), cut(dh)
+        h, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, cu_seqlens=cu, want_carry=True)
+        g = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl, cu_seqlens=cu)
+        state = h0.clone()
+        lm.gated_scan(x, r, i, lam, h0=state, cu_seqlens=cu, h_last=state)
+        assert torch.equal(state, last)
+        return [h, last, carry, *g.values()]
+
+    want = run(most, "dense")
+    for D in (1, 2, 3, 4, 5, 6, 7, 31, 62, 63, 64, 65, 66, 67, 68, 69, 127, 129, 130, 131, 193, 255):
+        for layout in ("dense", "slices"):
+            for a, b in zip(run(D, layout), want):
+                assert torch.equal(a, b[..., :D]), (D, layout)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("T,cu", [(7, None), (40, None), (108, None), (333, None), (333, [0, 20, 300, 333])])
 def test_planes_broadcast_over_time_or_overlapping(T, cu, dtype):
     # stride 0 over t (the gradient of a mean over time, for instance), steps closer than a row
