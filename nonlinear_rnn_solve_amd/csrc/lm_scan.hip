@@ -144,10 +144,10 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p, uint32_t c
 // Packed sequences: a wave finds its steps' sequences once and keeps them in shared memory (searched for at each boundary
 // by its lane: bf16 B = 4, T = 4096, D = 1000, 9 sequences 108 against 93 us in the gradient, 61 against 51 forward).
 //
-// Bound by memory for float32, by memory and vector instructions about equally for bfloat16 (56% and 54% of the issue
-// slots in the forward and the gradient kernel).  Measured, bf16 (wide: B = 2, T = 4096, D = 4096; long: B = 1, T = 131072,
+// Bound by memory for float32, by memory and vector instructions about equally for bfloat16 (57 to 60% of the issue
+// slots in both kernels).  Measured, bf16 (wide: B = 2, T = 4096, D = 4096; long: B = 1, T = 131072,
 // D = 1024): forward 62 and 260 us (4.2 TB/s), gradient 103 and 440 us (4.3 TB/s); a copy runs at 5.1 TB/s.
-//  - 64 steps a tile (4 waves) against 128 (8 waves): gradient 118 against 151 us (wide), since its 150 registers leave
+//  - 64 steps a tile (4 waves) against 128 (8 waves): gradient 118 against 151 us (wide), since its 154 registers leave
 //    12 waves on a CU in workgroups of 4 and 8 in workgroups of 8; forward 66 against 72.  32 elements a lane: 66 and 124.
 //  - groups against a look-back over the W tiles before: forward 257 against 297 us (long).  Groups of 16: 325.
 //  - stores that do not stay in the caches: float32 B = 8, T = 2048, D = 1000 forward 69 against 81 us; wide 62.6 against 64.0.
