@@ -253,17 +253,73 @@ struct LogpGradArgs {
   int64_t dstride, segments;
 };
 
-// LPR lanes of one row write a segment of kAhead chunks each
 constexpr int kGradThreads = 256;
+
+// f(j, chunk, columns from j on) for each of a lane's chunks of a row, kAhead loads at a time
+template <typename T, int LPR, bool LAST, class F> DEV void each_chunk(const T* z, int64_t columns, int lane, F f) {
+  constexpr int V = 16 / sizeof(T), S = LPR * V;
+  int64_t j = static_cast<int64_t>(lane) * V, left = columns;   // left: from the round's first column
+#pragma unroll 1
+  for (; left >= kAhead * S; left -= kAhead * S, j += kAhead * S) {   // whole chunks: no lane tests for a row's end
+    Vec<T, V> x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) x[u] = load_row<T, V, LAST>(z + j + u * S, V, T{});
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) f(j + u * S, x[u], V);
+  }
+  Vec<T, V> x[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (j + u * S < columns) x[u] = load_row<T, V, LAST>(z + j + u * S, columns - j - u * S, from_f32<T>(-INFINITY));
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (j + u * S < columns) f(j + u * S, x[u], columns - j - u * S);
+}
+
+// ln sum_j e^{z_j - lse} of a row: what the rounding of its lse left out, 0 up to half a unit of lse (up to ln V where lse
+// has no bits left for ln V).  The same value for each of the row's LPR lanes, in a fixed order.
+template <typename T, int LPR>
+DEV float log_rest(const T* z, int64_t columns, float lse, int lane, float (&sh)[LPR > WAVE ? LPR / WAVE : 1]) {
+  constexpr int V = 16 / sizeof(T);
+  float s = 0.0f;
+  each_chunk<T, LPR, false>(z, columns, lane, [&](int64_t, const Vec<T, V>& x, int64_t) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) s += hw_exp2(kLog2e * (x.get(e) - lse));
+  });
+  s = LPR == 16 ? row_sum(s) : wave_sum(s);
+  if constexpr (LPR > WAVE) {
+    if (threadIdx.x % WAVE == 0) sh[threadIdx.x / WAVE] = s;
+    __syncthreads();
+    s = sh[0];
+#pragma unroll
+    for (int w = 1; w < LPR / WAVE; ++w) s += sh[w];
+  }
+  return kLn2 * hw_log2(s);
+}
+
+// LPR lanes of one row write a segment of kAhead chunks each.  p_j = e^{z_j - lse}, where lse is one float32: half a unit of it
+// is a relative error of every p_j, 16 u (u = 2^-24) for |lse| up to kLseExact, as much as the rounding of z - lse costs a
+// token of p = e^-16.  Beyond that the error would grow with an offset that the logits have in common and that the softmax
+// does not see, up to a row of the type's lowest values, whose lse has lost all of ln V.  The normaliser of such a row is
+// summed again about lse, and one workgroup then writes the whole row (which may be the logits' own: nothing is written before
+// all of it has been summed).  For all rows below and all above the bound: float32 4096 x 32000 174 and 235 us, bf16 4096 x 131072
+// 342 and 492, 65536 x 256 14.2 and 18.7, 32 x 50001 4.4 and 13.6.
+constexpr float kLseExact = 32.0f;
 template <typename T, int LPR>
 __global__ __launch_bounds__(kGradThreads) void k_logp_grad(const LogpGradArgs p) {
   constexpr int V = 16 / sizeof(T), RG = kGradThreads / LPR;
+  __shared__ float sh[LPR > WAVE ? LPR / WAVE : 1];
   const int lane = threadIdx.x % LPR;
   const int64_t block = blockIdx.x, rows = block / p.segments, seg = block - rows * p.segments;
-  const int64_t n = rows * RG + threadIdx.x / LPR;
+  const int64_t n = LPR == kGradThreads ? rows : rows * RG + threadIdx.x / LPR;   // scalar where a row has the workgroup
   if (n >= p.N) return;
   const T* z = static_cast<const T*>(p.z) + n * p.stride;
   T* dz = static_cast<T*>(p.dz) + n * p.dstride;
+  const float lse = p.lse[n];
+  const bool again = fabsf(lse) > kLseExact && fabsf(lse) < INFINITY;   // the same for all lanes of the row
+  // the row's one workgroup, another segment's from row to row and from one run of rows to the next: each row's first would be
+  // on one XCD where there are 8 or 16 segments (1258 us in place of 235), and with the row number alone on a few of its CUs (511)
+  if (LPR == kGradThreads && again && seg != (rows + rows / p.segments) % p.segments) return;
   Vec<T, V> x[kAhead];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) {
@@ -271,17 +327,14 @@ __global__ __launch_bounds__(kGradThreads) void k_logp_grad(const LogpGradArgs p
     if (j < p.V) x[u] = load_row<T, V, true>(z + j, p.V - j, T{});
   }
   const int64_t t = p.targets ? target_of(p.targets, p.tbytes, n) : -1;
-  const float lse = p.lse[n], g = t < 0 ? 0.0f : t >= p.V ? NAN : p.g_logp[n];
+  const float g = t < 0 ? 0.0f : t >= p.V ? NAN : p.g_logp[n];
   const float ge = p.g_entropy ? p.g_entropy[n] : 0.0f, h = p.g_entropy ? p.entropy[n] : 0.0f;
   const bool none = lse == -INFINITY;
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
-    const int64_t j = ((seg * kAhead + u) * LPR + lane) * V;
-    if (j >= p.V) break;
+  const auto write = [&](int64_t j, const Vec<T, V>& v, int64_t left, float rest) {
     float o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float l = none ? -INFINITY : x[u].get(e) - lse, q = hw_exp2(kLog2e * l);
+      const float l = none ? -INFINITY : (v.get(e) - lse) - rest, q = hw_exp2(kLog2e * l);
       // below -104 q is 0, and ge l stays finite up to ge = 1e34
       o[e] = -q * fmaf(ge, fmaxf(l, -1e4f) + h, g);
     }
@@ -290,7 +343,18 @@ __global__ __launch_bounds__(kGradThreads) void k_logp_grad(const LogpGradArgs p
 #pragma unroll
       for (int e = 0; e < V; ++e)
         if (e == at) o[e] += g;
-    store_row<T, V>(dz + j, p.V - j, o);
+    store_row<T, V>(dz + j, left, o);
+  };
+  if (again) {
+    const float rest = log_rest<T, LPR>(z, p.V, lse, lane, sh);
+    each_chunk<T, LPR, true>(z, p.V, lane, [&](int64_t j, const Vec<T, V>& v, int64_t left) { write(j, v, left, rest); });
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int64_t j = ((seg * kAhead + u) * LPR + lane) * V;
+    if (j >= p.V) break;
+    write(j, x[u], p.V - j, 0.0f);
   }
 }
 

@@ -118,6 +118,7 @@ def token_logprobs(logits, targets=None, top=0):
 def token_logprobs_vjp(logits, targets, lse, entropy, g_logp, g_entropy=None, out=None):
     """Gradient with respect to logits of sum(g_logp * logp + g_entropy * entropy), from the lse and entropy that
     token_logprobs returned; g_logp, g_entropy float32 in lse's shape (g_entropy may be None).  The top alternatives
-    are reports and have no gradient.  Returns [..., V] in logits' type; out: a tensor for it, logits itself allowed.
+    are reports and have no gradient.  An offset that a row's logits have in common costs no accuracy, but time (rows with
+    |lse| > 32 are read twice).  Returns [..., V] in logits' type; out: a tensor for it, logits itself allowed.
     """
     return (_binding or load_library()).token_logprobs_vjp(logits, targets, lse, entropy, g_logp, g_entropy, out)

@@ -304,3 +304,87 @@ def test_refusals():
                 lambda: lm.token_logprobs_vjp(z, t, r.lse, r.entropy, g, out=z.bfloat16())):
         with pytest.raises(ValueError):
             bad()
+
+
+# The gradient's error must not grow with a common offset of a row's logits: the softmax has none.  z - lse and what the
+# gradient adds to it are rounded to u |ln p| each, the exponential's argument as well: 3 u |ln p|, and 48 u for the normaliser's
+# own roundings (half a unit of an lse of up to 32: 16 u; its logarithm of up to ln V: 12 u; a few for the exponential).
+def gradient_close(d, z, t, g, ge):
+    V = z.shape[1]
+    base = (V / 64 + 16) * U32
+    l = f64(z) - f64(z).amax(-1, keepdim=True)
+    l = l - torch.logsumexp(l, -1, keepdim=True)
+    p, fl = torch.exp(l), torch.where(torch.isinf(l), torch.zeros_like(l), l)
+    ent = -(p * fl).sum(-1)
+    gg, hh, at = f64(g) * (t.cpu() >= 0), f64(ge), t.cpu().long().clamp(min=0)
+    want = -gg[:, None] * p - hh[:, None] * p * (fl + ent[:, None])
+    want[torch.arange(len(gg)), at] += gg
+    rel = base + U32 * (3 * fl.abs() + 48)
+    size = gg.abs()[:, None] + hh.abs()[:, None] * (fl.abs() + ent[:, None] + 1)
+    tol = (rel * p + 2.0 ** -126) * size + 2 * base * (1 + math.log(V)) * p * hh.abs()[:, None] + U32 * want.abs()
+    tol += U32 * 2 * (gg.abs()[:, None] * (want != 0))
+    close(d, want, rounded(want, tol, z.dtype), "d_logits")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [5, 64, 200, 900, 3000, 9000, 40000])
+def test_gradient_of_rows_with_a_common_offset(V, dtype):
+    # rows of one tensor with different offsets, all of them exact in the storage type
+    gen = torch.Generator().manual_seed(V)
+    offsets = [0.0, 64.0, -64.0, 128.0, 0.0, -256.0, 31.0, -40.0] if dtype == BF else \
+        [0.0, 2.0 ** 10, -2.0 ** 10, 2.0 ** 15, 0.0, -2.0 ** 15, 31.0, -40.0]
+    rows = []
+    for o in offsets:
+        step = 2.0 ** (math.ceil(math.log2(max(abs(o), 32.0))) - 7) if dtype == BF else 2.0 ** -6
+        k = torch.randint(0, 32 if dtype == BF else 1024, (V,), generator=gen)
+        rows.append((o + (step * k if o >= 0 else -step * k)).to(dtype))
+        assert torch.equal(rows[-1].double(), o + (step if o >= 0 else -step) * k.double())
+    z = torch.stack(rows + [torch.zeros(V, dtype=dtype)]).cuda()
+    N = len(rows) + 1
+    t = torch.randint(0, V, (N,), generator=gen).cuda()
+    t[4] = -1
+    g, ge = torch.randn(N, generator=gen).cuda(), torch.randn(N, generator=gen).cuda()
+    res = lm.token_logprobs(z, t)
+    # the forward takes differences from the row's largest logit, which are exact here: the same bits without the offset
+    base = lm.token_logprobs((z.float() - z.float().amax(1, keepdim=True)).to(dtype), t)
+    assert torch.equal(res.entropy, base.entropy) and torch.equal(res.logp, base.logp)
+    d = lm.token_logprobs_vjp(z, t, res.lse, res.entropy, g, ge)
+    gradient_close(d, z, t, g, ge)
+    wide = torch.zeros(N, V + 3, dtype=dtype, device="cuda")     # rows off their alignment, in place
+    wide[:, 1:V + 1] = z
+    view = wide[:, 1:V + 1]
+    assert torch.equal(lm.token_logprobs_vjp(view, t, res.lse, res.entropy, g, ge, out=view), d)
+    assert (wide[:, 0] == 0).all() and (wide[:, V + 1:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [5, 700, 9000, 70000])
+def test_gradient_of_a_row_of_lowest_values(V, dtype):
+    # a mask of the lowest value all over leaves a uniform distribution, whose entropy has no gradient
+    z, t, g, ge = make(3, V, dtype, seed=V)
+    z[1] = torch.finfo(dtype).min
+    t[:] = torch.tensor([1, 2, -1])
+    res = lm.token_logprobs(z, t)
+    d = lm.token_logprobs_vjp(z, t, res.lse, res.entropy, g, ge)
+    gradient_close(d, z, t, g, ge)
+    one = torch.zeros(V, dtype=torch.float64)
+    one[2] = 1
+    want = f64(g)[1] * (one - 1 / V)
+    tol = 2 * (V / 64 + 64) * U32 * (abs(float(g[1])) + abs(float(ge[1])) * (1 + math.log(V))) / V + 4 * U32 * one * abs(float(g[1]))
+    close(d[1], want, rounded(want, tol, dtype), "uniform")
+
+
+@pytest.mark.parametrize("V", [300, 5000, 40000])
+def test_gradient_with_ruled_out_tokens_and_an_offset(V):
+    z, t, g, ge = make(6, V, F32, seed=V, banned=0.4)
+    z = torch.where(torch.isinf(z), z, torch.round(z * 64) / 64 + 4096.0)
+    z[2], z[3, 1:], t[2] = -INF, -INF, 1
+    res = lm.token_logprobs(z, t)
+    d = lm.token_logprobs_vjp(z, t, res.lse, res.entropy, g, ge)
+    assert (d[2] == 0).all()
+    keep = [0, 1, 3, 4, 5]
+    gradient_close(d[keep], z[keep], t[keep], g[keep], ge[keep])
+    z[4, 1] = float("nan")
+    res = lm.token_logprobs(z, t)
+    d2 = lm.token_logprobs_vjp(z, t, res.lse, res.entropy, g, ge)
+    assert torch.isnan(d2[4]).any() and torch.equal(d2[[0, 1, 2, 3, 5]], d[[0, 1, 2, 3, 5]])
