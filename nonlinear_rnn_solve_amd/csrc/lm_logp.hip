@@ -5,6 +5,7 @@
 // by memory in float32 (4096 x 32000: 93 us, 5.6 TB/s), by one CU's instructions for few rows (32 x 50001 with 20
 // alternatives: 11 us).  The gradient is bound by memory (4096 x 32000 float32: 168 us for 1.05 GB, 6.2 TB/s).
 
+#include <algorithm>
 #include <type_traits>
 
 #include "lm_common.h"
@@ -427,11 +428,17 @@ extern "C" pararnn_status pararnn_lm_token_logprobs_vjp(int dtype, int64_t N, in
   const auto run = [&](auto t, auto lanes) {
     using T = decltype(t);
     constexpr int LPR = decltype(lanes)::value;
+    constexpr int RG = kGradThreads / LPR;
     const int64_t segments = ceil_div(V, LPR * kAhead * 16 / static_cast<int64_t>(sizeof(T)));
-    const int64_t blocks = ceil_div(N, kGradThreads / LPR) * segments;
-    if (!grid_ok(blocks, kGradThreads)) return PARARNN_ERR_UNSUPPORTED;
-    const LogpGradArgs a{logits, stride, N, V, targets, target_bytes, lse, entropy, g_logp, g_entropy, d_logits, d_stride, segments};
-    k_logp_grad<T, LPR><<<static_cast<unsigned>(blocks), kGradThreads, 0, st>>>(a);
+    const int64_t most = INT64_C(0xffffffff) / kGradThreads / segments * RG;   // rows of a launch; V < 2^31: at least 32
+    for (int64_t n = 0; n < N; n += most) {
+      const int64_t rows = std::min(N - n, most);
+      const LogpGradArgs a{static_cast<const T*>(logits) + n * stride, stride, rows, V,
+                           targets ? static_cast<const char*>(targets) + n * target_bytes : nullptr, target_bytes, lse + n,
+                           entropy ? entropy + n : nullptr, g_logp ? g_logp + n : nullptr, g_entropy ? g_entropy + n : nullptr,
+                           static_cast<T*>(d_logits) + n * d_stride, d_stride, segments};
+      k_logp_grad<T, LPR><<<static_cast<unsigned>(ceil_div(rows, RG) * segments), kGradThreads, 0, st>>>(a);
+    }
     return launched();
   };
   const auto sized = [&](auto t) {

@@ -388,3 +388,24 @@ def test_gradient_with_ruled_out_tokens_and_an_offset(V):
     res = lm.token_logprobs(z, t)
     d2 = lm.token_logprobs_vjp(z, t, res.lse, res.entropy, g, ge)
     assert torch.isnan(d2[4]).any() and torch.equal(d2[[0, 1, 2, 3, 5]], d[[0, 1, 2, 3, 5]])
+
+
+@pytest.mark.parametrize("N,V", [((1 << 24) + 16, 2049), ((1 << 23) + 16, 8193)])
+def test_gradient_of_more_rows_than_a_launch_has_workgroups(N, V):
+    # as many rows as the forward takes, in more pieces than the 2^24 - 1 workgroups of 256 threads that a launch can have
+    P = 16
+    need = N * V * 2 + (4 << 30)
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip("%d GB of GPU memory needed" % (need >> 30))
+    z, t, g, ge = make(P, V, BF, seed=V)
+    z[3] = (z[3].float() * 4).round() * 0.25 + 64      # a row with an offset
+    want = lm.token_logprobs(z, t)
+    dwant = lm.token_logprobs_vjp(z, t, want.lse, want.entropy, g, ge)
+    many = lambda a: a.repeat(N // P, *[1] * (a.dim() - 1))  # noqa: E731
+    big = torch.empty(N, V, dtype=BF, device="cuda")
+    big.view(N // P, P, V).copy_(z)
+    out = lm.token_logprobs_vjp(big, many(t), many(want.lse), many(want.entropy), many(g), many(ge), out=big).view(N // P, P, V)
+    for part in out.split(1 << 13):
+        assert (part == dwant).all()
+    del big, out, part
+    torch.cuda.empty_cache()
