@@ -602,7 +602,20 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
 // The gradients: the same tiles from the last chunk to the first.  A lane holds its steps' gates; the state entering
 // the tile (carry) gives h_{t-1} by the forward walk, and the adjoint mu_t = a_t l_t, l_t = dh_t + mu_{t+1}, is the same
 // kind of scan (map mu -> a (dh + mu)) run backwards, whose maps share the products of a with the forward one.
+//
+// The gradients of the gates need both s = sig(v) and 1 - s, each with its own relative accuracy: of an open gate (v > 0) 1 - s
+// from s has lost it (1% off at v = 12, zero from 18 on).  e^-v s has it, and then 1 - (1 - s) gives s.  A lane keeps the smaller
+// of the two, its sign bit set where it is 1 - s: as many registers as s alone.
 // ------------------------------------------------------------------------------------------------
+struct Pair { float s, rest; };   // sig(v), 1 - sig(v)
+DEV float smaller(float v, float s) {
+  const float e = hw_exp2(-kLog2e * v);
+  return e < 1.0f ? -(e * s) : s;
+}
+DEV Pair both(float x) {
+  const float y = fabsf(x), z = 1.0f - y;
+  return __float_as_uint(x) >> 31 ? Pair{z, y} : Pair{y, z};
+}
 template <typename T, int V, bool SEG>
 __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k_scan_grad(const GradArgs q, const Grid g) {
   constexpr int L = Shape<V>::L, Q = Shape<V>::Q;
@@ -613,7 +626,7 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
   __shared__ float sh_h[NSEG][TW], sh_mu[NSEG][TW], sh_wh[NW][TW], sh_wmu[NW][TW];
   const Tile<V> tl(g, p, sh_ticket, true);
 
-  // kept of each element: a, m, the input m u, sig(r), sig(i); dh in its storage type
+  // kept of each element: a, m, the input m u, sig(r) and sig(i) or their complements; dh in its storage type
   Vec<T, V> dh[L];
   float a[L][V], in[L][V], m[L][V], sr[L][V], si[L][V], k[V];
   uint32_t starts = 0, ends = 0;
@@ -631,8 +644,8 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
         for (int v = 0; v < V; ++v) {
           const Gate t = gate<decltype(far)::value>(r[l].get(v), i[l].get(v), k[v]);
           a[l][v] = t.a;
-          sr[l][v] = t.sr;
-          si[l][v] = t.si;
+          sr[l][v] = smaller(r[l].get(v), t.sr);
+          si[l][v] = smaller(i[l].get(v), t.si);
           m[l][v] = root(t.w);
           in[l][v] = m[l][v] * (t.si * x[l].get(v));
         }
@@ -732,11 +745,12 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(3))) void k
         if (SEG && ends >> l & 1) mu[v] = at(q.d_last, l, v);
         const float lam = dh[l].get(v) + mu[v];
         mu[v] = a[l][v] * lam;
-        const float e = mu[v] * hq[l][v] * sr[l][v];
+        const Pair gr = both(sr[l][v]), gi = both(si[l][v]);
+        const float e = mu[v] * hq[l][v] * gr.s;
         sum[l / SL][v] += e;
-        og[v] = e * k[v] * (1.0f - sr[l][v]);
-        oi[v] = lam * in[l][v] * (1.0f - si[l][v]);
-        ox[v] = lam * m[l][v] * si[l][v];
+        og[v] = e * k[v] * gr.rest;
+        oi[v] = lam * in[l][v] * gi.rest;
+        ox[v] = lam * m[l][v] * gi.s;
       }
       dx.store(l, ox);
       dr.store(l, og);

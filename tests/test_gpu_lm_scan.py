@@ -493,3 +493,67 @@ def test_refusals():
         assert e.value.status == -1
     with pytest.raises(ValueError, match="carry"):
         lm.gated_scan_vjp(x, r, i, lam, None, dh)
+
+
+def parts_of_the_adjoint(x, r, i, lam, h0, dh, dl, c=8.0, cu=None):
+    """What the gradients are products of, in 64 bits, with 1 - sig(v) as sig(-v)."""
+    x, r, i, lam, dh = (f64(t) for t in (x, r, i, lam, dh))
+    B, T, D = x.shape
+    rate = c * torch.nn.functional.softplus(lam, threshold=700.0)
+    z = -rate * torch.sigmoid(r)
+    a, m, u = torch.exp(z), torch.sqrt(-torch.expm1(2 * z)), torch.sigmoid(i) * x
+    h0 = torch.zeros(B, len(cu) - 1 if cu else 1, D, dtype=torch.float64) if h0 is None else f64(h0).reshape(B, -1, D)
+    dl = torch.zeros_like(h0) if dl is None else f64(dl).reshape(B, -1, D)
+    before, l = torch.empty_like(x), torch.empty_like(x)
+    for j, (t0, t1) in enumerate(plain.sequences(cu, T)):
+        h, mu = h0[:, j], dl[:, j]
+        for t in range(t0, t1):
+            before[:, t] = h
+            h = a[:, t] * h + m[:, t] * u[:, t]
+        for t in range(t1 - 1, t0 - 1, -1):
+            l[:, t] = dh[:, t] + mu
+            mu = a[:, t] * l[:, t]
+    return dict(rate=rate, z=z, a=a, m=m, u=u, l=l, before=before, sr=torch.sigmoid(r), cr=torch.sigmoid(-r), si=torch.sigmoid(i),
+                ci=torch.sigmoid(-i))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,D", [(1, 64), (1, 3), (90, 70), (90, 2)])
+def test_gradients_of_open_and_closed_gates(T, D, dtype):
+    # sequences of one step without a state: every gradient is a product, and each element of it has its relative accuracy.
+    # Roundings, in u: the sigmoids' exponentials |v| <= 30 and 4, rates and roots 40, products 16 (90 in all)
+    g = torch.Generator().manual_seed(T + D)
+    r, i = ((torch.rand(1, T, D, generator=g) * 60 - 30).to(dtype).cuda() for _ in range(2))
+    r[0, 0, :3], i[0, 0, :3] = torch.tensor([10.0, 18.0, 30.0])[:D], torch.tensor([16.0, 12.0, 30.0])[:D]
+    x, dh = (torch.randn(1, T, D, generator=g).to(dtype).cuda() for _ in range(2))
+    lam = make(1, 1, D, F32, seed=1)[3]
+    cu = list(range(T + 1)) if T > 1 else None
+    carry = lm.gated_scan(x, r, i, lam, cu_seqlens=cuda_cu(cu), want_carry=True)[2]
+    got = lm.gated_scan_vjp(x, r, i, lam, carry, dh, cu_seqlens=cuda_cu(cu))
+    p = parts_of_the_adjoint(x, r, i, lam, None, dh, None, cu=cu)
+    e = -p["l"] * p["u"] * p["a"] ** 2 / p["m"]
+    for k, want in (("d_x", p["l"] * p["m"] * p["si"]), ("d_i", p["l"] * p["m"] * p["u"] * p["ci"]),
+                    ("d_r", -e * p["rate"] * p["sr"] * p["cr"])):
+        close(got[k], want, rounded(want, 96 * U32 * want.abs(), dtype), k)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [-30.0, -9.0, 0.0, 20.0])
+def test_small_gradients_have_their_own_scale(value, dtype):
+    # the adjoint is as exact as in the tests above, 2 unit of its largest value (h and l), and each factor of a gradient as
+    # exact as its roundings: 32 u and 4 u |log a|; an a below the smallest normal float32, 2^-126, may be 0
+    x, r, i, _, h0, dh, dl = make(1, 200, 8, dtype, seed=10)
+    lam = torch.full((8,), value, device="cuda")
+    unit = reference(x, r, i, lam, h0, dh, dl)[1]
+    carry = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)[2]
+    got = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl)
+    p = parts_of_the_adjoint(x, r, i, lam, h0, dh, dl)
+    L, H = float(p["l"].abs().max()), max(1.0, float(p["before"].abs().max()))
+    rel = 2 * unit + 32 * U32 + 4 * U32 * p["z"].abs()
+    jump = p["u"] * p["a"] ** 2 / p["m"]
+    gate = p["rate"] * p["sr"] * p["cr"]
+    for k, want, size in (("d_x", p["l"] * p["m"] * p["si"], L * p["m"] * p["si"]),
+                          ("d_i", p["l"] * p["m"] * p["u"] * p["ci"], L * p["m"] * (p["u"] * p["ci"]).abs()),
+                          ("d_r", -p["l"] * (p["a"] * p["before"] - jump) * gate, L * (p["a"] * H + jump.abs()) * gate)):
+        assert float(want.abs().max()) > 0
+        close(got[k], want, rounded(want, rel * size + 2.0 ** -126 * (1 + (L * H * gate if k == "d_r" else 0)), dtype), k)
