@@ -53,16 +53,30 @@ void plane(const Tensor& t, const char* name, const Tensor& like) {
   if (t.size(-1) > 1 && t.stride(-1) != 1) refuse(std::string(name) + " must be dense in its last dimension");
 }
 
-// the address of an optional contiguous tensor of n values
-template <typename P> P* dense(const Maybe& t, const char* name, at::ScalarType type, int64_t n, c10::Device device) {
+// Whether a contiguous tensor of sizes `got` holds the values of one of sizes `want` in the same order: dimensions of one entry
+// aside the sizes are equal, or it is flat.  (As many values are not enough: a transposed array would be read as another's rows.)
+bool same_order(at::IntArrayRef got, at::IntArrayRef want) {
+  if (got.size() == 1) return got[0] == c10::multiply_integers(want);
+  size_t a = 0, b = 0;
+  while (true) {
+    while (a < got.size() && got[a] == 1) ++a;
+    while (b < want.size() && want[b] == 1) ++b;
+    if (a == got.size() || b == want.size()) return a == got.size() && b == want.size();
+    if (got[a++] != want[b++]) return false;
+  }
+}
+
+// the address of an optional contiguous tensor of `sizes`
+template <typename P>
+P* dense(const Maybe& t, const char* name, at::ScalarType type, at::IntArrayRef sizes, c10::Device device) {
   if (!t) return nullptr;
   on_device(*t, name, type, device);
-  if (t->numel() != n || !t->is_contiguous())
-    refuse(std::string(name) + " must be contiguous and hold " + std::to_string(n) + " values, got " + text(t->sizes()));
+  if (!t->is_contiguous() || !same_order(t->sizes(), sizes))
+    refuse(std::string(name) + " must be " + text(sizes) + " and contiguous, got " + text(t->sizes()));
   return static_cast<P*>(t->data_ptr());
 }
-float* floats(const Maybe& t, const char* name, int64_t n, c10::Device device) {
-  return dense<float>(t, name, at::kFloat, n, device);
+float* floats(const Maybe& t, const char* name, at::IntArrayRef sizes, c10::Device device) {
+  return dense<float>(t, name, at::kFloat, sizes, device);
 }
 
 // [..., D] as rows of D: their number and stride, without a copy
@@ -127,7 +141,7 @@ void check(pararnn_status status, const char* entry) {
 // ---------------------------------------------------------------- gated linear recurrence
 struct Scan {
   pararnn_lm_scan p{};
-  int64_t n = 1, states = 0;      // sequences of a row; values of a state array
+  int64_t n = 1;                  // sequences of a row
   std::vector<int64_t> shape;     // of a state array
   Scan(const Tensor& x, const Tensor& r, const Tensor& i, const Tensor& lam, const Maybe& h0, double c, const Maybe& cu) {
     p.dtype = storage(x, "x");
@@ -140,13 +154,12 @@ struct Scan {
     if (cu) {
       if (cu->dim() != 1 || cu->numel() < 2) refuse("cu_seqlens must be a 1-D tensor of n_seqs + 1 offsets");
       n = cu->numel() - 1;
-      p.cu_seqlens = dense<int32_t>(cu, "cu_seqlens", at::kInt, n + 1, dev);
+      p.cu_seqlens = dense<int32_t>(cu, "cu_seqlens", at::kInt, {n + 1}, dev);
       p.n_seqs = n;
       shape = {p.B, n, p.D};
     } else {
       shape = {p.B, p.D};
     }
-    states = p.B * n * p.D;
     if (h0) {
       const auto s = h0->sizes();
       if (s != at::IntArrayRef(shape) && !(!cu && s == at::IntArrayRef({p.B, 1, p.D})))
@@ -155,8 +168,8 @@ struct Scan {
     }
     p.x = x.data_ptr(), p.r = r.data_ptr(), p.i = i.data_ptr();
     for (int k = 0; k < 2; ++k) p.sx[k] = x.stride(k), p.sr[k] = r.stride(k), p.si[k] = i.stride(k);
-    p.lam = floats(lam, "lam", p.D, dev);
-    p.h0 = floats(h0, "h0", states, dev);
+    p.lam = floats(lam, "lam", {p.D}, dev);
+    p.h0 = floats(h0, "h0", shape, dev);
     p.c = static_cast<float>(c);
   }
 };
@@ -168,7 +181,7 @@ std::tuple<Tensor, Tensor, Maybe> gated_scan(const Tensor& x, const Tensor& r, c
   const Call call(x.device());
   const Tensor h = output(out, "out", x);
   const Tensor last = h_last ? *h_last : new_floats(s.shape, x);
-  float* pl = floats(last, "h_last", s.states, x.device());
+  float* pl = floats(last, "h_last", s.shape, x.device());
   Maybe carry;
   if (want_carry) carry = new_floats({s.p.B, pararnn_lm_scan_chunks(s.p.T), s.p.D}, x);
   const int64_t sh[2] = {h.stride(0), h.stride(1)};
@@ -190,9 +203,9 @@ py::dict gated_scan_vjp(const Tensor& x, const Tensor& r, const Tensor& i, const
   Tensor d[3];
   for (int k = 0; k < 3; ++k) d[k] = output(out ? Maybe((*out)[k]) : Maybe(), "out", x);
   pararnn_lm_scan_grad g{};
-  g.carry = floats(carry, "carry", s.p.B * pararnn_lm_scan_chunks(s.p.T) * s.p.D, x.device());
+  g.carry = floats(carry, "carry", {s.p.B, pararnn_lm_scan_chunks(s.p.T), s.p.D}, x.device());
   g.dh = dh.data_ptr();
-  g.d_last = floats(d_last, "d_last", s.states, x.device());
+  g.d_last = floats(d_last, "d_last", s.shape, x.device());
   g.d_x = d[0].data_ptr(), g.d_r = d[1].data_ptr(), g.d_i = d[2].data_ptr();
   for (int k = 0; k < 2; ++k)
     g.sdh[k] = dh.stride(k), g.sdx[k] = d[0].stride(k), g.sdr[k] = d[1].stride(k), g.sdi[k] = d[2].stride(k);
@@ -237,7 +250,7 @@ std::tuple<Tensor, Tensor, Maybe> layer_norm(const Tensor& x, const Tensor& weig
   Maybe stats;
   if (want_stats) stats = new_floats({N, 2}, x);
   check(pararnn_lm_layer_norm(dt, N, D, x.data_ptr(), xs, residual ? residual->data_ptr() : nullptr, rs,
-                              floats(weight, "weight", D, dev), floats(bias, "bias", D, dev), static_cast<float>(eps),
+                              floats(weight, "weight", {D}, dev), floats(bias, "bias", {D}, dev), static_cast<float>(eps),
                               y.data_ptr(), rows(y, "out").second, residual ? s.data_ptr() : nullptr, ss,
                               stats ? static_cast<float*>(stats->data_ptr()) : nullptr, call.stream),
         "pararnn_lm_layer_norm");
@@ -254,6 +267,8 @@ py::dict layer_norm_vjp(const Tensor& dy, const Tensor& s, const Tensor& weight,
   const int64_t D = s.size(-1);
   const auto [N, ss] = rows(s, "s");
   if (!stats) refuse("stats are missing: call layer_norm with want_stats=True");
+  std::vector<int64_t> pairs{N, 2};   // or with s's leading dimensions
+  if (stats->dim() > 2) pairs.assign(s.sizes().begin(), s.sizes().end()), pairs.back() = 2;
   int64_t ps = 0;
   if (d_sum) {
     plane(*d_sum, "d_sum", s);
@@ -270,7 +285,7 @@ py::dict layer_norm_vjp(const Tensor& dy, const Tensor& s, const Tensor& weight,
   }
   const Tensor ws = call.workspace(pararnn_lm_layer_norm_vjp_workspace_bytes(N, D));
   check(pararnn_lm_layer_norm_vjp(dt, N, D, dy.data_ptr(), rows(dy, "dy").second, s.data_ptr(), ss,
-                                  floats(weight, "weight", D, dev), floats(stats, "stats", 2 * N, dev),
+                                  floats(weight, "weight", {D}, dev), floats(stats, "stats", pairs, dev),
                                   d_sum ? d_sum->data_ptr() : nullptr, ps, dx.data_ptr(), rows(dx, "out").second, pw, pb,
                                   ws.data_ptr(), static_cast<size_t>(ws.numel()), call.stream),
         "pararnn_lm_layer_norm_vjp");
@@ -285,7 +300,7 @@ std::pair<const void*, int> targets_of(const Maybe& t, const Tensor& logits) {
     refuse(std::string("targets must be int64 or int32, got ") + c10::toString(t->scalar_type()));
   if (t->sizes() != logits.sizes().slice(0, logits.dim() - 1))
     refuse("targets must be " + text(logits.sizes().slice(0, logits.dim() - 1)) + ", got " + text(t->sizes()));
-  return {dense<void>(t, "targets", t->scalar_type(), t->numel(), logits.device()), t->scalar_type() == at::kLong ? 8 : 4};
+  return {dense<void>(t, "targets", t->scalar_type(), t->sizes(), logits.device()), t->scalar_type() == at::kLong ? 8 : 4};
 }
 
 std::tuple<Maybe, Tensor, Tensor, Maybe, Maybe> token_logprobs(const Tensor& logits, const Maybe& targets, int64_t top) {
@@ -326,13 +341,14 @@ Tensor token_logprobs_vjp(const Tensor& logits, const Maybe& targets, const Tens
   const Call call(dev);
   const int64_t V = logits.size(-1);
   const auto [N, stride] = rows(logits, "logits");
+  const auto lead = logits.sizes().slice(0, logits.dim() - 1);
   const auto [tp, tb] = targets_of(targets, logits);
   if (tb && !g_logp) refuse("g_logp is missing");
   if (g_entropy && !entropy) refuse("entropy is missing");
   const Tensor dz = output(out, "out", logits);
-  check(pararnn_lm_token_logprobs_vjp(dt, N, V, logits.data_ptr(), stride, tp, tb, floats(lse, "lse", N, dev),
-                                      floats(entropy, "entropy", N, dev), tb ? floats(g_logp, "g_logp", N, dev) : nullptr,
-                                      floats(g_entropy, "g_entropy", N, dev), dz.data_ptr(), rows(dz, "out").second,
+  check(pararnn_lm_token_logprobs_vjp(dt, N, V, logits.data_ptr(), stride, tp, tb, floats(lse, "lse", lead, dev),
+                                      floats(entropy, "entropy", lead, dev), tb ? floats(g_logp, "g_logp", lead, dev) : nullptr,
+                                      floats(g_entropy, "g_entropy", lead, dev), dz.data_ptr(), rows(dz, "out").second,
                                       call.stream),
         "pararnn_lm_token_logprobs_vjp");
   return dz;

@@ -409,3 +409,19 @@ def test_gradient_of_more_rows_than_a_launch_has_workgroups(N, V):
         assert (part == dwant).all()
     del big, out, part
     torch.cuda.empty_cache()
+
+
+def test_arguments_of_another_shape_are_refused():
+    # as many values in another order would be numbers of other rows
+    z = torch.randn(3, 5, 40, device="cuda")
+    t = torch.zeros(3, 5, dtype=torch.int64, device="cuda")
+    r = lm.token_logprobs(z, t)
+    g = torch.randn(3, 5, device="cuda")
+    want = lm.token_logprobs_vjp(z, t, r.lse, r.entropy, g, g)
+    turned = g.t().contiguous()
+    for bad in (lambda: lm.token_logprobs_vjp(z, t, r.lse, r.entropy, turned), lambda: lm.token_logprobs_vjp(z, t, turned, r.entropy, g),
+                lambda: lm.token_logprobs_vjp(z, t, r.lse, turned, g, g), lambda: lm.token_logprobs_vjp(z, t, r.lse, r.entropy, g, turned)):
+        with pytest.raises(ValueError, match="must be"):
+            bad()
+    for same in (lambda a: a[..., None], lambda a: a[None], lambda a: a.flatten()):     # the same order of the same values
+        assert torch.equal(lm.token_logprobs_vjp(z, t, same(r.lse), same(r.entropy), same(g), same(g)), want)

@@ -221,3 +221,17 @@ def test_refusals():
     with pytest.raises(lm.PararnnError) as e:
         lm.layer_norm(x, w, eps=-1.0)
     assert e.value.status == -1
+
+
+def test_arguments_of_another_shape_are_refused():
+    x, res, w, b, dy, ds = make(5, 32, F32, seed=9)
+    y, s, stats = lm.layer_norm(x, w, b, residual=res, want_stats=True)
+    with pytest.raises(ValueError, match="must be"):
+        lm.layer_norm_vjp(dy, s, w, stats.t().contiguous())
+    with pytest.raises(ValueError, match="must be"):
+        lm.layer_norm(x, w.view(4, 8), b)
+    assert torch.equal(lm.layer_norm(x, w[None], b[None], residual=res)[0], y)     # the same order of the same values
+    want = lm.layer_norm_vjp(dy, s, w, stats)["d_x"]
+    assert torch.equal(lm.layer_norm_vjp(dy, s, w, stats.flatten())["d_x"], want)
+    got = lm.layer_norm_vjp(dy.view(5, 1, 32), s.view(5, 1, 32), w, stats.view(5, 1, 2))["d_x"]
+    assert torch.equal(got.view(5, 32), want)

@@ -557,3 +557,25 @@ def test_small_gradients_have_their_own_scale(value, dtype):
                           ("d_r", -p["l"] * (p["a"] * p["before"] - jump) * gate, L * (p["a"] * H + jump.abs()) * gate)):
         assert float(want.abs().max()) > 0
         close(got[k], want, rounded(want, rel * size + 2.0 ** -126 * (1 + (L * H * gate if k == "d_r" else 0)), dtype), k)
+
+
+def test_arguments_of_another_shape_are_refused():
+    # as many values in another order would be states of other rows
+    x, r, i, lam, h0, dh, dl = make(3, 70, 5, F32, seed=40, layout="dense")
+    h, last, carry = lm.gated_scan(x, r, i, lam, h0=h0, want_carry=True)
+    want = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=dl)
+    turn = lambda t: t.transpose(0, -1).contiguous()  # noqa: E731
+    for bad in (lambda: lm.gated_scan(x, r, i, lam, h0=h0, h_last=turn(h0)), lambda: lm.gated_scan_vjp(x, r, i, lam, turn(carry), dh, h0=h0, d_last=dl),
+                lambda: lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=turn(dl))):
+        with pytest.raises(ValueError, match="must be"):
+            bad()
+    cu = cuda_cu([0, 30, 70])
+    hp = torch.randn(3, 2, 5, device="cuda")
+    hc = lm.gated_scan(x, r, i, lam, h0=hp, cu_seqlens=cu, want_carry=True)[2]
+    with pytest.raises(ValueError, match="must be"):
+        lm.gated_scan_vjp(x, r, i, lam, hc, dh, h0=hp, d_last=hp.transpose(0, 1).contiguous(), cu_seqlens=cu)
+    for same in (lambda t: t[:, None], lambda t: t.flatten()):     # the same order of the same values
+        got = lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=same(dl))
+        assert all(torch.equal(got[k], want[k]) for k in want)
+    state = h0[:, None].clone()
+    assert torch.equal(lm.gated_scan(x, r, i, lam, h0=h0, h_last=state)[1][:, 0], last)
