@@ -54,20 +54,18 @@ class LayerNorm(torch.autograd.Function):
 
 
 class TokenLogprobs(torch.autograd.Function):
-    """(logp, entropy) of lm.token_logprobs; the gradient overwrites the logits, which nothing else needs."""
+    """(logp, entropy) of lm.token_logprobs; the gradient overwrites the logits (a second backward pass raises)."""
 
     @staticmethod
     def forward(ctx, logits, targets):
         t = lm.token_logprobs(logits, targets)
-        ctx.save_for_backward(targets, t.lse, t.entropy)
-        ctx.logits = logits
+        ctx.save_for_backward(logits, targets, t.lse, t.entropy)
         return t.logp, t.entropy
 
     @staticmethod
     def backward(ctx, g, ge):
-        targets, lse, entropy = ctx.saved_tensors
-        return lm.token_logprobs_vjp(ctx.logits, targets, lse, entropy, g.contiguous(), ge.contiguous(),
-                                     out=ctx.logits.detach()), None
+        logits, targets, lse, entropy = ctx.saved_tensors
+        return lm.token_logprobs_vjp(logits, targets, lse, entropy, g.contiguous(), ge.contiguous(), out=logits.detach()), None
 
 
 class GatedLM(torch.nn.Module):

@@ -95,6 +95,12 @@ std::pair<int64_t, int64_t> rows(const Tensor& t, const char* name) {
   return {n, stride};
 }
 
+// A caller's tensor has been written: autograd refuses to use what it has saved of it (tensors made in inference mode are
+// not counted).
+void written(const Maybe& t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 Tensor output(const Maybe& given, const char* name, const Tensor& like) {
   if (!given) return at::empty(like.sizes(), like.options());
   plane(*given, name, like);
@@ -189,6 +195,8 @@ std::tuple<Tensor, Tensor, Maybe> gated_scan(const Tensor& x, const Tensor& r, c
   check(pararnn_lm_gated_scan(&s.p, h.data_ptr(), sh, pl, carry ? static_cast<float*>(carry->data_ptr()) : nullptr,
                               ws.data_ptr(), static_cast<size_t>(ws.numel()), call.stream),
         "pararnn_lm_gated_scan");
+  written(out);
+  written(h_last);
   return {h, last, carry};
 }
 
@@ -224,6 +232,8 @@ py::dict gated_scan_vjp(const Tensor& x, const Tensor& r, const Tensor& i, const
   const Tensor ws = call.workspace(pararnn_lm_scan_workspace_bytes(s.p.B, s.p.T, s.p.D));
   check(pararnn_lm_gated_scan_vjp(&s.p, &g, ws.data_ptr(), static_cast<size_t>(ws.numel()), call.stream),
         "pararnn_lm_gated_scan_vjp");
+  if (out)
+    for (const Tensor& t : *out) written(t);
   return res;
 }
 
@@ -254,6 +264,8 @@ std::tuple<Tensor, Tensor, Maybe> layer_norm(const Tensor& x, const Tensor& weig
                               y.data_ptr(), rows(y, "out").second, residual ? s.data_ptr() : nullptr, ss,
                               stats ? static_cast<float*>(stats->data_ptr()) : nullptr, call.stream),
         "pararnn_lm_layer_norm");
+  written(out);
+  written(sum_out);
   return {y, s, stats};
 }
 
@@ -289,6 +301,7 @@ py::dict layer_norm_vjp(const Tensor& dy, const Tensor& s, const Tensor& weight,
                                   d_sum ? d_sum->data_ptr() : nullptr, ps, dx.data_ptr(), rows(dx, "out").second, pw, pb,
                                   ws.data_ptr(), static_cast<size_t>(ws.numel()), call.stream),
         "pararnn_lm_layer_norm_vjp");
+  written(out);
   return res;
 }
 
@@ -351,6 +364,7 @@ Tensor token_logprobs_vjp(const Tensor& logits, const Maybe& targets, const Tens
                                       floats(g_entropy, "g_entropy", lead, dev), dz.data_ptr(), rows(dz, "out").second,
                                       call.stream),
         "pararnn_lm_token_logprobs_vjp");
+  written(out);
   return dz;
 }
 

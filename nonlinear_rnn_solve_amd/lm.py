@@ -3,9 +3,11 @@ normalisation and the log probabilities of given tokens, each with its gradients
 
 The kernels are libpararnn_lm.so (C ABI in include/pararnn_lm.h); a compiled binding checks the arguments, allocates the
 results with torch and passes the current HIP stream.  There is no fallback -- if a library or a GPU is missing, calls
-raise.  Wrong tensors raise ValueError, statuses of the C ABI PararnnError.  Float32 arguments (states, statistics, per-token
-numbers, parameters) are contiguous and of the stated shape, dimensions of one entry aside, or flat.  Nothing here synchronises, so calls can be
-captured in a HIP graph (torch.cuda.graph; a captured call's workspace belongs to the graph).
+raise.  Wrong tensors raise ValueError, statuses of the C ABI PararnnError.  Float32 arguments (states, statistics,
+per-token numbers, parameters) are contiguous and of the stated shape, dimensions of one entry aside, or flat.  Results are
+detached from autograd (examples/gated_lm.py wraps the operators in autograd functions); a tensor given to be written
+counts as modified in place.  Nothing here synchronises, so calls can be captured in a HIP graph (torch.cuda.graph; a
+captured call's workspace belongs to the graph).
 """
 from __future__ import annotations
 

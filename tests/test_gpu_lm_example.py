@@ -61,3 +61,13 @@ def test_a_short_training_run_learns():
     losses = gated_lm.train(model, 60, 29, rows=4, total=128, count=3)
     assert torch.isfinite(losses).all()
     assert float(losses[-5:].mean()) < 0.6 * float(losses[:5].mean())
+
+
+def test_a_second_backward_pass_is_refused():
+    # the logits' gradient has taken the logits' place: a second pass over the graph has nothing to start from
+    model = gated_lm.GatedLM(29, 16, 1, dtype=torch.float32, seed=6)
+    tokens, targets, cu = gated_lm.documents(29, 2, 40, 2, torch.Generator().manual_seed(7))
+    loss = model.loss(tokens, targets, cu)
+    loss.backward(retain_graph=True)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()

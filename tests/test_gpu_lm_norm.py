@@ -235,3 +235,14 @@ def test_arguments_of_another_shape_are_refused():
     assert torch.equal(lm.layer_norm_vjp(dy, s, w, stats.flatten())["d_x"], want)
     got = lm.layer_norm_vjp(dy.view(5, 1, 32), s.view(5, 1, 32), w, stats.view(5, 1, 2))["d_x"]
     assert torch.equal(got.view(5, 32), want)
+
+
+def test_written_tensors_tell_autograd():
+    x, res, w, b, dy, ds = make(5, 32, F32, seed=10)
+    y, stream = torch.empty_like(x), res.clone()
+    before = y._version, stream._version, x._version
+    _, s, stats = lm.layer_norm(x, w, b, residual=stream, out=y, sum_out=stream, want_stats=True)
+    assert (y._version, stream._version, x._version) == (before[0] + 1, before[1] + 1, before[2])
+    v = dy._version
+    lm.layer_norm_vjp(dy, s, w, stats, out=dy)
+    assert dy._version == v + 1

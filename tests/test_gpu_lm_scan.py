@@ -579,3 +579,30 @@ def test_arguments_of_another_shape_are_refused():
         assert all(torch.equal(got[k], want[k]) for k in want)
     state = h0[:, None].clone()
     assert torch.equal(lm.gated_scan(x, r, i, lam, h0=h0, h_last=state)[1][:, 0], last)
+
+
+def test_written_tensors_tell_autograd():
+    # what autograd has saved and a call overwrites must not be used by a backward pass
+    x, r, i, lam, h0, dh, dl = make(2, 20, 16, F32, seed=41, layout="dense")
+    out, state = torch.empty_like(x), h0.clone()
+    before = out._version, state._version, x._version
+    carry = lm.gated_scan(x, r, i, lam, h0=state, out=out, h_last=state, want_carry=True)[2]
+    assert (out._version, state._version, x._version) == (before[0] + 1, before[1] + 1, before[2])
+    grads = [torch.empty_like(x) for _ in range(3)]
+    before = [t._version for t in grads]
+    lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, out=grads)
+    assert [t._version for t in grads] == [v + 1 for v in before]
+    with pytest.raises(ValueError):        # a refused call writes nothing
+        lm.gated_scan_vjp(x, r, i, lam, carry, dh, h0=h0, d_last=lam, out=grads)
+    assert [t._version for t in grads] == [v + 1 for v in before]
+    leaf = torch.ones_like(x, requires_grad=True)
+    y = leaf * 2
+    loss = (y * y).sum()
+    lm.gated_scan(x, r, i, lam, out=y.detach())
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    with torch.inference_mode():       # tensors without a counter
+        lm.gated_scan(x, r, i, lam, out=torch.empty_like(x))
+    with torch.inference_mode():
+        inference = torch.empty_like(x)
+    lm.gated_scan(x, r, i, lam, out=inference)
