@@ -15,12 +15,14 @@ pseudo-random times before publishing look-back words, so that scans walk far
 back.  Only the tests load it; its results must equal libpararnn.so's bit for bit.
 
 libpararnn_lm.so holds the language-model operators of include/pararnn_lm.h, one source file each, compiled in
-parallel and linked; _lm_binding.so is its Python binding (host C++ against torch's headers), and
-libpararnn_lm_stress.so its look-back stress variant.
+parallel and linked; _lm_binding.so is its Python binding (host C++ against torch's headers; without torch or g++ it
+is left out, with a message, since the C ABI needs neither), and libpararnn_lm_stress.so its look-back stress variant.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -61,6 +63,7 @@ def _command(out: str, stress: bool, asm: bool) -> list:
 def build(asm: bool = False, verbose: bool = True, stress: bool = True) -> str:
     """Compile libpararnn.so, libpararnn_lm.so (and, with stress, the stress variants), all in parallel;
     returns the path of libpararnn.so."""
+    binding = _binding_commands()   # before anything is started
     jobs = [(LIB, False)] + ([(STRESS_LIB, True)] if stress else [])
     if asm:
         os.makedirs(os.path.join(ROOT, "_build"), exist_ok=True)
@@ -69,13 +72,15 @@ def build(asm: bool = False, verbose: bool = True, stress: bool = True) -> str:
         tmp = lib + ".tmp%d" % os.getpid()
         cmd = _command(tmp, st, asm and not st)
         procs.append((_start(cmd, verbose, os.path.join(ROOT, "_build") if (asm and not st) else HERE), tmp, lib))
-    lm, binding = _start_lm(verbose), _start_binding(verbose)
+    lm = _start_lm(verbose)
+    compiling = _start_binding(binding, verbose) if binding else []
     lm_stress = _start_lm(verbose, LM_SRCS[:1], "PR_LB_STRESS=1") if stress else []
     failed = _finish(procs, verbose)
     failed += _finish_lm(lm, LM_LIB, verbose)
     if stress:
         failed += _finish_lm(lm_stress, LM_STRESS_LIB, verbose)
-    failed += _finish_binding(binding, verbose, not failed)
+    if binding:
+        failed += _finish_binding(binding, compiling, verbose, not failed)
     if failed:
         raise RuntimeError("hipcc failed: %s" % failed)
     return LIB
@@ -110,25 +115,37 @@ def _finish_lm(jobs, lib, verbose):
     return failed
 
 
-def _start_binding(verbose):
-    """Start compiling the binding; its object beside it until it is linked against libpararnn_lm.so."""
+def _binding_commands():
+    """(object, compile command, link command without its output) of the binding; None where torch or g++ is missing."""
+    missing = "torch" if importlib.util.find_spec("torch") is None else "g++" if shutil.which("g++") is None else None
+    if missing:
+        print("[build] %s is left out: no %s (nonlinear_rnn_solve_amd.lm needs it, the C ABI does not)"
+              % (os.path.basename(LM_BINDING), missing), flush=True)
+        return None
+    import torch
     from torch.utils.cpp_extension import include_paths
     obj = os.path.join(HERE, "lm_binding.tmp%d.o" % os.getpid())
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-I", INC]
     for p in include_paths() + [os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]:
         cmd += ["-isystem", p]
-    return [(_start(cmd + ["-c", LM_BINDING_SRC, "-o", obj], verbose), obj, obj)]
+    link = ["g++", "-shared", obj, "-L", HERE, "-lpararnn_lm", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    return obj, cmd + ["-c", LM_BINDING_SRC, "-o", obj], link
 
 
-def _finish_binding(jobs, verbose, link):
-    import torch
+def _start_binding(commands, verbose):
+    """Start compiling the binding; its object beside it until it is linked against libpararnn_lm.so."""
+    obj, compile_, _ = commands
+    return [(_start(compile_, verbose), obj, obj)]
+
+
+def _finish_binding(commands, jobs, verbose, link):
     failed = _finish(jobs, verbose)
-    obj, tmp = jobs[0][1], LM_BINDING + ".tmp%d" % os.getpid()
+    obj, _, cmd = commands
+    tmp = LM_BINDING + ".tmp%d" % os.getpid()
     if link and not failed:
-        cmd = ["g++", "-shared", obj, "-L", HERE, "-lpararnn_lm", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
-               "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-o", tmp]
-        failed = _finish([(_start(cmd, verbose), tmp, LM_BINDING)], verbose)
+        failed = _finish([(_start(cmd + ["-o", tmp], verbose), tmp, LM_BINDING)], verbose)
     if os.path.exists(obj):
         os.remove(obj)
     return failed

@@ -2,7 +2,9 @@
 import ctypes
 import os
 import re
+import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -190,3 +192,29 @@ def test_plain_norm_and_logprobs_against_torch():
     assert torch.allclose(ent, d.entropy()) and lp[2] == 0
     assert torch.allclose(lp[t >= 0], d.log_prob(t.clamp(min=0))[t >= 0])
     assert plain.top(torch.tensor([[1.0, float("nan"), 3.0, 1.0, -float("inf")]]), 5).tolist() == [[2, 0, 3, 1, 4]]
+
+
+class _Finished:
+    returncode = 0
+
+    def communicate(self):
+        return "", None
+
+
+@pytest.mark.parametrize("missing", ["torch", "g++"])
+def test_the_libraries_build_without_torch_or_a_host_compiler(missing, monkeypatch, capsys):
+    # the C ABI needs hipcc only; what the Python binding needs is looked for before anything is started
+    commands = []
+    monkeypatch.setattr(build, "_start", lambda cmd, *a, **k: commands.append(cmd) or _Finished())
+    for name in ("replace", "remove"):
+        monkeypatch.setattr(build.os, name, lambda *a: None)
+    if missing == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    else:
+        monkeypatch.setattr(shutil, "which", lambda *a, **k: None)
+    assert build.build(verbose=False) == build.LIB
+    made = [c[c.index("-o") + 1] for c in commands]
+    for lib in (build.LIB, build.STRESS_LIB, build.LM_LIB, build.LM_STRESS_LIB):
+        assert any(m.startswith(lib) for m in made), lib
+    assert not any("lm_binding" in " ".join(c) for c in commands)
+    assert missing in capsys.readouterr().out
