@@ -15,7 +15,7 @@ pseudo-random times before publishing look-back words, so that scans walk far
 back.  Only the tests load it; its results must equal libpararnn.so's bit for bit.
 
 libpararnn_lm.so holds the language-model operators of include/pararnn_lm.h, one source file each, compiled in
-parallel and linked; _lm_binding.so is its Python binding (host C++ against torch's headers; without torch or g++ it
+parallel and linked; _lm_binding.*.so is its Python binding (host C++ against torch's headers; without torch or g++ it
 is left out, with a message, since the C ABI needs neither), and libpararnn_lm_stress.so its look-back stress variant.
 """
 from __future__ import annotations
@@ -37,7 +37,7 @@ LM_SRCS = [os.path.join(HERE, "csrc", f) for f in ("lm_scan.hip", "lm_norm.hip",
 LM_LIB = os.path.join(HERE, "libpararnn_lm.so")
 LM_STRESS_LIB = os.path.join(HERE, "libpararnn_lm_stress.so")
 LM_BINDING_SRC = os.path.join(HERE, "csrc", "lm_binding.cpp")
-LM_BINDING = os.path.join(HERE, "_lm_binding.so")
+LM_BINDING = os.path.join(HERE, "_lm_binding" + sysconfig.get_config_var("EXT_SUFFIX"))   # of this interpreter
 ARCH = "gfx950"
 
 

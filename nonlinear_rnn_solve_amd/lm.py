@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import importlib
 import os
+import sysconfig
 from typing import NamedTuple
 
 import torch
@@ -21,7 +22,7 @@ from .api import PararnnError  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpararnn_lm.so")
-BINDING_PATH = os.path.join(_HERE, "_lm_binding.so")
+BINDING_PATH = os.path.join(_HERE, "_lm_binding" + sysconfig.get_config_var("EXT_SUFFIX"))   # of this interpreter
 ABI_VERSION = 1           # PARARNN_LM_ABI_VERSION
 SCAN_CHUNK = 64           # PARARNN_LM_SCAN_CHUNK
 NORM_MAX_D = 16384        # PARARNN_LM_NORM_MAX_D

@@ -5,6 +5,7 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 import pytest
 import torch
@@ -218,3 +219,7 @@ def test_the_libraries_build_without_torch_or_a_host_compiler(missing, monkeypat
         assert any(m.startswith(lib) for m in made), lib
     assert not any("lm_binding" in " ".join(c) for c in commands)
     assert missing in capsys.readouterr().out
+
+
+def test_the_binding_is_of_this_interpreter():
+    assert build.LM_BINDING == lm.BINDING_PATH and build.LM_BINDING.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
