@@ -89,7 +89,7 @@ pararnn_status pararnn_lm_gated_scan_vjp(const pararnn_lm_scan* prob, const para
 
 /* ------------------------------------------------------------------------------------------------
  * Layer normalisation of N rows of D channels (D <= PARARNN_LM_NORM_MAX_D, else UNSUPPORTED; so
- * is N of 2^28 or more, 2^26 where D > 256, 2^24 where D > 1024, 2^22 where D > 4096):
+ * is N above 2^28 - 16, 2^26 - 4 where D > 256, 2^24 - 1 where D > 1024, 2^22 - 1 where D > 4096):
  *     s = x + residual (rounded to dtype; s = x without one),  mean and variance of each row of s,
  *     y = (s - mean) / sqrt(var + eps) * weight + bias
  *   x, residual (or NULL), y, sum  [N][D] of dtype with row strides; weight [D], bias [D] or NULL float32

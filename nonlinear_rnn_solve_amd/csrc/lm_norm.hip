@@ -290,8 +290,14 @@ template <typename T, class F> static void shape_of(int64_t D, F f) {
   else lanes(std::integral_constant<int, 1024>{});
 }
 
-// threads that a row of k_norm takes at most
+// lanes of a row, threads of a workgroup of k_norm
 static int64_t norm_threads(int64_t D) { return D <= 256 ? 16 : D <= 1024 ? 64 : D <= 4096 ? 256 : 1024; }
+constexpr int norm_block(int64_t lanes) { return lanes > 256 ? 1024 : 256; }
+// k_norm's launch holds N rows, the last workgroup's idle lanes included
+static bool rows_ok(int64_t N, int64_t D) {
+  const int64_t lanes = norm_threads(D), threads = norm_block(lanes);
+  return grid_ok(ceil_div(N, threads / lanes), threads);
+}
 static int64_t grad_groups(int64_t N, int64_t D) {
   const int64_t lanes = norm_threads(D), threads = grad_threads(lanes);
   return std::min<int64_t>(ceil_div(N, threads / lanes), kGradAll / threads);
@@ -314,14 +320,14 @@ extern "C" pararnn_status pararnn_lm_layer_norm(int dtype, int64_t N, int64_t D,
     return PARARNN_ERR_INVALID_ARG;
   if (!plane_ok(N, x_stride) || !plane_ok(N, y_stride) || (residual && (!plane_ok(N, residual_stride) || !plane_ok(N, sum_stride))))
     return PARARNN_ERR_INVALID_ARG;
-  if (D > PARARNN_LM_NORM_MAX_D || !grid_ok(N, norm_threads(D))) return PARARNN_ERR_UNSUPPORTED;
+  if (D > PARARNN_LM_NORM_MAX_D || !rows_ok(N, D)) return PARARNN_ERR_UNSUPPORTED;
   const NormArgs a{x, residual, weight, bias, y, sum, stats, x_stride, residual_stride, y_stride, sum_stride, N, D, eps};
   hipStream_t st = static_cast<hipStream_t>(stream);
   const auto run = [&](auto t) {
     using T = decltype(t);
     shape_of<T>(D, [&](auto s) {
       using S = decltype(s);
-      constexpr int NT = S::LPR > 256 ? S::LPR : 256;
+      constexpr int NT = norm_block(S::LPR);
       k_norm<T, S, NT><<<static_cast<unsigned>(ceil_div(N, NT / S::LPR)), NT, 0, st>>>(a);
     });
   };
@@ -349,7 +355,7 @@ extern "C" pararnn_status pararnn_lm_layer_norm_vjp(int dtype, int64_t N, int64_
     return PARARNN_ERR_INVALID_ARG;
   if (!plane_ok(N, dy_stride) || !plane_ok(N, s_stride) || !plane_ok(N, d_x_stride) || (d_sum && !plane_ok(N, d_sum_stride)))
     return PARARNN_ERR_INVALID_ARG;
-  if (D > PARARNN_LM_NORM_MAX_D || !grid_ok(N, norm_threads(D))) return PARARNN_ERR_UNSUPPORTED;
+  if (D > PARARNN_LM_NORM_MAX_D || !rows_ok(N, D)) return PARARNN_ERR_UNSUPPORTED;
   if (!ptr_ok(ws, 256) || ws_bytes < pararnn_lm_layer_norm_vjp_workspace_bytes(N, D)) return PARARNN_ERR_WORKSPACE;
   const bool params = d_weight || d_bias;
   const int64_t groups = grad_groups(N, D);

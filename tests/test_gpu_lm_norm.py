@@ -246,3 +246,18 @@ def test_written_tensors_tell_autograd():
     v = dy._version
     lm.layer_norm_vjp(dy, s, w, stats, out=dy)
     assert dy._version == v + 1
+
+
+def test_as_many_rows_as_a_launch_holds():
+    N, D, P = (1 << 28) - 16, 3, 16
+    x, _, w, b, dy, _ = make(P, D, BF, seed=11, residual=False)
+    want, _, stats = lm.layer_norm(x, w, b, want_stats=True)
+    dwant = lm.layer_norm_vjp(dy, x, w, stats, want_params=False)["d_x"]
+    many = lambda t: t.repeat(N // P, 1)  # noqa: E731
+    y, s, st = lm.layer_norm(many(x), w, b, want_stats=True)
+    assert (y.view(-1, P, D) == want).all() and (st.view(-1, P, 2) == stats).all()
+    d = lm.layer_norm_vjp(many(dy), s, w, st, want_params=False)["d_x"]
+    assert (d.view(-1, P, D) == dwant).all()
+    with pytest.raises(lm.PararnnError) as e:
+        lm.layer_norm(x[:1].expand(N + 1, D), w, b, out=y.new_empty(N + 1, D))
+    assert e.value.status == -2

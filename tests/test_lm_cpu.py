@@ -223,3 +223,14 @@ def test_the_libraries_build_without_torch_or_a_host_compiler(missing, monkeypat
 
 def test_the_binding_is_of_this_interpreter():
     assert build.LM_BINDING == lm.BINDING_PATH and build.LM_BINDING.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def test_launch_limits_count_whole_workgroups(lib):
+    # a launch has fewer than 2^32 threads, the last workgroup's idle rows included: one row more than its limit
+    def fwd(N, D):
+        return lib.pararnn_lm_layer_norm(0, N, D, P, D, None, 0, P, None, 1e-5, P, D, None, 0, None, None)
+
+    for D, rows in ((1, 16), (256, 16), (257, 4), (1024, 4)):
+        limit = rows * ((1 << 24) - 1)
+        for N in (limit + 1, limit + rows):
+            assert fwd(N, D) == -2, (N, D)
