@@ -152,7 +152,7 @@ inline bool sizes_fit(int64_t a, int64_t b, int64_t c = 1) {
 // the last element of a plane of n rows with stride s and d dense elements has an offset that fits int64
 inline bool plane_ok(int64_t n, int64_t s) { return s >= 0 && (n <= 1 || s <= INT64_MAX / 16 / (n - 1)); }
 inline pararnn_status launched() { return hipGetLastError() == hipSuccess ? PARARNN_OK : PARARNN_ERR_HIP; }
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }   // a >= 0 of any size
 // a launch has fewer than 2^32 threads
 inline bool grid_ok(int64_t blocks, int64_t threads) { return blocks <= INT64_C(0xffffffff) / threads; }
 

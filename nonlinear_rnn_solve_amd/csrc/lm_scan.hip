@@ -872,8 +872,8 @@ struct Layout {
   int64_t chunks, ctiles, tiles, tickets, words, gwords, parts, total;   // the last five in bytes
 };
 static bool layout(int64_t B, int64_t T, int64_t D, Layout& o) {
-  if (!sizes_fit(B, T, D) || !sizes_fit(B, D + TW, CT)) return false;
-  o.chunks = T <= 0 ? 0 : ceil_div(T, CT);
+  if (!sizes_fit(B, T, D) || D > INT64_MAX - TW || !sizes_fit(B, D + TW, CT)) return false;
+  o.chunks = B > 0 && D > 0 ? ceil_div(T, CT) : 0;   // nothing to solve: T alone may be of any size
   o.ctiles = ceil_div(D, TW);
   o.tiles = B * o.ctiles * o.chunks;
   o.words = o.chunks > 1 ? o.tiles * TW * 8 : 0;

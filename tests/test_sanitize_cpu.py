@@ -1,6 +1,6 @@
 """Sanitizer builds of the host code (no GPU needed): the CPU oracle driven through every entry point,
 cell and option (tests/sanitize/oracle_run.c), and the C ABI's argument validation and workspace queries
-(tests/sanitize/abi_validation.cpp against the library source), each built with AddressSanitizer and
+(tests/sanitize/abi_validation.cpp and lm_abi_validation.cpp against the libraries' sources), each built with AddressSanitizer and
 UndefinedBehaviorSanitizer and required to run clean.  The library build puts the sanitizers on the host
 pass only: GPU code is built as usual."""
 import os
@@ -40,5 +40,21 @@ def test_abi_validation_runs_clean_under_host_sanitizers(tmp_path):
            "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer",
            "-I", os.path.join(ROOT, "include"), os.path.join(ROOT, "nonlinear_rnn_solve_amd", "csrc", "pararnn.hip"),
            os.path.join(SAN, "abi_validation.cpp"), "-o", exe]
+    subprocess.run(cmd, check=True, capture_output=True, text=True, timeout=900)
+    assert "checks passed" in _run(exe)
+
+
+@pytest.mark.skipif(shutil.which("hipcc") is None and not os.path.exists("/opt/rocm/bin/hipcc"), reason="no hipcc")
+def test_lm_abi_validation_runs_clean_under_host_sanitizers(tmp_path):
+    # host code only: what the queries and checks return does not depend on the kernels
+    exe = str(tmp_path / "lm_abi_validation")
+    hipcc = "/opt/rocm/bin/hipcc" if os.path.exists("/opt/rocm/bin/hipcc") else "hipcc"
+    csrc = os.path.join(ROOT, "nonlinear_rnn_solve_amd", "csrc")
+    cmd = [hipcc, "--offload-arch=gfx950", "-O1", "-g", "-std=c++17",
+           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+           "-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
+           "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer",
+           "-I", os.path.join(ROOT, "include"), *(os.path.join(csrc, f) for f in ("lm_scan.hip", "lm_norm.hip", "lm_logp.hip")),
+           os.path.join(SAN, "lm_abi_validation.cpp"), "-o", exe]
     subprocess.run(cmd, check=True, capture_output=True, text=True, timeout=900)
     assert "checks passed" in _run(exe)
