@@ -94,7 +94,7 @@ pararnn_status pararnn_lm_gated_scan_vjp(const pararnn_lm_scan* prob, const para
  *     y = (s - mean) / sqrt(var + eps) * weight + bias
  *   x, residual (or NULL), y, sum  [N][D] of dtype with row strides; weight [D], bias [D] or NULL float32
  *   sum     the rounded s; required with a residual, must be NULL without; it may be x or residual itself
- *   stats   [N][2] float32 (mean, 1 / sqrt(var + eps)) for the gradient, or NULL
+ *   stats   [N][2] float32 (mean, 1 / sqrt(var + eps)) for the gradient, or NULL; not written where D = 0
  * ---------------------------------------------------------------------------------------------- */
 #define PARARNN_LM_NORM_MAX_D 16384
 pararnn_status pararnn_lm_layer_norm(int dtype, int64_t N, int64_t D, const void* x, int64_t x_stride,
@@ -120,8 +120,9 @@ pararnn_status pararnn_lm_layer_norm_vjp(int dtype, int64_t N, int64_t D, const 
  * and the `top` largest logits in descending order, ties by ascending index (0 <= top <= min(V, PARARNN_LM_MAX_TOP)).
  *   targets [N] int32 or int64 (target_bytes 4 or 8).  A negative one means that no token is scored: logp = 0.
  *           One at or above V gives logp = NaN.
- *   lse, logp, entropy [N] float32 (entropy, or logp with targets, may be NULL);
+ *   lse, logp, entropy [N] float32: lse and entropy may be NULL; logp is given with targets and NULL without;
  *   top_logp [N][top] float32, top_ids [N][top] int64 (NULL when top = 0)
+ *   ws      of the queried size and aligned like any other; nothing is kept there at present
  * UNSUPPORTED: N of 2^26 or more, 2^24 where V > 4096, 2^22 where V > 32768.
  * Logits of -infinity are tokens ruled out.  A row with nothing left has lse = -infinity, logp = -infinity,
  * entropy = 0 and a gradient of zeros.  A NaN or +infinity makes its row's numbers NaN; a NaN ranks as -infinity.

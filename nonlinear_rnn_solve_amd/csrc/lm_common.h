@@ -19,11 +19,10 @@ namespace lm {
 constexpr int WAVE = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// v_exp_f32 is 2^x, v_log_f32 log2, v_rcp_f32 1/x, v_rsq_f32 1/sqrt, each about 1 ulp
+// v_exp_f32 is 2^x, v_log_f32 log2, v_rcp_f32 1/x, each about 1 ulp
 DEV float hw_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 DEV float hw_log2(float x) { return __builtin_amdgcn_logf(x); }
 DEV float hw_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
-DEV float hw_rsq(float x) { return __builtin_amdgcn_rsqf(x); }
 DEV float sigmoid(float x) { return hw_rcp(1.0f + hw_exp2(-kLog2e * x)); }
 
 struct bf16 { uint16_t u; };   // storage only
