@@ -403,7 +403,9 @@ extern "C" pararnn_status pararnn_lm_token_logprobs(int dtype, int64_t N, int64_
     };
     // Lanes of a row.  Few rows leave CUs idle, so theirs are read by more lanes: 32 rows, 20 alternatives, bf16: V = 3000
     // 8.2 us with 64 lanes and 6.7 with 256; V = 24000 9.9 with 256 and 8.8 with 1024 (float32 11.7 and 9.4).  Many rows fill
-    // the chip either way and waste less of a row's end: 4096 rows: V = 3000 16.5 and 19.7; V = 24000 50 and 79.
+    // the chip either way and waste less of a row's end: 4096 rows: V = 3000 16.5 and 19.7; V = 24000 50 and 79.  512 rows of
+    // 1024 lanes are what the chip holds at once: V = 24000 12.0 and 11.2 at 512, 14.1 and 16.0 at 640.  (At V = 3000 the lines
+    // cross later: 8.8 and 8.2 at 1024, 10.1 and 11.8 at 2048.)
     const bool few = N <= 512;
     if (V <= 512 && !top) run(t, std::integral_constant<int, 16>{}, std::false_type{});
     else if (V <= (few ? 2048 : 4096)) alt(std::integral_constant<int, 64>{});
