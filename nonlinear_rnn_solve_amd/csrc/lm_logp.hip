@@ -1,9 +1,11 @@
 // lm_logp.hip -- log probabilities of given tokens, entropy and top alternatives of pararnn_lm.h, and their gradient.
 //
-// One pass over the logits each way.  The forward kernel is bound by vector instructions in bfloat16 (11 an element, two of
-// them conversions and one an exponential; 97% of the issue slots at 4096 x 131072 with 5 alternatives, 192 us, 5.6 TB/s),
-// by memory in float32 (4096 x 32000: 93 us, 5.6 TB/s), by one CU's instructions for few rows (32 x 50001 with 20
-// alternatives: 11 us).  The gradient is bound by memory (4096 x 32000 float32: 168 us for 1.05 GB, 6.2 TB/s).
+// One pass over the logits each way (two for the gradient of rows whose lse is large).  The forward kernel is bound by vector
+// instructions in bfloat16 (11 an element, two of them conversions and one an exponential; 97% of the issue slots at 4096 x
+// 131072 with 5 alternatives, 192 us, 5.6 TB/s), by memory in float32 (4096 x 32000: 92 us, 5.7 TB/s), by one CU's instructions
+// for few rows (32 x 50001 with 20 alternatives: 11 us), by instructions and the launch's own start and end for short rows
+// (bf16 65536 x 256: 10 to 11 us, 46% of the issue slots of the whole launch).  The gradient is bound by memory (4096 x 32000
+// float32: 171 us for 1.05 GB, 6.1 TB/s).
 
 #include <algorithm>
 #include <type_traits>

@@ -144,10 +144,12 @@ __global__ __launch_bounds__(64) void k_scan_serial(const ScanArgs p, uint32_t c
 // Packed sequences: a wave finds its steps' sequences once and keeps them in shared memory (searched for at each boundary
 // by its lane: bf16 B = 4, T = 4096, D = 1000, 9 sequences 108 against 93 us in the gradient, 61 against 51 forward).
 //
-// Bound by memory for float32, by memory and vector instructions about equally for bfloat16 (57 to 60% of the issue
-// slots in both kernels).  Measured, bf16 (wide: B = 2, T = 4096, D = 4096; long: B = 1, T = 131072,
-// D = 1024): forward 62 and 260 us (4.2 TB/s), gradient 103 and 440 us (4.3 TB/s); a copy runs at 5.1 TB/s.
-//  - 64 steps a tile (4 waves) against 128 (8 waves): gradient 118 against 151 us (wide), since its 154 registers leave
+// Bound by memory for float32, by memory and vector instructions about equally for bfloat16 (57% of the issue slots forward,
+// 70% in the gradient).  Measured, bf16 (wide: B = 2, T = 4096, D = 4096; long: B = 1, T = 131072, D = 1024): forward 62 and
+// 260 us (4.2 TB/s), gradient 109 and 464 to 490 us (4.1 TB/s); a copy runs at 5.1 TB/s.  The forms without packing spill
+// nothing (V = 4).  The packed ones spill scalar registers to vector lanes (11 or 12 forward, 29 in the gradient with V = 4, 120
+// with V = 1), and the forward bf16 V = 4 one two vector registers: the boundaries' bases stay live through the walks.
+//  - 64 steps a tile (4 waves) against 128 (8 waves): gradient 118 against 151 us (wide, when chosen), since its 156 registers leave
 //    12 waves on a CU in workgroups of 4 and 8 in workgroups of 8; forward 66 against 72.  32 elements a lane: 66 and 124.
 //  - groups against a look-back over the W tiles before: forward 257 against 297 us (long).  Groups of 16: 325.
 //  - stores that do not stay in the caches: float32 B = 8, T = 2048, D = 1000 forward 69 against 81 us; wide 62.6 against 64.0.
@@ -605,8 +607,9 @@ __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(5))) void k
 //
 // The gradients of the gates need both s = sig(v) and 1 - s, each with its own relative accuracy: of an open gate (v > 0) 1 - s
 // from s has lost it (1% off at v = 12, zero from 18 on).  e^-v s has it, and then 1 - (1 - s) gives s.  A lane keeps the smaller
-// of the two, its sign bit set where it is 1 - s: as many registers as s alone.  The 12 instructions an element
-// that this takes cost 3% of a bfloat16 training pass (B = 2, T = 4096, D = 4096: 167 -> 172 us) and 0.5% of a packed float32 one (191 -> 192).
+// of the two, its sign bit set where it is 1 - s: as many registers as s alone.  The instructions that this takes (12 to 14 an
+// element) cost 3% of a bfloat16 training pass (B = 2, T = 4096, D = 4096: 167 -> 172 us) and 0.5% of a packed float32 one
+// (191 -> 192).
 // ------------------------------------------------------------------------------------------------
 DEV float smaller(float v, float s) {   // e^-v s of a shut gate may be infinity times 0: fminf passes a NaN over
   return __builtin_copysignf(fminf(hw_exp2(-kLog2e * v) * s, s), -v);
