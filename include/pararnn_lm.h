@@ -138,7 +138,8 @@ pararnn_status pararnn_lm_token_logprobs(int dtype, int64_t N, int64_t V, const 
  * are reports and have none):
  *     d_z_j = g_logp (1[j = target] - p_j) - g_entropy p_j (ln p_j + entropy)
  *   lse, entropy as the forward wrote them (entropy may be NULL when g_entropy is).  p does not carry the rounding of lse:
- *           rows with |lse| > 32 are read once more, and their normaliser is summed about lse
+ *           rows with |lse| > 32 are read once more, and their normaliser is summed about lse.  An lse that differs from
+ *           the row's by more than rounding (that of a longer row, of which these logits are a part) is used as it is
  *   g_logp [N] float32 (NULL with targets NULL), g_entropy [N] float32 or NULL
  *   d_logits [N][V] of dtype, row stride d_stride; it may be logits itself (same stride)                */
 pararnn_status pararnn_lm_token_logprobs_vjp(int dtype, int64_t N, int64_t V, const void* logits, int64_t stride,

@@ -280,7 +280,9 @@ template <typename T, int LPR, bool LAST, class F> DEV void each_chunk(const T* 
 }
 
 // ln sum_j e^{z_j - lse} of a row: what the rounding of its lse left out, 0 up to half a unit of lse (up to ln V where lse
-// has no bits left for ln V).  The same value for each of the row's LPR lanes, in a fixed order.
+// has no bits left for ln V).  More than a unit and 2^-18 (for the sums' own errors) is no rounding: the lse is that of
+// other logits, of a row that these are a part of for instance, and is taken as given.  The same value for each of the row's
+// LPR lanes, in a fixed order.
 template <typename T, int LPR>
 DEV float log_rest(const T* z, int64_t columns, float lse, int lane, float (&sh)[LPR > WAVE ? LPR / WAVE : 1]) {
   constexpr int V = 16 / sizeof(T);
@@ -297,7 +299,8 @@ DEV float log_rest(const T* z, int64_t columns, float lse, int lane, float (&sh)
 #pragma unroll
     for (int w = 1; w < LPR / WAVE; ++w) s += sh[w];
   }
-  return kLn2 * hw_log2(s);
+  const float rest = kLn2 * hw_log2(s);
+  return fabsf(rest) > fmaf(0x1p-23f, fabsf(lse), 0x1p-18f) ? 0.0f : rest;   // a NaN stays
 }
 
 // LPR lanes of one row write a segment of kAhead chunks each.  p_j = e^{z_j - lse}, where lse is one float32: half a unit of it

@@ -425,3 +425,24 @@ def test_arguments_of_another_shape_are_refused():
             bad()
     for same in (lambda a: a[..., None], lambda a: a[None], lambda a: a.flatten()):     # the same order of the same values
         assert torch.equal(lm.token_logprobs_vjp(z, t, same(r.lse), same(r.entropy), same(g), same(g)), want)
+
+
+@pytest.mark.parametrize("offset", [0.0, 100.0, -5000.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gradient_from_a_normaliser_of_more_logits(dtype, offset):
+    # logits that are a part of their row, with the whole row's lse and entropy: p sums to less than 1, and is not made to
+    gen = torch.Generator().manual_seed(11)
+    N, V, half = 6, 6000, 2500
+    step = 2.0 ** (math.ceil(math.log2(max(abs(offset), 32.0))) - 7) if dtype == BF else 2.0 ** -6
+    z = (offset + step * torch.randint(0, 16 if dtype == BF else 512, (N, V), generator=gen)).to(dtype).cuda()
+    t = torch.randint(0, half, (N,), generator=gen).cuda()
+    g, ge = torch.randn(N, generator=gen).cuda(), torch.randn(N, generator=gen).cuda()
+    whole = lm.token_logprobs(z, t)
+    part = z[:, :half]
+    got = lm.token_logprobs_vjp(part, t, whole.lse, whole.entropy, g, ge)
+    # the given lse has its own rounding, u |lse|, which nothing here can know
+    want = f64(lm.token_logprobs_vjp(z, t, whole.lse, whole.entropy, g, ge))[:, :half]
+    l = f64(part) - f64(whole.lse)[:, None]
+    size = torch.exp(l) * (f64(g).abs()[:, None] + f64(ge).abs()[:, None] * (l.abs() + f64(whole.entropy)[:, None] + 1))
+    tol = (V / 64 + 64 + 2 * f64(whole.lse).abs()[:, None] + 3 * l.abs()) * U32 * size + 2 * U32 * want.abs()
+    close(got, want, rounded(rounded(want, tol, dtype), rounded(want, tol, dtype), dtype), "part of a row")
