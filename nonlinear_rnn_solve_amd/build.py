@@ -1,4 +1,4 @@
-"""Build libpararnn.so and libpararnn_lm.so (HIP, gfx950 only) in-tree with hipcc.
+"""Build libpararnn.so, libpararnn_lm.so and libpararnn_block.so (HIP, gfx950 only) in-tree with hipcc.
 
     python -m nonlinear_rnn_solve_amd.build            # build the libraries and their look-back stress variants
     python -m nonlinear_rnn_solve_amd.build --asm      # also keep the gfx950 assembly for inspection
@@ -17,6 +17,7 @@ back.  Only the tests load it; its results must equal libpararnn.so's bit for bi
 libpararnn_lm.so holds the language-model operators of include/pararnn_lm.h, one source file each, compiled in
 parallel and linked; _lm_binding.*.so is its Python binding (host C++ against torch's headers; without torch or g++ it
 is left out, with a message, since the C ABI needs neither), and libpararnn_lm_stress.so its look-back stress variant.
+libpararnn_block.so and _block_binding.*.so are the same for the block operators of include/pararnn_block.h.
 """
 from __future__ import annotations
 
@@ -38,6 +39,10 @@ LM_LIB = os.path.join(HERE, "libpararnn_lm.so")
 LM_STRESS_LIB = os.path.join(HERE, "libpararnn_lm_stress.so")
 LM_BINDING_SRC = os.path.join(HERE, "csrc", "lm_binding.cpp")
 LM_BINDING = os.path.join(HERE, "_lm_binding" + sysconfig.get_config_var("EXT_SUFFIX"))   # of this interpreter
+BLOCK_SRCS = [os.path.join(HERE, "csrc", f) for f in ("block_ssm.hip", "block_conv.hip", "block_ffn.hip", "block_adamw.hip")]
+BLOCK_LIB = os.path.join(HERE, "libpararnn_block.so")
+BLOCK_BINDING_SRC = os.path.join(HERE, "csrc", "block_binding.cpp")
+BLOCK_BINDING = os.path.join(HERE, "_block_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = "gfx950"
 
 
@@ -61,9 +66,9 @@ def _command(out: str, stress: bool, asm: bool) -> list:
 
 
 def build(asm: bool = False, verbose: bool = True, stress: bool = True) -> str:
-    """Compile libpararnn.so, libpararnn_lm.so (and, with stress, the stress variants), all in parallel;
+    """Compile libpararnn.so, libpararnn_lm.so, libpararnn_block.so (and, with stress, the stress variants), all in parallel;
     returns the path of libpararnn.so."""
-    binding = _binding_commands()   # before anything is started
+    bindings = _binding_commands()   # before anything is started
     jobs = [(LIB, False)] + ([(STRESS_LIB, True)] if stress else [])
     if asm:
         os.makedirs(os.path.join(ROOT, "_build"), exist_ok=True)
@@ -72,15 +77,17 @@ def build(asm: bool = False, verbose: bool = True, stress: bool = True) -> str:
         tmp = lib + ".tmp%d" % os.getpid()
         cmd = _command(tmp, st, asm and not st)
         procs.append((_start(cmd, verbose, os.path.join(ROOT, "_build") if (asm and not st) else HERE), tmp, lib))
-    lm = _start_lm(verbose)
-    compiling = _start_binding(binding, verbose) if binding else []
-    lm_stress = _start_lm(verbose, LM_SRCS[:1], "PR_LB_STRESS=1") if stress else []
+    block = _start_objects(verbose, BLOCK_SRCS)
+    lm = _start_objects(verbose, LM_SRCS)
+    compiling = [_start_binding(b, verbose) for b in bindings]
+    lm_stress = _start_objects(verbose, LM_SRCS[:1], "PR_LB_STRESS=1") if stress else []
     failed = _finish(procs, verbose)
-    failed += _finish_lm(lm, LM_LIB, verbose)
+    failed += _finish_objects(lm, LM_LIB, verbose)
     if stress:
-        failed += _finish_lm(lm_stress, LM_STRESS_LIB, verbose)
-    if binding:
-        failed += _finish_binding(binding, compiling, verbose, not failed)
+        failed += _finish_objects(lm_stress, LM_STRESS_LIB, verbose)
+    failed += _finish_objects(block, BLOCK_LIB, verbose)
+    for b, jobs in zip(bindings, compiling):
+        failed += _finish_binding(b, jobs, verbose, not failed)
     if failed:
         raise RuntimeError("hipcc failed: %s" % failed)
     return LIB
@@ -92,8 +99,8 @@ def _start(cmd, verbose, cwd=HERE):
     return subprocess.Popen(cmd, cwd=cwd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
 
 
-def _start_lm(verbose, srcs=LM_SRCS, define=None):
-    """Start compiling the language-model operators' sources; objects beside the library until it is linked."""
+def _start_objects(verbose, srcs, define=None):
+    """Start compiling a library's sources; objects beside the library until it is linked."""
     jobs = []
     for src in srcs:
         obj = os.path.join(HERE, "%s%s.tmp%d.o" % (os.path.basename(src)[:-4], "_stress" if define else "", os.getpid()))
@@ -102,7 +109,7 @@ def _start_lm(verbose, srcs=LM_SRCS, define=None):
     return jobs
 
 
-def _finish_lm(jobs, lib, verbose):
+def _finish_objects(jobs, lib, verbose):
     failed = _finish(jobs, verbose)
     objs = [obj for _, _, obj in jobs]
     if not failed:
@@ -116,36 +123,40 @@ def _finish_lm(jobs, lib, verbose):
 
 
 def _binding_commands():
-    """(object, compile command, link command without its output) of the binding; None where torch or g++ is missing."""
+    """(object, compile command, link command without its output, binding) of each binding; none where torch or g++ is
+    missing."""
     missing = "torch" if importlib.util.find_spec("torch") is None else "g++" if shutil.which("g++") is None else None
     if missing:
-        print("[build] %s is left out: no %s (nonlinear_rnn_solve_amd.lm needs it, the C ABI does not)"
-              % (os.path.basename(LM_BINDING), missing), flush=True)
-        return None
+        print("[build] %s and %s are left out: no %s (nonlinear_rnn_solve_amd.lm and .block need them, the C ABI does not)"
+              % (os.path.basename(LM_BINDING), os.path.basename(BLOCK_BINDING), missing), flush=True)
+        return []
     import torch
     from torch.utils.cpp_extension import include_paths
-    obj = os.path.join(HERE, "lm_binding.tmp%d.o" % os.getpid())
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-I", INC]
     for p in include_paths() + [os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]:
         cmd += ["-isystem", p]
-    link = ["g++", "-shared", obj, "-L", HERE, "-lpararnn_lm", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
-            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
-    return obj, cmd + ["-c", LM_BINDING_SRC, "-o", obj], link
+    found = []
+    for src, lib, binding in ((LM_BINDING_SRC, "pararnn_lm", LM_BINDING), (BLOCK_BINDING_SRC, "pararnn_block", BLOCK_BINDING)):
+        obj = os.path.join(HERE, "%s.tmp%d.o" % (os.path.basename(src)[:-4], os.getpid()))
+        link = ["g++", "-shared", obj, "-L", HERE, "-l" + lib, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+                "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+        found.append((obj, cmd + ["-c", src, "-o", obj], link, binding))
+    return found
 
 
 def _start_binding(commands, verbose):
-    """Start compiling the binding; its object beside it until it is linked against libpararnn_lm.so."""
-    obj, compile_, _ = commands
+    """Start compiling a binding; its object beside it until it is linked against its library."""
+    obj, compile_, _, _ = commands
     return [(_start(compile_, verbose), obj, obj)]
 
 
 def _finish_binding(commands, jobs, verbose, link):
     failed = _finish(jobs, verbose)
-    obj, _, cmd = commands
-    tmp = LM_BINDING + ".tmp%d" % os.getpid()
+    obj, _, cmd, binding = commands
+    tmp = binding + ".tmp%d" % os.getpid()
     if link and not failed:
-        failed = _finish([(_start(cmd + ["-o", tmp], verbose), tmp, LM_BINDING)], verbose)
+        failed = _finish([(_start(cmd + ["-o", tmp], verbose), tmp, binding)], verbose)
     if os.path.exists(obj):
         os.remove(obj)
     return failed

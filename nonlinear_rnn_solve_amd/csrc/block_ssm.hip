@@ -1,0 +1,932 @@
+// block_ssm.hip -- the selective state space scan of pararnn_block.h and its gradients.
+//
+//   dt = softplus(delta + dt_bias),  h_t[n] = exp(dt A[n]) h_{t-1}[n] + dt x_t B_t[n],
+//   y_t = (sum_n C_t[n] h_t[n] + skip x_t) silu(z_t)
+
+#include <type_traits>
+
+#include "block_common.h"
+
+namespace lm {
+
+// ------------------------------------------------------------------------------------------------
+// A workgroup holds 64 channels of one row, a lane a channel; its WV waves split the states, NS each.  So B_t and C_t are the
+// same for all lanes of a wave and x, delta and z the same for all its states: per step and state a lane takes one
+// exponential and four other instructions, and what a channel's step takes once (softplus, SiLU) is shared out over the
+// waves.  Time goes in tiles of CT steps: all waves load the tile's x, delta, z, B, C (those of the next tile are in flight
+// while this one is walked), put dt, dt x, B and C in shared memory, walk the steps, leave their part of y there, and share out
+// the sums.  B and C are then held one value a lane, replicated over the wave's four rows of 16 lanes, and reach the
+// products by the row broadcast of their operand (no instruction, no access of its own).
+//
+// Bound by vector instructions (32 of a wave's cycles a step and state, half of them the exponential).
+//
+// Few rows and channels leave the chip empty, so long rows are cut into segments of whole tiles.  One launch finds what each
+// segment leaves from a zero state and the sum of its dt (the decay over the segment is exp(A sum)), the next walks the
+// segments, each from the state that the ones before it make together.  That walks everything but y twice, and pays where
+// the workgroups without it are fewer than the chip holds.
+// ------------------------------------------------------------------------------------------------
+constexpr int CT = PARARNN_BLOCK_SSM_CHUNK;
+constexpr int CH = 64;          // channels of a workgroup
+
+struct SsmArgs {
+  const void *x, *delta, *z, *b, *c;
+  int64_t sx[2], sdelta[2], sz[2], sb[3], sc[3];
+  const float *A, *skip, *dt_bias, *h0;
+  Seqs seqs;
+  int64_t B, D;
+  int32_t T, N, G, tiles;       // tiles: of CT steps, of a row
+  int32_t ctiles, group;        // channel tiles of a group, channels of a group
+  int32_t S, per;               // segments of a row, tiles of a segment
+  bool in_place;                // h_last takes h0's place
+  void* y;
+  int64_t sy[2];
+  float *h_last, *carry;
+  float *end, *sum, *head;      // [S][B][N][D], [S][B][D] of the segments; head: the last sequence's h0, in place only
+};
+
+struct SsmGradArgs {
+  SsmArgs f;
+  const float* carry;
+  const void* dy;
+  const float* d_last;
+  void *dx, *ddelta, *dz;
+  int64_t sdy[2], sdx[2], sddelta[2], sdz[2];
+  float *d_h0;
+  float *part_bc;               // [G ctiles][B][T][2][N]: a channel tile's sums for d_b and d_c
+  float *part_A;                // [S B][N][D]
+  float *part_d;                // [S B][2][D]: for d_skip, d_dt_bias
+};
+
+// the workgroup's channels, row and segment
+struct Where {
+  int32_t ct, g, d, left;       // channel tile over all groups, group, first channel, channels from it on in the group
+  int64_t b;
+  int32_t s;
+};
+DEV Where where(const SsmArgs& p) {
+  const uint32_t n = static_cast<uint32_t>(p.ctiles * p.G), rows = blockIdx.x / n;
+  Where w;
+  w.ct = static_cast<int32_t>(blockIdx.x - rows * n);
+  w.g = w.ct / p.ctiles;
+  const int32_t in = (w.ct - w.g * p.ctiles) * CH;
+  w.d = w.g * p.group + in;
+  w.left = p.group - in;
+  w.s = static_cast<int32_t>(rows / static_cast<uint32_t>(p.B));
+  w.b = rows - w.s * p.B;
+  return w;
+}
+
+template <typename T> DEV T zero_of() { return T{}; }
+// element (t, d) of a plane, uniform base
+template <typename T> DEV const T* row_of(const void* plane, const int64_t (&s)[2], int64_t b, int64_t t, int32_t d) {
+  return static_cast<const T*>(plane) + b * s[0] + t * s[1] + d;
+}
+
+// lane k of each row of 16, for all lanes of the row
+template <int K> DEV float row_lane(float v) { return dpp<0x150 + K>(v); }
+// STEP's value n of NS, of registers that hold 16 / NS steps each
+template <int NS, int STEP, int n> DEV float of_step(const float (&r)[NS]) {
+  constexpr int SPR = 16 / NS;
+  return row_lane<(STEP % SPR) * NS + n>(r[STEP / SPR]);
+}
+template <int I> using Int = std::integral_constant<int, I>;
+template <int FROM, int TO, typename F> DEV void for_up(F&& f) {
+  if constexpr (FROM < TO) {
+    f(Int<FROM>{});
+    for_up<FROM + 1, TO>(f);
+  }
+}
+
+// What the threads of a workgroup load of a tile: wave w the steps w, w + WV, ... of its lanes' channels, and each thread
+// some of B and C.
+template <typename T, int NS, int WV> struct Tile {
+  static constexpr int E = CT / WV;                            // steps of a wave
+  static constexpr int NP = NS * WV, TH = WV * WAVE;
+  static constexpr int BC = (CT * NP + TH - 1) / TH;           // values of B and of C of a thread
+};
+template <typename T, int E>
+DEV void load_plane(const void* plane, const int64_t (&s)[2], int64_t b, int32_t t0, int32_t T_, int wave, int wv, int32_t d, bool in,
+                    int lane, T (&v)[E]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int32_t t = t0 + wave + i * wv;
+    v[i] = T{};
+    if (t < T_ && in) v[i] = row_of<T>(plane, s, b, t, d)[lane];
+  }
+}
+template <typename T, int NS, int WV>
+DEV void load_shared(const void* plane, const int64_t (&s)[3], const SsmArgs& p, const Where& w, int32_t t0,
+                     T (&v)[Tile<T, NS, WV>::BC]) {
+  using L = Tile<T, NS, WV>;
+#pragma unroll
+  for (int i = 0; i < L::BC; ++i) {
+    const int k = threadIdx.x + i * L::TH, t = k / L::NP, n = k - t * L::NP;
+    v[i] = T{};
+    if (t < CT && t0 + t < p.T && n < p.N)
+      v[i] = static_cast<const T*>(plane)[w.b * s[0] + static_cast<int64_t>(t0 + t) * s[1] + w.g * s[2] + n];
+  }
+}
+template <typename T, int NS, int WV>
+DEV void put_shared(float* to, const T (&v)[Tile<T, NS, WV>::BC]) {
+  using L = Tile<T, NS, WV>;
+#pragma unroll
+  for (int i = 0; i < L::BC; ++i) {
+    const int k = threadIdx.x + i * L::TH;
+    if (k < CT * L::NP) to[k] = to_f32(v[i]);
+  }
+}
+// a wave's B or C of a tile, from [CT][NP] in shared memory: register r holds the steps r 16/NS and on
+template <int NS, int NP> DEV void get_shared(const float* from, int wave, int lane, float (&r)[NS]) {
+  constexpr int SPR = 16 / NS;
+#pragma unroll
+  for (int k = 0; k < NS; ++k) r[k] = from[(k * SPR + (lane & 15) / NS) * NP + wave * NS + (lane & 15) % NS];
+}
+
+// a wave's states of one channel, [n][D] (segments, carry) or [d][N] (h0, h_last)
+template <int NS> DEV void load_nd(const float* p, int64_t D, int32_t N, int n0, bool in, float (&v)[NS]) {
+#pragma unroll
+  for (int n = 0; n < NS; ++n) v[n] = in && n0 + n < N ? p[static_cast<int64_t>(n0 + n) * D] : 0.0f;
+}
+template <int NS> DEV void store_nd(float* p, int64_t D, int32_t N, int n0, bool in, const float (&v)[NS]) {
+#pragma unroll
+  for (int n = 0; n < NS; ++n)
+    if (in && n0 + n < N) p[static_cast<int64_t>(n0 + n) * D] = v[n];
+}
+template <int NS> DEV void load_dn(const float* p, int32_t N, int n0, bool in, float (&v)[NS]) {
+#pragma unroll
+  for (int n = 0; n < NS; ++n) v[n] = in && p && n0 + n < N ? p[n0 + n] : 0.0f;
+}
+template <int NS> DEV void store_dn(float* p, int32_t N, int n0, bool in, const float (&v)[NS]) {
+#pragma unroll
+  for (int n = 0; n < NS; ++n)
+    if (in && n0 + n < N) p[n0 + n] = v[n];
+}
+
+// The steps of a tile at which a sequence begins, as bits (uniform)
+DEV uint32_t starts_of(const Seqs& q, int32_t t0, int32_t T) {
+  uint32_t m = t0 == 0 ? 1u : 0u;
+  if (q.cu) {
+    // the boundaries from the first at or after t0 on
+    int64_t j = t0 == 0 ? 1 : q.of(t0 - 1) + 1;
+    const int32_t end = t0 + CT < T ? t0 + CT : T;
+    for (; j < q.n; ++j) {
+      const int64_t t = q.cu[j];
+      if (t >= end) break;
+      if (t >= t0) m |= 1u << (t - t0);
+    }
+  }
+  return __builtin_amdgcn_readfirstlane(m);
+}
+// Whether step t begins a sequence (t < T), or nothing follows (t = T)
+DEV bool boundary(const Seqs& q, int32_t t, int32_t T) {
+  if (t <= 0 || t >= T) return true;
+  if (!q.cu) return false;
+  return q.begin(q.of(t)) == t && q.of(t) > 0;
+}
+
+template <int NS> DEV float decay_to(float A2, float dt) { return hw_exp2(A2 * dt); }
+
+// ENDS: what each segment but the last leaves (from its last sequence's start, if one begins in it).  Otherwise the walk itself.
+template <typename T, int NS, int WV, bool ENDS>
+__global__ __launch_bounds__(WV * WAVE) void k_ssm(const SsmArgs p) {
+  using L = Tile<T, NS, WV>;
+  constexpr int E = L::E, NP = L::NP;
+  __shared__ float2 u[CT][CH];
+  __shared__ float sb[CT * NP], sc[CT * NP];
+  __shared__ float part[ENDS ? 1 : WV][CT][CH];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Where w = where(p);
+  const bool in = lane < w.left;
+  const int32_t d = w.d + lane;
+  const int n0 = wave * NS;
+  const int64_t own = static_cast<int64_t>(d) * p.N;            // [d][N]
+  const int64_t seq_step = p.D * p.N;                           // of h0 and h_last
+  const int64_t row_states = w.b * p.seqs.n * seq_step + own;
+  int32_t first = w.s * p.per, last = first + p.per < p.tiles ? first + p.per : p.tiles;   // tiles
+
+  float A2[NS], h[NS] = {};
+  load_dn<NS>(p.A + own, p.N, n0, in, A2);
+#pragma unroll
+  for (int n = 0; n < NS; ++n) A2[n] *= kLog2e;
+  const float bias = in && p.dt_bias ? p.dt_bias[d] : 0.0f, skip = in && p.skip ? p.skip[d] : 0.0f;
+
+  float sum = 0.0f;
+  const int32_t ta = first * CT, tb = last * CT < p.T ? last * CT : p.T;
+  int32_t begin = 0;            // ENDS: the segment's last start
+  if constexpr (ENDS) {
+    begin = p.seqs.cu ? static_cast<int32_t>(p.seqs.begin(p.seqs.of(tb - 1))) : 0;
+    if (begin > ta) first = begin / CT;
+  } else if (w.s > 0 && !boundary(p.seqs, ta, p.T)) {
+    // the state entering: from the segment in which its sequence begins, over those between
+    const int32_t from = p.seqs.cu ? static_cast<int32_t>(p.seqs.begin(p.seqs.of(ta))) : 0;
+    int32_t s = from / (p.per * CT);
+    const float* end = p.end + (s * p.B + w.b) * seq_step + d;
+    load_nd<NS>(end, p.D, p.N, n0, in, h);
+    for (++s; s < w.s; ++s) {
+      float e[NS];
+      load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, e);
+      const float total = in ? p.sum[(s * p.B + w.b) * p.D + d] : 0.0f;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) h[n] = fmaf(hw_exp2(A2[n] * total), h[n], e[n]);
+    }
+  }
+  // the last sequence that begins in this segment: later segments' workgroups write over its h0 where that is h_last's place
+  const int64_t last_seq = p.in_place && p.S > 1 ? p.seqs.of(tb - 1) : -1;
+
+  T x[E], dl[E], z[E], vb[L::BC], vc[L::BC];
+  const auto load = [&](int32_t t0) {
+    load_plane<T, E>(p.x, p.sx, w.b, t0, p.T, wave, WV, w.d, in, lane, x);
+    load_plane<T, E>(p.delta, p.sdelta, w.b, t0, p.T, wave, WV, w.d, in, lane, dl);
+    load_shared<T, NS, WV>(p.b, p.sb, p, w, t0, vb);
+    if constexpr (!ENDS) {
+      if (p.z) load_plane<T, E>(p.z, p.sz, w.b, t0, p.T, wave, WV, w.d, in, lane, z);
+      load_shared<T, NS, WV>(p.c, p.sc, p, w, t0, vc);
+    }
+  };
+  load(first * CT);
+
+  for (int32_t tile = first; tile < last; ++tile) {
+    const int32_t t0 = tile * CT;
+    const int32_t steps = p.T - t0 < CT ? p.T - t0 : CT;
+    float xf[E], zf[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int t = wave + i * WV;
+      xf[i] = to_f32(x[i]);
+      if constexpr (!ENDS) zf[i] = to_f32(z[i]);
+      const float dt = t < steps ? softplus(to_f32(dl[i]) + bias) : 0.0f;
+      u[t][lane] = make_float2(dt, t < steps ? dt * xf[i] : 0.0f);
+    }
+    put_shared<T, NS, WV>(sb, vb);
+    if constexpr (!ENDS) put_shared<T, NS, WV>(sc, vc);
+    __syncthreads();
+    if (tile + 1 < last) load((tile + 1) * CT);
+
+    if constexpr (!ENDS) {
+      if (p.carry) store_nd<NS>(p.carry + (w.b * p.tiles + tile) * seq_step + d, p.D, p.N, n0, in, h);
+    }
+    const uint32_t starts = starts_of(p.seqs, t0, p.T);
+    float rb[NS], rc[NS];
+    get_shared<NS, NP>(sb, wave, lane, rb);
+    if constexpr (!ENDS) get_shared<NS, NP>(sc, wave, lane, rc);
+    for_up<0, CT / 4>([&](auto quarter) {
+      constexpr int Q = quarter * 4;
+      if (Q < steps) {
+        for_up<Q, Q + 4>([&](auto step) {
+          constexpr int t = step;
+          if (starts >> t & 1) {
+            if constexpr (ENDS) {
+              if (t0 + t == begin) {
+                const int64_t j = p.seqs.cu ? p.seqs.of(begin) : 0;
+                load_dn<NS>(p.h0 ? p.h0 + row_states + j * seq_step : nullptr, p.N, n0, in, h);
+                if (p.head) store_nd<NS>(p.head + (w.s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, h);
+                sum = 0.0f;
+              }
+            } else {
+              const int64_t j = p.seqs.cu ? p.seqs.of(t0 + t) : 0;
+              if (t0 + t > ta && p.h_last)
+                store_dn<NS>(p.h_last + row_states + p.seqs.of(t0 + t - 1) * seq_step, p.N, n0, in, h);
+              if (j == last_seq && w.s + 1 < p.S)
+                load_nd<NS>(p.head + (w.s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, h);
+              else
+                load_dn<NS>(p.h0 ? p.h0 + row_states + j * seq_step : nullptr, p.N, n0, in, h);
+            }
+          }
+          const float2 v = u[t][lane];
+          if constexpr (ENDS) sum += v.x;
+          float y = 0.0f;
+          for_up<0, NS>([&](auto state) {
+            constexpr int n = state;
+            const float a = hw_exp2(A2[n] * v.x);
+            h[n] = fmaf(a, h[n], of_step<NS, t, n>(rb) * v.y);
+            if constexpr (!ENDS) y = fmaf(of_step<NS, t, n>(rc), h[n], y);
+          });
+          if constexpr (!ENDS) part[wave][t][lane] = y;
+        });
+      }
+    });
+    __syncthreads();
+    if constexpr (!ENDS) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int t = wave + i * WV;
+        float y = skip * xf[i];
+#pragma unroll
+        for (int k = 0; k < WV; ++k) y += part[k][t][lane];
+        if (p.z) y *= silu(zf[i]);
+        if (t < steps && in) const_cast<T*>(row_of<T>(p.y, p.sy, w.b, t0 + t, w.d))[lane] = from_f32<T>(y);
+      }
+    }
+  }
+  if constexpr (ENDS) {
+    store_nd<NS>(p.end + (w.s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, h);
+    if (wave == 0 && in) p.sum[(w.s * p.B + w.b) * p.D + d] = sum;
+  } else if (p.h_last) {
+    // the sequence that ends with the segment, and with the row those that have no steps
+    if (boundary(p.seqs, tb, p.T)) store_dn<NS>(p.h_last + row_states + p.seqs.of(tb - 1) * seq_step, p.N, n0, in, h);
+    if (tb == p.T && p.seqs.cu && !p.in_place) {
+      for (int64_t j0 = 0; j0 < p.seqs.n; j0 += WAVE) {
+        const int64_t j = j0 + lane;
+        uint64_t empty = __builtin_amdgcn_ballot_w64(j < p.seqs.n && p.seqs.end(j) <= p.seqs.begin(j));
+        for (; empty; empty &= empty - 1) {
+          const int64_t at = (j0 + __builtin_ctzll(empty)) * seq_step;
+          float v[NS];
+          load_dn<NS>(p.h0 ? p.h0 + row_states + at : nullptr, p.N, n0, in, v);
+          store_dn<NS>(p.h_last + row_states + at, p.N, n0, in, v);
+        }
+      }
+    }
+  }
+}
+
+// no steps: every state leaves as it came (rest: where d_last becomes d_h0)
+__global__ __launch_bounds__(256) void k_copy_states(const float* from, float* to, int64_t n) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) to[i] = from ? from[i] : 0.0f;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Gradients.  With G_t = dL/dy_t z sig(z) (G = dL/dy without a gate), q_t = dL/dh_t = C_t G_t + P_t, P_{t-1} = a_t q_t (plus d_last
+// at a sequence's last step) and e_t = P_{t-1} h_{t-1}:
+//   d(dt x) = sum_n q B,  d(dt) += sum_n e A,  d_A = sum_t e dt,  d_B = sum_d q dt x,  d_C = sum_d G h.
+// A tile's states are rebuilt from the carry and stay, with their decays, in registers; the way back walks them in reverse.  The
+// sums over states go through shared memory as y's do.  Those over channels are formed for 32 values at a time (two for
+// each step and state): halves, rows, half rows and quads of the wave are folded onto each other, each time leaving half the
+// registers, so a value costs two instructions and not six.  Each channel tile's sums go to the workspace, and one launch more
+// adds them up.  Segments as in the forward pass, from the right.
+// ------------------------------------------------------------------------------------------------
+template <int TO, int FROM, typename F> DEV void for_down(F&& f) {   // FROM - 1 .. TO
+  if constexpr (FROM > TO) {
+    f(Int<FROM - 1>{});
+    for_down<TO, FROM - 1>(f);
+  }
+}
+
+// Sums over the wave's lanes of 32 values; lane l gets that of value 16 l5 + 8 l4 + 4 l3 + 2 l2 + l0 (l5: bit 5 of l)
+DEV float fold(float (&v)[32], int lane) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 16]), false, false);
+    v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 8]), false, false);
+    v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = v[i] + dpp<0x128>(v[i]), b = v[i + 4] + dpp<0x128>(v[i + 4]);   // row_ror:8
+    v[i] = lane & 8 ? b : a;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float a = v[i] + dpp<0x141>(v[i]), b = v[i + 2] + dpp<0x141>(v[i + 2]);   // row_half_mirror
+    v[i] = lane & 4 ? b : a;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[i] += dpp<0xb1>(v[i]);
+    v[i] += dpp<0x4e>(v[i]);
+  }
+  return lane & 1 ? v[1] : v[0];
+}
+
+// What flows out of each segment but the first to the steps before it, if nothing enters it from the right, and the sum of dt over
+// the steps that it flows through
+template <typename T, int NS, int WV>
+__global__ __launch_bounds__(WV * WAVE) void k_ssm_back_ends(const SsmGradArgs g) {
+  const SsmArgs& p = g.f;
+  using L = Tile<T, NS, WV>;
+  constexpr int E = L::E, NP = L::NP;
+  __shared__ float2 u[CT][CH];
+  __shared__ float sc[CT * NP];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Where w = where(p);
+  ++w.s;
+  const bool in = lane < w.left;
+  const int32_t d = w.d + lane;
+  const int n0 = wave * NS;
+  const int64_t seq_step = p.D * p.N, own = static_cast<int64_t>(d) * p.N;
+  const int32_t first = w.s * p.per, last = first + p.per < p.tiles ? first + p.per : p.tiles;
+  const int32_t ta = first * CT, tb = last * CT < p.T ? last * CT : p.T;
+  // the steps [ta, end) of the sequence that ta belongs to
+  const int64_t j = p.seqs.cu ? p.seqs.of(ta) : 0;
+  int32_t stop = static_cast<int32_t>(p.seqs.end(j));
+  stop = stop > ta ? stop : ta + 1;
+  const int32_t end = stop < tb ? stop : tb;
+
+  float A2[NS], P[NS] = {}, sum = 0.0f;
+  load_dn<NS>(p.A + own, p.N, n0, in, A2);
+#pragma unroll
+  for (int n = 0; n < NS; ++n) A2[n] *= kLog2e;
+  const float bias = in && p.dt_bias ? p.dt_bias[d] : 0.0f;
+  if (stop <= tb) load_dn<NS>(g.d_last ? g.d_last + (w.b * p.seqs.n + j) * seq_step + own : nullptr, p.N, n0, in, P);
+
+  T dl[E], z[E], dy[E], vc[L::BC];
+  const auto load = [&](int32_t t0) {
+    load_plane<T, E>(p.delta, p.sdelta, w.b, t0, end, wave, WV, w.d, in, lane, dl);
+    load_plane<T, E>(g.dy, g.sdy, w.b, t0, end, wave, WV, w.d, in, lane, dy);
+    if (p.z) load_plane<T, E>(p.z, p.sz, w.b, t0, end, wave, WV, w.d, in, lane, z);
+    load_shared<T, NS, WV>(p.c, p.sc, p, w, t0, vc);
+  };
+  int32_t tile = (end - 1) / CT;
+  load(tile * CT);
+  for (; tile >= first; --tile) {
+    const int32_t t0 = tile * CT, steps = end - t0 < CT ? end - t0 : CT;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int t = wave + i * WV;
+      float G = to_f32(dy[i]);
+      if (p.z) G *= silu(to_f32(z[i]));
+      u[t][lane] = t < steps ? make_float2(softplus(to_f32(dl[i]) + bias), G) : make_float2(0.0f, 0.0f);
+    }
+    put_shared<T, NS, WV>(sc, vc);
+    __syncthreads();
+    if (tile > first) load(t0 - CT);
+    float rc[NS];
+    get_shared<NS, NP>(sc, wave, lane, rc);
+    for_down<0, CT / 4>([&](auto quarter) {
+      constexpr int Q = quarter * 4;
+      if (Q < steps) {
+        for_down<Q, Q + 4>([&](auto step) {
+          constexpr int t = step;
+          const float2 v = u[t][lane];
+          sum += v.x;
+          for_up<0, NS>([&](auto state) {
+            constexpr int n = state;
+            P[n] = hw_exp2(A2[n] * v.x) * fmaf(of_step<NS, t, n>(rc), v.y, P[n]);
+          });
+        });
+      }
+    });
+    __syncthreads();
+  }
+  store_nd<NS>(p.end + (w.s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, P);
+  if (wave == 0 && in) p.sum[(w.s * p.B + w.b) * p.D + d] = sum;
+}
+
+template <typename T, int NS, int WV>
+__global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) {
+  const SsmArgs& p = g.f;
+  using L = Tile<T, NS, WV>;
+  constexpr int E = L::E, NP = L::NP, RS = 16 / NS;
+  __shared__ float2 u[CT][CH];
+  __shared__ float sg[CT][CH];
+  __shared__ float sb[CT * NP], sc[CT * NP];
+  __shared__ float part[3][WV][CT][CH];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Where w = where(p);
+  const bool in = lane < w.left;
+  const int32_t d = w.d + lane;
+  const int n0 = wave * NS;
+  const int64_t seq_step = p.D * p.N, own = static_cast<int64_t>(d) * p.N;
+  const int64_t row_states = w.b * p.seqs.n * seq_step + own;
+  const int32_t first = w.s * p.per, last = first + p.per < p.tiles ? first + p.per : p.tiles;
+  const int32_t tb = last * CT < p.T ? last * CT : p.T;
+
+  float A[NS], P[NS] = {}, dA[NS] = {}, d_skip = 0.0f, d_bias = 0.0f;
+  load_dn<NS>(p.A + own, p.N, n0, in, A);
+  const float bias = in && p.dt_bias ? p.dt_bias[d] : 0.0f, skip = in && p.skip ? p.skip[d] : 0.0f;
+  if (!boundary(p.seqs, tb, p.T)) {
+    // what enters from the right: from the segment that the sequence ends in, over those between
+    int32_t stop = p.seqs.cu ? static_cast<int32_t>(p.seqs.end(p.seqs.of(tb))) : p.T;
+    stop = stop > tb ? stop : tb + 1;
+    int32_t s = (stop - 1) / (p.per * CT);
+    load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, P);
+    for (--s; s > w.s; --s) {
+      float e[NS];
+      load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, e);
+      const float total = in ? p.sum[(s * p.B + w.b) * p.D + d] : 0.0f;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) P[n] = fmaf(hw_exp2(A[n] * kLog2e * total), P[n], e[n]);
+    }
+  }
+
+  T x[E], dl[E], z[E], dy[E], vb[L::BC], vc[L::BC];
+  float h_in[NS];
+  const auto load = [&](int32_t tile) {
+    const int32_t t0 = tile * CT;
+    load_plane<T, E>(p.x, p.sx, w.b, t0, p.T, wave, WV, w.d, in, lane, x);
+    load_plane<T, E>(p.delta, p.sdelta, w.b, t0, p.T, wave, WV, w.d, in, lane, dl);
+    load_plane<T, E>(g.dy, g.sdy, w.b, t0, p.T, wave, WV, w.d, in, lane, dy);
+    if (p.z) load_plane<T, E>(p.z, p.sz, w.b, t0, p.T, wave, WV, w.d, in, lane, z);
+    load_shared<T, NS, WV>(p.b, p.sb, p, w, t0, vb);
+    load_shared<T, NS, WV>(p.c, p.sc, p, w, t0, vc);
+    load_nd<NS>(g.carry + (w.b * p.tiles + tile) * seq_step + d, p.D, p.N, n0, in, h_in);
+  };
+  load(last - 1);
+
+  for (int32_t tile = last - 1; tile >= first; --tile) {
+    const int32_t t0 = tile * CT, steps = p.T - t0 < CT ? p.T - t0 : CT;
+    float xf[E], zf[E], dyf[E], open[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int t = wave + i * WV;
+      xf[i] = to_f32(x[i]);
+      zf[i] = p.z ? to_f32(z[i]) : 0.0f;
+      dyf[i] = to_f32(dy[i]);
+      const float raw = to_f32(dl[i]) + bias, dt = t < steps ? softplus(raw) : 0.0f;
+      open[i] = sigmoid(raw);
+      u[t][lane] = make_float2(dt, t < steps ? dt * xf[i] : 0.0f);
+      sg[t][lane] = t < steps ? dyf[i] * (p.z ? silu(zf[i]) : 1.0f) : 0.0f;
+    }
+    put_shared<T, NS, WV>(sb, vb);
+    put_shared<T, NS, WV>(sc, vc);
+    float h0[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h0[n] = h_in[n];
+    __syncthreads();
+    if (tile > first) load(tile - 1);
+
+    const uint32_t starts = starts_of(p.seqs, t0, p.T);
+    const uint32_t ends = starts >> 1 | (boundary(p.seqs, t0 + steps, p.T) ? 1u << (steps - 1) : 0u);
+    const auto entering = [&](int32_t t, float (&v)[NS]) {      // the state entering the sequence that begins at step t
+      const int64_t j = p.seqs.cu ? p.seqs.of(t) : 0;
+      load_dn<NS>(p.h0 ? p.h0 + row_states + j * seq_step : nullptr, p.N, n0, in, v);
+    };
+    float rb[NS], rc[NS], hs[CT][NS], as[CT][NS];
+    get_shared<NS, NP>(sb, wave, lane, rb);
+    get_shared<NS, NP>(sc, wave, lane, rc);
+    for_up<0, CT / 4>([&](auto quarter) {
+      constexpr int Q = quarter * 4;
+      if (Q < steps) {
+        for_up<Q, Q + 4>([&](auto step) {
+          constexpr int t = step;
+          float h[NS], y = 0.0f;
+#pragma unroll
+          for (int n = 0; n < NS; ++n) h[n] = t == 0 ? h0[n] : hs[t - 1 < 0 ? 0 : t - 1][n];
+          if (starts >> t & 1) entering(t0 + t, h);
+          const float2 v = u[t][lane];
+          for_up<0, NS>([&](auto state) {
+            constexpr int n = state;
+            as[t][n] = hw_exp2(A[n] * kLog2e * v.x);
+            hs[t][n] = fmaf(as[t][n], h[n], of_step<NS, t, n>(rb) * v.y);
+            y = fmaf(of_step<NS, t, n>(rc), hs[t][n], y);
+          });
+          part[0][wave][t][lane] = y;
+        });
+      }
+    });
+    float tA[NS] = {};
+    for_down<0, CT / RS>([&](auto block) {
+      constexpr int Q = block * RS;
+      if (Q < steps) {
+        float v32[32];
+        for_down<Q, Q + RS>([&](auto step) {
+          constexpr int t = step;
+          if (NS > 1 || t < steps) {
+            if (ends >> t & 1) {
+              const int64_t j = p.seqs.cu ? p.seqs.of(t0 + t) : 0;
+              load_dn<NS>(g.d_last ? g.d_last + row_states + j * seq_step : nullptr, p.N, n0, in, P);
+            }
+            const float2 v = u[t][lane];
+            const float G = sg[t][lane];
+            float h[NS], s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NS; ++n) h[n] = t == 0 ? h0[n] : hs[t - 1 < 0 ? 0 : t - 1][n];
+            if (starts >> t & 1) entering(t0 + t, h);
+            for_up<0, NS>([&](auto state) {
+              constexpr int n = state;
+              const float q = fmaf(of_step<NS, t, n>(rc), G, P[n]);
+              s1 = fmaf(of_step<NS, t, n>(rb), q, s1);
+              v32[(t - Q) * NS + n] = q * v.y;
+              v32[16 + (t - Q) * NS + n] = G * hs[t][n];
+              P[n] = as[t][n] * q;
+              const float e = P[n] * h[n];
+              s2 = fmaf(e, A[n], s2);
+              tA[n] = fmaf(e, v.x, tA[n]);
+            });
+            part[1][wave][t][lane] = s1;
+            part[2][wave][t][lane] = s2;
+            if (starts >> t & 1) {
+              const int64_t j = p.seqs.cu ? p.seqs.of(t0 + t) : 0;
+              if (g.d_h0) store_dn<NS>(g.d_h0 + row_states + j * seq_step, p.N, n0, in, P);
+            }
+          } else {
+            v32[(t - Q) * NS] = v32[16 + (t - Q) * NS] = 0.0f;
+          }
+        });
+        const float sum = fold(v32, lane);
+        const int k = (lane & 1) | (lane >> 1 & 14), t = Q + k / NS, n = n0 + k % NS;
+        if (!(lane & 2) && t < steps && n < p.N)
+          g.part_bc[((static_cast<int64_t>(w.ct) * p.B + w.b) * p.T + t0 + t) * (2 * p.N) + (lane >> 5) * p.N + n] = sum;
+      }
+    });
+#pragma unroll
+    for (int n = 0; n < NS; ++n) dA[n] += tA[n];
+    __syncthreads();
+    float tskip = 0.0f, tbias = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int t = wave + i * WV;
+      if (t < steps) {
+      float y = skip * xf[i], s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+      for (int k = 0; k < WV; ++k) {
+        y += part[0][k][t][lane];
+        s1 += part[1][k][t][lane];
+        s2 += part[2][k][t][lane];
+      }
+      const float dt = u[t][lane].x, G = sg[t][lane];
+      const float dd = fmaf(s1, xf[i], s2) * open[i];
+      tskip = fmaf(G, xf[i], tskip);
+      tbias += dd;
+      if (in) {
+        const_cast<T*>(row_of<T>(g.dx, g.sdx, w.b, t0 + t, w.d))[lane] = from_f32<T>(fmaf(s1, dt, G * skip));
+        const_cast<T*>(row_of<T>(g.ddelta, g.sddelta, w.b, t0 + t, w.d))[lane] = from_f32<T>(dd);
+        if (p.z)
+          const_cast<T*>(row_of<T>(g.dz, g.sdz, w.b, t0 + t, w.d))[lane] =
+              from_f32<T>(dyf[i] * y * silu_slope(zf[i], sigmoid(zf[i])));
+      }
+      }
+    }
+    d_skip += tskip;
+    d_bias += tbias;
+    __syncthreads();            // u and sg are read above
+  }
+
+  // parameters: [S B][N + 2][D]
+  const int64_t row = (w.s * p.B + w.b) * static_cast<int64_t>(p.N + 2) * p.D + d;
+  store_nd<NS>(g.part_A + row, p.D, p.N, n0, in, dA);
+  part[0][wave][0][lane] = d_skip;
+  part[0][wave][1][lane] = d_bias;
+  __syncthreads();
+  if (wave == 0 && in) {
+    float s = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int k = 0; k < WV; ++k) {
+      s += part[0][k][0][lane];
+      b += part[0][k][1][lane];
+    }
+    g.part_A[row + p.N * p.D] = s;
+    g.part_A[row + (p.N + 1) * p.D] = b;
+  }
+}
+
+// d_b and d_c: a thread adds up the channel tiles' sums of one group for one value
+struct SharedArgs {
+  const float* part;
+  int64_t B, T;
+  int32_t N, G, ctiles;
+  void *db, *dc;
+  int64_t sdb[3], sdc[3];
+};
+template <typename T> __global__ __launch_bounds__(256) void k_ssm_shared(const SharedArgs p) {
+  const int64_t plane = p.B * p.T * (2 * p.N), id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (id >= plane * p.G) return;
+  const int64_t g = id / plane, e = id - g * plane, row = e / (2 * p.N), b = row / p.T, t = row - b * p.T;
+  const int32_t k = static_cast<int32_t>(e - row * (2 * p.N));
+  const float* from = p.part + g * p.ctiles * plane + e;
+  float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+  int32_t c = 0;
+  for (; c + 4 <= p.ctiles; c += 4, from += 4 * plane) {
+    s0 += from[0];
+    s1 += from[plane];
+    s2 += from[2 * plane];
+    s3 += from[3 * plane];
+  }
+  for (; c < p.ctiles; ++c, from += plane) s0 += *from;
+  const float s = (s0 + s1) + (s2 + s3);
+  if (k < p.N) static_cast<T*>(p.db)[b * p.sdb[0] + t * p.sdb[1] + g * p.sdb[2] + k] = from_f32<T>(s);
+  else static_cast<T*>(p.dc)[b * p.sdc[0] + t * p.sdc[1] + g * p.sdc[2] + k - p.N] = from_f32<T>(s);
+}
+// the column sums [N + 2][D] as d_A [D][N], d_skip and d_dt_bias [D]
+__global__ __launch_bounds__(256) void k_ssm_params(const float* sums, int64_t D, int32_t N, float* d_A, float* d_skip,
+                                                    float* d_bias) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= D * (N + 2)) return;
+  const int64_t n = i / D, d = i - n * D;
+  float* to = n < N ? (d_A ? d_A + d * N + n : nullptr) : n == N ? (d_skip ? d_skip + d : nullptr) : (d_bias ? d_bias + d : nullptr);
+  if (to) *to = sums[i];
+}
+// d_h0 of sequences without steps
+__global__ __launch_bounds__(256) void k_ssm_empty(const Seqs q, int64_t states, int64_t n, const float* d_last, float* d_h0) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n) return;
+  const int64_t j = i / states % q.n;
+  if (q.end(j) <= q.begin(j)) d_h0[i] = d_last ? d_last[i] : 0.0f;
+}
+
+// ---------------- host ----------------
+struct Split {
+  int64_t ctiles, tiles, rows;   // channel tiles of a group, tiles of a row, workgroups without segments
+  int64_t S, per;
+};
+// Segments of a row: as many as bring `want` workgroups, each of at least `least` tiles
+static Split split(int64_t B, int64_t T, int64_t D, int64_t G, int64_t want, int64_t least) {
+  Split s;
+  s.ctiles = ceil_div(D / G, CH);
+  s.tiles = ceil_div(T, CT);
+  s.rows = B * G * s.ctiles;
+  int64_t n = 1;
+  if (s.rows && s.rows < want / 2) n = want / s.rows;
+  if (n > s.tiles / least) n = s.tiles / least;
+  if (n < 1) n = 1;
+  s.per = s.tiles ? ceil_div(s.tiles, n) : 1;
+  s.S = s.tiles ? ceil_div(s.tiles, s.per) : 1;
+  return s;
+}
+constexpr int64_t kWant = 2048, kGradWant = 1024, kLeast = 4;
+static Split forward_split(int64_t B, int64_t T, int64_t D, int64_t G) { return split(B, T, D, G, kWant, kLeast); }
+static Split gradient_split(int64_t B, int64_t T, int64_t D, int64_t G) { return split(B, T, D, G, kGradWant, kLeast); }
+
+static bool sizes_ok(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G) {
+  if (N < 1 || G < 1 || !sizes_fit(B, T, D) || (D > 0 && (G > D || D % G))) return false;
+  return sizes_fit(D, N + 2) && sizes_fit(B, ceil_div(T, CT) + 1, D) &&
+         (D == 0 || B == 0 || N + 2 <= INT64_MAX / 64 / (D * B) / (ceil_div(T, CT) + 1)) &&
+         (B == 0 || T == 0 || N <= INT64_MAX / 64 / B / T / (D / 64 + G + 1));
+}
+struct Room {   // floats: the segments' parts, then (gradient) the sums
+  int64_t end, sum, head, bc, part, scratch, sums;
+  int64_t total() const { return end + sum + head + bc + part + scratch + sums; }
+};
+static int64_t round64(int64_t n) { return ceil_div(n, 64) * 64; }
+static Room room(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool gradient) {
+  const Split s = gradient ? gradient_split(B, T, D, G) : forward_split(B, T, D, G);
+  Room r{};
+  if (s.S > 1) {
+    r.end = round64(s.S * B * N * D);
+    r.sum = round64(s.S * B * D);
+    if (!gradient) r.head = r.end;
+  }
+  if (gradient) {
+    const int64_t rows = T ? s.S * B : 0;
+    r.bc = round64(G * s.ctiles * B * T * 2 * N);
+    r.part = round64(rows * (N + 2) * D);
+    r.scratch = round64(colsum_floats(rows, (N + 2) * D));
+    r.sums = round64((N + 2) * D);
+  }
+  return r;
+}
+
+static bool problem_ok(const pararnn_block_ssm* q) {
+  if (!q || !dtype_ok(q->dtype) || !sizes_ok(q->B, q->T, q->D, q->N, q->G)) return false;
+  const size_t e = dtype_size(q->dtype);
+  const bool any = q->B > 0 && q->D > 0, steps = any && q->T > 0;
+  if (!ptr_ok(q->x, e, steps) || !ptr_ok(q->delta, e, steps) || !ptr_ok(q->z, e, false) || !ptr_ok(q->b, e, steps) ||
+      !ptr_ok(q->c, e, steps) || !ptr_ok(q->A, 4, any) || !ptr_ok(q->skip, 4, false) || !ptr_ok(q->dt_bias, 4, false) ||
+      !ptr_ok(q->h0, 4, false) || !ptr_ok(q->cu_seqlens, 4, false))
+    return false;
+  if (q->cu_seqlens) {
+    if (q->n_seqs < 1 || q->T > INT32_MAX || !sizes_fit(q->B, q->n_seqs, q->D)) return false;
+    if (any && q->N > INT64_MAX / 16 / (q->B * q->n_seqs * q->D)) return false;
+  }
+  const int64_t(*s2[3])[2] = {&q->sx, &q->sdelta, &q->sz};
+  for (int k = 0; k < (q->z ? 3 : 2); ++k)
+    if (!plane_ok(q->B, (*s2[k])[0]) || !plane_ok(q->T, (*s2[k])[1])) return false;
+  const int64_t(*s3[2])[3] = {&q->sb, &q->sc};
+  for (const auto* s : s3)
+    if (!plane_ok(q->B, (*s)[0]) || !plane_ok(q->T, (*s)[1]) || !plane_ok(q->G, (*s)[2])) return false;
+  return true;
+}
+static bool supported(const pararnn_block_ssm* q, const Split& s, int threads) {
+  if (q->N > PARARNN_BLOCK_MAX_STATES || q->T > INT32_MAX - CT || q->D > INT32_MAX / 64) return false;
+  if (s.ctiles * q->G > INT32_MAX || q->B > INT32_MAX) return false;
+  return s.rows == 0 || (s.S <= INT64_C(0xffffffff) / s.rows && grid_ok(s.rows * s.S, threads));
+}
+static SsmArgs ssm_args(const pararnn_block_ssm* q, const Split& s) {
+  SsmArgs p{};
+  p.x = q->x, p.delta = q->delta, p.z = q->z, p.b = q->b, p.c = q->c;
+  for (int k = 0; k < 2; ++k) p.sx[k] = q->sx[k], p.sdelta[k] = q->sdelta[k], p.sz[k] = q->sz[k];
+  for (int k = 0; k < 3; ++k) p.sb[k] = q->sb[k], p.sc[k] = q->sc[k];
+  p.A = q->A, p.skip = q->skip, p.dt_bias = q->dt_bias, p.h0 = q->h0;
+  p.seqs = {q->cu_seqlens, q->cu_seqlens ? q->n_seqs : 1, q->T};
+  p.B = q->B, p.D = q->D;
+  p.T = static_cast<int32_t>(q->T), p.N = static_cast<int32_t>(q->N), p.G = static_cast<int32_t>(q->G);
+  p.tiles = static_cast<int32_t>(s.tiles);
+  p.ctiles = static_cast<int32_t>(s.ctiles), p.group = static_cast<int32_t>(q->D / q->G);
+  p.S = static_cast<int32_t>(s.S), p.per = static_cast<int32_t>(s.per);
+  return p;
+}
+
+template <typename T, int NS, int WV> struct Forward {
+  static pararnn_status run(const SsmArgs& p, const Split& s, hipStream_t st) {
+    if (s.S > 1)
+      k_ssm<T, NS, WV, true><<<dim3(static_cast<uint32_t>(s.rows * (s.S - 1))), dim3(WV * WAVE), 0, st>>>(p);
+    k_ssm<T, NS, WV, false><<<dim3(static_cast<uint32_t>(s.rows * s.S)), dim3(WV * WAVE), 0, st>>>(p);
+    return launched();
+  }
+};
+template <typename T, int NS, int WV> struct Backward {
+  static pararnn_status run(const SsmGradArgs& g, const Split& s, hipStream_t st) {
+    if (s.S > 1) k_ssm_back_ends<T, NS, WV><<<dim3(static_cast<uint32_t>(s.rows * (s.S - 1))), dim3(WV * WAVE), 0, st>>>(g);
+    k_ssm_back<T, NS, WV><<<dim3(static_cast<uint32_t>(s.rows * s.S)), dim3(WV * WAVE), 0, st>>>(g);
+    return launched();
+  }
+};
+// waves of a workgroup for N states: four states a wave
+static int waves_of(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
+template <template <typename, int, int> class F, typename T, typename A>
+static pararnn_status by_states(int64_t N, const A& a, const Split& s, hipStream_t st) {
+  if (N == 1) return F<T, 1, 1>::run(a, s, st);
+  switch (waves_of(N)) {
+    case 1: return F<T, 4, 1>::run(a, s, st);
+    case 2: return F<T, 4, 2>::run(a, s, st);
+    case 4: return F<T, 4, 4>::run(a, s, st);
+    default: return F<T, 4, 8>::run(a, s, st);
+  }
+}
+
+}  // namespace lm
+
+using namespace lm;
+
+extern "C" int64_t pararnn_block_ssm_chunks(int64_t T) { return T < 0 ? 0 : ceil_div(T, CT); }
+
+extern "C" size_t pararnn_block_ssm_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, int gradient) {
+  if (!sizes_ok(B, T, D, N, G) || N > PARARNN_BLOCK_MAX_STATES) return 0;
+  return static_cast<size_t>(room(B, T, D, N, G, gradient != 0).total()) * sizeof(float);
+}
+
+extern "C" pararnn_status pararnn_block_selective_scan(const pararnn_block_ssm* q, void* y, const int64_t sy[2], float* h_last,
+                                                       float* carry, void* ws, size_t ws_bytes, void* stream) {
+  if (!problem_ok(q) || !sy || !plane_ok(q->B, sy[0]) || !plane_ok(q->T, sy[1])) return PARARNN_ERR_INVALID_ARG;
+  const bool any = q->B > 0 && q->D > 0;
+  if (!ptr_ok(y, dtype_size(q->dtype), any && q->T > 0) || !ptr_ok(h_last, 4, false) || !ptr_ok(carry, 4, false))
+    return PARARNN_ERR_INVALID_ARG;
+  const Split s = forward_split(q->B, q->T, q->D, q->G);
+  if (!supported(q, s, waves_of(q->N) * WAVE)) return PARARNN_ERR_UNSUPPORTED;
+  const Room r = room(q->B, q->T, q->D, q->N, q->G, false);
+  if (!ws_ok(ws, ws_bytes, static_cast<size_t>(r.total()) * sizeof(float))) return PARARNN_ERR_WORKSPACE;
+  if (!any) return PARARNN_OK;
+  const auto st = static_cast<hipStream_t>(stream);
+  SsmArgs p = ssm_args(q, s);
+  if (q->T == 0) {
+    const int64_t n = q->B * p.seqs.n * q->D * q->N;
+    if (!h_last || h_last == q->h0) return PARARNN_OK;
+    if (!grid_ok(ceil_div(n, 256), 256)) return PARARNN_ERR_UNSUPPORTED;
+    k_copy_states<<<dim3(static_cast<uint32_t>(ceil_div(n, 256))), dim3(256), 0, st>>>(q->h0, h_last, n);
+    return launched();
+  }
+  p.y = y;
+  p.sy[0] = sy[0], p.sy[1] = sy[1];
+  p.h_last = h_last, p.carry = carry;
+  p.in_place = h_last && h_last == q->h0;
+  float* f = static_cast<float*>(ws);
+  p.end = f, p.sum = f + r.end;
+  p.head = p.in_place ? f + r.end + r.sum : nullptr;
+  return q->dtype == PARARNN_BF16 ? by_states<Forward, bf16>(q->N, p, s, st) : by_states<Forward, float>(q->N, p, s, st);
+}
+
+extern "C" pararnn_status pararnn_block_selective_scan_vjp(const pararnn_block_ssm* q, const pararnn_block_ssm_grad* grad, void* ws,
+                                                           size_t ws_bytes, void* stream) {
+  if (!problem_ok(q) || !grad) return PARARNN_ERR_INVALID_ARG;
+  const size_t e = dtype_size(q->dtype);
+  const bool any = q->B > 0 && q->D > 0, steps = any && q->T > 0;
+  if (!ptr_ok(grad->carry, 4, steps) || !ptr_ok(grad->dy, e, steps) || !ptr_ok(grad->d_last, 4, false) ||
+      !ptr_ok(grad->d_x, e, steps) || !ptr_ok(grad->d_delta, e, steps) || !ptr_ok(grad->d_z, e, steps && q->z) ||
+      !ptr_ok(grad->d_b, e, steps) || !ptr_ok(grad->d_c, e, steps) || !ptr_ok(grad->d_A, 4, false) ||
+      !ptr_ok(grad->d_skip, 4, false) || !ptr_ok(grad->d_dt_bias, 4, false) || !ptr_ok(grad->d_h0, 4, false))
+    return PARARNN_ERR_INVALID_ARG;
+  const int64_t(*s2[4])[2] = {&grad->sdy, &grad->sdx, &grad->sddelta, &grad->sdz};
+  for (int k = 0; k < (q->z ? 4 : 3); ++k)
+    if (!plane_ok(q->B, (*s2[k])[0]) || !plane_ok(q->T, (*s2[k])[1])) return PARARNN_ERR_INVALID_ARG;
+  const int64_t(*s3[2])[3] = {&grad->sdb, &grad->sdc};
+  for (const auto* s : s3)
+    if (!plane_ok(q->B, (*s)[0]) || !plane_ok(q->T, (*s)[1]) || !plane_ok(q->G, (*s)[2])) return PARARNN_ERR_INVALID_ARG;
+
+  const Split s = gradient_split(q->B, q->T, q->D, q->G);
+  const int64_t values = q->B * q->T * q->G * 2 * q->N, cols = q->D * (q->N + 2);
+  if (!supported(q, s, waves_of(q->N) * WAVE) || !grid_ok(ceil_div(values, 256), 256) || !grid_ok(ceil_div(cols, 64), 256))
+    return PARARNN_ERR_UNSUPPORTED;
+  const Room r = room(q->B, q->T, q->D, q->N, q->G, true);
+  if (!ws_ok(ws, ws_bytes, static_cast<size_t>(r.total()) * sizeof(float))) return PARARNN_ERR_WORKSPACE;
+  if (q->D == 0) return PARARNN_OK;
+  const auto st = static_cast<hipStream_t>(stream);
+  SsmGradArgs g{};
+  g.f = ssm_args(q, s);
+  SsmArgs& p = g.f;
+  float* f = static_cast<float*>(ws);
+  p.end = f, p.sum = f + r.end;
+  f += r.end + r.sum;
+  g.part_bc = f;
+  f += r.bc;
+  g.part_A = f;
+  float *scratch = f + r.part, *sums = scratch + r.scratch;
+  g.carry = grad->carry, g.dy = grad->dy, g.d_last = grad->d_last, g.d_h0 = grad->d_h0;
+  g.dx = grad->d_x, g.ddelta = grad->d_delta, g.dz = grad->d_z;
+  for (int k = 0; k < 2; ++k)
+    g.sdy[k] = grad->sdy[k], g.sdx[k] = grad->sdx[k], g.sddelta[k] = grad->sddelta[k], g.sdz[k] = grad->sdz[k];
+  if (steps) {
+    const pararnn_status st1 = q->dtype == PARARNN_BF16 ? by_states<Backward, bf16>(q->N, g, s, st)
+                                                        : by_states<Backward, float>(q->N, g, s, st);
+    if (st1 != PARARNN_OK) return st1;
+    SharedArgs a{g.part_bc, q->B, q->T, p.N, p.G, p.ctiles, grad->d_b, grad->d_c, {}, {}};
+    for (int k = 0; k < 3; ++k) a.sdb[k] = grad->sdb[k], a.sdc[k] = grad->sdc[k];
+    const dim3 grid(static_cast<uint32_t>(ceil_div(values, 256)));
+    if (q->dtype == PARARNN_BF16) k_ssm_shared<bf16><<<grid, dim3(256), 0, st>>>(a);
+    else k_ssm_shared<float><<<grid, dim3(256), 0, st>>>(a);
+  }
+  if (grad->d_h0 && any && (q->cu_seqlens || q->T == 0)) {
+    const int64_t states = q->D * q->N, n = q->B * p.seqs.n * states;
+    if (!grid_ok(ceil_div(n, 256), 256)) return PARARNN_ERR_UNSUPPORTED;
+    k_ssm_empty<<<dim3(static_cast<uint32_t>(ceil_div(n, 256))), dim3(256), 0, st>>>(p.seqs, states, n, grad->d_last, grad->d_h0);
+  }
+  if (grad->d_A || grad->d_skip || grad->d_dt_bias) {
+    if (!colsum(g.part_A, steps ? s.S * q->B : 0, cols, sums, scratch, st)) return PARARNN_ERR_UNSUPPORTED;
+    k_ssm_params<<<dim3(static_cast<uint32_t>(ceil_div(cols, 256))), dim3(256), 0, st>>>(sums, q->D, p.N, grad->d_A, grad->d_skip,
+                                                                                        grad->d_dt_bias);
+  }
+  return launched();
+}

@@ -25,6 +25,15 @@ DEV float hw_log2(float x) { return __builtin_amdgcn_logf(x); }
 DEV float hw_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 DEV float sigmoid(float x) { return hw_rcp(1.0f + hw_exp2(-kLog2e * x)); }
 
+// softplus(x) = max(x, 0) + log1p(e^-|x|); log1p(e) = log(w) e / (w - 1) with w = fl(1 + e), exact in the
+// rounding of w (W. Kahan's correction), since small rates (1e-4 and below) set the longest memories
+DEV float softplus(float x) {
+  const float e = hw_exp2(-kLog2e * fabsf(x));
+  const float w = 1.0f + e;
+  const float l = w == 1.0f ? e : kLn2 * hw_log2(w) * e * hw_rcp(w - 1.0f);
+  return fmaxf(x, 0.0f) + l;
+}
+
 struct bf16 { uint16_t u; };   // storage only
 
 DEV float to_f32(float x) { return x; }

@@ -36,15 +36,6 @@ struct GradArgs {
   float* d_h0;
 };
 
-// softplus(x) = max(x, 0) + log1p(e^-|x|); log1p(e) = log(w) e / (w - 1) with w = fl(1 + e), exact in the
-// rounding of w (W. Kahan's correction), since small rates (1e-4 and below) set the longest memories
-DEV float softplus(float x) {
-  const float e = hw_exp2(-kLog2e * fabsf(x));
-  const float w = 1.0f + e;
-  const float l = w == 1.0f ? e : kLn2 * hw_log2(w) * e * hw_rcp(w - 1.0f);
-  return fmaxf(x, 0.0f) + l;
-}
-
 // The gates of one element.  For small |log a| q = 1 - a comes first, from the Taylor series of expm1, so that
 // a = 1 - q is rounded to nearest and m^2 = 1 - a^2 = q (2 - q) has full relative accuracy (1 - exp() would lose
 // it all where a is near 1, which is where these recurrences live); for large |log a| a itself comes first.
