@@ -70,9 +70,11 @@ pararnn_status pararnn_block_causal_conv_vjp(const pararnn_block_conv* prob, con
  *     dt = softplus(delta_t[d] + dt_bias[d]),    h_t[d,n] = exp(dt A[d,n]) h_{t-1}[d,n] + dt x_t[d] B_t[g,n]
  *     y_t[d] = (sum_n C_t[g,n] h_t[d,n] + skip[d] x_t[d]) z_t[d] sig(z_t[d])
  * The D channels form G groups of D / G consecutive ones, which share B and C.  N <= PARARNN_BLOCK_MAX_STATES (else
- * UNSUPPORTED), and so is a T of 2^31 or more and a launch of 2^32 threads.  A's sign is not checked: positive rates grow.
+ * UNSUPPORTED); so are a T of 2^31 - 16 or more, strides over t of PARARNN_BLOCK_SSM_MAX_STEP or more, and a launch of 2^32
+ * threads.  A's sign is not checked: positive rates grow.
  * ---------------------------------------------------------------------------------------------- */
 #define PARARNN_BLOCK_MAX_STATES 32
+#define PARARNN_BLOCK_SSM_MAX_STEP (1 << 24)
 /* steps of one chunk (the state entering each is what the gradient rebuilds h from) */
 #define PARARNN_BLOCK_SSM_CHUNK 16
 

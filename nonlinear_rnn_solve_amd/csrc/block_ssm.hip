@@ -76,11 +76,45 @@ DEV Where where(const SsmArgs& p) {
   return w;
 }
 
-template <typename T> DEV T zero_of() { return T{}; }
-// element (t, d) of a plane, uniform base
-template <typename T> DEV const T* row_of(const void* plane, const int64_t (&s)[2], int64_t b, int64_t t, int32_t d) {
-  return static_cast<const T*>(plane) + b * s[0] + t * s[1] + d;
+// A launch's arguments, read anew: held in scalar registers over a tile they would not fit, and went through vector lanes (half of
+// the instructions outside the walks).
+template <typename A> DEV const A __attribute__((address_space(4)))* arguments() {
+  auto p = (const A __attribute__((address_space(4)))*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
 }
+
+// One channel's column of a plane, as its lane walks it tile by tile: the element of the tile's first step (made a vector
+// register's, for the same reason) and the step's stride, which each tile sets.  Rows past the last step are read as the last, lanes
+// past the last channel as the last: nothing branches, and what they give is left out later.  A tile's steps are less than 2^28
+// elements apart (checked), so that 32 bits hold their offsets.
+template <typename T> using Bits = std::conditional_t<sizeof(T) == 2, uint16_t, float>;
+template <typename T> using Global = __attribute__((address_space(1))) Bits<T>;
+template <typename T> DEV Global<T>* in_vector(const void* plane, int64_t at) {
+  auto p = (Global<T>*)plane + at;
+  asm("" : "+v"(p));
+  return p;
+}
+DEV float value(float x) { return x; }
+DEV float value(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+template <typename T> struct Column {
+  Global<T>* at;
+  int32_t s;
+  DEV Column(const void* plane, const int64_t (&st)[2], int64_t b, int64_t t, const Where& w, int lane)
+      : at(in_vector<T>(plane, b * st[0] + t * st[1] + w.d + (lane < w.left ? lane : w.left - 1))), s(static_cast<int32_t>(st[1])) {}
+  DEV void move(int32_t steps) { at += steps * s; }
+  template <int E> DEV void load(int wave, int wv, int32_t steps, Bits<T> (&v)[E]) const {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int32_t t = wave + i * wv;
+      v[i] = at[(t < steps ? t : steps - 1) * s];
+    }
+  }
+  DEV void store(int32_t t, float x) const {
+    if constexpr (sizeof(T) == 2) at[t * s] = bf16_bits(x);
+    else at[t * s] = x;
+  }
+};
 
 // lane k of each row of 16, for all lanes of the row
 template <int K> DEV float row_lane(float v) { return dpp<0x150 + K>(v); }
@@ -104,37 +138,30 @@ template <typename T, int NS, int WV> struct Tile {
   static constexpr int NP = NS * WV, TH = WV * WAVE;
   static constexpr int BC = (CT * NP + TH - 1) / TH;           // values of B and of C of a thread
 };
-template <typename T, int E>
-DEV void load_plane(const void* plane, const int64_t (&s)[2], int64_t b, int32_t t0, int32_t T_, int wave, int wv, int32_t d, bool in,
-                    int lane, T (&v)[E]) {
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int32_t t = t0 + wave + i * wv;
-    v[i] = T{};
-    if (t < T_ && in) v[i] = row_of<T>(plane, s, b, t, d)[lane];
-  }
-}
-template <typename T, int NS, int WV>
-DEV void load_shared(const void* plane, const int64_t (&s)[3], const SsmArgs& p, const Where& w, int32_t t0,
-                     T (&v)[Tile<T, NS, WV>::BC]) {
+// Some of a tile's B or C: thread k takes the values k, k + 64 WV, ... of [CT][NP]; zeros past the last step or state
+template <typename T, int NS, int WV> struct Shared {
   using L = Tile<T, NS, WV>;
+  Global<T>* at;                // of the tile's first value
+  int32_t s, N;
+  DEV Shared(const void* plane, const int64_t (&st)[3], int64_t b, int64_t t, int32_t g, int32_t n)
+      : at(in_vector<T>(plane, b * st[0] + t * st[1] + g * st[2])), s(static_cast<int32_t>(st[1])), N(n) {}
+  DEV void move(int32_t steps) { at += steps * s; }
+  DEV void load(int32_t steps, Bits<T> (&v)[L::BC]) const {
 #pragma unroll
-  for (int i = 0; i < L::BC; ++i) {
-    const int k = threadIdx.x + i * L::TH, t = k / L::NP, n = k - t * L::NP;
-    v[i] = T{};
-    if (t < CT && t0 + t < p.T && n < p.N)
-      v[i] = static_cast<const T*>(plane)[w.b * s[0] + static_cast<int64_t>(t0 + t) * s[1] + w.g * s[2] + n];
+    for (int i = 0; i < L::BC; ++i) {
+      const int k = threadIdx.x + i * L::TH, t = k / L::NP, n = k - t * L::NP;
+      v[i] = 0;
+      if (t < steps && n < N) v[i] = at[t * s + n];
+    }
   }
-}
-template <typename T, int NS, int WV>
-DEV void put_shared(float* to, const T (&v)[Tile<T, NS, WV>::BC]) {
-  using L = Tile<T, NS, WV>;
+  static DEV void put(float* to, const Bits<T> (&v)[L::BC]) {
 #pragma unroll
-  for (int i = 0; i < L::BC; ++i) {
-    const int k = threadIdx.x + i * L::TH;
-    if (k < CT * L::NP) to[k] = to_f32(v[i]);
+    for (int i = 0; i < L::BC; ++i) {
+      const int k = threadIdx.x + i * L::TH;
+      if (k < CT * L::NP) to[k] = value(v[i]);
+    }
   }
-}
+};
 // a wave's B or C of a tile, from [CT][NP] in shared memory: register r holds the steps r 16/NS and on
 template <int NS, int NP> DEV void get_shared(const float* from, int wave, int lane, float (&r)[NS]) {
   constexpr int SPR = 16 / NS;
@@ -142,41 +169,80 @@ template <int NS, int NP> DEV void get_shared(const float* from, int wave, int l
   for (int k = 0; k < NS; ++k) r[k] = from[(k * SPR + (lane & 15) / NS) * NP + wave * NS + (lane & 15) % NS];
 }
 
-// a wave's states of one channel, [n][D] (segments, carry) or [d][N] (h0, h_last)
-template <int NS> DEV void load_nd(const float* p, int64_t D, int32_t N, int n0, bool in, float (&v)[NS]) {
-#pragma unroll
-  for (int n = 0; n < NS; ++n) v[n] = in && n0 + n < N ? p[static_cast<int64_t>(n0 + n) * D] : 0.0f;
-}
-template <int NS> DEV void store_nd(float* p, int64_t D, int32_t N, int n0, bool in, const float (&v)[NS]) {
-#pragma unroll
-  for (int n = 0; n < NS; ++n)
-    if (in && n0 + n < N) p[static_cast<int64_t>(n0 + n) * D] = v[n];
-}
-template <int NS> DEV void load_dn(const float* p, int32_t N, int n0, bool in, float (&v)[NS]) {
-#pragma unroll
-  for (int n = 0; n < NS; ++n) v[n] = in && p && n0 + n < N ? p[n0 + n] : 0.0f;
-}
-template <int NS> DEV void store_dn(float* p, int32_t N, int n0, bool in, const float (&v)[NS]) {
-#pragma unroll
-  for (int n = 0; n < NS; ++n)
-    if (in && n0 + n < N) p[n0 + n] = v[n];
+// a wave's values of one step, the same for all lanes
+template <int NS, int NP> DEV void step_values(const float* from, int wave, int t, float (&v)[NS]) {
+  const float* q = from + t * NP + wave * NS;
+  if constexpr (NS == 4) {
+    const float4 r = *reinterpret_cast<const float4*>(q);
+    v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+  } else if constexpr (NS == 2) {
+    const float2 r = *reinterpret_cast<const float2*>(q);
+    v[0] = r.x, v[1] = r.y;
+  } else {
+    v[0] = *q;
+  }
 }
 
-// The steps of a tile at which a sequence begins, as bits (uniform)
-DEV uint32_t starts_of(const Seqs& q, int32_t t0, int32_t T) {
-  uint32_t m = t0 == 0 ? 1u : 0u;
-  if (q.cu) {
-    // the boundaries from the first at or after t0 on
-    int64_t j = t0 == 0 ? 1 : q.of(t0 - 1) + 1;
-    const int32_t end = t0 + CT < T ? t0 + CT : T;
-    for (; j < q.n; ++j) {
-      const int64_t t = q.cu[j];
-      if (t >= end) break;
-      if (t >= t0) m |= 1u << (t - t0);
-    }
+// a wave's states of one channel, [n][D] (segments, carry) or [d][N] (h0, h_last); zeros past the last state
+template <int NS> DEV void load_nd(const float* p, int32_t D, int32_t N, int n0, float (&v)[NS]) {
+#pragma unroll
+  for (int n = 0; n < NS; ++n) {
+    const int32_t k = n0 + n < N ? n0 + n : N - 1;
+    v[n] = p[k * D];
+    v[n] = n0 + n < N ? v[n] : 0.0f;
   }
-  return __builtin_amdgcn_readfirstlane(m);
 }
+template <int NS> DEV void store_nd(float* p, int32_t D, int32_t N, int n0, bool in, const float (&v)[NS]) {
+  if (!in) return;
+#pragma unroll
+  for (int n = 0; n < NS; ++n)
+    if (n0 + n < N) p[(n0 + n) * D] = v[n];
+}
+template <int NS> DEV void load_dn(const float* p, int32_t N, int n0, float (&v)[NS]) {
+#pragma unroll
+  for (int n = 0; n < NS; ++n) v[n] = 0.0f;
+  if (!p) return;
+#pragma unroll
+  for (int n = 0; n < NS; ++n) {
+    v[n] = p[n0 + n < N ? n0 + n : N - 1];
+    v[n] = n0 + n < N ? v[n] : 0.0f;
+  }
+}
+template <int NS> DEV void store_dn(float* p, int32_t N, int n0, bool in, const float (&v)[NS]) {
+  if (!in) return;
+#pragma unroll
+  for (int n = 0; n < NS; ++n)
+    if (n0 + n < N) p[n0 + n] = v[n];
+}
+
+// Where sequences begin in a tile, by step: which one does, and which one was before it (before[0]: the one of the step before the
+// tile).  Every wave writes the same.
+struct Marks {
+  int32_t start[CT], before[CT + 1];
+};
+// The steps of a tile of `steps` at which a sequence begins, as bits, and whether one ends with the tile (bit 16); uniform.
+DEV uint32_t marks_of(const Seqs& q, int32_t t0, int32_t steps, Marks& m) {
+  const int32_t end = t0 + steps;
+  if (!q.cu) return (t0 == 0 ? 1u : 0u) | (end == q.T ? 1u << CT : 0u);
+  uint32_t bits = 0;
+  int32_t now = t0 == 0 ? -1 : static_cast<int32_t>(q.of(t0 - 1)), t = 0, j = now + 1;
+  for (; j < q.n; ++j) {
+    t = j ? q.cu[j] : 0;
+    if (t >= end) break;
+    if (t >= t0) {
+      if (!(bits >> (t - t0) & 1)) m.before[t - t0] = now;
+      bits |= 1u << (t - t0);
+      m.start[t - t0] = j;
+    }
+    now = j;
+  }
+  m.before[steps] = now;
+  if (end == q.T || (j < q.n && t == end)) bits |= 1u << CT;
+  return __builtin_amdgcn_readfirstlane(bits);
+}
+constexpr uint32_t kSteps = (1u << CT) - 1;
+DEV int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // Whether step t begins a sequence (t < T), or nothing follows (t = T)
 DEV bool boundary(const Seqs& q, int32_t t, int32_t T) {
   if (t <= 0 || t >= T) return true;
@@ -184,20 +250,20 @@ DEV bool boundary(const Seqs& q, int32_t t, int32_t T) {
   return q.begin(q.of(t)) == t && q.of(t) > 0;
 }
 
-template <int NS> DEV float decay_to(float A2, float dt) { return hw_exp2(A2 * dt); }
-
 // ENDS: what each segment but the last leaves (from its last sequence's start, if one begins in it).  Otherwise the walk itself.
 template <typename T, int NS, int WV, bool ENDS>
 __global__ __launch_bounds__(WV * WAVE) void k_ssm(const SsmArgs p) {
   using L = Tile<T, NS, WV>;
   constexpr int E = L::E, NP = L::NP;
   __shared__ float2 u[CT][CH];
-  __shared__ float sb[CT * NP], sc[CT * NP];
+  __shared__ __attribute__((aligned(16))) float sb[CT * NP], sc[CT * NP];
   __shared__ float part[ENDS ? 1 : WV][CT][CH];
+  __shared__ Marks marks;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Where w = where(p);
+  const int32_t D_ = static_cast<int32_t>(p.D);
   const bool in = lane < w.left;
-  const int32_t d = w.d + lane;
+  const int32_t d = w.d + (in ? lane : w.left - 1);   // lanes past the last channel repeat it and store nothing
   const int n0 = wave * NS;
   const int64_t own = static_cast<int64_t>(d) * p.N;            // [d][N]
   const int64_t seq_step = p.D * p.N;                           // of h0 and h_last
@@ -205,7 +271,7 @@ __global__ __launch_bounds__(WV * WAVE) void k_ssm(const SsmArgs p) {
   int32_t first = w.s * p.per, last = first + p.per < p.tiles ? first + p.per : p.tiles;   // tiles
 
   float A2[NS], h[NS] = {};
-  load_dn<NS>(p.A + own, p.N, n0, in, A2);
+  load_dn<NS>(p.A + own, p.N, n0, A2);
 #pragma unroll
   for (int n = 0; n < NS; ++n) A2[n] *= kLog2e;
   const float bias = in && p.dt_bias ? p.dt_bias[d] : 0.0f, skip = in && p.skip ? p.skip[d] : 0.0f;
@@ -221,10 +287,10 @@ __global__ __launch_bounds__(WV * WAVE) void k_ssm(const SsmArgs p) {
     const int32_t from = p.seqs.cu ? static_cast<int32_t>(p.seqs.begin(p.seqs.of(ta))) : 0;
     int32_t s = from / (p.per * CT);
     const float* end = p.end + (s * p.B + w.b) * seq_step + d;
-    load_nd<NS>(end, p.D, p.N, n0, in, h);
+    load_nd<NS>(end, D_, p.N, n0, h);
     for (++s; s < w.s; ++s) {
       float e[NS];
-      load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, e);
+      load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, D_, p.N, n0, e);
       const float total = in ? p.sum[(s * p.B + w.b) * p.D + d] : 0.0f;
 #pragma unroll
       for (int n = 0; n < NS; ++n) h[n] = fmaf(hw_exp2(A2[n] * total), h[n], e[n]);
@@ -233,78 +299,107 @@ __global__ __launch_bounds__(WV * WAVE) void k_ssm(const SsmArgs p) {
   // the last sequence that begins in this segment: later segments' workgroups write over its h0 where that is h_last's place
   const int64_t last_seq = p.in_place && p.S > 1 ? p.seqs.of(tb - 1) : -1;
 
-  T x[E], dl[E], z[E], vb[L::BC], vc[L::BC];
-  const auto load = [&](int32_t t0) {
-    load_plane<T, E>(p.x, p.sx, w.b, t0, p.T, wave, WV, w.d, in, lane, x);
-    load_plane<T, E>(p.delta, p.sdelta, w.b, t0, p.T, wave, WV, w.d, in, lane, dl);
-    load_shared<T, NS, WV>(p.b, p.sb, p, w, t0, vb);
+  Bits<T> x[E], dl[E], z[E], vb[L::BC], vc[L::BC];
+  const int64_t from = static_cast<int64_t>(first) * CT;
+  Column<T> cx(p.x, p.sx, w.b, from, w, lane), cd(p.delta, p.sdelta, w.b, from, w, lane), cz(p.z, p.sz, w.b, from, w, lane);
+  Column<T> cy(p.y, p.sy, w.b, from, w, lane);
+  Shared<T, NS, WV> cb(p.b, p.sb, w.b, from, w.g, p.N), cc(p.c, p.sc, w.b, from, w.g, p.N);
+  float* carry = p.carry ? p.carry + (w.b * p.tiles + first) * seq_step + d : nullptr;
+  const int32_t T_ = p.T, N = p.N;
+  const bool gate = p.z;
+  const auto load = [&](int32_t steps) {
+    cx.load(wave, WV, steps, x);
+    cd.load(wave, WV, steps, dl);
+    cb.load(steps < CT ? steps : CT, vb);
     if constexpr (!ENDS) {
-      if (p.z) load_plane<T, E>(p.z, p.sz, w.b, t0, p.T, wave, WV, w.d, in, lane, z);
-      load_shared<T, NS, WV>(p.c, p.sc, p, w, t0, vc);
+      if (gate) cz.load(wave, WV, steps, z);
+      cc.load(steps < CT ? steps : CT, vc);
     }
   };
-  load(first * CT);
+  load(T_ - first * CT);
 
   for (int32_t tile = first; tile < last; ++tile) {
     const int32_t t0 = tile * CT;
-    const int32_t steps = p.T - t0 < CT ? p.T - t0 : CT;
+    const int32_t steps = T_ - t0 < CT ? T_ - t0 : CT;
+    const auto* q = arguments<SsmArgs>();
+    cx.s = q->sx[1], cd.s = q->sdelta[1], cb.s = q->sb[1];
+    if constexpr (!ENDS) cz.s = q->sz[1], cc.s = q->sc[1], cy.s = q->sy[1];
     float xf[E], zf[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int t = wave + i * WV;
-      xf[i] = to_f32(x[i]);
-      if constexpr (!ENDS) zf[i] = to_f32(z[i]);
-      const float dt = t < steps ? softplus(to_f32(dl[i]) + bias) : 0.0f;
-      u[t][lane] = make_float2(dt, t < steps ? dt * xf[i] : 0.0f);
+      xf[i] = value(x[i]);
+      if constexpr (!ENDS) zf[i] = value(z[i]);
+      const float dt = softplus(value(dl[i]) + bias);
+      u[t][lane] = t < steps ? make_float2(dt, dt * xf[i]) : make_float2(0.0f, 0.0f);
     }
-    put_shared<T, NS, WV>(sb, vb);
-    if constexpr (!ENDS) put_shared<T, NS, WV>(sc, vc);
+    Shared<T, NS, WV>::put(sb, vb);
+    if constexpr (!ENDS) Shared<T, NS, WV>::put(sc, vc);
     __syncthreads();
-    if (tile + 1 < last) load((tile + 1) * CT);
+    if (tile + 1 < last) {
+      cx.move(CT);
+      cd.move(CT);
+      cb.move(CT);
+      if constexpr (!ENDS) {
+        cz.move(CT);
+        cc.move(CT);
+      }
+      load(T_ - t0 - CT);
+    }
 
     if constexpr (!ENDS) {
-      if (p.carry) store_nd<NS>(p.carry + (w.b * p.tiles + tile) * seq_step + d, p.D, p.N, n0, in, h);
+      if (carry) {
+        store_nd<NS>(carry, D_, N, n0, in, h);
+        carry += seq_step;
+      }
     }
-    const uint32_t starts = starts_of(p.seqs, t0, p.T);
-    float rb[NS], rc[NS];
+    const uint32_t starts = marks_of(p.seqs, t0, steps, marks);
+    float rb[NS];
     get_shared<NS, NP>(sb, wave, lane, rb);
-    if constexpr (!ENDS) get_shared<NS, NP>(sc, wave, lane, rc);
+    // whole tiles in which no sequence begins are walked without a branch
+    const auto walk = [&](auto events) {
+    constexpr bool EVENTS = events;
     for_up<0, CT / 4>([&](auto quarter) {
       constexpr int Q = quarter * 4;
-      if (Q < steps) {
+      if (!EVENTS || Q < steps) {
         for_up<Q, Q + 4>([&](auto step) {
           constexpr int t = step;
-          if (starts >> t & 1) {
+          if (EVENTS && (starts >> t & 1)) {
             if constexpr (ENDS) {
               if (t0 + t == begin) {
-                const int64_t j = p.seqs.cu ? p.seqs.of(begin) : 0;
-                load_dn<NS>(p.h0 ? p.h0 + row_states + j * seq_step : nullptr, p.N, n0, in, h);
-                if (p.head) store_nd<NS>(p.head + (w.s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, h);
+                const int32_t j = p.seqs.cu ? uniform(marks.start[t]) : 0;
+                load_dn<NS>(p.h0 ? p.h0 + row_states + j * seq_step : nullptr, p.N, n0, h);
+                if (p.head) store_nd<NS>(p.head + (w.s * p.B + w.b) * seq_step + d, D_, p.N, n0, in, h);
                 sum = 0.0f;
               }
             } else {
-              const int64_t j = p.seqs.cu ? p.seqs.of(t0 + t) : 0;
-              if (t0 + t > ta && p.h_last)
-                store_dn<NS>(p.h_last + row_states + p.seqs.of(t0 + t - 1) * seq_step, p.N, n0, in, h);
-              if (j == last_seq && w.s + 1 < p.S)
-                load_nd<NS>(p.head + (w.s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, h);
+              const auto* e = arguments<SsmArgs>();
+              const int32_t j = e->seqs.cu ? uniform(marks.start[t]) : 0;
+              if (t0 + t > ta && e->h_last)
+                store_dn<NS>(e->h_last + row_states + uniform(marks.before[t]) * seq_step, e->N, n0, in, h);
+              if (j == last_seq && w.s + 1 < e->S)
+                load_nd<NS>(e->head + (w.s * e->B + w.b) * seq_step + d, D_, e->N, n0, h);
               else
-                load_dn<NS>(p.h0 ? p.h0 + row_states + j * seq_step : nullptr, p.N, n0, in, h);
+                load_dn<NS>(e->h0 ? e->h0 + row_states + j * seq_step : nullptr, e->N, n0, h);
             }
           }
           const float2 v = u[t][lane];
           if constexpr (ENDS) sum += v.x;
-          float y = 0.0f;
+          float y = 0.0f, c[NS];
+          if constexpr (!ENDS) step_values<NS, NP>(sc, wave, t, c);
           for_up<0, NS>([&](auto state) {
             constexpr int n = state;
             const float a = hw_exp2(A2[n] * v.x);
             h[n] = fmaf(a, h[n], of_step<NS, t, n>(rb) * v.y);
-            if constexpr (!ENDS) y = fmaf(of_step<NS, t, n>(rc), h[n], y);
+            if constexpr (!ENDS) y = n ? fmaf(c[n], h[n], y) : c[n] * h[n];
           });
           if constexpr (!ENDS) part[wave][t][lane] = y;
         });
       }
     });
+    };
+    if (steps < CT || (starts & kSteps)) walk(std::true_type{});
+    else walk(std::false_type{});
     __syncthreads();
     if constexpr (!ENDS) {
 #pragma unroll
@@ -313,13 +408,14 @@ __global__ __launch_bounds__(WV * WAVE) void k_ssm(const SsmArgs p) {
         float y = skip * xf[i];
 #pragma unroll
         for (int k = 0; k < WV; ++k) y += part[k][t][lane];
-        if (p.z) y *= silu(zf[i]);
-        if (t < steps && in) const_cast<T*>(row_of<T>(p.y, p.sy, w.b, t0 + t, w.d))[lane] = from_f32<T>(y);
+        if (gate) y *= silu(zf[i]);
+        if (t < steps && in) cy.store(t, y);
       }
+      cy.move(CT);
     }
   }
   if constexpr (ENDS) {
-    store_nd<NS>(p.end + (w.s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, h);
+    store_nd<NS>(p.end + (w.s * p.B + w.b) * seq_step + d, D_, p.N, n0, in, h);
     if (wave == 0 && in) p.sum[(w.s * p.B + w.b) * p.D + d] = sum;
   } else if (p.h_last) {
     // the sequence that ends with the segment, and with the row those that have no steps
@@ -331,7 +427,7 @@ __global__ __launch_bounds__(WV * WAVE) void k_ssm(const SsmArgs p) {
         for (; empty; empty &= empty - 1) {
           const int64_t at = (j0 + __builtin_ctzll(empty)) * seq_step;
           float v[NS];
-          load_dn<NS>(p.h0 ? p.h0 + row_states + at : nullptr, p.N, n0, in, v);
+          load_dn<NS>(p.h0 ? p.h0 + row_states + at : nullptr, p.N, n0, v);
           store_dn<NS>(p.h_last + row_states + at, p.N, n0, in, v);
         }
       }
@@ -364,31 +460,31 @@ template <int TO, int FROM, typename F> DEV void for_down(F&& f) {   // FROM - 1
 
 // Sums over the wave's lanes of 32 values; lane l gets that of value 16 l5 + 8 l4 + 4 l3 + 2 l2 + l0 (l5: bit 5 of l)
 DEV float fold(float (&v)[32], int lane) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for_up<0, 16>([&](auto k) {
+    constexpr int i = k;
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 16]), false, false);
     v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  });
+  for_up<0, 8>([&](auto k) {
+    constexpr int i = k;
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 8]), false, false);
     v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  });
+  for_up<0, 4>([&](auto k) {
+    constexpr int i = k;
     const float a = v[i] + dpp<0x128>(v[i]), b = v[i + 4] + dpp<0x128>(v[i + 4]);   // row_ror:8
     v[i] = lane & 8 ? b : a;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  });
+  for_up<0, 2>([&](auto k) {
+    constexpr int i = k;
     const float a = v[i] + dpp<0x141>(v[i]), b = v[i + 2] + dpp<0x141>(v[i + 2]);   // row_half_mirror
     v[i] = lane & 4 ? b : a;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  });
+  for_up<0, 2>([&](auto k) {
+    constexpr int i = k;
     v[i] += dpp<0xb1>(v[i]);
     v[i] += dpp<0x4e>(v[i]);
-  }
+  });
   return lane & 1 ? v[1] : v[0];
 }
 
@@ -400,12 +496,13 @@ __global__ __launch_bounds__(WV * WAVE) void k_ssm_back_ends(const SsmGradArgs g
   using L = Tile<T, NS, WV>;
   constexpr int E = L::E, NP = L::NP;
   __shared__ float2 u[CT][CH];
-  __shared__ float sc[CT * NP];
+  __shared__ __attribute__((aligned(16))) float sc[CT * NP];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Where w = where(p);
   ++w.s;
+  const int32_t D_ = static_cast<int32_t>(p.D);
   const bool in = lane < w.left;
-  const int32_t d = w.d + lane;
+  const int32_t d = w.d + (in ? lane : w.left - 1);   // lanes past the last channel repeat it and store nothing
   const int n0 = wave * NS;
   const int64_t seq_step = p.D * p.N, own = static_cast<int64_t>(d) * p.N;
   const int32_t first = w.s * p.per, last = first + p.per < p.tiles ? first + p.per : p.tiles;
@@ -417,52 +514,66 @@ __global__ __launch_bounds__(WV * WAVE) void k_ssm_back_ends(const SsmGradArgs g
   const int32_t end = stop < tb ? stop : tb;
 
   float A2[NS], P[NS] = {}, sum = 0.0f;
-  load_dn<NS>(p.A + own, p.N, n0, in, A2);
+  load_dn<NS>(p.A + own, p.N, n0, A2);
 #pragma unroll
   for (int n = 0; n < NS; ++n) A2[n] *= kLog2e;
   const float bias = in && p.dt_bias ? p.dt_bias[d] : 0.0f;
-  if (stop <= tb) load_dn<NS>(g.d_last ? g.d_last + (w.b * p.seqs.n + j) * seq_step + own : nullptr, p.N, n0, in, P);
+  if (stop <= tb) load_dn<NS>(g.d_last ? g.d_last + (w.b * p.seqs.n + j) * seq_step + own : nullptr, p.N, n0, P);
 
-  T dl[E], z[E], dy[E], vc[L::BC];
-  const auto load = [&](int32_t t0) {
-    load_plane<T, E>(p.delta, p.sdelta, w.b, t0, end, wave, WV, w.d, in, lane, dl);
-    load_plane<T, E>(g.dy, g.sdy, w.b, t0, end, wave, WV, w.d, in, lane, dy);
-    if (p.z) load_plane<T, E>(p.z, p.sz, w.b, t0, end, wave, WV, w.d, in, lane, z);
-    load_shared<T, NS, WV>(p.c, p.sc, p, w, t0, vc);
-  };
+  Bits<T> dl[E], z[E], dy[E], vc[L::BC];
   int32_t tile = (end - 1) / CT;
-  load(tile * CT);
+  const int64_t from = static_cast<int64_t>(tile) * CT;
+  Column<T> cd(p.delta, p.sdelta, w.b, from, w, lane), cz(p.z, p.sz, w.b, from, w, lane), cg(g.dy, g.sdy, w.b, from, w, lane);
+  Shared<T, NS, WV> cc(p.c, p.sc, w.b, from, w.g, p.N);
+  const bool gate = p.z;
+  const auto load = [&](int32_t steps) {
+    cd.load(wave, WV, steps, dl);
+    cg.load(wave, WV, steps, dy);
+    if (gate) cz.load(wave, WV, steps, z);
+    cc.load(steps < CT ? steps : CT, vc);
+  };
+  load(end - tile * CT);
   for (; tile >= first; --tile) {
     const int32_t t0 = tile * CT, steps = end - t0 < CT ? end - t0 : CT;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int t = wave + i * WV;
-      float G = to_f32(dy[i]);
-      if (p.z) G *= silu(to_f32(z[i]));
-      u[t][lane] = t < steps ? make_float2(softplus(to_f32(dl[i]) + bias), G) : make_float2(0.0f, 0.0f);
+      float G = value(dy[i]);
+      if (gate) G *= silu(value(z[i]));
+      u[t][lane] = t < steps ? make_float2(softplus(value(dl[i]) + bias), G) : make_float2(0.0f, 0.0f);
     }
-    put_shared<T, NS, WV>(sc, vc);
+    Shared<T, NS, WV>::put(sc, vc);
     __syncthreads();
-    if (tile > first) load(t0 - CT);
-    float rc[NS];
-    get_shared<NS, NP>(sc, wave, lane, rc);
+    if (tile > first) {
+      cd.move(-CT);
+      cz.move(-CT);
+      cg.move(-CT);
+      cc.move(-CT);
+      load(CT);
+    }
+    const auto walk = [&](auto whole) {
     for_down<0, CT / 4>([&](auto quarter) {
       constexpr int Q = quarter * 4;
-      if (Q < steps) {
+      if (whole || Q < steps) {
         for_down<Q, Q + 4>([&](auto step) {
           constexpr int t = step;
           const float2 v = u[t][lane];
+          float c[NS];
+          step_values<NS, NP>(sc, wave, t, c);
           sum += v.x;
           for_up<0, NS>([&](auto state) {
             constexpr int n = state;
-            P[n] = hw_exp2(A2[n] * v.x) * fmaf(of_step<NS, t, n>(rc), v.y, P[n]);
+            P[n] = hw_exp2(A2[n] * v.x) * fmaf(c[n], v.y, P[n]);
           });
         });
       }
     });
+    };
+    if (steps < CT) walk(std::false_type{});
+    else walk(std::true_type{});
     __syncthreads();
   }
-  store_nd<NS>(p.end + (w.s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, P);
+  store_nd<NS>(p.end + (w.s * p.B + w.b) * seq_step + d, D_, p.N, n0, in, P);
   if (wave == 0 && in) p.sum[(w.s * p.B + w.b) * p.D + d] = sum;
 }
 
@@ -470,149 +581,206 @@ template <typename T, int NS, int WV>
 __global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) {
   const SsmArgs& p = g.f;
   using L = Tile<T, NS, WV>;
-  constexpr int E = L::E, NP = L::NP, RS = 16 / NS;
+  constexpr int E = L::E, NP = L::NP;
+  constexpr int HT = CT / 2, RS = HT * NS < 16 ? HT : 16 / NS;   // steps of a half tile, and of those whose sums are formed at once
   __shared__ float2 u[CT][CH];
   __shared__ float sg[CT][CH];
-  __shared__ float sb[CT * NP], sc[CT * NP];
+  __shared__ __attribute__((aligned(16))) float sb[CT * NP], sc[CT * NP];
   __shared__ float part[3][WV][CT][CH];
+  __shared__ Marks marks;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Where w = where(p);
+  const int32_t D_ = static_cast<int32_t>(p.D);
   const bool in = lane < w.left;
-  const int32_t d = w.d + lane;
+  const int32_t d = w.d + (in ? lane : w.left - 1);   // lanes past the last channel repeat it and store nothing
   const int n0 = wave * NS;
   const int64_t seq_step = p.D * p.N, own = static_cast<int64_t>(d) * p.N;
   const int64_t row_states = w.b * p.seqs.n * seq_step + own;
   const int32_t first = w.s * p.per, last = first + p.per < p.tiles ? first + p.per : p.tiles;
   const int32_t tb = last * CT < p.T ? last * CT : p.T;
 
-  float A[NS], P[NS] = {}, dA[NS] = {}, d_skip = 0.0f, d_bias = 0.0f;
-  load_dn<NS>(p.A + own, p.N, n0, in, A);
+  float A2[NS], P[NS] = {}, dA[NS] = {}, d_skip = 0.0f, d_bias = 0.0f;
+  load_dn<NS>(p.A + own, p.N, n0, A2);
+#pragma unroll
+  for (int n = 0; n < NS; ++n) A2[n] *= kLog2e;
   const float bias = in && p.dt_bias ? p.dt_bias[d] : 0.0f, skip = in && p.skip ? p.skip[d] : 0.0f;
   if (!boundary(p.seqs, tb, p.T)) {
     // what enters from the right: from the segment that the sequence ends in, over those between
     int32_t stop = p.seqs.cu ? static_cast<int32_t>(p.seqs.end(p.seqs.of(tb))) : p.T;
     stop = stop > tb ? stop : tb + 1;
     int32_t s = (stop - 1) / (p.per * CT);
-    load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, P);
+    load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, D_, p.N, n0, P);
     for (--s; s > w.s; --s) {
       float e[NS];
-      load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, p.D, p.N, n0, in, e);
+      load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, D_, p.N, n0, e);
       const float total = in ? p.sum[(s * p.B + w.b) * p.D + d] : 0.0f;
 #pragma unroll
-      for (int n = 0; n < NS; ++n) P[n] = fmaf(hw_exp2(A[n] * kLog2e * total), P[n], e[n]);
+      for (int n = 0; n < NS; ++n) P[n] = fmaf(hw_exp2(A2[n] * total), P[n], e[n]);
     }
   }
 
-  T x[E], dl[E], z[E], dy[E], vb[L::BC], vc[L::BC];
+  Bits<T> x[E], dl[E], z[E], dy[E], vb[L::BC], vc[L::BC];
   float h_in[NS];
-  const auto load = [&](int32_t tile) {
-    const int32_t t0 = tile * CT;
-    load_plane<T, E>(p.x, p.sx, w.b, t0, p.T, wave, WV, w.d, in, lane, x);
-    load_plane<T, E>(p.delta, p.sdelta, w.b, t0, p.T, wave, WV, w.d, in, lane, dl);
-    load_plane<T, E>(g.dy, g.sdy, w.b, t0, p.T, wave, WV, w.d, in, lane, dy);
-    if (p.z) load_plane<T, E>(p.z, p.sz, w.b, t0, p.T, wave, WV, w.d, in, lane, z);
-    load_shared<T, NS, WV>(p.b, p.sb, p, w, t0, vb);
-    load_shared<T, NS, WV>(p.c, p.sc, p, w, t0, vc);
-    load_nd<NS>(g.carry + (w.b * p.tiles + tile) * seq_step + d, p.D, p.N, n0, in, h_in);
+  const int64_t from = static_cast<int64_t>(last - 1) * CT;
+  Column<T> cx(p.x, p.sx, w.b, from, w, lane), cd(p.delta, p.sdelta, w.b, from, w, lane), cz(p.z, p.sz, w.b, from, w, lane),
+      cg(g.dy, g.sdy, w.b, from, w, lane);
+  Column<T> ox(g.dx, g.sdx, w.b, from, w, lane), od(g.ddelta, g.sddelta, w.b, from, w, lane), oz(g.dz, g.sdz, w.b, from, w, lane);
+  Shared<T, NS, WV> cb(p.b, p.sb, w.b, from, w.g, p.N), cc(p.c, p.sc, w.b, from, w.g, p.N);
+  const float* carry = g.carry + (w.b * p.tiles + last - 1) * seq_step + d;
+  const int32_t T_ = p.T, N = p.N;
+  const bool gate = p.z;
+  const auto load = [&](int32_t steps) {
+    cx.load(wave, WV, steps, x);
+    cd.load(wave, WV, steps, dl);
+    cg.load(wave, WV, steps, dy);
+    if (gate) cz.load(wave, WV, steps, z);
+    cb.load(steps < CT ? steps : CT, vb);
+    cc.load(steps < CT ? steps : CT, vc);
+    load_nd<NS>(carry, D_, N, n0, h_in);
   };
-  load(last - 1);
+  load(T_ - (last - 1) * CT);
+  // where this lane's channel sums of a tile go
+  const int fk = (lane & 1) | (lane >> 1 & 14), ft = fk / NS, fn = n0 + fk % NS;
+  const bool sums = !(lane & 2) && fk < RS * NS && fn < N;
+  float* bc = g.part_bc + ((static_cast<int64_t>(w.ct) * p.B + w.b) * T_ + from + ft) * (2 * N) + (lane >> 5) * N + fn;
 
   for (int32_t tile = last - 1; tile >= first; --tile) {
-    const int32_t t0 = tile * CT, steps = p.T - t0 < CT ? p.T - t0 : CT;
+    const int32_t t0 = tile * CT, steps = T_ - t0 < CT ? T_ - t0 : CT;
+    const auto* q = arguments<SsmGradArgs>();
+    cx.s = q->f.sx[1], cd.s = q->f.sdelta[1], cz.s = q->f.sz[1], cg.s = q->sdy[1], cb.s = q->f.sb[1], cc.s = q->f.sc[1];
+    ox.s = q->sdx[1], od.s = q->sddelta[1], oz.s = q->sdz[1];
     float xf[E], zf[E], dyf[E], open[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int t = wave + i * WV;
-      xf[i] = to_f32(x[i]);
-      zf[i] = p.z ? to_f32(z[i]) : 0.0f;
-      dyf[i] = to_f32(dy[i]);
-      const float raw = to_f32(dl[i]) + bias, dt = t < steps ? softplus(raw) : 0.0f;
+      const bool there = t < steps && in;      // what other lanes hold must not enter the sums over channels
+      xf[i] = value(x[i]);
+      zf[i] = gate ? value(z[i]) : 0.0f;
+      dyf[i] = value(dy[i]);
+      const float raw = value(dl[i]) + bias, dt = softplus(raw);
       open[i] = sigmoid(raw);
-      u[t][lane] = make_float2(dt, t < steps ? dt * xf[i] : 0.0f);
-      sg[t][lane] = t < steps ? dyf[i] * (p.z ? silu(zf[i]) : 1.0f) : 0.0f;
+      u[t][lane] = there ? make_float2(dt, dt * xf[i]) : make_float2(0.0f, 0.0f);
+      sg[t][lane] = there ? dyf[i] * (gate ? silu(zf[i]) : 1.0f) : 0.0f;
     }
-    put_shared<T, NS, WV>(sb, vb);
-    put_shared<T, NS, WV>(sc, vc);
+    Shared<T, NS, WV>::put(sb, vb);
+    Shared<T, NS, WV>::put(sc, vc);
     float h0[NS];
 #pragma unroll
     for (int n = 0; n < NS; ++n) h0[n] = h_in[n];
     __syncthreads();
-    if (tile > first) load(tile - 1);
+    if (tile > first) {
+      cx.move(-CT);
+      cd.move(-CT);
+      cg.move(-CT);
+      cz.move(-CT);
+      cb.move(-CT);
+      cc.move(-CT);
+      carry -= seq_step;
+      load(CT);
+    }
 
-    const uint32_t starts = starts_of(p.seqs, t0, p.T);
-    const uint32_t ends = starts >> 1 | (boundary(p.seqs, t0 + steps, p.T) ? 1u << (steps - 1) : 0u);
-    const auto entering = [&](int32_t t, float (&v)[NS]) {      // the state entering the sequence that begins at step t
-      const int64_t j = p.seqs.cu ? p.seqs.of(t) : 0;
-      load_dn<NS>(p.h0 ? p.h0 + row_states + j * seq_step : nullptr, p.N, n0, in, v);
+    const uint32_t starts = marks_of(p.seqs, t0, steps, marks);
+    const uint32_t ends = (starts & kSteps) >> 1 | (starts >> CT & 1) << (steps - 1);
+    const auto entering = [&](int t, float (&v)[NS]) {          // the state entering the sequence that begins at step t
+      const auto* e = arguments<SsmGradArgs>();
+      const int32_t j = e->f.seqs.cu ? uniform(marks.start[t]) : 0;
+      load_dn<NS>(e->f.h0 ? e->f.h0 + row_states + j * seq_step : nullptr, e->f.N, n0, v);
     };
-    float rb[NS], rc[NS], hs[CT][NS], as[CT][NS];
+    float rb[NS], tA[NS] = {}, hm[NS];
     get_shared<NS, NP>(sb, wave, lane, rb);
-    get_shared<NS, NP>(sc, wave, lane, rc);
-    for_up<0, CT / 4>([&](auto quarter) {
-      constexpr int Q = quarter * 4;
-      if (Q < steps) {
-        for_up<Q, Q + 4>([&](auto step) {
-          constexpr int t = step;
-          float h[NS], y = 0.0f;
-#pragma unroll
-          for (int n = 0; n < NS; ++n) h[n] = t == 0 ? h0[n] : hs[t - 1 < 0 ? 0 : t - 1][n];
-          if (starts >> t & 1) entering(t0 + t, h);
-          const float2 v = u[t][lane];
-          for_up<0, NS>([&](auto state) {
-            constexpr int n = state;
-            as[t][n] = hw_exp2(A[n] * kLog2e * v.x);
-            hs[t][n] = fmaf(as[t][n], h[n], of_step<NS, t, n>(rb) * v.y);
-            y = fmaf(of_step<NS, t, n>(rc), hs[t][n], y);
-          });
-          part[0][wave][t][lane] = y;
+    // the state between the halves of the tile
+    for_up<0, NS>([&](auto state) { hm[state] = h0[state]; });
+    const auto middle = [&](auto events) {
+      for_up<0, HT>([&](auto step) {
+        constexpr int t = step;
+        if (events && (starts >> t & 1)) entering(t, hm);
+        const float2 v = u[t][lane];
+        for_up<0, NS>([&](auto state) {
+          constexpr int n = state;
+          hm[n] = fmaf(hw_exp2(A2[n] * v.x), hm[n], of_step<NS, t, n>(rb) * v.y);
         });
-      }
-    });
-    float tA[NS] = {};
-    for_down<0, CT / RS>([&](auto block) {
-      constexpr int Q = block * RS;
-      if (Q < steps) {
+      });
+    };
+    const auto back = [&](auto events, const int half) {
+      const int s0 = half * HT;
+      const uint32_t here = starts >> s0, over = ends >> s0;   // (the bit past the tile is asked for by no step)
+      float hb[NS], hi[NS], hs[HT][NS], as[HT][NS];
+      for_up<0, NS>([&](auto state) {
+        constexpr int n = state;
+        hi[n] = half ? hm[n] : h0[n];
+        if constexpr (NS > 1) {
+          hb[n] = half ? rb[(n + NS / 2) % NS] : rb[n];
+        } else {
+          hb[0] = half ? dpp<0x128>(rb[0]) : rb[0];   // row_ror:8
+        }
+      });
+      for_up<0, HT>([&](auto step) {
+        constexpr int t = step;
+        float h[NS], y = 0.0f;
+        for_up<0, NS>([&](auto state) { h[state] = t == 0 ? hi[state] : hs[t == 0 ? 0 : t - 1][state]; });
+        if (events && (here >> t & 1)) entering(s0 + t, h);
+        const float2 v = u[s0 + t][lane];
+        float c[NS];
+        step_values<NS, NP>(sc, wave, s0 + t, c);
+        for_up<0, NS>([&](auto state) {
+          constexpr int n = state;
+          as[t][n] = hw_exp2(A2[n] * v.x);
+          hs[t][n] = fmaf(as[t][n], h[n], of_step<NS, t, n>(hb) * v.y);
+          y = n ? fmaf(c[n], hs[t][n], y) : c[n] * hs[t][n];
+        });
+        part[0][wave][s0 + t][lane] = y;
+      });
+      for_down<0, HT / RS>([&](auto block) {
+        constexpr int Q = block * RS;
         float v32[32];
+        if constexpr (RS * NS < 16) for_up<0, 32>([&](auto i) { v32[i] = 0.0f; });
         for_down<Q, Q + RS>([&](auto step) {
           constexpr int t = step;
-          if (NS > 1 || t < steps) {
-            if (ends >> t & 1) {
-              const int64_t j = p.seqs.cu ? p.seqs.of(t0 + t) : 0;
-              load_dn<NS>(g.d_last ? g.d_last + row_states + j * seq_step : nullptr, p.N, n0, in, P);
-            }
-            const float2 v = u[t][lane];
-            const float G = sg[t][lane];
-            float h[NS], s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-            for (int n = 0; n < NS; ++n) h[n] = t == 0 ? h0[n] : hs[t - 1 < 0 ? 0 : t - 1][n];
-            if (starts >> t & 1) entering(t0 + t, h);
-            for_up<0, NS>([&](auto state) {
-              constexpr int n = state;
-              const float q = fmaf(of_step<NS, t, n>(rc), G, P[n]);
-              s1 = fmaf(of_step<NS, t, n>(rb), q, s1);
-              v32[(t - Q) * NS + n] = q * v.y;
-              v32[16 + (t - Q) * NS + n] = G * hs[t][n];
-              P[n] = as[t][n] * q;
-              const float e = P[n] * h[n];
-              s2 = fmaf(e, A[n], s2);
-              tA[n] = fmaf(e, v.x, tA[n]);
-            });
-            part[1][wave][t][lane] = s1;
-            part[2][wave][t][lane] = s2;
-            if (starts >> t & 1) {
-              const int64_t j = p.seqs.cu ? p.seqs.of(t0 + t) : 0;
-              if (g.d_h0) store_dn<NS>(g.d_h0 + row_states + j * seq_step, p.N, n0, in, P);
-            }
-          } else {
-            v32[(t - Q) * NS] = v32[16 + (t - Q) * NS] = 0.0f;
+          if (events && (over >> t & 1)) {
+            const auto* e = arguments<SsmGradArgs>();
+            const int32_t j = e->f.seqs.cu ? uniform(marks.before[s0 + t + 1]) : 0;
+            load_dn<NS>(e->d_last ? e->d_last + row_states + j * seq_step : nullptr, e->f.N, n0, P);
+          }
+          const float2 v = u[s0 + t][lane];
+          const float G = sg[s0 + t][lane];
+          float h[NS], b[NS], c[NS], s1 = 0.0f, s2 = 0.0f;
+          step_values<NS, NP>(sb, wave, s0 + t, b);
+          step_values<NS, NP>(sc, wave, s0 + t, c);
+          for_up<0, NS>([&](auto state) { h[state] = t == 0 ? hi[state] : hs[t == 0 ? 0 : t - 1][state]; });
+          if (events && (here >> t & 1)) entering(s0 + t, h);
+          for_up<0, NS>([&](auto state) {
+            constexpr int n = state;
+            const float q = fmaf(c[n], G, P[n]);
+            s1 = n ? fmaf(b[n], q, s1) : b[n] * q;
+            v32[(t - Q) * NS + n] = q * v.y;
+            v32[16 + (t - Q) * NS + n] = G * hs[t][n];
+            P[n] = as[t][n] * q;
+            const float e = P[n] * h[n];
+            s2 = n ? fmaf(e, A2[n], s2) : e * A2[n];
+            tA[n] = fmaf(e, v.x, tA[n]);
+          });
+          part[1][wave][s0 + t][lane] = s1;
+          part[2][wave][s0 + t][lane] = s2;
+          if (events && (here >> t & 1)) {
+            const auto* e = arguments<SsmGradArgs>();
+            const int32_t j = e->f.seqs.cu ? uniform(marks.start[s0 + t]) : 0;
+            if (e->d_h0) store_dn<NS>(e->d_h0 + row_states + j * seq_step, e->f.N, n0, in, P);
           }
         });
         const float sum = fold(v32, lane);
-        const int k = (lane & 1) | (lane >> 1 & 14), t = Q + k / NS, n = n0 + k % NS;
-        if (!(lane & 2) && t < steps && n < p.N)
-          g.part_bc[((static_cast<int64_t>(w.ct) * p.B + w.b) * p.T + t0 + t) * (2 * p.N) + (lane >> 5) * p.N + n] = sum;
-      }
-    });
+        if (sums && s0 + Q + ft < steps) bc[(s0 + Q) * (2 * N)] = sum;
+      });
+    };
+    // tiles in which no sequence begins or ends are walked without a branch
+    if (starts) {
+      if (steps > HT) middle(std::true_type{});
+#pragma unroll 1
+      for (int half = steps > HT ? 1 : 0; half >= 0; --half) back(std::true_type{}, half);
+    } else {
+      middle(std::false_type{});
+#pragma unroll 1
+      for (int half = 1; half >= 0; --half) back(std::false_type{}, half);
+    }
 #pragma unroll
     for (int n = 0; n < NS; ++n) dA[n] += tA[n];
     __syncthreads();
@@ -629,18 +797,20 @@ __global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) 
         s2 += part[2][k][t][lane];
       }
       const float dt = u[t][lane].x, G = sg[t][lane];
-      const float dd = fmaf(s1, xf[i], s2) * open[i];
+      const float dd = fmaf(s1, xf[i], kLn2 * s2) * open[i];   // s2 is of A log2(e)
       tskip = fmaf(G, xf[i], tskip);
       tbias += dd;
       if (in) {
-        const_cast<T*>(row_of<T>(g.dx, g.sdx, w.b, t0 + t, w.d))[lane] = from_f32<T>(fmaf(s1, dt, G * skip));
-        const_cast<T*>(row_of<T>(g.ddelta, g.sddelta, w.b, t0 + t, w.d))[lane] = from_f32<T>(dd);
-        if (p.z)
-          const_cast<T*>(row_of<T>(g.dz, g.sdz, w.b, t0 + t, w.d))[lane] =
-              from_f32<T>(dyf[i] * y * silu_slope(zf[i], sigmoid(zf[i])));
+        ox.store(t, fmaf(s1, dt, G * skip));
+        od.store(t, dd);
+        if (gate) oz.store(t, dyf[i] * y * silu_slope(zf[i], sigmoid(zf[i])));
       }
       }
     }
+    ox.move(-CT);
+    od.move(-CT);
+    oz.move(-CT);
+    bc -= static_cast<int64_t>(CT) * (2 * N);
     d_skip += tskip;
     d_bias += tbias;
     __syncthreads();            // u and sg are read above
@@ -648,7 +818,7 @@ __global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) 
 
   // parameters: [S B][N + 2][D]
   const int64_t row = (w.s * p.B + w.b) * static_cast<int64_t>(p.N + 2) * p.D + d;
-  store_nd<NS>(g.part_A + row, p.D, p.N, n0, in, dA);
+  store_nd<NS>(g.part_A + row, D_, p.N, n0, in, dA);
   part[0][wave][0][lane] = d_skip;
   part[0][wave][1][lane] = d_bias;
   __syncthreads();
@@ -780,7 +950,10 @@ static bool problem_ok(const pararnn_block_ssm* q) {
     if (!plane_ok(q->B, (*s)[0]) || !plane_ok(q->T, (*s)[1]) || !plane_ok(q->G, (*s)[2])) return false;
   return true;
 }
+// a step's stride that does not fit the offsets inside a tile
+static bool far(int64_t stride) { return stride >= PARARNN_BLOCK_SSM_MAX_STEP; }
 static bool supported(const pararnn_block_ssm* q, const Split& s, int threads) {
+  if (far(q->sx[1]) || far(q->sdelta[1]) || (q->z && far(q->sz[1])) || far(q->sb[1]) || far(q->sc[1])) return false;
   if (q->N > PARARNN_BLOCK_MAX_STATES || q->T > INT32_MAX - CT || q->D > INT32_MAX / 64) return false;
   if (s.ctiles * q->G > INT32_MAX || q->B > INT32_MAX) return false;
   return s.rows == 0 || (s.S <= INT64_C(0xffffffff) / s.rows && grid_ok(s.rows * s.S, threads));
@@ -815,13 +988,13 @@ template <typename T, int NS, int WV> struct Backward {
     return launched();
   }
 };
-// waves of a workgroup for N states: four states a wave
-static int waves_of(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
+// waves of a workgroup for N states: four states a wave, two for up to four (one wave would load a tile by itself, and spill)
+static int waves_of(int64_t N) { return N == 1 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
 template <template <typename, int, int> class F, typename T, typename A>
 static pararnn_status by_states(int64_t N, const A& a, const Split& s, hipStream_t st) {
   if (N == 1) return F<T, 1, 1>::run(a, s, st);
+  if (N <= 4) return F<T, 2, 2>::run(a, s, st);
   switch (waves_of(N)) {
-    case 1: return F<T, 4, 1>::run(a, s, st);
     case 2: return F<T, 4, 2>::run(a, s, st);
     case 4: return F<T, 4, 4>::run(a, s, st);
     default: return F<T, 4, 8>::run(a, s, st);
@@ -846,7 +1019,7 @@ extern "C" pararnn_status pararnn_block_selective_scan(const pararnn_block_ssm* 
   if (!ptr_ok(y, dtype_size(q->dtype), any && q->T > 0) || !ptr_ok(h_last, 4, false) || !ptr_ok(carry, 4, false))
     return PARARNN_ERR_INVALID_ARG;
   const Split s = forward_split(q->B, q->T, q->D, q->G);
-  if (!supported(q, s, waves_of(q->N) * WAVE)) return PARARNN_ERR_UNSUPPORTED;
+  if (far(sy[1]) || !supported(q, s, waves_of(q->N) * WAVE)) return PARARNN_ERR_UNSUPPORTED;
   const Room r = room(q->B, q->T, q->D, q->N, q->G, false);
   if (!ws_ok(ws, ws_bytes, static_cast<size_t>(r.total()) * sizeof(float))) return PARARNN_ERR_WORKSPACE;
   if (!any) return PARARNN_OK;
@@ -888,6 +1061,7 @@ extern "C" pararnn_status pararnn_block_selective_scan_vjp(const pararnn_block_s
 
   const Split s = gradient_split(q->B, q->T, q->D, q->G);
   const int64_t values = q->B * q->T * q->G * 2 * q->N, cols = q->D * (q->N + 2);
+  if (far(grad->sdy[1]) || far(grad->sdx[1]) || far(grad->sddelta[1]) || (q->z && far(grad->sdz[1]))) return PARARNN_ERR_UNSUPPORTED;
   if (!supported(q, s, waves_of(q->N) * WAVE) || !grid_ok(ceil_div(values, 256), 256) || !grid_ok(ceil_div(cols, 64), 256))
     return PARARNN_ERR_UNSUPPORTED;
   const Room r = room(q->B, q->T, q->D, q->N, q->G, true);
