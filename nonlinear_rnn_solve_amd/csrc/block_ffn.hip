@@ -44,14 +44,18 @@ struct GemmArgs {
   void *c0, *c1;                // rows from `split` on go to c1
   int64_t sc0, sc1, split;
   void* pre;
+  float* sums;                  // of parts of k
+  int64_t per_part;
+  int32_t parts;
 };
 
-// 16 bytes of a row from element k on, zeros past its n elements or where the row is none
-template <typename T> DEV v4u load16(const T* row, int64_t k, int64_t n, bool there) {
+// 16 bytes of a row from element k on, zeros past its n elements
+template <typename T> DEV v4u load16(const T* row, int64_t k, int64_t n) {
   constexpr int V = 16 / sizeof(T);
-  const Vec<T, V> v = load_row<T, V>(row + k, there ? n - k : 0, T{});
+  const Vec<T, V> v = load_row<T, V>(row + k, n - k, T{});
   return v4u{v.w[0], v.w[1], v.w[2], v.w[3]};
 }
+DEV int64_t at_most(int64_t i, int64_t last) { return i < last ? i : last; }
 
 // the products of 16 bytes of k of each lane: 32 rows by 32 columns, two lanes a row (their halves of k)
 template <typename T> DEV void mma(const v4u& a, const v4u& b, v16f& c) {
@@ -66,56 +70,138 @@ template <typename T> DEV void mma(const v4u& a, const v4u& b, v16f& c) {
 // row of value i of a lane's 16 (its column is the lane modulo 32)
 DEV int row_of_acc(int i, int lane) { return 8 * (i / 4) + 4 * (lane / 32) + i % 4; }
 
-// A workgroup of four waves forms 128 by 128 of C (forward: 128 by 64 of both products), each wave 64 by 64.  The next
-// tile's rows are in registers while this one is multiplied from shared memory; its 16-byte pieces are exchanged within a row by the row's
-// number, so that no two of the eight lanes that read together meet in a bank.  Any alignment and size.
-template <typename T, bool GATED, int ACT>
-__global__ __launch_bounds__(256) void k_gemm(const GemmArgs p, uint32_t mtiles) {
-  constexpr int V = 16 / sizeof(T), BK = kKBytes / sizeof(T);
-  __shared__ v4u sa[128][8], sb[128][8];
+// What a wave does with 32 by 32 of results of the lanes' rows and columns.  GATED: of the gate's and of the other product's at once.
+template <typename T, int ACT> DEV void put_gated(const GemmArgs& p, int64_t m, int64_t n, float g, float u) {
+  if (m >= p.M || n >= p.N) return;
+  static_cast<T*>(p.c0)[m * p.sc0 + n] = from_f32<T>(act<ACT>(g) * u);
+  if (p.pre) {
+    T* pre = static_cast<T*>(p.pre) + m * 2 * p.N + n;
+    pre[0] = from_f32<T>(g);
+    pre[p.N] = from_f32<T>(u);
+  }
+}
+template <typename T> DEV void put_plain(const GemmArgs& p, int64_t m, int64_t n, float v) {
+  if (m >= p.M || n >= p.N) return;
+  T* c = m < p.split ? static_cast<T*>(p.c0) + m * p.sc0 : static_cast<T*>(p.c1) + (m - p.split) * p.sc1;
+  c[n] = from_f32<T>(v);
+}
+
+// ---- any alignment and size ----
+// A workgroup of four waves forms 128 by BN of C (forward: 128 by BN / 2 of both products), each wave 64 by BN / 2.  The next tile's
+// rows are in registers while this one is multiplied from shared memory; its 16-byte pieces are exchanged within a row by the
+// row's number, so that no two of the lanes that read together meet in a bank.  Rows past the end are read as the last.  With p.parts > 1 the workgroups split k, and
+// each writes float32 sums of its own to p.sums, [parts][M][N].
+//
+// Float32.  The matrix units multiply bfloat16 16 times as fast as float32.  A float32 is the exact sum of three bfloat16 of eight
+// bits each (its leading bits, cut off, then those of the rest); of the nine products of two such numbers the six that are
+// larger than 2^-24 of theirs are formed, exactly, and summed in float32 like any product's terms.  That is float32's accuracy at 2.7
+// times its rate: 6 instructions of 32 cycles in place of 8 of 64.  (An infinity less itself is a NaN: a float32
+// infinity makes its row's or column's results NaN.)
+template <typename T> struct Parts {
+  static constexpr int PL = sizeof(T) == 4 ? 3 : 1;             // numbers that make one
+  static constexpr int CPR = sizeof(T) == 4 ? 4 : 8;            // 16-byte pieces of a row in shared memory
+  static DEV int swap(int r, int c) { return CPR == 8 ? c ^ (r & 7) : c ^ (r >> 2 & 3); }
+};
+DEV uint32_t upper_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }   // a's, then b's
+DEV void split3(const v4u& x, uint32_t (&hi)[2], uint32_t (&mid)[2], uint32_t (&lo)[2]) {
+  float r[4], q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = __uint_as_float(x[i]) - __uint_as_float(x[i] & 0xffff0000u);
+    q[i] = r[i] - __uint_as_float(__float_as_uint(r[i]) & 0xffff0000u);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    hi[i] = upper_halves(x[2 * i], x[2 * i + 1]);
+    mid[i] = upper_halves(__float_as_uint(r[2 * i]), __float_as_uint(r[2 * i + 1]));
+    lo[i] = upper_halves(__float_as_uint(q[2 * i]), __float_as_uint(q[2 * i + 1]));
+  }
+}
+// 16 bytes that a thread has loaded (piece c of the 8 of row r) to shared memory of ROWS rows
+template <typename T, int ROWS> DEV void put16(v4u (*to)[ROWS][Parts<T>::CPR], int r, int c, const v4u& v) {
+  if constexpr (sizeof(T) == 2) {
+    to[0][r][Parts<T>::swap(r, c)] = v;
+  } else {
+    uint32_t part[3][2];
+    split3(v, part[0], part[1], part[2]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      using v2u = uint32_t __attribute__((ext_vector_type(2)));
+      reinterpret_cast<v2u*>(&to[k][r][Parts<T>::swap(r, c / 2)])[c & 1] = v2u{part[k][0], part[k][1]};
+    }
+  }
+}
+template <typename T, int BN, bool GATED, int ACT>
+__global__ __launch_bounds__(256) void k_gemm(const GemmArgs p, uint32_t mtiles, uint32_t tiles) {
+  constexpr int V = 16 / sizeof(T), BK = kKBytes / sizeof(T), NF = BN / 64;   // NF: 32-column pieces of a wave
+  constexpr int PL = Parts<T>::PL, CPR = Parts<T>::CPR;
+  static_assert(BN == 64 || BN == 128, "pieces of 32 columns for two waves");
+  __shared__ v4u sa[PL][128][CPR], sb[PL][BN][CPR];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
-  const int64_t mt = blockIdx.x % mtiles, nt = blockIdx.x / mtiles;
-  const int64_t m0 = mt * 128, n0 = nt * (GATED ? 64 : 128);
+  const uint32_t part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
+  const int64_t mt = tile % mtiles, nt = tile / mtiles;
+  const int64_t m0 = mt * 128, n0 = nt * (GATED ? BN / 2 : BN);
+  const int64_t k_begin = part * p.per_part, k_end = k_begin + p.per_part < p.K ? k_begin + p.per_part : p.K;
   const T* a = static_cast<const T*>(p.a);
-  v4u ra[4], rb[4];
+  v4u ra[4], rb[BN / 32];
   const auto load = [&](int64_t k0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int id = threadIdx.x + i * 256, r = id / 8, c = id % 8;
-      ra[i] = load16<T>(a + (m0 + r) * p.sa, k0 + c * V, p.K, m0 + r < p.M);
-      const bool second = GATED && r >= 64;
-      const int64_t n = n0 + (second ? r - 64 : r);
+      ra[i] = load16<T>(a + at_most(m0 + r, p.M - 1) * p.sa, k0 + c * V, k_end);
+    }
+#pragma unroll
+    for (int i = 0; i < BN / 32; ++i) {
+      const int id = threadIdx.x + i * 256, r = id / 8, c = id % 8;
+      const bool second = GATED && r >= BN / 2;
+      const int64_t n = at_most(n0 + (second ? r - BN / 2 : r), p.N - 1);
       const T* b = static_cast<const T*>(second ? p.b1 : p.b0);
-      rb[i] = load16<T>(b + n * (second ? p.sb1 : p.sb0), k0 + c * V, p.K, n < p.N);
+      rb[i] = load16<T>(b + n * (second ? p.sb1 : p.sb0), k0 + c * V, k_end);
     }
   };
-  v16f acc[2][2] = {};
-  load(0);
-  for (int64_t k0 = 0; k0 < p.K; k0 += BK) {
+  v16f acc[2][NF] = {};
+  load(k_begin);
+  for (int64_t k0 = k_begin; k0 < k_end; k0 += BK) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int id = threadIdx.x + i * 256, r = id / 8, c = id % 8;
-      sa[r][c ^ (r & 7)] = ra[i];
-      sb[r][c ^ (r & 7)] = rb[i];
+      put16<T, 128>(sa, r, c, ra[i]);
+      if (i < BN / 32) put16<T, BN>(sb, r, c, rb[i < BN / 32 ? i : 0]);
     }
     __syncthreads();
-    if (k0 + BK < p.K) load(k0 + BK);
+    if (k0 + BK < k_end) load(k0 + BK);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      v4u fa[2], fb[2];
+    for (int kk = 0; kk < CPR / 2; ++kk) {
+      v4u fa[2][PL], fb[NF][PL];
+      const int c = kk * 2 + lane / 32;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = wm * 64 + i * 32 + (lane & 31);
-        // gated: 32 columns of the gate, then the same of the other product
-        const int n = GATED ? i * 64 + wn * 32 + (lane & 31) : wn * 64 + i * 32 + (lane & 31);
-        const int c = kk * 2 + lane / 32;
-        fa[i] = sa[r][c ^ (r & 7)];
-        fb[i] = sb[n][c ^ (n & 7)];
+#pragma unroll
+        for (int q = 0; q < PL; ++q) fa[i][q] = sa[q][r][Parts<T>::swap(r, c)];
+      }
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        // gated, two pieces: 32 columns of the gate, then the same of the other product; one piece: 16 of each
+        const int n = GATED ? (NF == 2 ? j * 64 + wn * 32 + (lane & 31) : (lane >> 4 & 1) * 32 + wn * 16 + (lane & 15))
+                            : wn * (BN / 2) + j * 32 + (lane & 31);
+#pragma unroll
+        for (int q = 0; q < PL; ++q) fb[j][q] = sb[q][n][Parts<T>::swap(n, c)];
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) mma<T>(fa[i], fb[j], acc[i][j]);
+        for (int j = 0; j < NF; ++j) {
+          // the small products first
+          if constexpr (PL == 3) {
+            mma<bf16>(fa[i][2], fb[j][0], acc[i][j]);
+            mma<bf16>(fa[i][0], fb[j][2], acc[i][j]);
+            mma<bf16>(fa[i][1], fb[j][1], acc[i][j]);
+            mma<bf16>(fa[i][1], fb[j][0], acc[i][j]);
+            mma<bf16>(fa[i][0], fb[j][1], acc[i][j]);
+          }
+          mma<bf16>(fa[i][0], fb[j][0], acc[i][j]);
+        }
     }
     __syncthreads();
   }
@@ -124,66 +210,297 @@ __global__ __launch_bounds__(256) void k_gemm(const GemmArgs p, uint32_t mtiles)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int64_t m = m0 + wm * 64 + i * 32 + row_of_acc(e, lane);
-      if (m >= p.M) continue;
-      if constexpr (GATED) {
-        const int64_t n = n0 + wn * 32 + (lane & 31);
-        if (n >= p.N) continue;
-        const float g = acc[i][0][e], u = acc[i][1][e];
-        static_cast<T*>(p.c0)[m * p.sc0 + n] = from_f32<T>(act<ACT>(g) * u);
-        if (p.pre) {
-          T* pre = static_cast<T*>(p.pre) + m * 2 * p.N + n;
-          pre[0] = from_f32<T>(g);
-          pre[p.N] = from_f32<T>(u);
-        }
+      if constexpr (GATED && NF == 2) {
+        put_gated<T, ACT>(p, m, n0 + wn * 32 + (lane & 31), acc[i][0][e], acc[i][1][e]);
+      } else if constexpr (GATED) {
+        const float u = __shfl_xor(acc[i][0][e], 16);      // of the lane with the same column of the other product
+        if (!(lane & 16)) put_gated<T, ACT>(p, m, n0 + wn * 16 + (lane & 15), acc[i][0][e], u);
       } else {
-        T* c = m < p.split ? static_cast<T*>(p.c0) + m * p.sc0 : static_cast<T*>(p.c1) + (m - p.split) * p.sc1;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int64_t n = n0 + wn * 64 + j * 32 + (lane & 31);
-          if (n < p.N) c[n] = from_f32<T>(acc[i][j][e]);
+        for (int j = 0; j < NF; ++j) {
+          const int64_t n = n0 + wn * (BN / 2) + j * 32 + (lane & 31);
+          if (p.parts > 1) {
+            if (m < p.M && n < p.N) p.sums[(part * p.M + m) * p.N + n] = acc[i][j][e];
+          } else {
+            put_plain<T>(p, m, n, acc[i][j][e]);
+          }
         }
       }
     }
 }
+// C from the parts' sums, added in order
+template <typename T> __global__ __launch_bounds__(256) void k_join(const GemmArgs p) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, size = p.M * p.N;
+  if (i >= size) return;
+  float s = p.sums[i];
+  for (int32_t k = 1; k < p.parts; ++k) s += p.sums[k * size + i];
+  const int64_t m = i / p.N;
+  put_plain<T>(p, m, i - m * p.N, s);
+}
+
+// ---- large, aligned, bfloat16 ----
+// 256 by 256 of C (forward: 256 by 128 of both products) a workgroup of eight waves, two by four, each 128 by 64.  With 64 by 64 a
+// wave, as above, shared memory has to give 128 bytes a cycle, all that it has; here it is 96.  Four stages of 64 bytes of k
+// lie in shared memory: the loads go there past the registers, and those of the next three stages are in flight while one is
+// multiplied, with one barrier a stage.  A load puts down its lanes' 16 bytes in a row, so the exchange that keeps reads off each other's banks
+// is made by which piece each lane asks for: rows of 64 bytes, four a bank turn, pieces exchanged by the quarter row number.
+// Rows past the end are read as the last and left out of the result.  k is a multiple of the stage, everything 16-byte aligned.
+// Neighbouring tiles share rows and columns: each of the eight L2 caches gets a run of tiles of its own, in bands of eight rows of tiles.
+constexpr int kStages = 4, kStageBytes = 512 * 64;
+DEV void load_to_lds(const void* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+// all but the newest n loads have landed, all reads of the past stage are done, in every wave
+template <int N> DEV void stage_ready() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+template <bool GATED, int ACT>
+__global__ __launch_bounds__(512) void k_gemm_large(const GemmArgs p, uint32_t mtiles, uint32_t ntiles) {
+  using T = bf16;
+  constexpr int BK = 64 / sizeof(T);
+  __shared__ __attribute__((aligned(128))) char smem[kStages * kStageBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
+  // the tile: a run of tiles for each XCD (the block number modulo 8), in bands
+  const uint32_t tiles = mtiles * ntiles, xcd = blockIdx.x & 7, q = tiles >> 3, r8 = tiles & 7;
+  const uint32_t id = xcd * q + (xcd < r8 ? xcd : r8) + (blockIdx.x >> 3);
+  const uint32_t band = id / (8 * ntiles), in = id - band * (8 * ntiles), rows = mtiles - band * 8 < 8 ? mtiles - band * 8 : 8;
+  const int64_t m0 = static_cast<int64_t>(band * 8 + in % rows) * 256, n0 = static_cast<int64_t>(in / rows) * (GATED ? 128 : 256);
+
+  // wave w loads the rows w 32 .. w 32 + 31 of A and of B, 16 a load: lane l has piece l % 4 of row l / 4
+  const T* from[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = wave * 32 + (i & 1) * 16 + lane / 4, c = (lane & 3) ^ (r >> 2 & 3);
+    if (i < 2) {
+      int64_t m = m0 + r;
+      m = m < p.M ? m : p.M - 1;
+      from[i] = static_cast<const T*>(p.a) + m * p.sa + c * (16 / sizeof(T));
+    } else {
+      const bool second = GATED && r >= 128;
+      int64_t n = n0 + (second ? r - 128 : r);
+      n = n < p.N ? n : p.N - 1;
+      from[i] = static_cast<const T*>(second ? p.b1 : p.b0) + n * (second ? p.sb1 : p.sb0) + c * (16 / sizeof(T));
+    }
+  }
+  const uint32_t base = static_cast<uint32_t>((uintptr_t)(__attribute__((address_space(3))) char*)smem);   // its place in the LDS
+  const auto load = [&](int stage) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t row = (i >> 1) * 256 + wave * 32 + (i & 1) * 16;
+      load_to_lds(from[i], base + stage * kStageBytes + row * 64);
+      from[i] += BK;
+    }
+  };
+  const int64_t count = p.K / BK;
+  v16f acc[4][2] = {};
+  for (int s = 0; s < kStages - 1; ++s) load(s);                 // count >= kStages - 1 (checked)
+  const int half = lane / 32, l32 = lane & 31;
+  int stage = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    // the loads of the last stages: fewer are behind them
+    if (k + kStages - 1 <= count) stage_ready<4 * (kStages - 2)>();
+    else if (k + 2 == count) stage_ready<4>();
+    else stage_ready<0>();
+    if (k + kStages - 1 < count) load((stage + kStages - 1) % kStages);
+    const v4u* a = reinterpret_cast<const v4u*>(smem + stage * kStageBytes);
+    const v4u* b = a + 256 * 4;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      v4u fa[4], fb[2];
+      const int c = kk * 2 + half;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = wm * 128 + i * 32 + l32;
+        fa[i] = a[r * 4 + (c ^ (r >> 2 & 3))];
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = GATED ? j * 128 + wn * 32 + l32 : wn * 64 + j * 32 + l32;
+        fb[j] = b[n * 4 + (c ^ (n >> 2 & 3))];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mma<T>(fa[i], fb[j], acc[i][j]);
+    }
+    stage = (stage + 1) % kStages;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int64_t m = m0 + wm * 128 + i * 32 + row_of_acc(e, lane);
+      if constexpr (GATED) {
+        put_gated<T, ACT>(p, m, n0 + wn * 32 + l32, acc[i][0][e], acc[i][1][e]);
+      } else {
+        put_plain<T>(p, m, n0 + wn * 64 + l32, acc[i][0][e]);
+        put_plain<T>(p, m, n0 + wn * 64 + 32 + l32, acc[i][1][e]);
+      }
+    }
+}
+
+// ---- few rows ----
+// The weights are read once, from global memory straight into the matrix operands: a workgroup has 16 columns of the gate and the
+// same 16 of the other product side by side, and its eight waves take every eighth 128 bytes of k; a lane reads 64 of them,
+// four pieces that are four steps of k, x's rows alike.  The waves' sums meet in shared memory.  MT: 32-row pieces of x.
+// Rows beyond 64 are for other workgroups, eight blocks on (the same XCD), which read the weights again.
+template <typename T, int MT, int ACT>
+__global__ __launch_bounds__(512) void k_few_rows(const GemmArgs p, uint32_t groups) {
+  constexpr int V = 16 / sizeof(T), BK = kKBytes / sizeof(T), W = 8;
+  __shared__ float part[W * MT * 32 * 33];                      // 33: rows of 32 begin in banks of their own
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, half = lane / 32;
+  const uint32_t turn = blockIdx.x >> 3;
+  const int64_t f0 = (static_cast<int64_t>(turn / groups) * 8 + (blockIdx.x & 7)) * 16, m0 = static_cast<int64_t>(turn % groups) * (MT * 32);
+  if (f0 >= p.N) return;
+  int64_t f = f0 + (l32 & 15);
+  f = f < p.N ? f : p.N - 1;
+  const T* w = (l32 < 16 ? static_cast<const T*>(p.b0) + f * p.sb0 : static_cast<const T*>(p.b1) + f * p.sb1);
+  const T* x[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = m0 + i * 32 + l32;
+    x[i] = static_cast<const T*>(p.a) + (m < p.M ? m : p.M - 1) * p.sa;
+  }
+  v4u rw[2][4], rx[2][MT][4];
+  const auto load = [&](int64_t k0, v4u (&bw)[4], v4u (&bx)[MT][4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t k = k0 + (half * 4 + j) * V;
+      bw[j] = load16<T>(w, k, p.K);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) bx[i][j] = load16<T>(x[i], k, p.K);
+    }
+  };
+  v16f acc[MT] = {};
+  const auto multiply = [&](const v4u (&bw)[4], const v4u (&bx)[MT][4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) mma<T>(bx[i][j], bw[j], acc[i]);
+  };
+  int64_t k = static_cast<int64_t>(wave) * BK;
+  constexpr int64_t STEP = W * BK;
+  if (k < p.K) load(k, rw[0], rx[0]);
+  for (; k < p.K; k += 2 * STEP) {
+    if (k + STEP < p.K) load(k + STEP, rw[1], rx[1]);
+    multiply(rw[0], rx[0]);
+    if (k + STEP >= p.K) break;
+    if (k + 2 * STEP < p.K) load(k + 2 * STEP, rw[0], rx[0]);
+    multiply(rw[1], rx[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) part[((wave * MT + i) * 32 + row_of_acc(e, lane)) * 33 + l32] = acc[i][e];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int m = i * 32 + (threadIdx.x >> 4), c = threadIdx.x & 15;
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      g += part[(k * MT * 32 + m) * 33 + c];
+      u += part[(k * MT * 32 + m) * 33 + c + 16];
+    }
+    put_gated<T, ACT>(p, m0 + m, f0 + c, g, u);
+  }
+}
 
 // ---------------- what the gradients' products are made of ----------------
-// dg and du of R rows as [R][2 F] and as [2 F][Rp], zeros from R to Rp; 64 by 64 of each a workgroup
+// 64 by 64 values that go through shared memory to be written along their other dimension, 16 bytes a lane both ways.  Rows of an
+// odd number of words: the eight lanes that gather eight rows each, and the words of their columns, fall into banks of their own.
+template <typename T> struct Turn {
+  static constexpr int V = 16 / sizeof(T), PER = 64 / V, N = 64 * PER / 256;   // pieces of a row; pieces of a thread
+  static constexpr int ROW = 64 * sizeof(T) / 4 + 1;
+  uint32_t w[64 * ROW];
+  DEV void put(int r, int c, const v4u& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[r * ROW + c * 4 + i] = v[i];
+  }
+  // column c, rows V k .. V k + V - 1
+  DEV v4u get(int c, int k) const {
+    v4u v;
+    if constexpr (sizeof(T) == 2) {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = h[(k * 8 + 2 * i) * ROW * 2 + c] | static_cast<uint32_t>(h[(k * 8 + 2 * i + 1) * ROW * 2 + c]) << 16;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = w[(k * 4 + i) * ROW + c];
+    }
+    return v;
+  }
+};
+// the first n elements of 16 bytes
+template <typename T> DEV void store16(T* p, int64_t n, const v4u& v) {
+  constexpr int V = 16 / sizeof(T);
+  if (n >= V) {
+    LooseWords<T, V> q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = v[i];
+    *reinterpret_cast<LooseWords<T, V>*>(p) = q;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 2) p[i].u = static_cast<uint16_t>(v[i / 2] >> (i % 2 * 16));
+        else p[i] = __uint_as_float(v[i]);
+      }
+  }
+}
+
+// dg and du of R rows as [R][Fp2] and as [2 F][Rp], zeros from 2 F to Fp2 and from R to Rp; 64 by 64 of each a workgroup
 struct SplitArgs {
   const void *pre, *dh;
   int64_t sdh, R, F, Rp, Fp2;   // Fp2: row stride of `rows`
   void *rows, *cols;
 };
 template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_split(const SplitArgs p, uint32_t rtiles) {
-  __shared__ T tg[64][65], tu[64][65];
+  using L = Turn<T>;
+  __shared__ L tg, tu;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x % rtiles) * 64, f0 = static_cast<int64_t>(blockIdx.x / rtiles) * 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int64_t r = r0 + wave * 16 + i, f = f0 + lane;
-    float dg = 0.0f, du = 0.0f;
-    if (r < p.R && f < p.F) {
-      const T* pre = static_cast<const T*>(p.pre) + r * 2 * p.F + f;
-      const float g = to_f32(pre[0]), u = to_f32(pre[p.F]), dh = to_f32(static_cast<const T*>(p.dh)[r * p.sdh + f]);
-      dg = dh * u * slope<ACT>(g);
-      du = dh * act<ACT>(g);
-      if (p.rows) {
-        T* to = static_cast<T*>(p.rows) + r * p.Fp2 + f;
-        to[0] = from_f32<T>(dg);
-        to[p.F] = from_f32<T>(du);
-      }
+#pragma unroll
+  for (int k = 0; k < L::N; ++k) {
+    const int id = threadIdx.x + k * 256, i = id / L::PER, c = id % L::PER;
+    const int64_t r = r0 + i, f = f0 + c * L::V, n = r < p.R ? p.F - f : 0;
+    const T* pre = static_cast<const T*>(p.pre) + r * 2 * p.F + f;
+    const Vec<T, L::V> vg = load_row<T, L::V>(pre, n, T{}), vu = load_row<T, L::V>(pre + p.F, n, T{}),
+                       vh = load_row<T, L::V, true>(static_cast<const T*>(p.dh) + r * p.sdh + f, n, T{});
+    float dg[L::V], du[L::V];
+#pragma unroll
+    for (int e = 0; e < L::V; ++e) {
+      const float g = vg.get(e), dh = vh.get(e);
+      dg[e] = dh * vu.get(e) * slope<ACT>(g);
+      du[e] = dh * act<ACT>(g);
     }
-    tg[wave * 16 + i][lane] = from_f32<T>(dg);
-    tu[wave * 16 + i][lane] = from_f32<T>(du);
+    const Vec<T, L::V> og = pack_vec<T, L::V>(dg), ou = pack_vec<T, L::V>(du);
+    const v4u bg{og.w[0], og.w[1], og.w[2], og.w[3]}, bu{ou.w[0], ou.w[1], ou.w[2], ou.w[3]};
+    if (p.rows && n > 0) {
+      T* to = static_cast<T*>(p.rows) + r * p.Fp2 + f;
+      store16<T>(to, n, bg);
+      store16<T>(to + p.F, n, bu);
+    }
+    if (p.cols) {
+      tg.put(i, c, bg);
+      tu.put(i, c, bu);
+    }
+  }
+  if (p.rows && f0 == 0) {                                      // k's padding
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int i = 0; i < 16 && r0 + wave * 16 + i < p.R; ++i)
+      if (2 * p.F + lane < p.Fp2) static_cast<T*>(p.rows)[(r0 + wave * 16 + i) * p.Fp2 + 2 * p.F + lane] = T{};
   }
   if (!p.cols) return;
   __syncthreads();
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int64_t f = f0 + wave * 16 + i, r = r0 + lane;
-    if (f < p.F && r < p.Rp) {
+#pragma unroll
+  for (int k = 0; k < L::N; ++k) {
+    const int id = threadIdx.x + k * 256, c = id / L::PER, q = id % L::PER;
+    const int64_t f = f0 + c, r = r0 + q * L::V;
+    if (f < p.F) {
       T* to = static_cast<T*>(p.cols) + f * p.Rp + r;
-      to[0] = tg[lane][wave * 16 + i];
-      to[p.F * p.Rp] = tu[lane][wave * 16 + i];
+      store16<T>(to, p.Rp - r, tg.get(c, q));
+      store16<T>(to + p.F * p.Rp, p.Rp - r, tu.get(c, q));
     }
   }
 }
@@ -192,30 +509,85 @@ template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_spli
 template <typename T>
 __global__ __launch_bounds__(256) void k_transpose(const T* from, int64_t sf, int64_t R, int64_t C, T* to, int64_t st, int64_t Rp,
                                                    uint32_t rtiles) {
-  __shared__ T tile[64][65];
+  using L = Turn<T>;
+  __shared__ L tile;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x % rtiles) * 64, c0 = static_cast<int64_t>(blockIdx.x / rtiles) * 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int64_t r = r0 + wave * 16 + i, c = c0 + lane;
-    tile[wave * 16 + i][lane] = r < R && c < C ? from[r * sf + c] : T{};
+#pragma unroll
+  for (int k = 0; k < L::N; ++k) {
+    const int id = threadIdx.x + k * 256, i = id / L::PER, c = id % L::PER;
+    const int64_t r = r0 + i;
+    tile.put(i, c, load16<T>(from + r * sf, c0 + c * L::V, r < R ? C : 0));
   }
   __syncthreads();
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int64_t c = c0 + wave * 16 + i, r = r0 + lane;
-    if (c < C && r < Rp) to[c * st + r] = tile[lane][wave * 16 + i];
+#pragma unroll
+  for (int k = 0; k < L::N; ++k) {
+    const int id = threadIdx.x + k * 256, c = id / L::PER, q = id % L::PER;
+    const int64_t r = r0 + q * L::V;
+    if (c0 + c < C) store16<T>(to + (c0 + c) * st + r, Rp - r, tile.get(c, q));
   }
 }
 
 // ---------------- host ----------------
 inline int64_t padded(int64_t n) { return ceil_div(n, kPad) * kPad; }
-template <typename T, bool GATED, int ACT> static bool gemm(const GemmArgs& p, hipStream_t st) {
-  const int64_t mt = ceil_div(p.M, 128), nt = ceil_div(p.N, GATED ? 64 : 128);
-  if (mt == 0 || nt == 0) return true;
-  if (!grid_ok(mt * nt, 256)) return false;
-  k_gemm<T, GATED, ACT><<<dim3(static_cast<uint32_t>(mt * nt)), dim3(256), 0, st>>>(p, static_cast<uint32_t>(mt));
+constexpr int64_t kCus = 256, kMostParts = 8;
+// whether the large tiles are for C of M by N (forward: by 2 N): they have to fill the chip
+static bool large(int64_t M, int64_t N, bool gated) { return ceil_div(M, 256) * ceil_div(N, gated ? 128 : 256) >= kCus / 2; }
+static bool aligned16(const void* p, int64_t stride, size_t e) { return aligned(p, 16) && stride * static_cast<int64_t>(e) % 16 == 0; }
+// columns of a workgroup of k_gemm, and parts of k
+static int columns_of(int64_t M, int64_t N, bool gated) {
+  return ceil_div(M, 128) * ceil_div(N, gated ? 64 : 128) >= 4 * kCus ? 128 : 64;
+}
+static int64_t parts_of(size_t e, int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ceil_div(M, 128) * ceil_div(N, columns_of(M, N, false)), most = K * static_cast<int64_t>(e) / (8 * kKBytes);
+  if (tiles == 0 || tiles >= kCus) return 1;
+  return std::max<int64_t>(1, std::min({2 * kCus / tiles, most, kMostParts}));
+}
+
+template <typename T, int BN, bool GATED, int ACT> static bool gemm_of(const GemmArgs& p, hipStream_t st) {
+  const int64_t mt = ceil_div(p.M, 128), nt = ceil_div(p.N, GATED ? BN / 2 : BN);
+  if (!grid_ok(mt * nt * p.parts, 256)) return false;
+  k_gemm<T, BN, GATED, ACT><<<dim3(static_cast<uint32_t>(mt * nt * p.parts)), dim3(256), 0, st>>>(
+      p, static_cast<uint32_t>(mt), static_cast<uint32_t>(mt * nt));
   return true;
+}
+// `sums`: room for parts_of() M N floats, or null for one part
+template <typename T, bool GATED, int ACT> static bool gemm(GemmArgs p, float* sums, hipStream_t st) {
+  if (p.M == 0 || p.N == 0) return true;
+  const size_t e = sizeof(T);
+  p.parts = 1;
+  p.per_part = p.K;
+  if constexpr (sizeof(T) == 2) if (large(p.M, p.N, GATED) && p.K * static_cast<int64_t>(e) % 64 == 0 && p.K * static_cast<int64_t>(e) >= 64 * kStages &&
+      aligned16(p.a, p.sa, e) && aligned16(p.b0, p.sb0, e) && (!GATED || aligned16(p.b1, p.sb1, e))) {
+    const int64_t mt = ceil_div(p.M, 256), nt = ceil_div(p.N, GATED ? 128 : 256);
+    if (!grid_ok(mt * nt, 512)) return false;
+    k_gemm_large<GATED, ACT><<<dim3(static_cast<uint32_t>(mt * nt)), dim3(512), 0, st>>>(
+        p, static_cast<uint32_t>(mt), static_cast<uint32_t>(nt));
+    return true;
+  }
+  if (sums) {
+    const int64_t parts = parts_of(e, p.M, p.N, p.K), bk = kKBytes / e;
+    p.sums = sums;
+    p.per_part = ceil_div(ceil_div(p.K, parts), bk) * bk;
+    p.parts = p.K ? static_cast<int32_t>(ceil_div(p.K, p.per_part)) : 1;
+  }
+  if (!(columns_of(p.M, p.N, GATED) == 128 ? gemm_of<T, 128, GATED, ACT>(p, st) : gemm_of<T, 64, GATED, ACT>(p, st))) return false;
+  if (p.parts > 1) {
+    const int64_t blocks = ceil_div(p.M * p.N, 256);
+    if (!grid_ok(blocks, 256)) return false;
+    k_join<T><<<dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, st>>>(p);
+  }
+  return true;
+}
+constexpr int64_t kFewRows = 64;
+template <typename T, int MT, int ACT> static bool few_rows(const GemmArgs& p, hipStream_t st) {
+  const int64_t groups = ceil_div(p.M, MT * 32), blocks = ceil_div(ceil_div(p.N, 16), 8) * 8 * groups;
+  if (!grid_ok(blocks, 512)) return false;
+  k_few_rows<T, MT, ACT><<<dim3(static_cast<uint32_t>(blocks)), dim3(512), 0, st>>>(p, static_cast<uint32_t>(groups));
+  return true;
+}
+template <typename T, int ACT> static bool forward(const GemmArgs& p, hipStream_t st) {
+  if (p.M > kFewRows) return gemm<T, true, ACT>(p, nullptr, st);
+  return p.M <= 32 ? few_rows<T, 1, ACT>(p, st) : few_rows<T, 2, ACT>(p, st);
 }
 template <typename T> static bool transpose(const void* from, int64_t sf, int64_t R, int64_t C, T* to, int64_t st, int64_t Rp,
                                             hipStream_t stream) {
@@ -232,12 +604,15 @@ static bool sizes_ok(int64_t R, int64_t D, int64_t F) {
   return R >= 0 && D >= 0 && F >= 0 && (R > kMost || D > kMost || F > kMost || (sizes_fit(R, D) && sizes_fit(R, F, 2) && sizes_fit(F, D, 2)));
 }
 // elements of the gradient's workspace: d_pre [R][F2], d_pre^T [2 F][Rp], x^T [D][Rp], weights^T [D][F2]
+// and float32 sums of parts of k
 struct GradRoom {
-  int64_t F2, Rp, rows, cols, xt, wt;
-  int64_t total() const { return rows + cols + xt + wt; }
+  int64_t F2, Rp, rows, cols, xt, wt, sums;
+  int64_t bytes(size_t e) const { return (rows + cols + xt + wt) * static_cast<int64_t>(e) + sums * 4; }
 };
-static GradRoom grad_room(int64_t R, int64_t D, int64_t F) {
+static GradRoom grad_room(size_t e, int64_t R, int64_t D, int64_t F) {
   GradRoom g;
+  const int64_t px = parts_of(e, R, D, padded(2 * F)), pw = parts_of(e, 2 * F, D, padded(R));
+  g.sums = std::max(px > 1 ? px * R * D : 0, pw > 1 ? pw * 2 * F * D : 0);
   g.F2 = padded(2 * F), g.Rp = padded(R);
   g.rows = padded(R * g.F2), g.cols = padded(2 * F * g.Rp), g.xt = padded(D * g.Rp), g.wt = padded(D * g.F2);
   return g;
@@ -247,8 +622,9 @@ template <typename T, int ACT>
 static pararnn_status backward(int64_t R, int64_t D, int64_t F, const void* x, int64_t sx, const void* wg, int64_t sg, const void* wu,
                                int64_t su, const void* pre, const void* dh, int64_t sdh, void* dx, int64_t sdx, void* dwg,
                                int64_t sdg, void* dwu, int64_t sdu, T* ws, hipStream_t st) {
-  const GradRoom room = grad_room(R, D, F);
+  const GradRoom room = grad_room(sizeof(T), R, D, F);
   T *rows = ws, *cols = rows + room.rows, *xt = cols + room.cols, *wt = xt + room.xt;
+  float* sums = reinterpret_cast<float*>(wt + room.wt);
   const int64_t rt = ceil_div(room.Rp, 64), ft = ceil_div(F, 64);
   if (!grid_ok(rt * ft, 256)) return PARARNN_ERR_UNSUPPORTED;
   bool ok = true;
@@ -257,15 +633,14 @@ static pararnn_status backward(int64_t R, int64_t D, int64_t F, const void* x, i
     k_ffn_split<T, ACT><<<dim3(static_cast<uint32_t>(rt * ft)), dim3(256), 0, st>>>(s, static_cast<uint32_t>(rt));
   }
   if (dx && R && D) {
-    // the columns between 2 F and its padding are read by no product: k ends at 2 F
-    ok = ok && transpose<T>(wg, sg, F, D, wt, room.F2, F, st) && transpose<T>(wu, su, F, D, wt + F, room.F2, F, st);
-    GemmArgs p{rows, wt, nullptr, room.F2, room.F2, 0, R, D, 2 * F, dx, nullptr, sdx, 0, R, nullptr};
-    ok = ok && gemm<T, false, 0>(p, st);
+    ok = ok && transpose<T>(wg, sg, F, D, wt, room.F2, F, st) && transpose<T>(wu, su, F, D, wt + F, room.F2, room.F2 - F, st);
+    const GemmArgs p{rows, wt, nullptr, room.F2, room.F2, 0, R, D, room.F2, dx, nullptr, sdx, 0, R};
+    ok = ok && gemm<T, false, 0>(p, room.sums ? sums : nullptr, st);
   }
   if (dwg && F && D) {
     ok = ok && transpose<T>(x, sx, R, D, xt, room.Rp, room.Rp, st);
-    GemmArgs p{cols, xt, nullptr, room.Rp, room.Rp, 0, 2 * F, D, R, dwg, dwu, sdg, sdu, F, nullptr};
-    ok = ok && gemm<T, false, 0>(p, st);
+    const GemmArgs p{cols, xt, nullptr, room.Rp, room.Rp, 0, 2 * F, D, room.Rp, dwg, dwu, sdg, sdu, F};
+    ok = ok && gemm<T, false, 0>(p, room.sums ? sums : nullptr, st);
   }
   return ok ? launched() : PARARNN_ERR_UNSUPPORTED;
 }
@@ -276,7 +651,7 @@ using namespace lm;
 
 extern "C" size_t pararnn_block_gated_linear_workspace_bytes(int dtype, int64_t R, int64_t D, int64_t F, int gradient) {
   if (!dtype_ok(dtype) || !sizes_ok(R, D, F) || R > kMost || D > kMost || F > kMost) return 0;
-  return gradient ? static_cast<size_t>(grad_room(R, D, F).total()) * dtype_size(dtype) : 0;
+  return gradient ? static_cast<size_t>(grad_room(dtype_size(dtype), R, D, F).bytes(dtype_size(dtype))) : 0;
 }
 
 extern "C" pararnn_status pararnn_block_gated_linear(int dtype, int act, int64_t R, int64_t D, int64_t F, const void* x,
@@ -293,13 +668,13 @@ extern "C" pararnn_status pararnn_block_gated_linear(int dtype, int act, int64_t
   if (R > kMost || D > kMost || F > kMost) return PARARNN_ERR_UNSUPPORTED;
   if (!ws_ok(ws, ws_bytes, pararnn_block_gated_linear_workspace_bytes(dtype, R, D, F, 0))) return PARARNN_ERR_WORKSPACE;
   if (R == 0 || F == 0) return PARARNN_OK;
-  const GemmArgs p{x, w_gate, w_up, x_stride, gate_stride, up_stride, R, F, D, h, nullptr, h_stride, 0, R, pre};
+  const GemmArgs p{x, w_gate, w_up, x_stride, gate_stride, up_stride, R, F, D, h, nullptr, h_stride, 0, R, pre, nullptr, D, 1};
   const auto st = static_cast<hipStream_t>(stream);
   bool ok;
   if (dtype == PARARNN_BF16)
-    ok = act == PARARNN_BLOCK_SILU ? gemm<bf16, true, PARARNN_BLOCK_SILU>(p, st) : gemm<bf16, true, PARARNN_BLOCK_GELU>(p, st);
+    ok = act == PARARNN_BLOCK_SILU ? forward<bf16, PARARNN_BLOCK_SILU>(p, st) : forward<bf16, PARARNN_BLOCK_GELU>(p, st);
   else
-    ok = act == PARARNN_BLOCK_SILU ? gemm<float, true, PARARNN_BLOCK_SILU>(p, st) : gemm<float, true, PARARNN_BLOCK_GELU>(p, st);
+    ok = act == PARARNN_BLOCK_SILU ? forward<float, PARARNN_BLOCK_SILU>(p, st) : forward<float, PARARNN_BLOCK_GELU>(p, st);
   return ok ? launched() : PARARNN_ERR_UNSUPPORTED;
 }
 

@@ -80,6 +80,28 @@ def test_product_and_gradients(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(4353, 128, 1100), (4200, 256, 1040), (1100, 160, 4357)])
+def test_large_tiles(shape, dtype):
+    # 256 by 256 tiles (bfloat16, k of whole stages), their last rows and columns cut, and what is just not aligned for them
+    check(make(*shape, dtype, seed=9))
+
+
+def test_split_float32_keeps_what_float32_has():
+    # values whose 24 bits all matter, sums that cancel to their last ones: three products of 8-bit parts would leave 2^-16
+    g = torch.Generator().manual_seed(10)
+    x = torch.randn(40, 512, generator=g)
+    x[:, 256:] = -x[:, :256] * (1 + 2.0 ** -12)
+    w = torch.randn(48, 512, generator=g)
+    w[:, 256:] = w[:, :256]
+    x, w = x.repeat(5, 1).cuda(), w.cuda()
+    _, pre = block.gated_linear(x, w, w, want_pre=True)
+    want = f64(x) @ f64(w).t()
+    mag = f64(x).abs() @ f64(w).abs().t()
+    close(pre[:, :48], want, 514 * U32 * mag, "gate")
+    assert float((f64(pre[:, :48]) - want).norm()) <= 4 * U32 * float(mag.norm())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("shape", [(5, 40, 24), (70, 130, 96), (260, 256, 272)])
 def test_strides_and_gelu(shape, dtype):
     check(make(*shape, dtype, seed=2, layout="wide"), "gelu")
