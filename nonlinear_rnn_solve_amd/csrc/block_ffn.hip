@@ -539,8 +539,8 @@ static int columns_of(int64_t M, int64_t N, bool gated) {
 }
 static int64_t parts_of(size_t e, int64_t M, int64_t N, int64_t K) {
   const int64_t tiles = ceil_div(M, 128) * ceil_div(N, columns_of(M, N, false)), most = K * static_cast<int64_t>(e) / (8 * kKBytes);
-  if (tiles == 0 || tiles >= kCus) return 1;
-  return std::max<int64_t>(1, std::min({2 * kCus / tiles, most, kMostParts}));
+  if (tiles == 0) return 1;
+  return std::max<int64_t>(1, std::min({3 * kCus / tiles, most, kMostParts}));
 }
 
 template <typename T, int BN, bool GATED, int ACT> static bool gemm_of(const GemmArgs& p, hipStream_t st) {
