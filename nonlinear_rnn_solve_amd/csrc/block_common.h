@@ -32,17 +32,23 @@ DEV float silu(float p) { return p * sigmoid(p); }
 // d silu / dp, from p and its sigmoid
 DEV float silu_slope(float p, float s) { return s * fmaf(p, 1.0f - s, 1.0f); }
 
-// ---------------- column sums: out[m] = sum over rows of in[row][m], in one or two launches ----------------
-constexpr int64_t kSumRows = 256;     // rows that one workgroup adds up
+// ---------------- column sums: the sum over rows of in[row][col], put where `out` has it, in one or two launches ----------------
+constexpr int64_t kSumRows = 256;     // rows that one workgroup adds up where there are more than twice as many
 inline int64_t colsum_groups(int64_t rows) { return rows > 2 * kSumRows ? ceil_div(rows, kSumRows) : 1; }
 // floats of scratch for the sums of `rows` rows of `cols`
 inline int64_t colsum_floats(int64_t rows, int64_t cols) {
   const int64_t g = colsum_groups(rows);
   return g > 1 ? g * cols : 0;
 }
+struct ToScratch {
+  float* p;
+  int64_t cols;
+  DEV void operator()(int64_t group, int64_t col, float v) const { p[group * cols + col] = v; }
+};
 
-// 64 columns a workgroup, its four waves take every fourth row; sums in 64 bits, added in a fixed order.
-static __global__ __launch_bounds__(256) void k_colsum(const float* in, int64_t rows, int64_t cols, int64_t per, float* out) {
+// 64 columns a workgroup, its four waves take every fourth row; sums in 64 bits, added in a fixed order
+template <typename Out>
+static __global__ __launch_bounds__(256) void k_colsum(const float* in, int64_t rows, int64_t cols, int64_t per, const Out out) {
   __shared__ double part[4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t cblocks = (cols + 63) / 64, g = blockIdx.x / cblocks, col = (blockIdx.x - g * cblocks) * 64 + lane;
@@ -60,21 +66,21 @@ static __global__ __launch_bounds__(256) void k_colsum(const float* in, int64_t 
   }
   part[wave][lane] = a0 + a1;
   __syncthreads();
-  if (wave == 0 && col < cols)
-    out[g * cols + col] = static_cast<float>((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]));
+  if (wave == 0 && col < cols) out(g, col, static_cast<float>((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane])));
 }
 
 // `scratch`: colsum_floats() floats.  rows = 0 gives zeros.  False: the launch would be too large.
-inline bool colsum(const float* in, int64_t rows, int64_t cols, float* out, float* scratch, hipStream_t stream) {
+template <typename Out>
+inline bool colsum(const float* in, int64_t rows, int64_t cols, const Out& out, float* scratch, hipStream_t stream) {
   if (cols == 0) return true;
   const int64_t g = colsum_groups(rows), cb = ceil_div(cols, 64);
   if (!grid_ok(cb * g, 256)) return false;
-  if (g == 1) {
-    k_colsum<<<dim3(static_cast<uint32_t>(cb)), dim3(256), 0, stream>>>(in, rows, cols, rows, out);
-    return true;
+  if (g > 1) {
+    k_colsum<<<dim3(static_cast<uint32_t>(cb * g)), dim3(256), 0, stream>>>(in, rows, cols, kSumRows, ToScratch{scratch, cols});
+    in = scratch;
+    rows = g;
   }
-  k_colsum<<<dim3(static_cast<uint32_t>(cb * g)), dim3(256), 0, stream>>>(in, rows, cols, kSumRows, scratch);
-  k_colsum<<<dim3(static_cast<uint32_t>(cb)), dim3(256), 0, stream>>>(scratch, g, cols, g, out);
+  k_colsum<<<dim3(static_cast<uint32_t>(cb)), dim3(256), 0, stream>>>(in, rows, cols, rows, out);
   return true;
 }
 

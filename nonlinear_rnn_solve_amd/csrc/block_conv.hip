@@ -33,8 +33,10 @@ struct ConvGradArgs {
   const float* d_last;
   void* dx;
   int64_t sdy[2], sdx[2];
-  float* part;                  // [B chunks][K + 1][D]: sums over a chunk, the bias's last; or null
+  float* part;                  // [B groups][K + 1][D]: sums over a group of chunks, the bias's last; or null
   float* d_state;
+  int32_t log_quads;            // a workgroup's threads are 2^log_quads quads by chunks
+  int64_t groups, qgroups;      // groups of chunks of a row, of quads
 };
 
 // V float32 values of a row of n channels, `fill`ed past its end
@@ -159,14 +161,15 @@ __global__ __launch_bounds__(256) void k_conv(const ConvArgs p) {
 // Gradients.  dp_t = dy_t silu'(p_t);  a row's gradient is sum_k w[k] dp of the step k taps later, within its sequence, plus
 // d_last where it leaves as state.  A thread walks each sequence's part of its chunk [a, e) and the K - 1 steps after it, whose
 // dp it needs too (computed twice, by this chunk and the next), and gives out the gradient of the step K - 1 before; at a
-// sequence's start those are its state's.
+// sequence's start those are its state's.  A workgroup's threads are some quads of channels by as many chunks as make 256: it
+// adds up the parameters' sums of its chunks.
 template <typename T, int K, bool SEG>
 __global__ __launch_bounds__(256) void k_conv_vjp(const ConvGradArgs g) {
   const ConvArgs& p = g.f;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (id >= p.threads) return;
-  if (id >= p.main) {           // the states of empty sequences
-    const Place q = place(id - p.main, p.quads, p.seqs.n, p.D);
+  if (blockIdx.x >= p.main) {   // the states of empty sequences
+    const int64_t id = (blockIdx.x - p.main) * 256 + threadIdx.x;
+    if (id >= p.B * p.seqs.n * p.quads) return;
+    const Place q = place(id, p.quads, p.seqs.n, p.D);
     if (p.seqs.end(q.chunk) > p.seqs.begin(q.chunk)) return;
     for (int i = 0; i + 1 < K; ++i) {
       const int64_t at = ((q.b * p.seqs.n + q.chunk) * (K - 1) + i) * p.D + q.d;
@@ -176,10 +179,14 @@ __global__ __launch_bounds__(256) void k_conv_vjp(const ConvGradArgs g) {
     }
     return;
   }
-  const Place q = place(id, p.quads, p.chunks, p.D);
-  const int64_t t0 = q.chunk * p.L, t1 = p.T - t0 < p.L ? p.T : t0 + p.L;
+  const int lane_q = threadIdx.x & ((1 << g.log_quads) - 1), lane_c = threadIdx.x >> g.log_quads, rows = 256 >> g.log_quads;
+  const int64_t qg = blockIdx.x % g.qgroups, rest = blockIdx.x / g.qgroups, b = rest / g.groups, group = rest - b * g.groups;
+  Place q{b, group * rows + lane_c, ((qg << g.log_quads) + lane_q) * V, 0};
+  const bool there = q.d < p.D && q.chunk < p.chunks;
+  q.left = p.D - q.d;
+  const int64_t t0 = q.chunk * p.L, t1 = !there ? t0 : p.T - t0 < p.L ? p.T : t0 + p.L;
   float w[K][V], bias[V], dw[K][V] = {}, db[V] = {};
-  load_taps<K>(p, q.d, q.left, w, bias);
+  load_taps<K>(p, q.d, there ? q.left : 0, w, bias);
   const T* x = static_cast<const T*>(p.x) + q.b * p.sx[0] + q.d;
   const T* dy = static_cast<const T*>(g.dy) + q.b * g.sdy[0] + q.d;
   T* dx = static_cast<T*>(g.dx) + q.b * g.sdx[0] + q.d;
@@ -253,25 +260,38 @@ __global__ __launch_bounds__(256) void k_conv_vjp(const ConvGradArgs g) {
     }
     a = e;
   }
-  if (g.part) {
-    float* part = g.part + (q.b * p.chunks + q.chunk) * (K + 1) * p.D + q.d;
+  if (g.part) {                 // uniform
+    __shared__ float4 sums[256];
+    float* part = g.part + (b * g.groups + group) * (K + 1) * p.D + q.d;
 #pragma unroll
-    for (int k = 0; k < K; ++k) store_f(part + k * p.D, q.left, dw[k]);
-    store_f(part + K * p.D, q.left, db);
+    for (int k = 0; k <= K; ++k) {
+      const float* v = k < K ? dw[k < K ? k : 0] : db;
+      sums[threadIdx.x] = make_float4(v[0], v[1], v[2], v[3]);
+      __syncthreads();
+      if (lane_c == 0 && q.d < p.D) {
+        float o[V] = {};
+        for (int c = 0; c < rows; ++c) {
+          const float4 e = sums[(c << g.log_quads) + lane_q];
+          o[0] += e.x, o[1] += e.y, o[2] += e.z, o[3] += e.w;
+        }
+        store_f(part + k * p.D, q.left, o);
+      }
+      __syncthreads();
+    }
   }
 }
 
-// the column sums [K + 1][D] as d_weight [D][K] and d_bias [D]
-__global__ __launch_bounds__(256) void k_conv_params(const float* sums, int64_t D, int32_t K, float* d_weight, float* d_bias) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= D * (K + 1)) return;
-  const int64_t k = i / D, d = i - k * D;
-  if (k < K) {
-    if (d_weight) d_weight[d * K + k] = sums[i];
-  } else if (d_bias) {
-    d_bias[d] = sums[i];
+// where the column sums [K + 1][D] go: d_weight [D][K] and d_bias [D]
+struct ToTaps {
+  int64_t D;
+  int32_t K;
+  float *d_weight, *d_bias;
+  DEV void operator()(int64_t, int64_t i, float v) const {
+    const int64_t k = i / D, d = i - k * D;
+    float* to = k < K ? d_weight : d_bias;
+    if (to) to[k < K ? d * K + k : d] = v;
   }
-}
+};
 
 // ---------------- host ----------------
 // Steps of a chunk: as many as leave `want` threads, since longer chunks read and compute fewer shared rows
@@ -319,7 +339,7 @@ template <typename T, int K> static pararnn_status forward_k(const ConvArgs& p, 
   return launched();
 }
 template <typename T, int K> static pararnn_status backward_k(const ConvGradArgs& g, hipStream_t stream) {
-  const int64_t blocks = ceil_div(g.f.threads, 256);
+  const int64_t blocks = g.f.threads;
   if (g.f.seqs.cu) k_conv_vjp<T, K, true><<<dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, stream>>>(g);
   else k_conv_vjp<T, K, false><<<dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, stream>>>(g);
   return launched();
@@ -343,15 +363,22 @@ template <typename A> static pararnn_status dispatch(int64_t K, int dtype, const
   }
 }
 
-// floats of the gradient's workspace: chunks' sums, the column sums' scratch and their result
+// the gradient's workgroups, and the floats of its workspace: groups' sums and the column sums' scratch
 struct Parts {
-  int64_t rows, cols, part, scratch;
+  int32_t L, log_quads;
+  int64_t chunks, groups, qgroups, rows, cols, part, scratch;
 };
 static Parts parts(int64_t B, int64_t T, int64_t D, int64_t K) {
   Parts s;
-  s.rows = B * ceil_div(T, gradient_steps(B, T, D));
+  s.L = gradient_steps(B, T, D);
+  s.chunks = ceil_div(T, s.L);
+  s.log_quads = 0;
+  while (s.log_quads < 5 && (INT64_C(1) << s.log_quads) < ceil_div(D, V)) ++s.log_quads;
+  s.groups = ceil_div(s.chunks, 256 >> s.log_quads);
+  s.qgroups = ceil_div(ceil_div(D, V), INT64_C(1) << s.log_quads);
+  s.rows = B * s.groups;
   s.cols = D * (K + 1);
-  s.part = s.rows * s.cols;
+  s.part = ceil_div(s.rows * s.cols, 64) * 64;
   s.scratch = colsum_floats(s.rows, s.cols);
   return s;
 }
@@ -363,7 +390,7 @@ using namespace lm;
 extern "C" size_t pararnn_block_conv_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t K) {
   if (!sizes_ok(B, T, D, K) || K > PARARNN_BLOCK_MAX_TAPS) return 0;
   const Parts s = parts(B, T, D, K);
-  return static_cast<size_t>(s.part + s.scratch + s.cols) * sizeof(float) + 256;
+  return static_cast<size_t>(s.part + s.scratch) * sizeof(float);
 }
 
 extern "C" pararnn_status pararnn_block_causal_conv(const pararnn_block_conv* q, void* y, const int64_t sy[2], float* last,
@@ -417,27 +444,25 @@ extern "C" pararnn_status pararnn_block_causal_conv_vjp(const pararnn_block_conv
   ConvGradArgs g{};
   g.f = conv_args(q);
   ConvArgs& p = g.f;
-  p.L = gradient_steps(p.B, p.T, p.D);
-  p.chunks = ceil_div(p.T, p.L);
-  p.main = p.B * p.chunks * p.quads;
+  const Parts s = parts(p.B, p.T, p.D, q->K);
+  p.L = s.L, p.chunks = s.chunks;
+  g.log_quads = s.log_quads, g.groups = s.groups, g.qgroups = s.qgroups;
+  p.main = s.rows * s.qgroups;  // workgroups here, and p.threads all of them
   g.dy = grad->dy, g.d_last = grad->d_last, g.dx = grad->d_x;
   for (int k = 0; k < 2; ++k) g.sdy[k] = grad->sdy[k], g.sdx[k] = grad->sdx[k];
   g.d_state = q->K > 1 ? grad->d_state : nullptr;
-  const Parts s = parts(p.B, p.T, p.D, q->K);
   float* base = static_cast<float*>(ws);
   if (params) g.part = base;
-  p.threads = p.main + (g.d_state && (p.seqs.cu || p.T == 0) ? p.B * p.seqs.n * p.quads : 0);
-  if (!grid_ok(ceil_div(p.threads, 256), 256) || !grid_ok(ceil_div(s.cols, 256), 256)) return PARARNN_ERR_UNSUPPORTED;
+  p.threads = p.main + (g.d_state && (p.seqs.cu || p.T == 0) ? ceil_div(p.B * p.seqs.n * p.quads, 256) : 0);
+  if (!grid_ok(p.threads, 256)) return PARARNN_ERR_UNSUPPORTED;
   const auto st = static_cast<hipStream_t>(stream);
   if (p.threads) {
     const pararnn_status r = dispatch(q->K, q->dtype, g, st);
     if (r != PARARNN_OK) return r;
   }
   if (!params) return PARARNN_OK;
-  float* sums = base + s.part + s.scratch;
-  if (!colsum(base, s.rows, s.cols, sums, base + s.part, st)) return PARARNN_ERR_UNSUPPORTED;
-  k_conv_params<<<dim3(static_cast<uint32_t>(ceil_div(s.cols, 256))), dim3(256), 0, st>>>(sums, q->D, static_cast<int32_t>(q->K),
-                                                                                         grad->d_weight, grad->d_bias);
+  if (!colsum(base, s.rows, s.cols, ToTaps{q->D, static_cast<int32_t>(q->K), grad->d_weight, grad->d_bias}, base + s.part, st))
+    return PARARNN_ERR_UNSUPPORTED;
   return launched();
 }
 

@@ -4,6 +4,7 @@
 //   d_x = dg Wg + du Wu,  d_Wg = dg^T x,  d_Wu = du^T x
 
 #include <algorithm>
+#include <type_traits>
 
 #include "block_common.h"
 
@@ -239,25 +240,32 @@ template <typename T> __global__ __launch_bounds__(256) void k_join(const GemmAr
 }
 
 // ---- large, aligned, bfloat16 ----
-// 256 by 256 of C (forward: 256 by 128 of both products) a workgroup of eight waves, two by four, each 128 by 64.  With 64 by 64 a
-// wave, as above, shared memory has to give 128 bytes a cycle, all that it has; here it is 96.  Four stages of 64 bytes of k
-// lie in shared memory: the loads go there past the registers, and those of the next three stages are in flight while one is
-// multiplied, with one barrier a stage.  A load puts down its lanes' 16 bytes in a row, so the exchange that keeps reads off each other's banks
-// is made by which piece each lane asks for: rows of 64 bytes, four a bank turn, pieces exchanged by the quarter row number.
-// Rows past the end are read as the last and left out of the result.  k is a multiple of the stage, everything 16-byte aligned.
-// Neighbouring tiles share rows and columns: each of the eight L2 caches gets a run of tiles of its own, in bands of eight rows of tiles.
-constexpr int kStages = 4, kStageBytes = 512 * 64;
+// 256 by 256 of C (forward: 256 by 128 of both products) a workgroup of four waves, two by two, each 128 by 128 with its sums in 256
+// registers: the only wave of its SIMD.  Shared memory gives 128 bytes a cycle: with 64 by 64 a wave (above) the operands alone
+// take all of them, with 128 by 64 (eight waves) 96 and the loads' 32 the rest; here 64 and 32.  Two stages of 128 bytes of k
+// lie in shared memory: the loads go there past the registers, those of one stage while the other is multiplied.  (Four stages of
+// 64 bytes ask for every cache line twice, and the cache between has forgotten it: OLD us.)  A load puts down
+// its lanes' 16 bytes in a row, so the exchange that keeps reads off each other's banks is made by which piece each lane asks
+// for.  Reads and loads are issued between the products, each of which keeps the matrix unit busy for eight instructions' time.
+// Rows past the end are read as the last and left out of the result.  k is a multiple of the stage, everything 16-byte
+// aligned.  Neighbouring tiles share rows and columns: each of the eight L2 caches gets a run of tiles of its own, in bands of
+// eight rows of tiles.
+constexpr int kStages = 2, kStageBytes = 512 * 128, kLoads = 16;   // loads of a thread for a stage
 DEV void load_to_lds(const void* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
 }
-// all but the newest n loads have landed, all reads of the past stage are done, in every wave
-template <int N> DEV void stage_ready() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+// all loads have landed, all reads of the past stage are done, in every wave
+DEV void stage_ready() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+template <int FROM, int TO, typename F> DEV void unrolled(F&& f) {
+  if constexpr (FROM < TO) {
+    f(std::integral_constant<int, FROM>{});
+    unrolled<FROM + 1, TO>(f);
+  }
 }
 template <bool GATED, int ACT>
-__global__ __launch_bounds__(512) void k_gemm_large(const GemmArgs p, uint32_t mtiles, uint32_t ntiles) {
+__global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_t mtiles, uint32_t ntiles) {
   using T = bf16;
-  constexpr int BK = 64 / sizeof(T);
+  constexpr int BK = 128 / sizeof(T);
   __shared__ __attribute__((aligned(128))) char smem[kStages * kStageBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
   // the tile: a run of tiles for each XCD (the block number modulo 8), in bands
@@ -266,75 +274,88 @@ __global__ __launch_bounds__(512) void k_gemm_large(const GemmArgs p, uint32_t m
   const uint32_t band = id / (8 * ntiles), in = id - band * (8 * ntiles), rows = mtiles - band * 8 < 8 ? mtiles - band * 8 : 8;
   const int64_t m0 = static_cast<int64_t>(band * 8 + in % rows) * 256, n0 = static_cast<int64_t>(in / rows) * (GATED ? 128 : 256);
 
-  // wave w loads the rows w 32 .. w 32 + 31 of A and of B, 16 a load: lane l has piece l % 4 of row l / 4
-  const T* from[4];
+  // wave w loads the rows w 64 .. w 64 + 63 of A and of B, 8 a load: lane l puts down piece l % 8 of row l / 8
+  const T* from[kLoads];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = wave * 32 + (i & 1) * 16 + lane / 4, c = (lane & 3) ^ (r >> 2 & 3);
-    if (i < 2) {
-      int64_t m = m0 + r;
-      m = m < p.M ? m : p.M - 1;
-      from[i] = static_cast<const T*>(p.a) + m * p.sa + c * (16 / sizeof(T));
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = wave * 64 + (i & 7) * 8 + lane / 8, c = (lane & 7) ^ (lane / 8);
+    if (i < 8) {
+      from[i] = static_cast<const T*>(p.a) + at_most(m0 + r, p.M - 1) * p.sa + c * (16 / sizeof(T));
     } else {
       const bool second = GATED && r >= 128;
-      int64_t n = n0 + (second ? r - 128 : r);
-      n = n < p.N ? n : p.N - 1;
+      const int64_t n = at_most(n0 + (second ? r - 128 : r), p.N - 1);
       from[i] = static_cast<const T*>(second ? p.b1 : p.b0) + n * (second ? p.sb1 : p.sb0) + c * (16 / sizeof(T));
     }
   }
-  const uint32_t base = static_cast<uint32_t>((uintptr_t)(__attribute__((address_space(3))) char*)smem);   // its place in the LDS
-  const auto load = [&](int stage) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t row = (i >> 1) * 256 + wave * 32 + (i & 1) * 16;
-      load_to_lds(from[i], base + stage * kStageBytes + row * 64);
-      from[i] += BK;
+  const uint32_t base = static_cast<uint32_t>((uintptr_t)(__attribute__((address_space(3))) char*)smem) + wave * 8192;   // in the LDS
+  // the stage that is next, to its place; behind the last one that one again, so that nothing branches (`step` is 0 then)
+  const auto load = [&](int stage, int step, auto which) {
+    constexpr int i = which;
+    load_to_lds(from[i], base + stage * kStageBytes + (i >> 3) * 32768 + (i & 7) * 1024);
+    from[i] += step;
+  };
+  const int count = static_cast<int>(p.K / BK), half = lane / 32, l32 = lane & 31;
+  v16f acc[4][4] = {};
+  struct Pieces { v4u a[4], b[4]; };
+  const auto read = [&](int stage, int kk, Pieces& f, auto which) {
+    constexpr int i = which;
+    const v4u* at = reinterpret_cast<const v4u*>(smem + stage * kStageBytes);
+    const int c = kk * 2 + half;
+    if constexpr (i < 4) {
+      const int r = wm * 128 + i * 32 + l32;
+      f.a[i] = at[r * 8 + (c ^ (r & 7))];
+    } else {
+      // gated: 64 columns of the gate, then the same of the other product
+      constexpr int j = i - 4;
+      const int n = GATED ? (j >> 1) * 128 + wn * 64 + (j & 1) * 32 + l32 : wn * 128 + j * 32 + l32;
+      f.b[j] = at[256 * 8 + n * 8 + (c ^ (n & 7))];
     }
   };
-  const int64_t count = p.K / BK;
-  v16f acc[4][2] = {};
-  for (int s = 0; s < kStages - 1; ++s) load(s);                 // count >= kStages - 1 (checked)
-  const int half = lane / 32, l32 = lane & 31;
-  int stage = 0;
-  for (int64_t k = 0; k < count; ++k) {
-    // the loads of the last stages: fewer are behind them
-    if (k + kStages - 1 <= count) stage_ready<4 * (kStages - 2)>();
-    else if (k + 2 == count) stage_ready<4>();
-    else stage_ready<0>();
-    if (k + kStages - 1 < count) load((stage + kStages - 1) % kStages);
-    const v4u* a = reinterpret_cast<const v4u*>(smem + stage * kStageBytes);
-    const v4u* b = a + 256 * 4;
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      v4u fa[4], fb[2];
-      const int c = kk * 2 + half;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = wm * 128 + i * 32 + l32;
-        fa[i] = a[r * 4 + (c ^ (r >> 2 & 3))];
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = GATED ? j * 128 + wn * 32 + l32 : wn * 64 + j * 32 + l32;
-        fb[j] = b[n * 4 + (c ^ (n >> 2 & 3))];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) mma<T>(fa[i], fb[j], acc[i][j]);
-    }
-    stage = (stage + 1) % kStages;
+  // the products of f, `beside(k)` after the k-th of the sixteen
+  const auto multiply = [&](const Pieces& f, auto&& beside) {
+    unrolled<0, 16>([&](auto which) {
+      constexpr int k = which;
+      mma<T>(f.a[k >> 2], f.b[k & 3], acc[k >> 2][k & 3]);
+      beside(which);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  // quarter kk of a stage, with the reads of the next one beside it
+  const auto quarter = [&](int stage, int kk, const Pieces& f, Pieces& next) {
+    multiply(f, [&](auto which) {
+      constexpr int k = which;
+      if constexpr (k % 2 == 0) read(stage, kk + 1, next, std::integral_constant<int, k / 2>{});
+    });
+  };
+  Pieces even, odd;
+  unrolled<0, kLoads>([&](auto i) { load(0, count > 1 ? BK : 0, i); });
+  stage_ready();
+  unrolled<0, kLoads>([&](auto i) { load(1, count > 2 ? BK : 0, i); });
+  unrolled<0, 8>([&](auto i) { read(0, 0, even, i); });
+#pragma unroll 1
+  for (int k = 0; k < count; ++k) {
+    const int stage = k & 1, step = k + 3 < count ? BK : 0;
+    quarter(stage, 0, even, odd);
+    quarter(stage, 1, odd, even);
+    quarter(stage, 2, even, odd);
+    // the last quarter's operands are in registers: when every wave is here, this stage's place is free, and the next one is there
+    stage_ready();
+    multiply(odd, [&](auto which) {
+      constexpr int i = which;
+      load(stage, step, which);
+      if constexpr (i % 2 == 0) read(stage ^ 1, 0, even, std::integral_constant<int, i / 2>{});
+    });
   }
+  stage_ready();                // nothing is on its way to shared memory when the workgroup ends
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int64_t m = m0 + wm * 128 + i * 32 + row_of_acc(e, lane);
-      if constexpr (GATED) {
-        put_gated<T, ACT>(p, m, n0 + wn * 32 + l32, acc[i][0][e], acc[i][1][e]);
-      } else {
-        put_plain<T>(p, m, n0 + wn * 64 + l32, acc[i][0][e]);
-        put_plain<T>(p, m, n0 + wn * 64 + 32 + l32, acc[i][1][e]);
+#pragma unroll
+      for (int j = 0; j < (GATED ? 2 : 4); ++j) {
+        if constexpr (GATED) put_gated<T, ACT>(p, m, n0 + wn * 64 + j * 32 + l32, acc[i][j][e], acc[i][j + 2][e]);
+        else put_plain<T>(p, m, n0 + wn * 128 + j * 32 + l32, acc[i][j][e]);
       }
     }
 }
@@ -450,10 +471,11 @@ template <typename T> DEV void store16(T* p, int64_t n, const v4u& v) {
   }
 }
 
-// dg and du of R rows as [R][Fp2] and as [2 F][Rp], zeros from 2 F to Fp2 and from R to Rp; 64 by 64 of each a workgroup
+// dg and du of R rows as [R][F2] and as [2 F][Rp], zeros from 2 F to F2 and from R to Rp; 64 by 64 of each a workgroup
 struct SplitArgs {
   const void *pre, *dh;
-  int64_t sdh, R, F, Rp, Fp2;   // Fp2: row stride of `rows`
+  int64_t sdh, R, F;
+  int64_t Rp, Rs, F2, Fs;       // lengths of a row of `cols` and of `rows` with their zeros, and row strides
   void *rows, *cols;
 };
 template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_split(const SplitArgs p, uint32_t rtiles) {
@@ -477,7 +499,7 @@ template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_spli
     const Vec<T, L::V> og = pack_vec<T, L::V>(dg), ou = pack_vec<T, L::V>(du);
     const v4u bg{og.w[0], og.w[1], og.w[2], og.w[3]}, bu{ou.w[0], ou.w[1], ou.w[2], ou.w[3]};
     if (p.rows && n > 0) {
-      T* to = static_cast<T*>(p.rows) + r * p.Fp2 + f;
+      T* to = static_cast<T*>(p.rows) + r * p.Fs + f;
       store16<T>(to, n, bg);
       store16<T>(to + p.F, n, bu);
     }
@@ -489,7 +511,7 @@ template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_spli
   if (p.rows && f0 == 0) {                                      // k's padding
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int i = 0; i < 16 && r0 + wave * 16 + i < p.R; ++i)
-      if (2 * p.F + lane < p.Fp2) static_cast<T*>(p.rows)[(r0 + wave * 16 + i) * p.Fp2 + 2 * p.F + lane] = T{};
+      if (2 * p.F + lane < p.F2) static_cast<T*>(p.rows)[(r0 + wave * 16 + i) * p.Fs + 2 * p.F + lane] = T{};
   }
   if (!p.cols) return;
   __syncthreads();
@@ -498,9 +520,9 @@ template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_spli
     const int id = threadIdx.x + k * 256, c = id / L::PER, q = id % L::PER;
     const int64_t f = f0 + c, r = r0 + q * L::V;
     if (f < p.F) {
-      T* to = static_cast<T*>(p.cols) + f * p.Rp + r;
+      T* to = static_cast<T*>(p.cols) + f * p.Rs + r;
       store16<T>(to, p.Rp - r, tg.get(c, q));
-      store16<T>(to + p.F * p.Rp, p.Rp - r, tu.get(c, q));
+      store16<T>(to + p.F * p.Rs, p.Rp - r, tu.get(c, q));
     }
   }
 }
@@ -556,11 +578,11 @@ template <typename T, bool GATED, int ACT> static bool gemm(GemmArgs p, float* s
   const size_t e = sizeof(T);
   p.parts = 1;
   p.per_part = p.K;
-  if constexpr (sizeof(T) == 2) if (large(p.M, p.N, GATED) && p.K * static_cast<int64_t>(e) % 64 == 0 && p.K * static_cast<int64_t>(e) >= 64 * kStages &&
+  if constexpr (sizeof(T) == 2) if (large(p.M, p.N, GATED) && p.K > 0 && p.K * static_cast<int64_t>(e) % kKBytes == 0 &&
       aligned16(p.a, p.sa, e) && aligned16(p.b0, p.sb0, e) && (!GATED || aligned16(p.b1, p.sb1, e))) {
     const int64_t mt = ceil_div(p.M, 256), nt = ceil_div(p.N, GATED ? 128 : 256);
-    if (!grid_ok(mt * nt, 512)) return false;
-    k_gemm_large<GATED, ACT><<<dim3(static_cast<uint32_t>(mt * nt)), dim3(512), 0, st>>>(
+    if (!grid_ok(mt * nt, 256)) return false;
+    k_gemm_large<GATED, ACT><<<dim3(static_cast<uint32_t>(mt * nt)), dim3(256), 0, st>>>(
         p, static_cast<uint32_t>(mt), static_cast<uint32_t>(nt));
     return true;
   }
@@ -603,10 +625,13 @@ constexpr int64_t kMost = INT32_MAX - 512;
 static bool sizes_ok(int64_t R, int64_t D, int64_t F) {
   return R >= 0 && D >= 0 && F >= 0 && (R > kMost || D > kMost || F > kMost || (sizes_fit(R, D) && sizes_fit(R, F, 2) && sizes_fit(F, D, 2)));
 }
-// elements of the gradient's workspace: d_pre [R][F2], d_pre^T [2 F][Rp], x^T [D][Rp], weights^T [D][F2]
+// Row stride of n elements in the workspace: not a large power of two, which would put the rows of a tile behind each other in few
+// of the memory's channels (8192 x 4096 x 8192: PADNOTE).
+static int64_t spread(int64_t n, size_t e) { return n * static_cast<int64_t>(e) % 4096 ? n : n + kPad; }
+// elements of the gradient's workspace: d_pre [R][F2], d_pre^T [2 F][Rp], x^T [D][Rp], weights^T [D][F2], with row strides Fs, Rs,
 // and float32 sums of parts of k
 struct GradRoom {
-  int64_t F2, Rp, rows, cols, xt, wt, sums;
+  int64_t F2, Rp, Fs, Rs, rows, cols, xt, wt, sums;
   int64_t bytes(size_t e) const { return (rows + cols + xt + wt) * static_cast<int64_t>(e) + sums * 4; }
 };
 static GradRoom grad_room(size_t e, int64_t R, int64_t D, int64_t F) {
@@ -614,7 +639,8 @@ static GradRoom grad_room(size_t e, int64_t R, int64_t D, int64_t F) {
   const int64_t px = parts_of(e, R, D, padded(2 * F)), pw = parts_of(e, 2 * F, D, padded(R));
   g.sums = std::max(px > 1 ? px * R * D : 0, pw > 1 ? pw * 2 * F * D : 0);
   g.F2 = padded(2 * F), g.Rp = padded(R);
-  g.rows = padded(R * g.F2), g.cols = padded(2 * F * g.Rp), g.xt = padded(D * g.Rp), g.wt = padded(D * g.F2);
+  g.Fs = spread(g.F2, e), g.Rs = spread(g.Rp, e);
+  g.rows = padded(R * g.Fs), g.cols = padded(2 * F * g.Rs), g.xt = padded(D * g.Rs), g.wt = padded(D * g.Fs);
   return g;
 }
 
@@ -629,17 +655,17 @@ static pararnn_status backward(int64_t R, int64_t D, int64_t F, const void* x, i
   if (!grid_ok(rt * ft, 256)) return PARARNN_ERR_UNSUPPORTED;
   bool ok = true;
   if (rt * ft) {
-    const SplitArgs s{pre, dh, sdh, R, F, room.Rp, room.F2, dx ? rows : nullptr, dwg ? cols : nullptr};
+    const SplitArgs s{pre, dh, sdh, R, F, room.Rp, room.Rs, room.F2, room.Fs, dx ? rows : nullptr, dwg ? cols : nullptr};
     k_ffn_split<T, ACT><<<dim3(static_cast<uint32_t>(rt * ft)), dim3(256), 0, st>>>(s, static_cast<uint32_t>(rt));
   }
   if (dx && R && D) {
-    ok = ok && transpose<T>(wg, sg, F, D, wt, room.F2, F, st) && transpose<T>(wu, su, F, D, wt + F, room.F2, room.F2 - F, st);
-    const GemmArgs p{rows, wt, nullptr, room.F2, room.F2, 0, R, D, room.F2, dx, nullptr, sdx, 0, R};
+    ok = ok && transpose<T>(wg, sg, F, D, wt, room.Fs, F, st) && transpose<T>(wu, su, F, D, wt + F, room.Fs, room.F2 - F, st);
+    const GemmArgs p{rows, wt, nullptr, room.Fs, room.Fs, 0, R, D, room.F2, dx, nullptr, sdx, 0, R};
     ok = ok && gemm<T, false, 0>(p, room.sums ? sums : nullptr, st);
   }
   if (dwg && F && D) {
-    ok = ok && transpose<T>(x, sx, R, D, xt, room.Rp, room.Rp, st);
-    const GemmArgs p{cols, xt, nullptr, room.Rp, room.Rp, 0, 2 * F, D, room.Rp, dwg, dwu, sdg, sdu, F};
+    ok = ok && transpose<T>(x, sx, R, D, xt, room.Rs, room.Rp, st);
+    const GemmArgs p{cols, xt, nullptr, room.Rs, room.Rs, 0, 2 * F, D, room.Rp, dwg, dwu, sdg, sdu, F};
     ok = ok && gemm<T, false, 0>(p, room.sums ? sums : nullptr, st);
   }
   return ok ? launched() : PARARNN_ERR_UNSUPPORTED;

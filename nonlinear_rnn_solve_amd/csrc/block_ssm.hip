@@ -243,6 +243,26 @@ DEV bool boundary(const Seqs& q, int32_t t, int32_t T) {
   return q.begin(q.of(t)) == t && q.of(t) > 0;
 }
 
+// A state carried over `count` (at most K of them here) segments from segment s on, in steps of `dir`: the loads of all before
+// the first is used
+constexpr int BATCH = 8;
+template <int NS, int K>
+DEV void over_segments(const SsmArgs& p, const Where& w, int32_t s, int32_t count, int dir, int32_t d, int n0, const float (&A2)[NS],
+                       float (&h)[NS]) {
+  float e[K][NS], total[K];
+  const int32_t D = static_cast<int32_t>(p.D);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int64_t at = (s + dir * (k < count ? k : count - 1)) * p.B + w.b;
+    load_nd<NS>(p.end + at * p.D * p.N + d, D, p.N, n0, e[k]);
+    total[k] = p.sum[at * p.D + d];
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[n] = k < count ? fmaf(hw_exp2(A2[n] * total[k]), h[n], e[k][n]) : h[n];
+}
+
 // ENDS: what each segment but the last leaves (from its last sequence's start, if one begins in it).  Otherwise the walk itself.
 template <typename T, int NS, int WV, bool ENDS>
 __global__ __launch_bounds__(WV * WAVE) void k_ssm(const SsmArgs p) {
@@ -281,13 +301,7 @@ __global__ __launch_bounds__(WV * WAVE) void k_ssm(const SsmArgs p) {
     int32_t s = from / (p.per * CT);
     const float* end = p.end + (s * p.B + w.b) * seq_step + d;
     load_nd<NS>(end, D_, p.N, n0, h);
-    for (++s; s < w.s; ++s) {
-      float e[NS];
-      load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, D_, p.N, n0, e);
-      const float total = in ? p.sum[(s * p.B + w.b) * p.D + d] : 0.0f;
-#pragma unroll
-      for (int n = 0; n < NS; ++n) h[n] = fmaf(hw_exp2(A2[n] * total), h[n], e[n]);
-    }
+    for (++s; s < w.s; s += BATCH) over_segments<NS, BATCH>(p, w, s, w.s - s, 1, d, n0, A2, h);
   }
   // the last sequence that begins in this segment: later segments' workgroups write over its h0 where that is h_last's place
   const int64_t last_seq = p.in_place && p.S > 1 ? p.seqs.of(tb - 1) : -1;
@@ -658,13 +672,7 @@ __global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) 
     stop = stop > tb ? stop : tb + 1;
     int32_t s = (stop - 1) / (p.per * CT);
     load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, D_, p.N, n0, P);
-    for (--s; s > w.s; --s) {
-      float e[NS];
-      load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, D_, p.N, n0, e);
-      const float total = in ? p.sum[(s * p.B + w.b) * p.D + d] : 0.0f;
-#pragma unroll
-      for (int n = 0; n < NS; ++n) P[n] = fmaf(hw_exp2(A2[n] * total), P[n], e[n]);
-    }
+    for (--s; s > w.s; s -= BATCH) over_segments<NS, BATCH>(p, w, s, s - w.s, -1, d, n0, A2, P);
   }
 
   Bits<T> x[E], dl[E], z[E], dy[E], vb[L::BC], vc[L::BC];
@@ -909,15 +917,17 @@ template <typename T> __global__ __launch_bounds__(256) void k_ssm_shared(const 
   if (k < p.N) static_cast<T*>(p.db)[b * p.sdb[0] + t * p.sdb[1] + g * p.sdb[2] + k] = from_f32<T>(s);
   else static_cast<T*>(p.dc)[b * p.sdc[0] + t * p.sdc[1] + g * p.sdc[2] + k - p.N] = from_f32<T>(s);
 }
-// the column sums [N + 2][D] as d_A [D][N], d_skip and d_dt_bias [D]
-__global__ __launch_bounds__(256) void k_ssm_params(const float* sums, int64_t D, int32_t N, float* d_A, float* d_skip,
-                                                    float* d_bias) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= D * (N + 2)) return;
-  const int64_t n = i / D, d = i - n * D;
-  float* to = n < N ? (d_A ? d_A + d * N + n : nullptr) : n == N ? (d_skip ? d_skip + d : nullptr) : (d_bias ? d_bias + d : nullptr);
-  if (to) *to = sums[i];
-}
+// where the column sums [N + 2][D] go: d_A [D][N], d_skip and d_dt_bias [D]
+struct ToParams {
+  int64_t D;
+  int32_t N;
+  float *d_A, *d_skip, *d_bias;
+  DEV void operator()(int64_t, int64_t i, float v) const {
+    const int64_t n = i / D, d = i - n * D;
+    float* to = n < N ? d_A : n == N ? d_skip : d_bias;
+    if (to) to[n < N ? d * N + n : d] = v;
+  }
+};
 // d_h0 of sequences without steps
 __global__ __launch_bounds__(256) void k_ssm_empty(const Seqs q, int64_t states, int64_t n, const float* d_last, float* d_h0) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -931,23 +941,26 @@ struct Split {
   int64_t ctiles, tiles, rows;   // channel tiles of a group, tiles of a row, workgroups without segments
   int64_t S, per;
 };
-// Segments of a row: as many as bring `want` workgroups, each of at least `least` tiles
-static Split split(int64_t B, int64_t T, int64_t D, int64_t G, int64_t want, int64_t least) {
+// Segments of a row: as many as bring `want` workgroups, each of at least kLeast tiles, where those without fill less than the chip
+// holds at a time.  bf16, N = 16, forward and gradient: B = 8, T = 2048, D = 2048 (256 workgroups) 228 and 593 us against 284 and 782
+// whole; B = 16 (512) 412 and 1155 against 353 and 1046.
+constexpr int64_t kFull = 448, kWant = 2048, kGradWant = 1536, kLeast = 2, kMost = 96;
+static Split split(int64_t B, int64_t T, int64_t D, int64_t G, int64_t want) {
   Split s;
   s.ctiles = ceil_div(D / G, CH);
   s.tiles = ceil_div(T, CT);
   s.rows = B * G * s.ctiles;
   int64_t n = 1;
-  if (s.rows && s.rows < want / 2) n = want / s.rows;
-  if (n > s.tiles / least) n = s.tiles / least;
+  if (s.rows && s.rows < kFull) n = want / s.rows;
+  if (n > s.tiles / kLeast) n = s.tiles / kLeast;
+  if (n > kMost) n = kMost;     // each is entered over those before it
   if (n < 1) n = 1;
   s.per = s.tiles ? ceil_div(s.tiles, n) : 1;
   s.S = s.tiles ? ceil_div(s.tiles, s.per) : 1;
   return s;
 }
-constexpr int64_t kWant = 2048, kGradWant = 1024, kLeast = 4;
-static Split forward_split(int64_t B, int64_t T, int64_t D, int64_t G) { return split(B, T, D, G, kWant, kLeast); }
-static Split gradient_split(int64_t B, int64_t T, int64_t D, int64_t G) { return split(B, T, D, G, kGradWant, kLeast); }
+static Split forward_split(int64_t B, int64_t T, int64_t D, int64_t G) { return split(B, T, D, G, kWant); }
+static Split gradient_split(int64_t B, int64_t T, int64_t D, int64_t G) { return split(B, T, D, G, kGradWant); }
 
 static bool sizes_ok(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G) {
   if (N < 1 || G < 1 || !sizes_fit(B, T, D) || (D > 0 && (G > D || D % G))) return false;
@@ -956,8 +969,8 @@ static bool sizes_ok(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G) {
          (B == 0 || T == 0 || N <= INT64_MAX / 64 / B / T / (D / 64 + G + 1));
 }
 struct Room {   // floats: the segments' parts, then (gradient) the sums
-  int64_t end, sum, head, bc, part, scratch, sums;
-  int64_t total() const { return end + sum + head + bc + part + scratch + sums; }
+  int64_t end, sum, head, bc, part, scratch;
+  int64_t total() const { return end + sum + head + bc + part + scratch; }
 };
 static int64_t round64(int64_t n) { return ceil_div(n, 64) * 64; }
 static Room room(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool gradient) {
@@ -973,7 +986,6 @@ static Room room(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G, bool gra
     r.bc = round64(G * s.ctiles * B * T * 2 * N);
     r.part = round64(rows * (N + 2) * D);
     r.scratch = round64(colsum_floats(rows, (N + 2) * D));
-    r.sums = round64((N + 2) * D);
   }
   return r;
 }
@@ -1130,7 +1142,7 @@ extern "C" pararnn_status pararnn_block_selective_scan_vjp(const pararnn_block_s
   g.part_bc = f;
   f += r.bc;
   g.part_A = f;
-  float *scratch = f + r.part, *sums = scratch + r.scratch;
+  float* scratch = f + r.part;
   g.carry = grad->carry, g.dy = grad->dy, g.d_last = grad->d_last, g.d_h0 = grad->d_h0;
   g.dx = grad->d_x, g.ddelta = grad->d_delta, g.dz = grad->d_z;
   for (int k = 0; k < 2; ++k)
@@ -1151,9 +1163,8 @@ extern "C" pararnn_status pararnn_block_selective_scan_vjp(const pararnn_block_s
     k_ssm_empty<<<dim3(static_cast<uint32_t>(ceil_div(n, 256))), dim3(256), 0, st>>>(p.seqs, states, n, grad->d_last, grad->d_h0);
   }
   if (grad->d_A || grad->d_skip || grad->d_dt_bias) {
-    if (!colsum(g.part_A, steps ? s.S * q->B : 0, cols, sums, scratch, st)) return PARARNN_ERR_UNSUPPORTED;
-    k_ssm_params<<<dim3(static_cast<uint32_t>(ceil_div(cols, 256))), dim3(256), 0, st>>>(sums, q->D, p.N, grad->d_A, grad->d_skip,
-                                                                                        grad->d_dt_bias);
+    const ToParams to{q->D, p.N, grad->d_A, grad->d_skip, grad->d_dt_bias};
+    if (!colsum(g.part_A, steps ? s.S * q->B : 0, cols, to, scratch, st)) return PARARNN_ERR_UNSUPPORTED;
   }
   return launched();
 }
