@@ -1,0 +1,205 @@
+"""A small language model of selective state space blocks on the operators of nonlinear_rnn_solve_amd: packed training with
+the AdamW step over all tensors, and generation token by token.
+
+    python examples/selective_lm.py --steps 200 --bits 8
+
+A block normalises the residual stream, projects it to values and a gate, runs the values through the short causal convolution
+(block.causal_conv) and the selective scan (block.selective_scan, packed documents in one row), projects back, and adds a gated
+feed-forward part (block.gated_linear).  The head scores the next token (lm.token_logprobs).  Training follows the gradients of
+all operators through torch's autograd and ends with block.adamw_step on all tensors at once, its moments in 32 or in 8 bits;
+generation carries the convolution's and the scan's states from token to token.  The other matrix products are torch's.
+"""
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+from gated_lm import LayerNorm, TokenLogprobs, documents  # noqa: E402
+from nonlinear_rnn_solve_amd import block, lm  # noqa: E402
+
+
+class CausalConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, state, cu):
+        ctx.save_for_backward(x, weight, bias, state, cu)
+        return block.causal_conv(x, weight, bias, state=state, cu_seqlens=cu)
+
+    @staticmethod
+    def backward(ctx, dy, d_last):
+        x, weight, bias, state, cu = ctx.saved_tensors
+        g = block.causal_conv_vjp(x, weight, dy.contiguous(), bias, state=state, d_last=d_last.contiguous(), cu_seqlens=cu,
+                                  want_state=state is not None)
+        return g["d_x"], g["d_weight"], g["d_bias"], g.get("d_state"), None
+
+
+class SelectiveScan(torch.autograd.Function):
+    """(y, h_last); low holds the low-rank form of the step sizes, B and C side by side, and so does its gradient (that of
+    the step sizes comes from elsewhere)."""
+
+    @staticmethod
+    def forward(ctx, x, dt, A, low, rank, skip, z, dt_bias, h0, cu):
+        n = A.shape[1]
+        y, h_last, carry = block.selective_scan(x, dt, A, low[..., rank:rank + n], low[..., rank + n:], skip=skip, z=z, dt_bias=dt_bias,
+                                                h0=h0, cu_seqlens=cu, want_carry=True)
+        ctx.save_for_backward(x, dt, A, low, skip, z, dt_bias, h0, cu, carry)
+        ctx.rank = rank
+        return y, h_last
+
+    @staticmethod
+    def backward(ctx, dy, d_last):
+        x, dt, A, low, skip, z, dt_bias, h0, cu, carry = ctx.saved_tensors
+        n, rank = A.shape[1], ctx.rank
+        d_low = torch.zeros_like(low)
+        g = block.selective_scan_vjp(x, dt, A, low[..., rank:rank + n], low[..., rank + n:], carry, dy.contiguous(), skip=skip, z=z,
+                                     dt_bias=dt_bias, h0=h0, d_last=d_last.contiguous(), cu_seqlens=cu,
+                                     out=[None, None, None, d_low[..., rank:rank + n], d_low[..., rank + n:]], want_h0=h0 is not None)
+        return g["d_x"], g["d_dt"], g["d_A"], d_low, None, g["d_skip"], g["d_z"], g["d_dt_bias"], g.get("d_h0"), None
+
+
+class GatedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up):
+        h, pre = block.gated_linear(x, w_gate, w_up, want_pre=True)
+        ctx.save_for_backward(x, w_gate, w_up, pre)
+        return h
+
+    @staticmethod
+    def backward(ctx, dh):
+        x, w_gate, w_up, pre = ctx.saved_tensors
+        g = block.gated_linear_vjp(x, w_gate, w_up, pre, dh.contiguous())
+        return g["d_x"], g["d_w_gate"], g["d_w_up"]
+
+
+class SelectiveLM(torch.nn.Module):
+    def __init__(self, vocab, width, blocks, states=16, rank=8, taps=4, dtype=torch.bfloat16, device="cuda", seed=0):
+        super().__init__()
+        g = torch.Generator().manual_seed(seed)
+        self.dtype, self.width, self.rank, self.blocks = dtype, width, rank, blocks
+
+        def matrix(rows, cols):
+            return torch.nn.Parameter((torch.randn(rows, cols, generator=g) / cols ** 0.5).to(device))
+
+        def vector(value):
+            return torch.nn.Parameter(value.to(device))
+
+        self.embed = matrix(vocab, width)
+        self.layers = torch.nn.ModuleList()
+        for _ in range(blocks):
+            p = torch.nn.Module()
+            p.norm1, p.bias1, p.norm2, p.bias2 = (vector(torch.full((width,), v)) for v in (1.0, 0.0, 1.0, 0.0))
+            p.into, p.low, p.steps, p.back = matrix(2 * width, width), matrix(rank + 2 * states, width), matrix(width, rank), matrix(width, width)
+            p.taps, p.taps_bias = vector((torch.rand(width, taps, generator=g) * 2 - 1) / taps ** 0.5), vector(torch.zeros(width))
+            # steps between 0.001 and 0.1, rates 1 .. states
+            step = torch.exp(torch.rand(width, generator=g) * 4.6 - 6.9)
+            p.dt_bias = vector(torch.log(torch.expm1(step)))
+            p.log_A = vector(torch.log(torch.arange(1, states + 1, dtype=torch.float32)).repeat(width, 1))
+            p.skip = vector(torch.ones(width))
+            p.gate, p.up, p.down = matrix(2 * width, width), matrix(2 * width, width), matrix(width, 2 * width)
+            self.layers.append(p)
+        self.norm, self.bias = vector(torch.ones(width)), vector(torch.zeros(width))
+
+    def forward(self, tokens, cu=None, states=None):
+        """Logits [B, T, V] of the tokens that follow `tokens` [B, T], and each block's states: the convolution's and the scan's."""
+        cast = lambda w: w.to(self.dtype)  # noqa: E731
+        stream = cast(self.embed[tokens])
+        out, last = torch.zeros_like(stream), []
+        for k, p in enumerate(self.layers):
+            conv_state, h0 = (None, None) if states is None else states[k]
+            y, stream = LayerNorm.apply(out, stream, p.norm1, p.bias1)
+            x, z = (y @ cast(p.into).t()).chunk(2, -1)
+            x, conv_last = CausalConv.apply(x, p.taps, p.taps_bias, conv_state, cu)
+            low = x @ cast(p.low).t()
+            dt = low[..., :self.rank] @ cast(p.steps).t()
+            y, h_last = SelectiveScan.apply(x, dt, -torch.exp(p.log_A), low, self.rank, p.skip, z, p.dt_bias, h0, cu)
+            last.append((conv_last, h_last))
+            y, stream = LayerNorm.apply(y @ cast(p.back).t(), stream, p.norm2, p.bias2)
+            out = GatedLinear.apply(y, cast(p.gate), cast(p.up)) @ cast(p.down).t()
+        y, _ = LayerNorm.apply(out, stream, self.norm, self.bias)
+        return y @ cast(self.embed).t(), last
+
+    def loss(self, tokens, targets, cu=None):
+        logits, _ = self(tokens, cu)
+        logp, _ = TokenLogprobs.apply(logits, targets)
+        return -logp.sum() / (targets >= 0).sum().clamp(min=1)
+
+    @torch.no_grad()
+    def generate(self, prompt, count):
+        """`count` tokens after prompt [B, T], each the most probable one; the prompt in one call, then token by token with
+        the states updated in place."""
+        cast = lambda w: w.to(self.dtype)  # noqa: E731
+        logits, states = self(prompt)
+        got = []
+        for _ in range(count):
+            token = lm.token_logprobs(logits[:, -1], top=1).top_ids
+            got.append(token)
+            stream = cast(self.embed[token])
+            out = torch.zeros_like(stream)
+            for p, (conv, h) in zip(self.layers, states):
+                y, stream, _ = lm.layer_norm(out, p.norm1, p.bias1, residual=stream)
+                x, z = (y @ cast(p.into).t()).chunk(2, -1)
+                x, _ = block.causal_conv(x, p.taps, p.taps_bias, state=conv, last=conv)
+                low = x @ cast(p.low).t()
+                dt, b, c = low.split([self.rank, p.log_A.shape[1], p.log_A.shape[1]], -1)
+                y, _, _ = block.selective_scan(x, dt @ cast(p.steps).t(), -torch.exp(p.log_A), b, c, skip=p.skip, z=z, dt_bias=p.dt_bias,
+                                               h0=h, h_last=h)
+                y, stream, _ = lm.layer_norm(y @ cast(p.back).t(), p.norm2, p.bias2, residual=stream)
+                out = block.gated_linear(y, cast(p.gate), cast(p.up))[0] @ cast(p.down).t()
+            y, _, _ = lm.layer_norm(out, self.norm, self.bias, residual=stream)
+            logits = y @ cast(self.embed).t()
+        return torch.cat(got, 1)
+
+
+class AdamW:
+    """block.adamw_step over a model's parameters; bits: 32 or 8 for the moments."""
+
+    def __init__(self, params, lr=3e-3, bits=32, **hyper):
+        self.params, self.lr, self.hyper, self.steps = list(params), lr, hyper, 0
+        n, dev = block.adamw_state_size(self.params), self.params[0].device
+        kind = torch.uint8 if bits == 8 else torch.float32
+        self.m, self.v = (torch.zeros(n, dtype=kind, device=dev) for _ in range(2))
+        self.scales = {}
+        if bits == 8:
+            self.scales = {k: torch.zeros(n // block.ADAMW_BLOCK, device=dev) for k in ("m_scale", "v_scale")}
+
+    def step(self):
+        self.steps += 1
+        grads = [torch.zeros_like(p) if p.grad is None else p.grad for p in self.params]
+        block.adamw_step(self.params, grads, self.m, self.v, self.steps, lr=self.lr, **self.scales, **self.hyper)
+
+
+def train(model, steps, vocab, rows=8, total=256, count=4, lr=3e-3, bits=32, seed=1, every=0):
+    """AdamW over fresh documents; the losses."""
+    g = torch.Generator().manual_seed(seed)
+    opt = AdamW(model.parameters(), lr=lr, bits=bits, betas=(0.9, 0.95))
+    losses = []
+    for n in range(steps):
+        tokens, targets, cu = documents(vocab, rows, total, count, g)
+        loss = model.loss(tokens, targets, cu)
+        model.zero_grad()
+        loss.backward()
+        opt.step()
+        losses.append(loss.detach())
+        if every and n % every == 0:
+            print("step %4d  loss %.4f" % (n, float(losses[-1])), flush=True)
+    return torch.stack(losses)
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+    ap.add_argument("--steps", type=int, default=200)
+    ap.add_argument("--vocab", type=int, default=97)
+    ap.add_argument("--width", type=int, default=256)
+    ap.add_argument("--blocks", type=int, default=2)
+    ap.add_argument("--bits", type=int, default=32, choices=(8, 32))
+    a = ap.parse_args()
+    model = SelectiveLM(a.vocab, a.width, a.blocks)
+    train(model, a.steps, a.vocab, bits=a.bits, every=max(1, a.steps // 10))
+    prompt = torch.tensor([[5, 7, 9, 11, 13, 15], [90, 93, 96, 2, 5, 8]]) % a.vocab
+    print("continuing 5 7 9 11 13 15 and 90 93 96 2 5 8:", model.generate(prompt.cuda(), 6).tolist())
+
+
+if __name__ == "__main__":
+    main()
