@@ -123,21 +123,22 @@ pararnn_status pararnn_block_selective_scan_vjp(const pararnn_block_ssm* prob, c
 /* ------------------------------------------------------------------------------------------------
  * Gated feed-forward product of R rows:  g = x w_gate^T,  u = x w_up^T,  h = act(g) u, with act(g) = g sig(g) or
  * g Phi(g) in its tanh form.  x [R][D], w_gate, w_up [F][D], h [R][F] of dtype, with row strides.
- *   pre  [R][2F] of dtype, dense: g and u of each row side by side, rounded, for the gradient; or NULL
- * Bfloat16 products are exact and summed in float32; float32 ones are float32 throughout.
+ *   pre  [R][2F] float32, dense: g and u of each row side by side, for the gradient; or NULL
+ * Bfloat16 products are exact and summed in float32.  Float32 products have float32's accuracy; an infinity among float32 values
+ * makes the results it enters NaN.
  * UNSUPPORTED: R, D or F of 2^31 - 512 or more.
  * ---------------------------------------------------------------------------------------------- */
 typedef enum { PARARNN_BLOCK_SILU = 0, PARARNN_BLOCK_GELU = 1 } pararnn_block_act;
 size_t pararnn_block_gated_linear_workspace_bytes(int dtype, int64_t R, int64_t D, int64_t F, int gradient);
 pararnn_status pararnn_block_gated_linear(int dtype, int act, int64_t R, int64_t D, int64_t F, const void* x, int64_t x_stride,
                                           const void* w_gate, int64_t gate_stride, const void* w_up, int64_t up_stride,
-                                          void* h, int64_t h_stride, void* pre, void* ws, size_t ws_bytes, void* stream);
+                                          void* h, int64_t h_stride, float* pre, void* ws, size_t ws_bytes, void* stream);
 /* Gradients for dh [R][F] of dtype, from the forward's pre:  dg = dh u act'(g),  du = dh act(g), rounded to dtype,
  *     d_x = dg w_gate + du w_up,  d_w_gate = dg^T x,  d_w_up = du^T x, in dtype; d_x [R][D] with a row stride or NULL,
  *     d_w_gate, d_w_up [F][D] with row strides, both or none NULL                                        */
 pararnn_status pararnn_block_gated_linear_vjp(int dtype, int act, int64_t R, int64_t D, int64_t F, const void* x,
                                               int64_t x_stride, const void* w_gate, int64_t gate_stride, const void* w_up,
-                                              int64_t up_stride, const void* pre, const void* dh, int64_t dh_stride, void* d_x,
+                                              int64_t up_stride, const float* pre, const void* dh, int64_t dh_stride, void* d_x,
                                               int64_t d_x_stride, void* d_w_gate, int64_t d_gate_stride, void* d_w_up,
                                               int64_t d_up_stride, void* ws, size_t ws_bytes, void* stream);
 

@@ -108,8 +108,9 @@ def gated_linear(x, w_gate, w_up, activation="silu", want_pre=False, out=None):
         h = act(x w_gate^T) * (x w_up^T)
 
     x: [..., D], rows of any one stride; w_gate, w_up: [F, D] in x's type (two halves of one tensor, for instance);
-    activation: "silu" or "gelu" (its tanh form).  Products are summed in float32.
-    Returns (h, pre): h [..., F] in x's type; pre, [rows, 2 F] in x's type, what gated_linear_vjp needs, or None without
+    activation: "silu" or "gelu" (its tanh form).  Products are summed in float32 (an infinity among float32 values makes the
+    results it enters NaN).
+    Returns (h, pre): h [..., F] in x's type; pre, float32 [rows, 2 F], what gated_linear_vjp needs, or None without
     want_pre.  out: a tensor for h.
     """
     return (_binding or load_library()).gated_linear(x, w_gate, w_up, activation, want_pre, out)

@@ -56,7 +56,7 @@ template <int BIAS> DEV float decode(uint32_t code, float scale) {
   if constexpr (BIAS == 15) x = __uint_as_float(__float_as_uint(x) | (code & 128) << 24);
   return x;
 }
-// of |x| <= 1.875 2^e, rounded up where its place between two codes and `number` / 2^20 add up to one
+// of |x| <= 1.875 2^e, rounded up where its place between two codes and `number` / 2^20 add up to one or more
 template <int BIAS> DEV uint32_t encode(float x, int e, uint32_t number) {
   const float y = ldexpf(fabsf(x), -e);
   const uint32_t normal = ((__float_as_uint(y) + number) >> 20) - (127 - BIAS) * 8;
@@ -145,8 +145,12 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
       const float x = g[k].get(i) * r.grad_scale;
       const float m0 = EIGHT ? decode<15>(mc[k] >> (8 * i) & 255, ms[k]) : m[k].get(i);
       const float v0 = EIGHT ? decode<31>(vc[k] >> (8 * i) & 255, vs[k]) : v[k].get(i);
-      nm[i] = fmaf(a.beta1, m0, a.rest1 * x);
-      nv[i] = fmaf(a.beta2, v0, a.rest2 * x * x);
+      // each product and sum rounded by itself: a moment in 8 bits then depends on no compiler's choice of fused steps, of which one
+      // in 400 000 would round it the other way
+      const float m1 = a.beta1 * m0, m2 = a.rest1 * x, v1 = a.beta2 * v0, v2 = a.rest2 * x;
+      const float v3 = v2 * x;
+      nm[i] = m1 + m2;
+      nv[i] = v1 + v3;
       np[i] = new_param(a, r, p[k].get(i), nm[i], nv[i]);
     }
     store_row<PT, V>(param + k * PIECE, n, np);
@@ -168,7 +172,9 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
         const uint64_t e = static_cast<uint64_t>(place) + i;
         const uint32_t h = mix(static_cast<uint32_t>(e) ^ mix(key ^ static_cast<uint32_t>(e >> 32)));
         cm |= encode<15>(nm[i], em, (h & 0xffff) << 4) << (8 * i);
-        cv |= encode<31>(nv[i], ev, (h >> 16) << 4) << (8 * i);
+        // more than one, for v: a tie goes down, so that no 1/2^20 of all second moments grows where nothing is to be added
+        const uint32_t up = (h >> 16) << 4;
+        cv |= encode<31>(nv[i], ev, up ? up - 1 : 0) << (8 * i);
       }
       *reinterpret_cast<Loose<uint32_t>*>(static_cast<uint8_t*>(a.m) + place) = bad ? 0 : cm;
       *reinterpret_cast<Loose<uint32_t>*>(static_cast<uint8_t*>(a.v) + place) = bad ? 0 : cv;

@@ -282,11 +282,11 @@ std::tuple<Tensor, Maybe> gated_linear(const Tensor& x, const Tensor& w_gate, co
     h = at::empty(l.with(l.F), x.options());
   }
   Maybe pre;
-  if (want_pre) pre = at::empty({l.R, 2 * l.F}, x.options());
+  if (want_pre) pre = new_floats({l.R, 2 * l.F}, x);
   const Tensor ws = call.workspace(pararnn_block_gated_linear_workspace_bytes(l.dtype, l.R, l.D, l.F, 0));
   check(pararnn_block_gated_linear(l.dtype, l.act, l.R, l.D, l.F, x.data_ptr(), l.sx, w_gate.data_ptr(), w_gate.stride(0),
                                    w_up.data_ptr(), w_up.stride(0), h.data_ptr(), rows(h, "out").second,
-                                   pre ? pre->data_ptr() : nullptr, ws.data_ptr(), static_cast<size_t>(ws.numel()), call.stream),
+                                   pre ? floats_of(*pre) : nullptr, ws.data_ptr(), static_cast<size_t>(ws.numel()), call.stream),
         "pararnn_block_gated_linear");
   written(out);
   return {h, pre};
@@ -313,7 +313,7 @@ py::dict gated_linear_vjp(const Tensor& x, const Tensor& w_gate, const Tensor& w
   const Tensor ws = call.workspace(pararnn_block_gated_linear_workspace_bytes(l.dtype, l.R, l.D, l.F, 1));
   check(pararnn_block_gated_linear_vjp(l.dtype, l.act, l.R, l.D, l.F, x.data_ptr(), l.sx, w_gate.data_ptr(), w_gate.stride(0),
                                        w_up.data_ptr(), w_up.stride(0),
-                                       dense<void>(pre, "pre", x.scalar_type(), {l.R, 2 * l.F}, x.device()), dh.data_ptr(),
+                                       floats(pre, "pre", {l.R, 2 * l.F}, x.device()), dh.data_ptr(),
                                        rows(dh, "dh").second, want_x ? dx.data_ptr() : nullptr,
                                        want_x ? rows(dx, "out").second : 0, want_params ? dg.data_ptr() : nullptr,
                                        want_params ? dg.stride(0) : 0, want_params ? du.data_ptr() : nullptr,

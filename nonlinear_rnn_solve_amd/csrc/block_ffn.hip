@@ -44,7 +44,7 @@ struct GemmArgs {
   int64_t M, N, K;              // N: of one weight
   void *c0, *c1;                // rows from `split` on go to c1
   int64_t sc0, sc1, split;
-  void* pre;
+  float* pre;
   float* sums;                  // of parts of k
   int64_t per_part;
   int32_t parts;
@@ -76,9 +76,8 @@ template <typename T, int ACT> DEV void put_gated(const GemmArgs& p, int64_t m, 
   if (m >= p.M || n >= p.N) return;
   static_cast<T*>(p.c0)[m * p.sc0 + n] = from_f32<T>(act<ACT>(g) * u);
   if (p.pre) {
-    T* pre = static_cast<T*>(p.pre) + m * 2 * p.N + n;
-    pre[0] = from_f32<T>(g);
-    pre[p.N] = from_f32<T>(u);
+    p.pre[m * 2 * p.N + n] = g;
+    p.pre[m * 2 * p.N + p.N + n] = u;
   }
 }
 template <typename T> DEV void put_plain(const GemmArgs& p, int64_t m, int64_t n, float v) {
@@ -473,7 +472,8 @@ template <typename T> DEV void store16(T* p, int64_t n, const v4u& v) {
 
 // dg and du of R rows as [R][F2] and as [2 F][Rp], zeros from 2 F to F2 and from R to Rp; 64 by 64 of each a workgroup
 struct SplitArgs {
-  const void *pre, *dh;
+  const float* pre;
+  const void* dh;
   int64_t sdh, R, F;
   int64_t Rp, Rs, F2, Fs;       // lengths of a row of `cols` and of `rows` with their zeros, and row strides
   void *rows, *cols;
@@ -486,15 +486,18 @@ template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_spli
   for (int k = 0; k < L::N; ++k) {
     const int id = threadIdx.x + k * 256, i = id / L::PER, c = id % L::PER;
     const int64_t r = r0 + i, f = f0 + c * L::V, n = r < p.R ? p.F - f : 0;
-    const T* pre = static_cast<const T*>(p.pre) + r * 2 * p.F + f;
-    const Vec<T, L::V> vg = load_row<T, L::V>(pre, n, T{}), vu = load_row<T, L::V>(pre + p.F, n, T{}),
-                       vh = load_row<T, L::V, true>(static_cast<const T*>(p.dh) + r * p.sdh + f, n, T{});
+    const float* pre = p.pre + r * 2 * p.F + f;
+    const Vec<T, L::V> vh = load_row<T, L::V, true>(static_cast<const T*>(p.dh) + r * p.sdh + f, n, T{});
     float dg[L::V], du[L::V];
 #pragma unroll
-    for (int e = 0; e < L::V; ++e) {
-      const float g = vg.get(e), dh = vh.get(e);
-      dg[e] = dh * vu.get(e) * slope<ACT>(g);
-      du[e] = dh * act<ACT>(g);
+    for (int h = 0; h < L::V; h += 4) {
+      const Vec<float, 4> vg = load_row<float, 4, true>(pre + h, n - h, 0.0f), vu = load_row<float, 4, true>(pre + p.F + h, n - h, 0.0f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float g = vg.get(e), dh = vh.get(h + e);
+        dg[h + e] = dh * vu.get(e) * slope<ACT>(g);
+        du[h + e] = dh * act<ACT>(g);
+      }
     }
     const Vec<T, L::V> og = pack_vec<T, L::V>(dg), ou = pack_vec<T, L::V>(du);
     const v4u bg{og.w[0], og.w[1], og.w[2], og.w[3]}, bu{ou.w[0], ou.w[1], ou.w[2], ou.w[3]};
@@ -646,7 +649,7 @@ static GradRoom grad_room(size_t e, int64_t R, int64_t D, int64_t F) {
 
 template <typename T, int ACT>
 static pararnn_status backward(int64_t R, int64_t D, int64_t F, const void* x, int64_t sx, const void* wg, int64_t sg, const void* wu,
-                               int64_t su, const void* pre, const void* dh, int64_t sdh, void* dx, int64_t sdx, void* dwg,
+                               int64_t su, const float* pre, const void* dh, int64_t sdh, void* dx, int64_t sdx, void* dwg,
                                int64_t sdg, void* dwu, int64_t sdu, T* ws, hipStream_t st) {
   const GradRoom room = grad_room(sizeof(T), R, D, F);
   T *rows = ws, *cols = rows + room.rows, *xt = cols + room.cols, *wt = xt + room.xt;
@@ -682,13 +685,13 @@ extern "C" size_t pararnn_block_gated_linear_workspace_bytes(int dtype, int64_t 
 
 extern "C" pararnn_status pararnn_block_gated_linear(int dtype, int act, int64_t R, int64_t D, int64_t F, const void* x,
                                                      int64_t x_stride, const void* w_gate, int64_t gate_stride, const void* w_up,
-                                                     int64_t up_stride, void* h, int64_t h_stride, void* pre, void* ws,
+                                                     int64_t up_stride, void* h, int64_t h_stride, float* pre, void* ws,
                                                      size_t ws_bytes, void* stream) {
   if (!dtype_ok(dtype) || (act != PARARNN_BLOCK_SILU && act != PARARNN_BLOCK_GELU) || !sizes_ok(R, D, F))
     return PARARNN_ERR_INVALID_ARG;
   const size_t e = dtype_size(dtype);
   if (!ptr_ok(x, e, R > 0 && D > 0) || !ptr_ok(w_gate, e, F > 0 && D > 0) || !ptr_ok(w_up, e, F > 0 && D > 0) ||
-      !ptr_ok(h, e, R > 0 && F > 0) || !ptr_ok(pre, e, false) || !plane_ok(R, x_stride) || !plane_ok(F, gate_stride) ||
+      !ptr_ok(h, e, R > 0 && F > 0) || !ptr_ok(pre, 4, false) || !plane_ok(R, x_stride) || !plane_ok(F, gate_stride) ||
       !plane_ok(F, up_stride) || !plane_ok(R, h_stride))
     return PARARNN_ERR_INVALID_ARG;
   if (R > kMost || D > kMost || F > kMost) return PARARNN_ERR_UNSUPPORTED;
@@ -706,14 +709,14 @@ extern "C" pararnn_status pararnn_block_gated_linear(int dtype, int act, int64_t
 
 extern "C" pararnn_status pararnn_block_gated_linear_vjp(int dtype, int act, int64_t R, int64_t D, int64_t F, const void* x,
                                                          int64_t x_stride, const void* w_gate, int64_t gate_stride, const void* w_up,
-                                                         int64_t up_stride, const void* pre, const void* dh, int64_t dh_stride,
+                                                         int64_t up_stride, const float* pre, const void* dh, int64_t dh_stride,
                                                          void* d_x, int64_t d_x_stride, void* d_w_gate, int64_t d_gate_stride,
                                                          void* d_w_up, int64_t d_up_stride, void* ws, size_t ws_bytes, void* stream) {
   if (!dtype_ok(dtype) || (act != PARARNN_BLOCK_SILU && act != PARARNN_BLOCK_GELU) || !sizes_ok(R, D, F))
     return PARARNN_ERR_INVALID_ARG;
   const size_t e = dtype_size(dtype);
   if (!ptr_ok(x, e, R > 0 && D > 0) || !ptr_ok(w_gate, e, F > 0 && D > 0) || !ptr_ok(w_up, e, F > 0 && D > 0) ||
-      !ptr_ok(pre, e, R > 0 && F > 0) || !ptr_ok(dh, e, R > 0 && F > 0) || !ptr_ok(d_x, e, false) || !ptr_ok(d_w_gate, e, false) ||
+      !ptr_ok(pre, 4, R > 0 && F > 0) || !ptr_ok(dh, e, R > 0 && F > 0) || !ptr_ok(d_x, e, false) || !ptr_ok(d_w_gate, e, false) ||
       !ptr_ok(d_w_up, e, false) || (d_w_gate == nullptr) != (d_w_up == nullptr) || !plane_ok(R, x_stride) ||
       !plane_ok(F, gate_stride) || !plane_ok(F, up_stride) || !plane_ok(R, dh_stride) || !plane_ok(R, d_x_stride) ||
       !plane_ok(F, d_gate_stride) || !plane_ok(F, d_up_stride))
