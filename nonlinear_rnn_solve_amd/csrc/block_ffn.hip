@@ -478,10 +478,11 @@ struct SplitArgs {
   int64_t Rp, Rs, F2, Fs;       // lengths of a row of `cols` and of `rows` with their zeros, and row strides
   void *rows, *cols;
 };
-template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_split(const SplitArgs p, uint32_t rtiles) {
+template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_split(const SplitArgs p, uint32_t ftiles) {
   using L = Turn<T>;
   __shared__ L tg, tu;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x % rtiles) * 64, f0 = static_cast<int64_t>(blockIdx.x / rtiles) * 64;
+  // neighbouring workgroups take neighbouring columns: rows may lie a large power of two apart, in few of the memory's channels
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x / ftiles) * 64, f0 = static_cast<int64_t>(blockIdx.x % ftiles) * 64;
 #pragma unroll
   for (int k = 0; k < L::N; ++k) {
     const int id = threadIdx.x + k * 256, i = id / L::PER, c = id % L::PER;
@@ -533,10 +534,10 @@ template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_spli
 // to[c][r] = from[r][c] for R rows of C, zeros for r from R to Rp; `to` has row stride st
 template <typename T>
 __global__ __launch_bounds__(256) void k_transpose(const T* from, int64_t sf, int64_t R, int64_t C, T* to, int64_t st, int64_t Rp,
-                                                   uint32_t rtiles) {
+                                                   uint32_t ctiles) {
   using L = Turn<T>;
   __shared__ L tile;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x % rtiles) * 64, c0 = static_cast<int64_t>(blockIdx.x / rtiles) * 64;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x / ctiles) * 64, c0 = static_cast<int64_t>(blockIdx.x % ctiles) * 64;
 #pragma unroll
   for (int k = 0; k < L::N; ++k) {
     const int id = threadIdx.x + k * 256, i = id / L::PER, c = id % L::PER;
@@ -620,7 +621,7 @@ template <typename T> static bool transpose(const void* from, int64_t sf, int64_
   if (rt == 0 || ct == 0) return true;
   if (!grid_ok(rt * ct, 256)) return false;
   k_transpose<T><<<dim3(static_cast<uint32_t>(rt * ct)), dim3(256), 0, stream>>>(static_cast<const T*>(from), sf, R, C, to, st, Rp,
-                                                                                 static_cast<uint32_t>(rt));
+                                                                                 static_cast<uint32_t>(ct));
   return true;
 }
 
@@ -659,7 +660,7 @@ static pararnn_status backward(int64_t R, int64_t D, int64_t F, const void* x, i
   bool ok = true;
   if (rt * ft) {
     const SplitArgs s{pre, dh, sdh, R, F, room.Rp, room.Rs, room.F2, room.Fs, dx ? rows : nullptr, dwg ? cols : nullptr};
-    k_ffn_split<T, ACT><<<dim3(static_cast<uint32_t>(rt * ft)), dim3(256), 0, st>>>(s, static_cast<uint32_t>(rt));
+    k_ffn_split<T, ACT><<<dim3(static_cast<uint32_t>(rt * ft)), dim3(256), 0, st>>>(s, static_cast<uint32_t>(ft));
   }
   if (dx && R && D) {
     ok = ok && transpose<T>(wg, sg, F, D, wt, room.Fs, F, st) && transpose<T>(wu, su, F, D, wt + F, room.Fs, room.F2 - F, st);
