@@ -243,9 +243,11 @@ template <typename T> __global__ __launch_bounds__(256) void k_join(const GemmAr
 // registers: the only wave of its SIMD.  Shared memory gives 128 bytes a cycle: with 64 by 64 a wave (above) the operands alone
 // take all of them, with 128 by 64 (eight waves) 96 and the loads' 32 the rest; here 64 and 32.  Two stages of 128 bytes of k
 // lie in shared memory: the loads go there past the registers, those of one stage while the other is multiplied.  (Four stages of
-// 64 bytes ask for every cache line twice, and the cache between has forgotten it: OLD us.)  A load puts down
+// 64 bytes ask for every cache line twice, and the cache between has forgotten it by then.)  A load puts down
 // its lanes' 16 bytes in a row, so the exchange that keeps reads off each other's banks is made by which piece each lane asks
 // for.  Reads and loads are issued between the products, each of which keeps the matrix unit busy for eight instructions' time.
+// Forward, R = 8192, D = 4096, F = 8192 (1.1 TFLOP): 925 to 960 us, 1.15 to 1.19 PFLOP/s; four stages of 64 bytes and eight waves took
+// 1033, four stages and four waves 1143, 128 by 128 tiles (k_gemm) 1430.  A large library product of this shape runs at 1.26 PFLOP/s.
 // Rows past the end are read as the last and left out of the result.  k is a multiple of the stage, everything 16-byte
 // aligned.  Neighbouring tiles share rows and columns: each of the eight L2 caches gets a run of tiles of its own, in bands of
 // eight rows of tiles.
@@ -360,27 +362,56 @@ __global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_
 }
 
 // ---- few rows ----
-// The weights are read once, from global memory straight into the matrix operands: a workgroup has 16 columns of the gate and the
-// same 16 of the other product side by side, and its eight waves take every eighth 128 bytes of k; a lane reads 64 of them,
-// four pieces that are four steps of k, x's rows alike.  The waves' sums meet in shared memory.  MT: 32-row pieces of x.
-// Rows beyond 64 are for other workgroups, eight blocks on (the same XCD), which read the weights again.
-template <typename T, int MT, int ACT>
-__global__ __launch_bounds__(512) void k_few_rows(const GemmArgs p, uint32_t groups) {
-  constexpr int V = 16 / sizeof(T), BK = kKBytes / sizeof(T), W = 8;
-  __shared__ float part[W * MT * 32 * 33];                      // 33: rows of 32 begin in banks of their own
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, half = lane / 32;
+// The weights are read once: a workgroup has 16 columns of the gate and the same 16 of the other product side by side, and its eight
+// waves take every eighth 128 bytes of k, each by itself; their sums meet in shared memory.  MT: 32-row pieces of x.  Rows
+// beyond MT 32 are for other workgroups, eight blocks on (the same XCD), which read the weights again.
+constexpr int kFewWaves = 8;
+struct FewPlace {
+  int64_t f0, m0;
+};
+DEV FewPlace few_place(uint32_t groups, int rows) {
   const uint32_t turn = blockIdx.x >> 3;
-  const int64_t f0 = (static_cast<int64_t>(turn / groups) * 8 + (blockIdx.x & 7)) * 16, m0 = static_cast<int64_t>(turn % groups) * (MT * 32);
-  if (f0 >= p.N) return;
-  int64_t f = f0 + (l32 & 15);
-  f = f < p.N ? f : p.N - 1;
-  const T* w = (l32 < 16 ? static_cast<const T*>(p.b0) + f * p.sb0 : static_cast<const T*>(p.b1) + f * p.sb1);
-  const T* x[MT];
+  return {(static_cast<int64_t>(turn / groups) * 8 + (blockIdx.x & 7)) * 16, static_cast<int64_t>(turn % groups) * rows};
+}
+// row r of the 32 of both weights
+template <typename T> DEV const T* few_weight(const GemmArgs& p, int64_t f0, int r) {
+  const int64_t f = at_most(f0 + (r & 15), p.N - 1);
+  return r < 16 ? static_cast<const T*>(p.b0) + f * p.sb0 : static_cast<const T*>(p.b1) + f * p.sb1;
+}
+// part: [waves][MT 32][33] floats; 33: rows of 32 begin in banks of their own
+template <typename T, int MT, int ACT> DEV void few_join(const GemmArgs& p, float* part, const v16f (&acc)[MT], const FewPlace& at) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) part[((wave * MT + i) * 32 + row_of_acc(e, lane)) * 33 + (lane & 31)] = acc[i][e];
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int64_t m = m0 + i * 32 + l32;
-    x[i] = static_cast<const T*>(p.a) + (m < p.M ? m : p.M - 1) * p.sa;
+    const int m = i * 32 + (threadIdx.x >> 4), c = threadIdx.x & 15;
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kFewWaves; ++k) {
+      g += part[(k * MT * 32 + m) * 33 + c];
+      u += part[(k * MT * 32 + m) * 33 + c + 16];
+    }
+    put_gated<T, ACT>(p, at.m0 + m, at.f0 + c, g, u);
   }
+}
+
+// Any alignment: from global memory straight into the matrix operands.  A lane reads 64 bytes of its row's 128, four pieces that are
+// four steps of k, x's rows alike; so a load asks for 64 cache lines, and these bound it.
+template <typename T, int MT, int ACT>
+__global__ __launch_bounds__(512) void k_few_rows(const GemmArgs p, uint32_t groups) {
+  constexpr int V = 16 / sizeof(T), BK = kKBytes / sizeof(T);
+  __shared__ float part[kFewWaves * MT * 32 * 33];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l32 = lane & 31, half = lane / 32;
+  const FewPlace at = few_place(groups, MT * 32);
+  if (at.f0 >= p.N) return;
+  const T* w = few_weight<T>(p, at.f0, l32);
+  const T* x[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) x[i] = static_cast<const T*>(p.a) + at_most(at.m0 + i * 32 + l32, p.M - 1) * p.sa;
   v4u rw[2][4], rx[2][MT][4];
   const auto load = [&](int64_t k0, v4u (&bw)[4], v4u (&bx)[MT][4]) {
 #pragma unroll
@@ -399,7 +430,7 @@ __global__ __launch_bounds__(512) void k_few_rows(const GemmArgs p, uint32_t gro
       for (int i = 0; i < MT; ++i) mma<T>(bx[i][j], bw[j], acc[i]);
   };
   int64_t k = static_cast<int64_t>(wave) * BK;
-  constexpr int64_t STEP = W * BK;
+  constexpr int64_t STEP = kFewWaves * BK;
   if (k < p.K) load(k, rw[0], rx[0]);
   for (; k < p.K; k += 2 * STEP) {
     if (k + STEP < p.K) load(k + STEP, rw[1], rx[1]);
@@ -408,22 +439,63 @@ __global__ __launch_bounds__(512) void k_few_rows(const GemmArgs p, uint32_t gro
     if (k + 2 * STEP < p.K) load(k + 2 * STEP, rw[0], rx[0]);
     multiply(rw[1], rx[1]);
   }
+  few_join<T, MT, ACT>(p, part, acc, at);
+}
+
+// k in whole 128 bytes, everything 16-byte aligned: each wave's weights and rows of x go to two places of its own in shared memory,
+// past the registers, eight whole cache lines a load; no wave waits for another.  32 rows, bf16, D = 4096, F = 8192: 29 us, 4.6 TB/s
+// of weights (a copy runs at 5.06), against 52 straight into the operands.
+template <typename T, int ACT>
+__global__ __launch_bounds__(512) void k_few_rows_aligned(const GemmArgs p, uint32_t groups) {
+  constexpr int MT = 1, BK = kKBytes / sizeof(T), ROWS = 32 * (1 + MT), LOADS = ROWS / 8, PLACE = ROWS * 128;
+  __shared__ __attribute__((aligned(128))) char smem[kFewWaves * 2 * PLACE];
+  static_assert(sizeof(smem) >= kFewWaves * MT * 32 * 33 * sizeof(float), "the sums meet in the same place");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l32 = lane & 31, half = lane / 32;
+  const FewPlace at = few_place(groups, MT * 32);
+  if (at.f0 >= p.N) return;
+  // load i: rows 8 i .. 8 i + 7 of the weights' 32, then of x's; lane l puts down piece l % 8 of row l / 8, exchanged by the row
+  const T* from[LOADS];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) part[((wave * MT + i) * 32 + row_of_acc(e, lane)) * 33 + l32] = acc[i][e];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = i * 32 + (threadIdx.x >> 4), c = threadIdx.x & 15;
-    float g = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      g += part[(k * MT * 32 + m) * 33 + c];
-      u += part[(k * MT * 32 + m) * 33 + c + 16];
-    }
-    put_gated<T, ACT>(p, m0 + m, f0 + c, g, u);
+  for (int i = 0; i < LOADS; ++i) {
+    const int r = i * 8 + lane / 8;
+    const T* row = i < 4 ? few_weight<T>(p, at.f0, r) : static_cast<const T*>(p.a) + at_most(at.m0 + r - 32, p.M - 1) * p.sa;
+    from[i] = row + static_cast<int64_t>(wave) * BK + ((lane & 7) ^ (lane / 8)) * (16 / sizeof(T));
   }
+  char* own = smem + wave * 2 * PLACE;
+  const uint32_t base = static_cast<uint32_t>((uintptr_t)(__attribute__((address_space(3))) char*)own);
+  const auto load = [&](int place) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      load_to_lds(from[i], base + place * PLACE + i * 1024);
+      from[i] += kFewWaves * BK;
+    }
+  };
+  const int blocks = static_cast<int>(p.K / BK), count = wave < blocks ? (blocks - wave + kFewWaves - 1) / kFewWaves : 0;
+  v16f acc[MT] = {};
+  if (count > 0) load(0);
+  if (count > 1) load(1);
+  for (int k = 0; k < count; ++k) {
+    // this place's loads have landed; those of the other one, if any, are behind them
+    if (k + 1 < count) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const v4u* rows = reinterpret_cast<const v4u*>(own + (k & 1) * PLACE);
+    v4u fw[4], fx[MT][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = (j * 2 + half) ^ (l32 & 7);
+      fw[j] = rows[l32 * 8 + c];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fx[i][j] = rows[((1 + i) * 32 + l32) * 8 + c];
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // what was read here may be written over
+    if (k + 2 < count) load(k & 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) mma<T>(fx[i][j], fw[j], acc[i]);
+  }
+  __syncthreads();
+  few_join<T, MT, ACT>(p, reinterpret_cast<float*>(smem), acc, at);
 }
 
 // ---------------- what the gradients' products are made of ----------------
@@ -604,15 +676,26 @@ template <typename T, bool GATED, int ACT> static bool gemm(GemmArgs p, float* s
   }
   return true;
 }
-constexpr int64_t kFewRows = 64;
+// k in whole 128 bytes and everything 16-byte aligned
+template <typename T> static bool whole(const GemmArgs& p) {
+  return p.K > 0 && p.K * static_cast<int64_t>(sizeof(T)) % kKBytes == 0 && aligned16(p.a, p.sa, sizeof(T)) &&
+         aligned16(p.b0, p.sb0, sizeof(T)) && aligned16(p.b1, p.sb1, sizeof(T));
+}
 template <typename T, int MT, int ACT> static bool few_rows(const GemmArgs& p, hipStream_t st) {
-  const int64_t groups = ceil_div(p.M, MT * 32), blocks = ceil_div(ceil_div(p.N, 16), 8) * 8 * groups;
+  const bool w = whole<T>(p);
+  const int64_t groups = ceil_div(p.M, w ? 32 : MT * 32), blocks = ceil_div(ceil_div(p.N, 16), 8) * 8 * groups;
   if (!grid_ok(blocks, 512)) return false;
-  k_few_rows<T, MT, ACT><<<dim3(static_cast<uint32_t>(blocks)), dim3(512), 0, st>>>(p, static_cast<uint32_t>(groups));
+  const dim3 grid(static_cast<uint32_t>(blocks));
+  if (w) k_few_rows_aligned<T, ACT><<<grid, dim3(512), 0, st>>>(p, static_cast<uint32_t>(groups));
+  else k_few_rows<T, MT, ACT><<<grid, dim3(512), 0, st>>>(p, static_cast<uint32_t>(groups));
   return true;
 }
+// Up to which row count the weights are streamed past few rows.  bf16, D = 4096, F = 8192: 64, 96, 128 rows 44, 63, 80 us, 129 in tiles
+// 75; D = 1024, F = 4096: 128 rows 13.6 us, 129 in tiles 18.0.  Float32, bound by its matrix instructions: 64 rows 115 us, 96
+// in tiles 168.
+template <typename T> static int64_t few_most(const GemmArgs& p) { return sizeof(T) == 2 && whole<T>(p) ? 128 : 64; }
 template <typename T, int ACT> static bool forward(const GemmArgs& p, hipStream_t st) {
-  if (p.M > kFewRows) return gemm<T, true, ACT>(p, nullptr, st);
+  if (p.M > few_most<T>(p)) return gemm<T, true, ACT>(p, nullptr, st);
   return p.M <= 32 ? few_rows<T, 1, ACT>(p, st) : few_rows<T, 2, ACT>(p, st);
 }
 template <typename T> static bool transpose(const void* from, int64_t sf, int64_t R, int64_t C, T* to, int64_t st, int64_t Rp,
@@ -627,10 +710,11 @@ template <typename T> static bool transpose(const void* from, int64_t sf, int64_
 
 constexpr int64_t kMost = INT32_MAX - 512;
 static bool sizes_ok(int64_t R, int64_t D, int64_t F) {
-  return R >= 0 && D >= 0 && F >= 0 && (R > kMost || D > kMost || F > kMost || (sizes_fit(R, D) && sizes_fit(R, F, 2) && sizes_fit(F, D, 2)));
+  return R >= 0 && D >= 0 && F >= 0 &&
+         (R > kMost || D > kMost || F > kMost || (sizes_fit(R, D, 4) && sizes_fit(R, F, 4) && sizes_fit(F, D, 4)));
 }
 // Row stride of n elements in the workspace: not a large power of two, which would put the rows of a tile behind each other in few
-// of the memory's channels (8192 x 4096 x 8192: PADNOTE).
+// of the memory's channels (the two gradient products of R = 8192, D = 4096, F = 8192: 970 -> 882 us each).
 static int64_t spread(int64_t n, size_t e) { return n * static_cast<int64_t>(e) % 4096 ? n : n + kPad; }
 // elements of the gradient's workspace: d_pre [R][F2], d_pre^T [2 F][Rp], x^T [D][Rp], weights^T [D][F2], with row strides Fs, Rs,
 // and float32 sums of parts of k
