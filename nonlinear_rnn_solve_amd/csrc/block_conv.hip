@@ -306,7 +306,8 @@ inline int32_t forward_steps(int64_t B, int64_t T, int64_t D) { return chunk_ste
 inline int32_t gradient_steps(int64_t B, int64_t T, int64_t D) { return chunk_steps(B, T, D, kGradThreads, 64); }
 
 static bool sizes_ok(int64_t B, int64_t T, int64_t D, int64_t K) {
-  return K >= 1 && sizes_fit(B, T, D) && sizes_fit(D, K < PARARNN_BLOCK_MAX_TAPS ? K + 1 : 1);
+  // every product of sizes fits, also where a third one is zero
+  return K >= 1 && sizes_fit(B, T, D) && sizes_fit(B, T) && sizes_fit(T, D) && sizes_fit(B, D, 8) && sizes_fit(D, 9);
 }
 static bool problem_ok(const pararnn_block_conv* q) {
   if (!q || !dtype_ok(q->dtype) || (q->silu != 0 && q->silu != 1) || !sizes_ok(q->B, q->T, q->D, q->K)) return false;

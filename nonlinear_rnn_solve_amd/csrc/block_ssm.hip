@@ -947,6 +947,7 @@ struct Split {
 constexpr int64_t kFull = 448, kWant = 2048, kGradWant = 1536, kLeast = 2, kMost = 96;
 static Split split(int64_t B, int64_t T, int64_t D, int64_t G, int64_t want) {
   Split s;
+  if (D == 0) G = 1;
   s.ctiles = ceil_div(D / G, CH);
   s.tiles = ceil_div(T, CT);
   s.rows = B * G * s.ctiles;
@@ -963,7 +964,8 @@ static Split forward_split(int64_t B, int64_t T, int64_t D, int64_t G) { return 
 static Split gradient_split(int64_t B, int64_t T, int64_t D, int64_t G) { return split(B, T, D, G, kGradWant); }
 
 static bool sizes_ok(int64_t B, int64_t T, int64_t D, int64_t N, int64_t G) {
-  if (N < 1 || G < 1 || !sizes_fit(B, T, D) || (D > 0 && (G > D || D % G))) return false;
+  if (N < 1 || N > INT64_MAX / 128 || G < 1 || G > INT32_MAX || !sizes_fit(B, T, D) || (D > 0 && (G > D || D % G))) return false;
+  if (D == 0) G = 1;            // no channels: any number of groups
   return sizes_fit(D, N + 2) && sizes_fit(B, ceil_div(T, CT) + 1, D) &&
          (D == 0 || B == 0 || N + 2 <= INT64_MAX / 64 / (D * B) / (ceil_div(T, CT) + 1)) &&
          (B == 0 || T == 0 || N <= INT64_MAX / 64 / B / T / (D / 64 + G + 1));
