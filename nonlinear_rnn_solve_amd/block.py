@@ -7,7 +7,8 @@ the results with torch and passes the current HIP stream.  As in ``lm``, there i
 ValueError, statuses of the C ABI PararnnError; big planes are float32 or bfloat16, dense in their last dimension and strided
 as they like in the others; float32 arguments (states, parameters) are contiguous and of the stated shape, dimensions of one
 entry aside, or flat; results are detached from autograd (examples/selective_lm.py wraps the operators in autograd functions) and a
-tensor given to be written counts as modified in place.  Nothing here synchronises, so calls can be captured in a HIP graph.
+tensor given to be written counts as modified in place; it shares no memory with an input or another output unless its operator
+says so.  Nothing here synchronises, so calls can be captured in a HIP graph.
 """
 from __future__ import annotations
 
@@ -84,6 +85,7 @@ def selective_scan(x, dt, A, b, c, skip=None, z=None, dt_bias=None, h0=None, cu_
     [B, n_seqs, D, N].  Returns (y, h_last, carry): y [B, T, D] in x's type; h_last, the float32 states leaving the
     sequences, in h0's shape; carry, what selective_scan_vjp needs (float32 [B, chunks, N, D], or None without want_carry).
     out, h_last: tensors to write into; h_last may be h0 itself (a decoder's state updated in place).
+    Steps of any plane are less than 2^24 elements apart (PararnnError otherwise).
     """
     return (_binding or load_library()).selective_scan(x, dt, A, b, c, skip, z, dt_bias, h0, cu_seqlens, want_carry, out, h_last)
 

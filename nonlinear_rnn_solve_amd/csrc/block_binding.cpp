@@ -37,6 +37,13 @@ void copy_strides(int64_t* to, const Tensor& t, int n) {
 }
 float* floats_of(const Tensor& t) { return static_cast<float*>(t.data_ptr()); }
 Maybe given_at(const std::optional<std::vector<Maybe>>& out, size_t k) { return out ? (*out)[k] : Maybe(); }
+// a caller's output takes no input's place (slices of one tensor interleave, so only the same beginning is told from them)
+void apart(const Maybe& out, const char* name, std::initializer_list<std::pair<const Tensor*, const char*>> others) {
+  if (!out || !out->numel()) return;
+  for (const auto& [t, what] : others)
+    if (t && t->numel() && t->data_ptr() == out->data_ptr()) refuse(std::string(name) + " must not share memory with " + what);
+}
+const Tensor* maybe(const Maybe& t) { return t ? &*t : nullptr; }
 
 // ---------------------------------------------------------------- causal convolution
 struct Conv {
@@ -69,6 +76,7 @@ std::tuple<Tensor, Tensor> causal_conv(const Tensor& x, const Tensor& weight, co
   const Conv c(x, weight, bias, state, cu, silu);
   const Call call(x.device());
   const Tensor y = output(out, "out", x);
+  apart(out, "out", {{&x, "x"}});
   const Tensor left = last ? *last : new_floats(c.shape, x);
   float* pl = floats(left, "last", c.shape, x.device());
   const int64_t sy[2] = {y.stride(0), y.stride(1)};
@@ -84,6 +92,7 @@ py::dict causal_conv_vjp(const Tensor& x, const Tensor& weight, const Tensor& dy
   const Call call(x.device());
   plane(dy, "dy", x);
   const Tensor dx = output(out, "out", x);
+  apart(out, "out", {{&x, "x"}, {&dy, "dy"}});
   pararnn_block_conv_grad g{};
   g.dy = dy.data_ptr();
   g.d_last = floats(d_last, "d_last", c.shape, x.device());
@@ -166,6 +175,7 @@ std::tuple<Tensor, Tensor, Maybe> selective_scan(const Tensor& x, const Tensor& 
   const Ssm s(x, dt, A, b, c, skip, z, dt_bias, h0, cu);
   const Call call(x.device());
   const Tensor y = output(out, "out", x);
+  apart(out, "out", {{&x, "x"}, {&dt, "dt"}, {maybe(z), "z"}, {&b, "b"}, {&c, "c"}});
   const Tensor last = h_last ? *h_last : new_floats(s.shape, x);
   float* pl = floats(last, "h_last", s.shape, x.device());
   Maybe carry;
@@ -201,6 +211,10 @@ py::dict selective_scan_vjp(const Tensor& x, const Tensor& dt, const Tensor& A, 
   if (!z && given_at(out, 2)) refuse("out holds a d_z, but there is no z");
   const Tensor dx = output(given_at(out, 0), "out", x), dd = output(given_at(out, 1), "out", x);
   const Tensor db = shared_output(given_at(out, 3), "out", x, b), dc = shared_output(given_at(out, 4), "out", x, b);
+  for (size_t k = 0; out && k < 5; ++k) {
+    apart((*out)[k], "out", {{&x, "x"}, {&dt, "dt"}, {maybe(z), "z"}, {&b, "b"}, {&c, "c"}, {&dy, "dy"}});
+    for (size_t j = 0; j < k; ++j) apart((*out)[k], "out", {{maybe((*out)[j]), "another of out"}});
+  }
   pararnn_block_ssm_grad g{};
   g.carry = floats(carry, "carry", s.carry_shape(), x.device());
   g.dy = dy.data_ptr();
@@ -278,6 +292,7 @@ std::tuple<Tensor, Maybe> gated_linear(const Tensor& x, const Tensor& w_gate, co
     on_device(*out, "out", x.scalar_type(), x.device());
     if (out->sizes() != at::IntArrayRef(l.with(l.F))) refuse("out must be " + text(l.with(l.F)) + ", got " + text(out->sizes()));
     h = output(out, "out", *out);
+    apart(out, "out", {{&x, "x"}, {&w_gate, "w_gate"}, {&w_up, "w_up"}});
   } else {
     h = at::empty(l.with(l.F), x.options());
   }
@@ -310,6 +325,10 @@ py::dict gated_linear_vjp(const Tensor& x, const Tensor& w_gate, const Tensor& w
     res["d_w_gate"] = dg = output(given_at(w_out, 0), "w_out", w_gate);
     res["d_w_up"] = du = output(given_at(w_out, 1), "w_out", w_up);
   }
+  for (const Maybe& t : {out, given_at(w_out, 0), given_at(w_out, 1)})
+    apart(t, "an output", {{&x, "x"}, {&w_gate, "w_gate"}, {&w_up, "w_up"}, {&dh, "dh"}});
+  apart(given_at(w_out, 1), "w_out", {{maybe(given_at(w_out, 0)), "another of w_out"}, {maybe(out), "out"}});
+  apart(given_at(w_out, 0), "w_out", {{maybe(out), "out"}});
   const Tensor ws = call.workspace(pararnn_block_gated_linear_workspace_bytes(l.dtype, l.R, l.D, l.F, 1));
   check(pararnn_block_gated_linear_vjp(l.dtype, l.act, l.R, l.D, l.F, x.data_ptr(), l.sx, w_gate.data_ptr(), w_gate.stride(0),
                                        w_up.data_ptr(), w_up.stride(0),
@@ -384,9 +403,15 @@ void adamw_step(const std::vector<Tensor>& params, const std::vector<Tensor>& gr
     }
     list.push_back(t);
   }
+  for (const Tensor* t : {&m, &v, maybe(m_scale), maybe(v_scale)})
+    if (t && t->is_cuda() && t->numel()) {
+      const char* a = static_cast<const char*>(t->data_ptr());
+      places.emplace_back(a, a + t->nbytes());
+    }
   std::sort(places.begin(), places.end());
   for (size_t k = 1; k < places.size(); ++k)
-    if (places[k].first < places[k - 1].second) refuse("params must not overlap (a tensor is given twice, or two share memory)");
+    if (places[k].first < places[k - 1].second)
+      refuse("params must not overlap, nor the moments and their scales (a tensor is given twice, or two share memory)");
   pararnn_block_adamw_args a{};
   a.bits = eight ? 8 : 32;
   a.beta1 = betas.first, a.beta2 = betas.second, a.eps = eps, a.weight_decay = weight_decay;

@@ -10,7 +10,8 @@ namespace lm {
 
 // A thread holds V channels and walks L consecutive steps with the K - 1 steps before them in registers, so every input is
 // read once, but for the K - 1 rows that a chunk shares with the next (from the caches).  Threads are numbered over channels
-// first, then chunks, then rows: narrow widths fill their waves with several chunks.  Bound by memory.
+// first, then chunks, then rows: narrow widths fill their waves with several chunks.  Bound by memory: B = 2, T = 4096, D = 4096,
+// K = 4, bf16: 30 us forward (134 MB, 4.5 TB/s), 63 us backward (201 MB, 3.2 TB/s; of a fresh dx and three planes at once).
 constexpr int V = 4, U = 4;     // channels of a thread; rows it has in flight
 
 struct ConvArgs {
@@ -294,7 +295,9 @@ struct ToTaps {
 };
 
 // ---------------- host ----------------
-// Steps of a chunk: as many as leave `want` threads, since longer chunks read and compute fewer shared rows
+// Steps of a chunk: as many as leave `want` threads, since longer chunks read and compute fewer shared rows.  Forward with 2^16, 2^18
+// and 2^20 threads: 35.7, 21.5, 21.6 us (T = 81708, D = 145, K = 5, bf16), 25.2, 28.1, 28.1 (B = 8, T = 2048, D = 1000, K = 4, f32).
+// Gradient with 2^15, 2^17 and 2^19: 110, 112, 124 and 96, 75, 90 there, 81, 79, 86 at B = 2, T = 4096, D = 4096, K = 4, bf16.
 inline int32_t chunk_steps(int64_t B, int64_t T, int64_t D, int64_t want, int32_t most) {
   const int64_t quads = ceil_div(D, V);
   int32_t L = most;

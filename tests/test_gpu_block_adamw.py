@@ -287,3 +287,18 @@ def test_refusals():
         with pytest.raises(block.PararnnError):
             block.adamw_step(params, grads, m, v, **{"step": 1, **bad})
     block.adamw_step([], [], m[:0], v[:0], 1)
+
+
+def test_moments_that_share_memory_are_refused():
+    p, g = torch.zeros(600, device="cuda"), torch.ones(600, device="cuda")
+    n = block.adamw_state_size([p])
+    m = torch.zeros(n, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):
+        block.adamw_step([p], [g], m, m, 1)
+    q = torch.zeros(n, device="cuda")[:600]
+    with pytest.raises(ValueError, match="overlap"):
+        block.adamw_step([q], [g], q.new_empty(0).set_(q.untyped_storage()), m, 1)
+    m8, v8, s = (torch.zeros(k, dtype=t, device="cuda") for k, t in ((n, torch.uint8), (n, torch.uint8), (n // 256, torch.float32)))
+    with pytest.raises(ValueError, match="overlap"):
+        block.adamw_step([p], [g], m8, v8, 1, m_scale=s, v_scale=s)
+    assert not p.any() and not m8.any()

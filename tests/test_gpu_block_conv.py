@@ -238,3 +238,13 @@ def test_refusals():
                 lambda: block.causal_conv(x, w, b.cpu())):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_outputs_in_an_inputs_place_are_refused():
+    x, w = torch.randn(2, 9, 8, device="cuda"), torch.randn(8, 4, device="cuda")
+    dy = torch.randn_like(x)
+    with pytest.raises(ValueError, match="share memory"):
+        block.causal_conv(x, w, out=x)
+    for t in (x, dy):
+        with pytest.raises(ValueError, match="share memory"):
+            block.causal_conv_vjp(x, w, dy, out=t)

@@ -219,3 +219,14 @@ def test_refusals():
                 lambda: block.gated_linear_vjp(x, wg, wu, pre, dh, want_x=False, out=x)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_outputs_in_an_inputs_place_are_refused():
+    x, wg, wu, dh = (torch.randn(16, 16, device="cuda") for _ in range(4))
+    pre = block.gated_linear(x, wg, wu, want_pre=True)[1]
+    with pytest.raises(ValueError, match="share memory"):
+        block.gated_linear(x, wg, wu, out=x)
+    one = torch.empty_like(x)
+    for kw in (dict(out=x), dict(out=dh), dict(w_out=[wg, None]), dict(w_out=[one, one]), dict(out=one, w_out=[None, one])):
+        with pytest.raises(ValueError, match="share memory"):
+            block.gated_linear_vjp(x, wg, wu, pre, dh, **kw)

@@ -313,3 +313,26 @@ def test_refusals():
                 lambda: k.backward(carry, out=[k.x[:, :1].expand(2, 5, 6)] + [None] * 4)):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("B,T,D,cu", [(2, 5, 33, None), (2, 21, 65, None), (1, 1003, 64, None), (1, 1003, 40, [0, 18, 18, 519, 1003])])
+def test_state_that_forgets_at_once(B, T, D, cu):
+    # exp(s A) is 0 for A = -inf and for -1e30 alike (s > 1e-20 here): the same bits
+    k = Case(B, T, D, 5, F32, 71, n=len(cu) - 1 if cu else 0)
+    k.A[:, 2] = -1e30
+    want = k.forward(cu)[:2]
+    k.A[:, 2] = float("-inf")
+    for a, w in zip(k.forward(cu)[:2], want):
+        assert torch.isfinite(a).all() and torch.equal(a, w)
+
+
+def test_outputs_in_an_inputs_place_are_refused():
+    k = Case(1, 20, 8, 4, F32, 72)
+    carry = k.forward(want_carry=True)[2]
+    for t in (k.x, k.z, k.dt):
+        with pytest.raises(ValueError, match="share memory"):
+            k.forward(out=t)
+    one = torch.empty_like(k.dy)
+    for out in ([k.dy] + [None] * 4, [one, one, None, None, None], [None, None, None, k.b, None]):
+        with pytest.raises(ValueError, match="share memory"):
+            k.backward(carry, out=out)
