@@ -88,8 +88,8 @@ template <typename T> DEV void put_plain(const GemmArgs& p, int64_t m, int64_t n
 
 // ---- any alignment and size ----
 // A workgroup of four waves forms 128 by BN of C (forward: 128 by BN / 2 of both products), each wave 64 by BN / 2.  The next tile's
-// rows are in registers while this one is multiplied from shared memory; its 16-byte pieces are exchanged within a row by the
-// row's number, so that no two of the lanes that read together meet in a bank.  Rows past the end are read as the last.  With
+// rows are in registers while this one is multiplied from shared memory; its 16-byte pieces are exchanged within a row by
+// half of the row's number, so that no two of the sixteen lanes that read together meet in a bank.  Rows past the end are read as the last.  With
 // p.parts > 1 the workgroups split k, and each writes float32 sums of its own to p.sums, [parts][M][N].
 //
 // Float32.  The matrix units multiply bfloat16 16 times as fast as float32.  A float32 is the exact sum of three bfloat16 of eight
@@ -100,7 +100,7 @@ template <typename T> DEV void put_plain(const GemmArgs& p, int64_t m, int64_t n
 template <typename T> struct Parts {
   static constexpr int PL = sizeof(T) == 4 ? 3 : 1;             // numbers that make one
   static constexpr int CPR = sizeof(T) == 4 ? 4 : 8;            // 16-byte pieces of a row in shared memory
-  static DEV int swap(int r, int c) { return CPR == 8 ? c ^ (r & 7) : c ^ (r >> 2 & 3); }
+  static DEV int swap(int r, int c) { return CPR == 8 ? c ^ (r >> 1 & 7) : c ^ (r >> 2 & 3); }
 };
 DEV uint32_t upper_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }   // a's, then b's
 DEV void split3(const v4u& x, uint32_t (&hi)[2], uint32_t (&mid)[2], uint32_t (&lo)[2]) {
@@ -244,8 +244,8 @@ template <typename T> __global__ __launch_bounds__(256) void k_join(const GemmAr
 // take all of them, with 128 by 64 (eight waves) 96 and the loads' 32 the rest; here 64 and 32.  Two stages of 128 bytes of k
 // lie in shared memory: the loads go there past the registers, those of one stage while the other is multiplied.  (Four stages of
 // 64 bytes ask for every cache line twice, and the cache between has forgotten it by then.)  A load puts down
-// its lanes' 16 bytes in a row, so the exchange that keeps reads off each other's banks is made by which piece each lane asks
-// for.  Reads and loads are issued between the products, each of which keeps the matrix unit busy for eight instructions' time.
+// its lanes' 16 bytes in a row, so the exchange that keeps reads off each other's banks (sixteen rows' pieces fill 256 bytes twice over
+// where they are exchanged by a row's number, once by half of it) is made by which piece each lane asks for.  Reads and loads are issued between the products, each of which keeps the matrix unit busy for eight instructions' time.
 // Forward, R = 8192, D = 4096, F = 8192 (1.1 TFLOP): 925 to 960 us, 1.15 to 1.19 PFLOP/s; four stages of 64 bytes and eight waves took
 // 1033, four stages and four waves 1143, 128 by 128 tiles (k_gemm) 1430.  A large library product of this shape runs at 1.26 PFLOP/s.
 // Rows past the end are read as the last and left out of the result.  k is a multiple of the stage, everything 16-byte
@@ -279,7 +279,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_
   const T* from[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = wave * 64 + (i & 7) * 8 + lane / 8, c = (lane & 7) ^ (lane / 8);
+    const int r = wave * 64 + (i & 7) * 8 + lane / 8, c = (lane & 7) ^ (r >> 1 & 7);
     if (i < 8) {
       from[i] = static_cast<const T*>(p.a) + at_most(m0 + r, p.M - 1) * p.sa + c * (16 / sizeof(T));
     } else {
@@ -304,12 +304,12 @@ __global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_
     const int c = kk * 2 + half;
     if constexpr (i < 4) {
       const int r = wm * 128 + i * 32 + l32;
-      f.a[i] = at[r * 8 + (c ^ (r & 7))];
+      f.a[i] = at[r * 8 + (c ^ (r >> 1 & 7))];
     } else {
       // gated: 64 columns of the gate, then the same of the other product
       constexpr int j = i - 4;
       const int n = GATED ? (j >> 1) * 128 + wn * 64 + (j & 1) * 32 + l32 : wn * 128 + j * 32 + l32;
-      f.b[j] = at[256 * 8 + n * 8 + (c ^ (n & 7))];
+      f.b[j] = at[256 * 8 + n * 8 + (c ^ (n >> 1 & 7))];
     }
   };
   // the products of f, `beside(k)` after the k-th of the sixteen
@@ -453,13 +453,13 @@ __global__ __launch_bounds__(512) void k_few_rows_aligned(const GemmArgs p, uint
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l32 = lane & 31, half = lane / 32;
   const FewPlace at = few_place(groups, MT * 32);
   if (at.f0 >= p.N) return;
-  // load i: rows 8 i .. 8 i + 7 of the weights' 32, then of x's; lane l puts down piece l % 8 of row l / 8, exchanged by the row
+  // load i: rows 8 i .. 8 i + 7 of the weights' 32, then of x's; lane l puts down piece l % 8 of row l / 8, exchanged as above
   const T* from[LOADS];
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
     const int r = i * 8 + lane / 8;
     const T* row = i < 4 ? few_weight<T>(p, at.f0, r) : static_cast<const T*>(p.a) + at_most(at.m0 + r - 32, p.M - 1) * p.sa;
-    from[i] = row + static_cast<int64_t>(wave) * BK + ((lane & 7) ^ (lane / 8)) * (16 / sizeof(T));
+    from[i] = row + static_cast<int64_t>(wave) * BK + ((lane & 7) ^ (r >> 1 & 7)) * (16 / sizeof(T));
   }
   char* own = smem + wave * 2 * PLACE;
   const uint32_t base = static_cast<uint32_t>((uintptr_t)(__attribute__((address_space(3))) char*)own);
@@ -482,7 +482,7 @@ __global__ __launch_bounds__(512) void k_few_rows_aligned(const GemmArgs p, uint
     v4u fw[4], fx[MT][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int c = (j * 2 + half) ^ (l32 & 7);
+      const int c = (j * 2 + half) ^ (l32 >> 1 & 7);
       fw[j] = rows[l32 * 8 + c];
 #pragma unroll
       for (int i = 0; i < MT; ++i) fx[i][j] = rows[((1 + i) * 32 + l32) * 8 + c];
