@@ -239,19 +239,18 @@ template <typename T> __global__ __launch_bounds__(256) void k_join(const GemmAr
 }
 
 // ---- large, aligned, bfloat16 ----
-// 256 by 256 of C (forward: 256 by 128 of both products) a workgroup of four waves, two by two, each 128 by 128 with its sums in 256
-// registers: the only wave of its SIMD.  Shared memory gives 128 bytes a cycle: with 64 by 64 a wave (above) the operands alone
-// take all of them, with 128 by 64 (eight waves) 96 and the loads' 32 the rest; here 64 and 32.  Two stages of 128 bytes of k
-// lie in shared memory: the loads go there past the registers, those of one stage while the other is multiplied.  (Four stages of
-// 64 bytes ask for every cache line twice, and the cache between has forgotten it by then.)  A load puts down
-// its lanes' 16 bytes in a row, so the exchange that keeps reads off each other's banks (sixteen rows' pieces fill 256 bytes twice over
-// where they are exchanged by a row's number, once by half of it) is made by which piece each lane asks for.  Reads and loads are issued between the products, each of which keeps the matrix unit busy for eight instructions' time.
-// Forward, R = 8192, D = 4096, F = 8192 (1.1 TFLOP): 925 to 960 us, 1.15 to 1.19 PFLOP/s; four stages of 64 bytes and eight waves took
-// 1033, four stages and four waves 1143, 128 by 128 tiles (k_gemm) 1430.  A large library product of this shape runs at 1.26 PFLOP/s.
+// 256 by 256 of C (forward: 256 by 128 of both products) a workgroup of eight waves, two by four, each 128 by 64 with its sums in 128
+// registers, two waves a SIMD.  Two stages of 128 bytes of k lie in shared memory: the loads go there past the registers, those of one
+// stage while the other is multiplied.  (Four stages of 64 bytes ask for every cache line twice, and the cache between has forgotten
+// it by then.)  A load puts down its lanes' 16 bytes in a row, so the exchange that keeps reads off each other's banks (the pieces of
+// sixteen rows fill 256 bytes twice over where they are exchanged by a row's number, once by half of it) is made by which piece each
+// lane asks for.  Reads and loads are issued between the products, each of which keeps the matrix unit busy for eight instructions'
+// time.  Eight waves against four of 128 by 128 (one a SIMD, so that a wait is a stall), forward with pre: R = D = F = 2048 54 and 61 us,
+// R = 4096, D = 1024, F = 4096 80 and 90, R = 8192, D = 4096, F = 8192 (1.1 TFLOP) 1018 and 1007, gradient 2126 and 2186.
 // Rows past the end are read as the last and left out of the result.  k is a multiple of the stage, everything 16-byte
 // aligned.  Neighbouring tiles share rows and columns: each of the eight L2 caches gets a run of tiles of its own, in bands of
 // eight rows of tiles.
-constexpr int kStages = 2, kStageBytes = 512 * 128, kLoads = 16;   // loads of a thread for a stage
+constexpr int kStages = 2, kStageBytes = 512 * 128, kLoads = 8;   // loads of a thread for a stage
 DEV void load_to_lds(const void* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
 }
@@ -264,7 +263,7 @@ template <int FROM, int TO, typename F> DEV void unrolled(F&& f) {
   }
 }
 template <bool GATED, int ACT>
-__global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_t mtiles, uint32_t ntiles) {
+__global__ __launch_bounds__(512, 2) void k_gemm_large(const GemmArgs p, uint32_t mtiles, uint32_t ntiles) {
   using T = bf16;
   constexpr int BK = 128 / sizeof(T);
   __shared__ __attribute__((aligned(128))) char smem[kStages * kStageBytes];
@@ -275,12 +274,12 @@ __global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_
   const uint32_t band = id / (8 * ntiles), in = id - band * (8 * ntiles), rows = mtiles - band * 8 < 8 ? mtiles - band * 8 : 8;
   const int64_t m0 = static_cast<int64_t>(band * 8 + in % rows) * 256, n0 = static_cast<int64_t>(in / rows) * (GATED ? 128 : 256);
 
-  // wave w loads the rows w 64 .. w 64 + 63 of A and of B, 8 a load: lane l puts down piece l % 8 of row l / 8
+  // wave w loads the rows w 32 .. w 32 + 31 of A and of B, 8 a load: lane l puts down piece l % 8 of row l / 8
   const T* from[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = wave * 64 + (i & 7) * 8 + lane / 8, c = (lane & 7) ^ (r >> 1 & 7);
-    if (i < 8) {
+    const int r = wave * 32 + (i & 3) * 8 + lane / 8, c = (lane & 7) ^ (r >> 1 & 7);
+    if (i < 4) {
       from[i] = static_cast<const T*>(p.a) + at_most(m0 + r, p.M - 1) * p.sa + c * (16 / sizeof(T));
     } else {
       const bool second = GATED && r >= 128;
@@ -288,16 +287,16 @@ __global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_
       from[i] = static_cast<const T*>(second ? p.b1 : p.b0) + n * (second ? p.sb1 : p.sb0) + c * (16 / sizeof(T));
     }
   }
-  const uint32_t base = static_cast<uint32_t>((uintptr_t)(__attribute__((address_space(3))) char*)smem) + wave * 8192;   // in the LDS
+  const uint32_t base = static_cast<uint32_t>((uintptr_t)(__attribute__((address_space(3))) char*)smem) + wave * 4096;   // in the LDS
   // the stage that is next, to its place; behind the last one that one again, so that nothing branches (`step` is 0 then)
   const auto load = [&](int stage, int step, auto which) {
     constexpr int i = which;
-    load_to_lds(from[i], base + stage * kStageBytes + (i >> 3) * 32768 + (i & 7) * 1024);
+    load_to_lds(from[i], base + stage * kStageBytes + (i >> 2) * 32768 + (i & 3) * 1024);
     from[i] += step;
   };
   const int count = static_cast<int>(p.K / BK), half = lane / 32, l32 = lane & 31;
-  v16f acc[4][4] = {};
-  struct Pieces { v4u a[4], b[4]; };
+  v16f acc[4][2] = {};
+  struct Pieces { v4u a[4], b[2]; };
   const auto read = [&](int stage, int kk, Pieces& f, auto which) {
     constexpr int i = which;
     const v4u* at = reinterpret_cast<const v4u*>(smem + stage * kStageBytes);
@@ -306,17 +305,17 @@ __global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_
       const int r = wm * 128 + i * 32 + l32;
       f.a[i] = at[r * 8 + (c ^ (r >> 1 & 7))];
     } else {
-      // gated: 64 columns of the gate, then the same of the other product
+      // gated: 32 columns of the gate, then the same of the other product
       constexpr int j = i - 4;
-      const int n = GATED ? (j >> 1) * 128 + wn * 64 + (j & 1) * 32 + l32 : wn * 128 + j * 32 + l32;
+      const int n = GATED ? j * 128 + wn * 32 + l32 : wn * 64 + j * 32 + l32;
       f.b[j] = at[256 * 8 + n * 8 + (c ^ (n >> 1 & 7))];
     }
   };
   // the products of f, `beside(k)` after the k-th of the sixteen
   const auto multiply = [&](const Pieces& f, auto&& beside) {
-    unrolled<0, 16>([&](auto which) {
+    unrolled<0, 8>([&](auto which) {
       constexpr int k = which;
-      mma<T>(f.a[k >> 2], f.b[k & 3], acc[k >> 2][k & 3]);
+      mma<T>(f.a[k >> 1], f.b[k & 1], acc[k >> 1][k & 1]);
       beside(which);
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -325,14 +324,14 @@ __global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_
   const auto quarter = [&](int stage, int kk, const Pieces& f, Pieces& next) {
     multiply(f, [&](auto which) {
       constexpr int k = which;
-      if constexpr (k % 2 == 0) read(stage, kk + 1, next, std::integral_constant<int, k / 2>{});
+      if constexpr (k < 6) read(stage, kk + 1, next, which);
     });
   };
   Pieces even, odd;
   unrolled<0, kLoads>([&](auto i) { load(0, count > 1 ? BK : 0, i); });
   stage_ready();
   unrolled<0, kLoads>([&](auto i) { load(1, count > 2 ? BK : 0, i); });
-  unrolled<0, 8>([&](auto i) { read(0, 0, even, i); });
+  unrolled<0, 6>([&](auto i) { read(0, 0, even, i); });
 #pragma unroll 1
   for (int k = 0; k < count; ++k) {
     const int stage = k & 1, step = k + 3 < count ? BK : 0;
@@ -344,7 +343,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_
     multiply(odd, [&](auto which) {
       constexpr int i = which;
       load(stage, step, which);
-      if constexpr (i % 2 == 0) read(stage ^ 1, 0, even, std::integral_constant<int, i / 2>{});
+      if constexpr (i < 6) read(stage ^ 1, 0, even, which);
     });
   }
   stage_ready();                // nothing is on its way to shared memory when the workgroup ends
@@ -354,9 +353,9 @@ __global__ __launch_bounds__(256, 1) void k_gemm_large(const GemmArgs p, uint32_
     for (int e = 0; e < 16; ++e) {
       const int64_t m = m0 + wm * 128 + i * 32 + row_of_acc(e, lane);
 #pragma unroll
-      for (int j = 0; j < (GATED ? 2 : 4); ++j) {
-        if constexpr (GATED) put_gated<T, ACT>(p, m, n0 + wn * 64 + j * 32 + l32, acc[i][j][e], acc[i][j + 2][e]);
-        else put_plain<T>(p, m, n0 + wn * 128 + j * 32 + l32, acc[i][j][e]);
+      for (int j = 0; j < (GATED ? 1 : 2); ++j) {
+        if constexpr (GATED) put_gated<T, ACT>(p, m, n0 + wn * 32 + l32, acc[i][0][e], acc[i][1][e]);
+        else put_plain<T>(p, m, n0 + wn * 64 + j * 32 + l32, acc[i][j][e]);
       }
     }
 }
@@ -658,7 +657,7 @@ template <typename T, bool GATED, int ACT> static bool gemm(GemmArgs p, float* s
       aligned16(p.a, p.sa, e) && aligned16(p.b0, p.sb0, e) && (!GATED || aligned16(p.b1, p.sb1, e))) {
     const int64_t mt = ceil_div(p.M, 256), nt = ceil_div(p.N, GATED ? 128 : 256);
     if (!grid_ok(mt * nt, 256)) return false;
-    k_gemm_large<GATED, ACT><<<dim3(static_cast<uint32_t>(mt * nt)), dim3(256), 0, st>>>(
+    k_gemm_large<GATED, ACT><<<dim3(static_cast<uint32_t>(mt * nt)), dim3(512), 0, st>>>(
         p, static_cast<uint32_t>(mt), static_cast<uint32_t>(nt));
     return true;
   }
