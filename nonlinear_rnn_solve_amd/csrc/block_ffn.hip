@@ -627,15 +627,20 @@ __global__ __launch_bounds__(256) void k_transpose(const T* from, int64_t sf, in
 // ---------------- host ----------------
 inline int64_t padded(int64_t n) { return ceil_div(n, kPad) * kPad; }
 constexpr int64_t kCus = 256, kMostParts = 8;
-// whether the large tiles are for C of M by N (forward: by 2 N): they have to fill the chip
+// Whether the large tiles are for C of M by N (forward: by 2 N): they have to fill half of the chip.  Forward, D = 1024, bf16: 64 of them
+// (R = 1024, F = 2048) 27 us and 20 in k_gemm's, 128 (F = 4096) 30 and 34, 256 (R = 2048) 37 and 54.
 static bool large(int64_t M, int64_t N, bool gated) { return ceil_div(M, 256) * ceil_div(N, gated ? 128 : 256) >= kCus / 2; }
 static bool aligned16(const void* p, int64_t stride, size_t e) { return aligned(p, 16) && stride * static_cast<int64_t>(e) % 16 == 0; }
-// columns of a workgroup of k_gemm, and parts of k
-static int columns_of(int64_t M, int64_t N, bool gated) {
-  return ceil_div(M, 128) * ceil_div(N, gated ? 64 : 128) >= 4 * kCus ? 128 : 64;
+// Columns of a workgroup of k_gemm: 128 where those workgroups are twice the chip's units, with two products in bfloat16 as many.
+// 128 and 64, float32: 387 (gradient, R = 1001, D = 1025, F = 2731) 124 and 116 us, 512 (R = 700, D = 1024, F = 4096) 86 and 97;
+// forward 344 (the first) 98 and 96, 512 (R = 1024) 106 and 118; bfloat16 forward 344 (the first) 34 and 40, 384 30 and 33, gradient 256
+// (R = 1500, D = 1000, F = 2000) 57 and 44.
+static int columns_of(size_t e, int64_t M, int64_t N, bool gated) {
+  return ceil_div(M, 128) * ceil_div(N, gated ? 64 : 128) >= (gated && e == 2 ? kCus : 2 * kCus) ? 128 : 64;
 }
+// parts of k: they fill the chip three times (twice, four and six times make no difference)
 static int64_t parts_of(size_t e, int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = ceil_div(M, 128) * ceil_div(N, columns_of(M, N, false)), most = K * static_cast<int64_t>(e) / (8 * kKBytes);
+  const int64_t tiles = ceil_div(M, 128) * ceil_div(N, columns_of(e, M, N, false)), most = K * static_cast<int64_t>(e) / (8 * kKBytes);
   if (tiles == 0) return 1;
   return std::max<int64_t>(1, std::min({3 * kCus / tiles, most, kMostParts}));
 }
@@ -667,7 +672,7 @@ template <typename T, bool GATED, int ACT> static bool gemm(GemmArgs p, float* s
     p.per_part = ceil_div(ceil_div(p.K, parts), bk) * bk;
     p.parts = p.K ? static_cast<int32_t>(ceil_div(p.K, p.per_part)) : 1;
   }
-  if (!(columns_of(p.M, p.N, GATED) == 128 ? gemm_of<T, 128, GATED, ACT>(p, st) : gemm_of<T, 64, GATED, ACT>(p, st))) return false;
+  if (!(columns_of(sizeof(T), p.M, p.N, GATED) == 128 ? gemm_of<T, 128, GATED, ACT>(p, st) : gemm_of<T, 64, GATED, ACT>(p, st))) return false;
   if (p.parts > 1) {
     const int64_t blocks = ceil_div(p.M * p.N, 256);
     if (!grid_ok(blocks, 256)) return false;
