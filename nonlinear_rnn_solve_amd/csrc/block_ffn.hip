@@ -631,12 +631,13 @@ constexpr int64_t kCus = 256, kMostParts = 8;
 // (R = 1024, F = 2048) 27 us and 20 in k_gemm's, 128 (F = 4096) 30 and 34, 256 (R = 2048) 37 and 54.
 static bool large(int64_t M, int64_t N, bool gated) { return ceil_div(M, 256) * ceil_div(N, gated ? 128 : 256) >= kCus / 2; }
 static bool aligned16(const void* p, int64_t stride, size_t e) { return aligned(p, 16) && stride * static_cast<int64_t>(e) % 16 == 0; }
-// Columns of a workgroup of k_gemm: 128 where those workgroups are twice the chip's units, with two products in bfloat16 as many.
+// Columns of a workgroup of k_gemm: 128 where those workgroups are twice the chip's units, or once for two products in bfloat16.
 // 128 and 64, float32: 387 (gradient, R = 1001, D = 1025, F = 2731) 124 and 116 us, 512 (R = 700, D = 1024, F = 4096) 86 and 97;
-// forward 344 (the first) 98 and 96, 512 (R = 1024) 106 and 118; bfloat16 forward 344 (the first) 34 and 40, 384 30 and 33, gradient 256
-// (R = 1500, D = 1000, F = 2000) 57 and 44.
+// forward 344 (the first) 98 and 96, 512 (R = 1024) 106 and 118; bfloat16 forward 344 (the first) 34 and 40, 384 30 and 33.
+// (bfloat16 gradients of so many are in the large tiles: 256, R = 1500, D = 1000, F = 2000, took 57 us with 128 columns, 44 with 64.)
 static int columns_of(size_t e, int64_t M, int64_t N, bool gated) {
-  return ceil_div(M, 128) * ceil_div(N, gated ? 64 : 128) >= (gated && e == 2 ? kCus : 2 * kCus) ? 128 : 64;
+  if (e == 2 && !gated) return 64;
+  return ceil_div(M, 128) * ceil_div(N, gated ? 64 : 128) >= (e == 2 ? kCus : 2 * kCus) ? 128 : 64;
 }
 // parts of k: they fill the chip three times (twice, four and six times make no difference)
 static int64_t parts_of(size_t e, int64_t M, int64_t N, int64_t K) {
@@ -672,7 +673,13 @@ template <typename T, bool GATED, int ACT> static bool gemm(GemmArgs p, float* s
     p.per_part = ceil_div(ceil_div(p.K, parts), bk) * bk;
     p.parts = p.K ? static_cast<int32_t>(ceil_div(p.K, p.per_part)) : 1;
   }
-  if (!(columns_of(sizeof(T), p.M, p.N, GATED) == 128 ? gemm_of<T, 128, GATED, ACT>(p, st) : gemm_of<T, 64, GATED, ACT>(p, st))) return false;
+  bool wide = false, ok = true;
+  if constexpr (GATED || sizeof(T) == 4) {
+    wide = columns_of(e, p.M, p.N, GATED) == 128;
+    if (wide) ok = gemm_of<T, 128, GATED, ACT>(p, st);
+  }
+  if (!wide) ok = gemm_of<T, 64, GATED, ACT>(p, st);
+  if (!ok) return false;
   if (p.parts > 1) {
     const int64_t blocks = ceil_div(p.M * p.N, 256);
     if (!grid_ok(blocks, 256)) return false;

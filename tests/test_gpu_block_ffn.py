@@ -230,3 +230,10 @@ def test_outputs_in_an_inputs_place_are_refused():
     for kw in (dict(out=x), dict(out=dh), dict(w_out=[wg, None]), dict(w_out=[one, one]), dict(out=one, w_out=[None, one])):
         with pytest.raises(ValueError, match="share memory"):
             block.gated_linear_vjp(x, wg, wu, pre, dh, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(70, 1000, 4100), (1500, 130, 1700), (4100, 2040, 40)])
+def test_many_narrow_and_wide_tiles(shape, dtype):
+    # as many tiles as make them 128 columns wide: of the weights' gradients, of the forward pass, of x's gradient; 256 and more else
+    check(make(*shape, dtype, seed=12))
