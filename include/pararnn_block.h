@@ -133,7 +133,8 @@ size_t pararnn_block_gated_linear_workspace_bytes(int dtype, int64_t R, int64_t 
 pararnn_status pararnn_block_gated_linear(int dtype, int act, int64_t R, int64_t D, int64_t F, const void* x, int64_t x_stride,
                                           const void* w_gate, int64_t gate_stride, const void* w_up, int64_t up_stride,
                                           void* h, int64_t h_stride, float* pre, void* ws, size_t ws_bytes, void* stream);
-/* Gradients for dh [R][F] of dtype, from the forward's pre:  dg = dh u act'(g),  du = dh act(g), rounded to dtype,
+/* Gradients for dh [R][F] of dtype, from the forward's pre:  dg = dh u act'(g),  du = dh act(g) (with bfloat16 planes held as a
+ * sum of two bfloat16, off by at most 2^-16 of each value: the products' operands),
  *     d_x = dg w_gate + du w_up,  d_w_gate = dg^T x,  d_w_up = du^T x, in dtype; d_x [R][D] with a row stride or NULL,
  *     d_w_gate, d_w_up [F][D] with row strides, both or none NULL                                        */
 pararnn_status pararnn_block_gated_linear_vjp(int dtype, int act, int64_t R, int64_t D, int64_t F, const void* x,

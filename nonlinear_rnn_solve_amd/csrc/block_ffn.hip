@@ -22,6 +22,7 @@ using v4u = uint32_t __attribute__((ext_vector_type(4)));
 
 constexpr int kKBytes = 128;    // of k in a tile: 64 bfloat16 or 32 float32
 constexpr int kPad = 64;        // k of a transposed operand is a multiple of it
+constexpr int planes_of(size_t e) { return e == 2 ? 2 : 1; }    // numbers that make one of dg and du in the gradient's products
 
 // activations and their slopes
 template <int ACT> DEV float act(float g) {
@@ -42,6 +43,7 @@ struct GemmArgs {
   const void *a, *b0, *b1;      // b1: the second weight (forward)
   int64_t sa, sb0, sb1;
   int64_t M, N, K;              // N: of one weight
+  int64_t Kb;                   // of B, which is walked anew for each Kb of A's K (K but for two planes, see below)
   void *c0, *c1;                // rows from `split` on go to c1
   int64_t sc0, sc1, split;
   float* pre;
@@ -150,13 +152,14 @@ __global__ __launch_bounds__(256) void k_gemm(const GemmArgs p, uint32_t mtiles,
       const int id = threadIdx.x + i * 256, r = id / 8, c = id % 8;
       ra[i] = load16<T>(a + at_most(m0 + r, p.M - 1) * p.sa, k0 + c * V, k_end);
     }
+    const int64_t past = !GATED && PL == 1 && k0 >= p.Kb ? p.Kb : 0;      // Kb is a multiple of BK then
 #pragma unroll
     for (int i = 0; i < BN / 32; ++i) {
       const int id = threadIdx.x + i * 256, r = id / 8, c = id % 8;
       const bool second = GATED && r >= BN / 2;
       const int64_t n = at_most(n0 + (second ? r - BN / 2 : r), p.N - 1);
       const T* b = static_cast<const T*>(second ? p.b1 : p.b0);
-      rb[i] = load16<T>(b + n * (second ? p.sb1 : p.sb0), k0 + c * V, k_end);
+      rb[i] = load16<T>(b + n * (second ? p.sb1 : p.sb0), k0 - past + c * V, k_end - past);
     }
   };
   v16f acc[2][NF] = {};
@@ -288,13 +291,17 @@ __global__ __launch_bounds__(512, 2) void k_gemm_large(const GemmArgs p, uint32_
     }
   }
   const uint32_t base = static_cast<uint32_t>((uintptr_t)(__attribute__((address_space(3))) char*)smem) + wave * 4096;   // in the LDS
-  // the stage that is next, to its place; behind the last one that one again, so that nothing branches (`step` is 0 then)
-  const auto load = [&](int stage, int step, auto which) {
+  const int count = static_cast<int>(p.K / BK), half = lane / 32, l32 = lane & 31;
+  // stage n's way to the next one: nowhere behind the last, which is loaded again, so that nothing branches; B's may begin anew
+  const int again = GATED ? 0 : static_cast<int>(p.Kb / BK);
+  const auto step_a = [&](int n) -> int64_t { return n + 1 < count ? BK : 0; };
+  const auto step_b = [&](int n) -> int64_t { return n + 1 >= count ? 0 : !GATED && n + 1 == again ? BK - p.Kb : BK; };
+  // stage n, which is next, to its place
+  const auto load = [&](int stage, int n, auto which) {
     constexpr int i = which;
     load_to_lds(from[i], base + stage * kStageBytes + (i >> 2) * 32768 + (i & 3) * 1024);
-    from[i] += step;
+    from[i] += i < 4 ? step_a(n) : step_b(n);
   };
-  const int count = static_cast<int>(p.K / BK), half = lane / 32, l32 = lane & 31;
   v16f acc[4][2] = {};
   struct Pieces { v4u a[4], b[2]; };
   const auto read = [&](int stage, int kk, Pieces& f, auto which) {
@@ -328,13 +335,13 @@ __global__ __launch_bounds__(512, 2) void k_gemm_large(const GemmArgs p, uint32_
     });
   };
   Pieces even, odd;
-  unrolled<0, kLoads>([&](auto i) { load(0, count > 1 ? BK : 0, i); });
+  unrolled<0, kLoads>([&](auto i) { load(0, 0, i); });
   stage_ready();
-  unrolled<0, kLoads>([&](auto i) { load(1, count > 2 ? BK : 0, i); });
+  unrolled<0, kLoads>([&](auto i) { load(1, 1, i); });
   unrolled<0, 6>([&](auto i) { read(0, 0, even, i); });
 #pragma unroll 1
   for (int k = 0; k < count; ++k) {
-    const int stage = k & 1, step = k + 3 < count ? BK : 0;
+    const int stage = k & 1;
     quarter(stage, 0, even, odd);
     quarter(stage, 1, odd, even);
     quarter(stage, 2, even, odd);
@@ -342,7 +349,7 @@ __global__ __launch_bounds__(512, 2) void k_gemm_large(const GemmArgs p, uint32_
     stage_ready();
     multiply(odd, [&](auto which) {
       constexpr int i = which;
-      load(stage, step, which);
+      load(stage, k + 2, which);
       if constexpr (i < 6) read(stage ^ 1, 0, even, which);
     });
   }
@@ -541,17 +548,36 @@ template <typename T> DEV void store16(T* p, int64_t n, const v4u& v) {
   }
 }
 
-// dg and du of R rows as [R][F2] and as [2 F][Rp], zeros from 2 F to F2 and from R to Rp; 64 by 64 of each a workgroup
+// A float32 as the sum of two bfloat16, off by 2^-16 of it at most: dg and du, which the matrix units multiply in bfloat16.  (One
+// bfloat16 would put d_x and d_w off by 2.3e-3 where their own rounding is 1.7e-3.)  Finite values stay finite, infinities are the first's.
+template <int V> DEV void two_bf16(float (&x)[V], Vec<bf16, V>& first, Vec<bf16, V>& rest) {
+  constexpr float most = 3.3895313892515355e38f;                // bfloat16's largest value
+  float r[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float a = fabsf(x[i]);
+    r[i] = x[i];
+    if (a > most && a < __builtin_huge_valf()) x[i] = copysignf(most, x[i]);
+  }
+  first = pack_vec<bf16, V>(x);
+#pragma unroll
+  for (int i = 0; i < V; ++i) r[i] = fabsf(r[i]) < __builtin_huge_valf() ? r[i] - first.get(i) : 0.0f;
+  rest = pack_vec<bf16, V>(r);
+}
+
+// dg and du of R rows as [R][F2] and as [2 F][Rp], zeros from 2 F to F2 and from R to Rp; 64 by 64 of each a workgroup.  In bfloat16
+// two planes of each, side by side in a row: [R][2][F2] and [2 F][2][Rp].
 struct SplitArgs {
   const float* pre;
   const void* dh;
   int64_t sdh, R, F;
-  int64_t Rp, Rs, F2, Fs;       // lengths of a row of `cols` and of `rows` with their zeros, and row strides
+  int64_t Rp, Rs, F2, Fs;       // lengths of a plane's row of `cols` and of `rows` with their zeros, and row strides
   void *rows, *cols;
 };
 template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_split(const SplitArgs p, uint32_t ftiles) {
   using L = Turn<T>;
-  __shared__ L tg, tu;
+  constexpr int PL = planes_of(sizeof(T));
+  __shared__ L tg[PL], tu[PL];
   // neighbouring workgroups take neighbouring columns: rows may lie a large power of two apart, in few of the memory's channels
   const int64_t r0 = static_cast<int64_t>(blockIdx.x / ftiles) * 64, f0 = static_cast<int64_t>(blockIdx.x % ftiles) * 64;
 #pragma unroll
@@ -571,33 +597,48 @@ template <typename T, int ACT> __global__ __launch_bounds__(256) void k_ffn_spli
         du[h + e] = dh * act<ACT>(g);
       }
     }
-    const Vec<T, L::V> og = pack_vec<T, L::V>(dg), ou = pack_vec<T, L::V>(du);
-    const v4u bg{og.w[0], og.w[1], og.w[2], og.w[3]}, bu{ou.w[0], ou.w[1], ou.w[2], ou.w[3]};
-    if (p.rows && n > 0) {
-      T* to = static_cast<T*>(p.rows) + r * p.Fs + f;
-      store16<T>(to, n, bg);
-      store16<T>(to + p.F, n, bu);
+    Vec<T, L::V> og[PL], ou[PL];
+    if constexpr (PL == 2) {
+      two_bf16<L::V>(dg, og[0], og[1]);
+      two_bf16<L::V>(du, ou[0], ou[1]);
+    } else {
+      og[0] = pack_vec<T, L::V>(dg);
+      ou[0] = pack_vec<T, L::V>(du);
     }
-    if (p.cols) {
-      tg.put(i, c, bg);
-      tu.put(i, c, bu);
+#pragma unroll
+    for (int q = 0; q < PL; ++q) {
+      const v4u bg{og[q].w[0], og[q].w[1], og[q].w[2], og[q].w[3]}, bu{ou[q].w[0], ou[q].w[1], ou[q].w[2], ou[q].w[3]};
+      if (p.rows && n > 0) {
+        T* to = static_cast<T*>(p.rows) + r * p.Fs + q * p.F2 + f;
+        store16<T>(to, n, bg);
+        store16<T>(to + p.F, n, bu);
+      }
+      if (p.cols) {
+        tg[q].put(i, c, bg);
+        tu[q].put(i, c, bu);
+      }
     }
   }
   if (p.rows && f0 == 0) {                                      // k's padding
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int i = 0; i < 16 && r0 + wave * 16 + i < p.R; ++i)
-      if (2 * p.F + lane < p.F2) static_cast<T*>(p.rows)[(r0 + wave * 16 + i) * p.Fs + 2 * p.F + lane] = T{};
+      if (2 * p.F + lane < p.F2)
+#pragma unroll
+        for (int q = 0; q < PL; ++q) static_cast<T*>(p.rows)[(r0 + wave * 16 + i) * p.Fs + q * p.F2 + 2 * p.F + lane] = T{};
   }
   if (!p.cols) return;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < L::N; ++k) {
-    const int id = threadIdx.x + k * 256, c = id / L::PER, q = id % L::PER;
-    const int64_t f = f0 + c, r = r0 + q * L::V;
+    const int id = threadIdx.x + k * 256, c = id / L::PER, v = id % L::PER;
+    const int64_t f = f0 + c, r = r0 + v * L::V;
     if (f < p.F) {
-      T* to = static_cast<T*>(p.cols) + f * p.Rs + r;
-      store16<T>(to, p.Rp - r, tg.get(c, q));
-      store16<T>(to + p.F * p.Rs, p.Rp - r, tu.get(c, q));
+#pragma unroll
+      for (int q = 0; q < PL; ++q) {
+        T* to = static_cast<T*>(p.cols) + f * p.Rs + q * p.Rp + r;
+        store16<T>(to, p.Rp - r, tg[q].get(c, v));
+        store16<T>(to + p.F * p.Rs, p.Rp - r, tu[q].get(c, v));
+      }
     }
   }
 }
@@ -727,19 +768,20 @@ static bool sizes_ok(int64_t R, int64_t D, int64_t F) {
 // Row stride of n elements in the workspace: not a large power of two, which would put the rows of a tile behind each other in few
 // of the memory's channels (the two gradient products of R = 8192, D = 4096, F = 8192: 970 -> 882 us each).
 static int64_t spread(int64_t n, size_t e) { return n * static_cast<int64_t>(e) % 4096 ? n : n + kPad; }
-// elements of the gradient's workspace: d_pre [R][F2], d_pre^T [2 F][Rp], x^T [D][Rp], weights^T [D][F2], with row strides Fs, Rs,
-// and float32 sums of parts of k
+// elements of the gradient's workspace: d_pre [R][planes][F2], d_pre^T [2 F][planes][Rp], x^T [D][Rp], weights^T [D][F2], with row
+// strides Fs, Rs, Xs and Ws, and float32 sums of parts of k
 struct GradRoom {
-  int64_t F2, Rp, Fs, Rs, rows, cols, xt, wt, sums;
+  int64_t F2, Rp, Fs, Rs, Xs, Ws, rows, cols, xt, wt, sums;
   int64_t bytes(size_t e) const { return (rows + cols + xt + wt) * static_cast<int64_t>(e) + sums * 4; }
 };
 static GradRoom grad_room(size_t e, int64_t R, int64_t D, int64_t F) {
   GradRoom g;
-  const int64_t px = parts_of(e, R, D, padded(2 * F)), pw = parts_of(e, 2 * F, D, padded(R));
-  g.sums = std::max(px > 1 ? px * R * D : 0, pw > 1 ? pw * 2 * F * D : 0);
+  const int64_t n = planes_of(e);
   g.F2 = padded(2 * F), g.Rp = padded(R);
-  g.Fs = spread(g.F2, e), g.Rs = spread(g.Rp, e);
-  g.rows = padded(R * g.Fs), g.cols = padded(2 * F * g.Rs), g.xt = padded(D * g.Rs), g.wt = padded(D * g.Fs);
+  const int64_t px = parts_of(e, R, D, n * g.F2), pw = parts_of(e, 2 * F, D, n * g.Rp);
+  g.sums = std::max(px > 1 ? px * R * D : 0, pw > 1 ? pw * 2 * F * D : 0);
+  g.Fs = spread(n * g.F2, e), g.Rs = spread(n * g.Rp, e), g.Xs = spread(g.Rp, e), g.Ws = spread(g.F2, e);
+  g.rows = padded(R * g.Fs), g.cols = padded(2 * F * g.Rs), g.xt = padded(D * g.Xs), g.wt = padded(D * g.Ws);
   return g;
 }
 
@@ -758,13 +800,13 @@ static pararnn_status backward(int64_t R, int64_t D, int64_t F, const void* x, i
     k_ffn_split<T, ACT><<<dim3(static_cast<uint32_t>(rt * ft)), dim3(256), 0, st>>>(s, static_cast<uint32_t>(ft));
   }
   if (dx && R && D) {
-    ok = ok && transpose<T>(wg, sg, F, D, wt, room.Fs, F, st) && transpose<T>(wu, su, F, D, wt + F, room.Fs, room.F2 - F, st);
-    const GemmArgs p{rows, wt, nullptr, room.Fs, room.Fs, 0, R, D, room.F2, dx, nullptr, sdx, 0, R};
+    ok = ok && transpose<T>(wg, sg, F, D, wt, room.Ws, F, st) && transpose<T>(wu, su, F, D, wt + F, room.Ws, room.F2 - F, st);
+    const GemmArgs p{rows, wt, nullptr, room.Fs, room.Ws, 0, R, D, planes_of(sizeof(T)) * room.F2, room.F2, dx, nullptr, sdx, 0, R};
     ok = ok && gemm<T, false, 0>(p, room.sums ? sums : nullptr, st);
   }
   if (dwg && F && D) {
-    ok = ok && transpose<T>(x, sx, R, D, xt, room.Rs, room.Rp, st);
-    const GemmArgs p{cols, xt, nullptr, room.Rs, room.Rs, 0, 2 * F, D, room.Rp, dwg, dwu, sdg, sdu, F};
+    ok = ok && transpose<T>(x, sx, R, D, xt, room.Xs, room.Rp, st);
+    const GemmArgs p{cols, xt, nullptr, room.Rs, room.Xs, 0, 2 * F, D, planes_of(sizeof(T)) * room.Rp, room.Rp, dwg, dwu, sdg, sdu, F};
     ok = ok && gemm<T, false, 0>(p, room.sums ? sums : nullptr, st);
   }
   return ok ? launched() : PARARNN_ERR_UNSUPPORTED;
@@ -793,7 +835,7 @@ extern "C" pararnn_status pararnn_block_gated_linear(int dtype, int act, int64_t
   if (R > kMost || D > kMost || F > kMost) return PARARNN_ERR_UNSUPPORTED;
   if (!ws_ok(ws, ws_bytes, pararnn_block_gated_linear_workspace_bytes(dtype, R, D, F, 0))) return PARARNN_ERR_WORKSPACE;
   if (R == 0 || F == 0) return PARARNN_OK;
-  const GemmArgs p{x, w_gate, w_up, x_stride, gate_stride, up_stride, R, F, D, h, nullptr, h_stride, 0, R, pre, nullptr, D, 1};
+  const GemmArgs p{x, w_gate, w_up, x_stride, gate_stride, up_stride, R, F, D, D, h, nullptr, h_stride, 0, R, pre, nullptr, D, 1};
   const auto st = static_cast<hipStream_t>(stream);
   bool ok;
   if (dtype == PARARNN_BF16)

@@ -237,3 +237,57 @@ def test_outputs_in_an_inputs_place_are_refused():
 def test_many_narrow_and_wide_tiles(shape, dtype):
     # as many tiles as make them 128 columns wide: of the weights' gradients, of the forward pass, of x's gradient; 256 and more else
     check(make(*shape, dtype, seed=12))
+
+
+@pytest.mark.parametrize("shape", [(33, 129, 31), (300, 257, 513), (70, 1000, 4100), (4100, 2040, 40), (1300, 64, 70)])
+def test_bfloat16_gradients_are_rounded_once(shape):
+    # dg and du are off by 2^-16 and float32's roundings (as in check), the products' sums by float32's: of twice as many terms, dg's and du's
+    # two bfloat16.  Only the result is rounded to bfloat16.  Few terms (the first and the last shape) show a rounding of each term best
+    x, wg, wu, dh = make(*shape, BF, seed=21)
+    (R, D), F = x.shape, wg.shape[0]
+    got = block.gated_linear_vjp(x, wg, wu, block.gated_linear(x, wg, wu, want_pre=True)[1], dh)
+    X, G, U, dH = f64(x), f64(wg), f64(wu), f64(dh)
+    g, u = X @ G.t(), X @ U.t()
+    eg, eu = (D + 2) * U32 * (X.abs() @ G.abs().t()), (D + 2) * U32 * (X.abs() @ U.abs().t())
+    s = torch.sigmoid(g)
+    dg, du = dH * u * (s * (1 + g * (1 - s))), dH * g * s
+    sg, su = 1.13 * (dH * u).abs(), (dH * g).abs()                   # magnitudes
+    one = U16 ** 2 + 32 * U32
+    og, ou = one * sg + dH.abs() * (1.13 * eu + u.abs() * eg), one * su + dH.abs() * 1.13 * eg
+    for name, w, t in (("d_x", dg @ G + du @ U, og @ G.abs() + ou @ U.abs() + 4 * F * U32 * (sg @ G.abs() + su @ U.abs())),
+                       ("d_w_gate", dg.t() @ X, og.t() @ X.abs() + 2 * R * U32 * (sg.t() @ X.abs())),
+                       ("d_w_up", du.t() @ X, ou.t() @ X.abs() + 2 * R * U32 * (su.t() @ X.abs()))):
+        close(got[name], w, rounded(w, t, BF), name)
+
+
+def test_bfloat16_gradients_of_huge_and_infinite_values():
+    # dg = 3.4e38, which rounds to a bfloat16 infinity, stays finite; an infinite one stays infinite; u = 0 in the other rows
+    x, half = torch.ones(70, 1, device="cuda", dtype=BF), torch.full((1, 1), 0.5, device="cuda", dtype=BF)
+    pre = torch.zeros(70, 2, device="cuda")
+    pre[:, 0] = 2.0
+    slope = float(plain.silu(torch.tensor(2.0)) + torch.sigmoid(torch.tensor(2.0)) * (1 - plain.silu(torch.tensor(2.0))))
+    pre[0, 1], pre[1, 1] = 3.4e38 / slope, float("inf")
+    got = block.gated_linear_vjp(x, half, half * 0, pre, torch.ones(70, 1, device="cuda", dtype=BF))
+    want = torch.tensor([1.7e38, float("inf")] + [0.0] * 68, dtype=torch.float64)[:, None]
+    close(got["d_x"], want, 1.01 * U16 * 1.7e38, "d_x")
+
+
+def test_large_tiles_repeat_their_bits():
+    # 256 by 256 tiles forward and in both of the gradient's products
+    x, wg, wu, dh = make(4100, 2048, 2048, BF, seed=7)
+
+    def both():
+        h, pre = block.gated_linear(x, wg, wu, want_pre=True)
+        return [h, pre] + list(block.gated_linear_vjp(x, wg, wu, pre, dh).values())
+
+    first = both()
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(first, both()))
+
+
+def test_pre_is_float32():
+    # of bfloat16 inputs too: sums of exact products, off by float32's roundings only
+    x, wg, wu, _ = make(300, 128, 96, BF, seed=7)
+    _, pre = block.gated_linear(x, wg, wu, want_pre=True)
+    for got, w in ((pre[:, :96], wg), (pre[:, 96:], wu)):
+        close(got, f64(x) @ f64(w).t(), 130 * U32 * (f64(x).abs() @ f64(w).abs().t()), "pre")
