@@ -94,29 +94,36 @@ template <typename T> DEV void put_plain(const GemmArgs& p, int64_t m, int64_t n
 // half of the row's number, so that no two of the sixteen lanes that read together meet in a bank.  Rows past the end are read as the last.  With
 // p.parts > 1 the workgroups split k, and each writes float32 sums of its own to p.sums, [parts][M][N].
 //
-// Float32.  The matrix units multiply bfloat16 16 times as fast as float32.  A float32 is the exact sum of three bfloat16 of eight
-// bits each (its leading bits, cut off, then those of the rest); of the nine products of two such numbers the six that are
-// larger than 2^-24 of theirs are formed, exactly, and summed in float32 like any product's terms.  That is float32's accuracy at 2.7
-// times its rate: 6 instructions of 32 cycles in place of 8 of 64.  (An infinity less itself is a NaN: a float32
-// infinity makes its row's or column's results NaN.)
+// Float32.  The matrix units multiply bfloat16 16 times as fast as float32.  A float32 is the exact sum of three bfloat16, each
+// the nearest to what those before it leave: the second is at most 2^-8 of the value and the third 2^-16, of either sign.  Of the nine
+// products of two such numbers six are formed, exactly, and summed in float32 like any product's terms; the three left out
+// are 2^-24 of a term each at most, 2^-24 together in what was measured, and without a bias.  (Cut off and not rounded the parts have the
+// value's sign and twice the size: what was left out reached 2^-21 and shrank every term, by 0.7 2^-24 on average.)  That is float32's
+// accuracy at 2.7 times its rate: 6 instructions of 32 cycles in place of 8 of 64.  (An infinity less itself is a NaN: a
+// float32 infinity makes its row's or column's results NaN.)
 template <typename T> struct Parts {
   static constexpr int PL = sizeof(T) == 4 ? 3 : 1;             // numbers that make one
   static constexpr int CPR = sizeof(T) == 4 ? 4 : 8;            // 16-byte pieces of a row in shared memory
   static DEV int swap(int r, int c) { return CPR == 8 ? c ^ (r >> 1 & 7) : c ^ (r >> 2 & 3); }
 };
-DEV uint32_t upper_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }   // a's, then b's
+// two values as bfloat16, each to the nearest, in one instruction
+DEV uint32_t pair_bf16(float a, float b) {
+  using v2f = float __attribute__((ext_vector_type(2)));
+  using v2b = __bf16 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2b));
+}
 DEV void split3(const v4u& x, uint32_t (&hi)[2], uint32_t (&mid)[2], uint32_t (&lo)[2]) {
-  float r[4], q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r[i] = __uint_as_float(x[i]) - __uint_as_float(x[i] & 0xffff0000u);
-    q[i] = r[i] - __uint_as_float(__float_as_uint(r[i]) & 0xffff0000u);
-  }
+  constexpr float most = 3.3895313892515355e38f;                // bfloat16's largest value: no finite value becomes an infinity
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    hi[i] = upper_halves(x[2 * i], x[2 * i + 1]);
-    mid[i] = upper_halves(__float_as_uint(r[2 * i]), __float_as_uint(r[2 * i + 1]));
-    lo[i] = upper_halves(__float_as_uint(q[2 * i]), __float_as_uint(q[2 * i + 1]));
+    float v[2], r[2], q[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) v[k] = __uint_as_float(x[2 * i + k]);
+    hi[i] = pair_bf16(__builtin_amdgcn_fmed3f(v[0], -most, most), __builtin_amdgcn_fmed3f(v[1], -most, most));
+    r[0] = v[0] - __uint_as_float(hi[i] << 16), r[1] = v[1] - __uint_as_float(hi[i] & 0xffff0000u);
+    mid[i] = pair_bf16(r[0], r[1]);
+    q[0] = r[0] - __uint_as_float(mid[i] << 16), q[1] = r[1] - __uint_as_float(mid[i] & 0xffff0000u);
+    lo[i] = pair_bf16(q[0], q[1]);
   }
 }
 // 16 bytes that a thread has loaded (piece c of the 8 of row r) to shared memory of ROWS rows

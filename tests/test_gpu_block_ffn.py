@@ -291,3 +291,35 @@ def test_pre_is_float32():
     _, pre = block.gated_linear(x, wg, wu, want_pre=True)
     for got, w in ((pre[:, :96], wg), (pre[:, 96:], wu)):
         close(got, f64(x) @ f64(w).t(), 130 * U32 * (f64(x).abs() @ f64(w).abs().t()), "pre")
+
+
+@pytest.mark.parametrize("D", [1, 2, 3, 4])
+def test_float32_of_few_terms(D):
+    # of the split's nine products three are left out: at most 2 u of a term; sums of D terms are off by D u more.  These values' second and
+    # third parts, were they cut off and not rounded, would be the largest there are
+    v = 1 + 2.0 ** -7 - 2.0 ** -23
+    x, w = torch.full((100, D), v, device="cuda"), torch.full((40, D), v, device="cuda")
+    pre = block.gated_linear(x, w, -w, want_pre=True)[1]
+    want = f64(x) @ f64(w).t()
+    close(pre[:, :40], want, (D + 2) * U32 * want, "gate")
+    close(pre[:, 40:], -want, (D + 2) * U32 * want, "up")
+
+
+def test_float32_products_have_no_bias():
+    # one term each, off by at most 3 u, upwards as often as downwards: as the mean of 4096 independent ones that is 6 3 / 64 u at most
+    g = torch.Generator().manual_seed(31)
+    x, w = torch.randn(4096, 1, generator=g).cuda(), torch.randn(4096, 1, generator=g).cuda()
+    pre = block.gated_linear(x, w, w, want_pre=True)[1]
+    want = f64(x) @ f64(w).t()
+    off = (f64(pre[:, :4096]) - want) / want / U32
+    assert float(off.abs().max()) <= 3 and abs(float(off.mean())) <= 18 / 64, (float(off.abs().max()), float(off.mean()))
+
+
+def test_float32_at_its_lowest_value():
+    # values that round to an infinite bfloat16, as masks have them
+    low = torch.finfo(F32).min
+    x = torch.tensor([[low, 1.0], [-low, -3.0]] * 40, device="cuda")
+    w = torch.tensor([[2.0 ** -10, 1.0], [0.25, -(2.0 ** 100)]], device="cuda")
+    pre = block.gated_linear(x, w, w, want_pre=True)[1]
+    want = f64(x) @ f64(w).t()
+    close(pre[:, :2], want, 4 * U32 * (f64(x).abs() @ f64(w).abs().t()), "gate")
