@@ -78,11 +78,14 @@ DEV uint32_t load_codes(const void* p, int64_t at) {
 }
 
 struct Rates {
-  float decay, rate, c2, grad_scale;
+  float decay, rate, c2, grad_scale;   // decay: lr weight_decay
 };
 
+// What a step takes from p is summed by itself: 1 - lr weight_decay would be rounded to a multiple of 2^-24, a decay of 1e-7 to 1.2e-7
+// and one below 3e-8 to nothing, for all parameters and steps alike.  (An infinite p would be taken from itself.)
 DEV float new_param(const AdamwArgs& a, const Rates& r, float p, float m, float v) {
-  return fmaf(p, r.decay, -(r.rate * m) / fmaf(sqrtf(v), r.c2, a.eps));
+  const float step = (r.rate * m) / fmaf(sqrtf(v), r.c2, a.eps);
+  return p - (fabsf(p) < __builtin_huge_valf() ? fmaf(p, r.decay, step) : step);
 }
 
 // PT, GT: types of parameters and gradients.  Bound by memory: 28 bytes an element with float32 and 32-bit moments, 12 to 16
@@ -132,7 +135,7 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
     c1 = static_cast<float>(1.0 / (1.0 - power(a.b1, step)));
     c2 = static_cast<float>(1.0 / sqrt(1.0 - power(a.b2, step)));
   }
-  const Rates r{fmaf(-lr, a.decay, 1.0f), lr * c1, c2, a.grad_scale_ptr ? *a.grad_scale_ptr : a.grad_scale};
+  const Rates r{lr * a.decay, lr * c1, c2, a.grad_scale_ptr ? *a.grad_scale_ptr : a.grad_scale};
   const uint32_t lo = static_cast<uint32_t>(a.seed), hi = static_cast<uint32_t>(a.seed >> 32);
   const uint32_t key = mix(lo ^ mix(hi) ^ mix(static_cast<uint32_t>(step) ^ mix(static_cast<uint32_t>(step >> 32))));
 

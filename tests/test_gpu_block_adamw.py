@@ -302,3 +302,23 @@ def test_moments_that_share_memory_are_refused():
     with pytest.raises(ValueError, match="overlap"):
         block.adamw_step([p], [g], m8, v8, 1, m_scale=s, v_scale=s)
     assert not p.any() and not m8.any()
+
+
+@pytest.mark.parametrize("lr,decay", [(1e-6, 0.1), (1e-7, 0.25), (1e-5, 0.01), (1e-4, 0.1), (1e-3, 0.1)])
+def test_small_decays(lr, decay):
+    # without gradients p is taken p lr decay, off by 4 u of that (lr, decay, their product, the product), and rounded once: by half a step
+    p = torch.randn(1 << 16, generator=torch.Generator().manual_seed(12)).cuda()
+    want = f64(p) * (1 - lr * decay)
+    m, v = torch.zeros_like(p), torch.zeros_like(p)
+    block.adamw_step([p], [torch.zeros_like(p)], m, v, 1, lr=lr, weight_decay=decay)
+    half = 2.0 ** (torch.floor(torch.log2(want.abs())) - 24)
+    close(p, want, half + 5 * U32 * lr * decay * want.abs(), "param")
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.1])
+def test_infinite_parameters_stay(decay):
+    p = torch.tensor([float("inf"), float("-inf"), 1.0], device="cuda")
+    m, v = (torch.zeros(256, device="cuda") for _ in range(2))
+    block.adamw_step([p], [torch.tensor([0.5, 0.0, 0.0], device="cuda")], m, v, 1, lr=0.5, weight_decay=decay)
+    assert p[:2].tolist() == [float("inf"), float("-inf")]
+    close(p[2:], torch.tensor([1.0 - 0.5 * decay], dtype=torch.float64), U32, "param")        # one rounding below 1, and decay's own
