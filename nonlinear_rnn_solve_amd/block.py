@@ -98,6 +98,7 @@ def selective_scan_vjp(x, dt, A, b, c, carry, dy, skip=None, z=None, dt_bias=Non
     Returns dict: d_x, d_dt, d_z (with z) [B, T, D], d_b, d_c in b's shape, in x's type; d_A [D, N], d_skip, d_dt_bias [D]
     float32 (want_params); d_h0 float32 (want_h0).
     out: five tensors or None (d_x, d_dt, d_z, d_b, d_c) to write into, strided as they like.
+    A channel with a rate A of -inf has a d_dt and d_dt_bias of NaN; the other gradients are finite.
     """
     return (_binding or load_library()).selective_scan_vjp(x, dt, A, b, c, carry, dy, skip, z, dt_bias, h0, d_last, cu_seqlens, out,
                                                            want_params, want_h0)

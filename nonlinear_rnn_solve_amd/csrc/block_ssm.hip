@@ -621,6 +621,7 @@ __global__ __launch_bounds__(WV * WAVE) void k_ssm_back_ends(const SsmGradArgs g
         if (whole || Q < steps) {
           for_down<Q, Q + 4>([&](auto step) {
             constexpr int t = step;
+            if (!whole && t >= steps) return;     // exp(0 A) is no 1 for an infinite A
             const float2 v = u[t][lane];
             float c[NS];
             step_values<NS, NP>(sc, wave, t, c);
@@ -663,8 +664,14 @@ __global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) 
   const int32_t first = w.s * p.per, last = first + p.per < p.tiles ? first + p.per : p.tiles;
   const int32_t tb = last * CT < p.T ? last * CT : p.T;
 
+  // lanes past the last channel have rates and states of zero, like their steps: 0 NaN would enter the sums over channels
   float A2[NS], P[NS] = {}, dA[NS] = {}, d_skip = 0.0f, d_bias = 0.0f;
   load_dn<NS>(p.A + own, p.N, n0, A2);
+  const auto inside = [&](float (&v)[NS]) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) v[n] = in ? v[n] : 0.0f;
+  };
+  inside(A2);
 #pragma unroll
   for (int n = 0; n < NS; ++n) A2[n] *= kLog2e;
   const float bias = in && p.dt_bias ? p.dt_bias[d] : 0.0f, skip = in && p.skip ? p.skip[d] : 0.0f;
@@ -675,6 +682,7 @@ __global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) 
     int32_t s = (stop - 1) / (p.per * CT);
     load_nd<NS>(p.end + (s * p.B + w.b) * seq_step + d, D_, p.N, n0, P);
     for (--s; s > w.s; s -= BATCH) over_segments<NS, BATCH>(p, w, s, s - w.s, -1, d, n0, A2, P);
+    inside(P);
   }
 
   Bits<T> x[E], dl[E], z[E], dy[E], vb[L::BC], vc[L::BC];
@@ -724,7 +732,7 @@ __global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) 
     Shared<T, NS, WV>::put(sc, vc);
     float h0[NS];
 #pragma unroll
-    for (int n = 0; n < NS; ++n) h0[n] = h_in[n];
+    for (int n = 0; n < NS; ++n) h0[n] = in ? h_in[n] : 0.0f;
     __syncthreads();
     if (tile > first) {
       cx.move(-CT);
@@ -743,6 +751,7 @@ __global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) 
       const auto* e = arguments<SsmGradArgs>();
       const int32_t j = e->f.seqs.cu ? uniform(marks.start[t]) : 0;
       load_dn<NS>(e->f.h0 ? e->f.h0 + row_states + j * seq_step : nullptr, e->f.N, n0, v);
+      inside(v);
     };
     float rb[NS], tA[NS] = {}, hm[NS];
     get_shared<NS, NP>(sb, wave, lane, rb);
@@ -780,9 +789,10 @@ __global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) 
         const float2 v = u[s0 + t][lane];
         float c[NS];
         step_values<NS, NP>(sc, wave, s0 + t, c);
+        const bool past = events && s0 + t >= steps;            // exp(0 A) is no 1 for an infinite A
         for_up<0, NS>([&](auto state) {
           constexpr int n = state;
-          as[t][n] = hw_exp2(A2[n] * v.x);
+          as[t][n] = past ? 1.0f : hw_exp2(A2[n] * v.x);
           hs[t][n] = fmaf(as[t][n], h[n], of_step<NS, t, n>(hb) * v.y);
           y = n ? fmaf(c[n], hs[t][n], y) : c[n] * hs[t][n];
         });
@@ -798,6 +808,7 @@ __global__ __launch_bounds__(WV * WAVE, 2) void k_ssm_back(const SsmGradArgs g) 
             const auto* e = arguments<SsmGradArgs>();
             const int32_t j = e->f.seqs.cu ? uniform(marks.before[s0 + t + 1]) : 0;
             load_dn<NS>(e->d_last ? e->d_last + row_states + j * seq_step : nullptr, e->f.N, n0, P);
+            inside(P);
           }
           const float2 v = u[s0 + t][lane];
           const float G = sg[s0 + t][lane];

@@ -336,3 +336,26 @@ def test_outputs_in_an_inputs_place_are_refused():
     for out in ([k.dy] + [None] * 4, [one, one, None, None, None], [None, None, None, k.b, None]):
         with pytest.raises(ValueError, match="share memory"):
             k.backward(carry, out=out)
+
+
+@pytest.mark.parametrize("B,T,D,cu", [(2, 5, 33, None), (2, 21, 65, None), (2, 33, 64, None), (1, 1003, 64, None), (1, 1003, 40, [0, 18, 18, 519, 1003])])
+def test_gradients_of_a_state_that_forgets_at_once(B, T, D, cu):
+    # as forward: A = -inf gives the bits of A = -1e30, and nothing past a row's end or its last channel reaches the sums
+    k = Case(B, T, D, 5, F32, 71, n=len(cu) - 1 if cu else 0)
+    k.A[:, 2] = -1e30
+    want = k.backward(k.forward(cu, want_carry=True)[2], cu)
+    k.A[:, 2] = float("-inf")
+    got = k.backward(k.forward(cu, want_carry=True)[2], cu)
+    for name in set(want) - {"d_dt", "d_dt_bias"}:
+        assert torch.isfinite(got[name]).all() and torch.equal(got[name], want[name]), name
+
+
+def test_one_channels_infinite_state_leaves_the_others_sums():
+    # the last channel's state is infinite: lanes past it must not make a NaN of the sums over channels, where its own term is infinite
+    k = Case(1, 40, 65, 4, F32, 74, gate=False)
+    k.h0 = k.h0.clone()
+    k.h0[0, 64, 1] = float("inf")
+    k.dy = torch.ones_like(k.dy)
+    got = k.backward(k.forward(want_carry=True)[2])
+    assert torch.isposinf(got["d_c"][..., 1]).all() and torch.isfinite(got["d_c"][..., [0, 2, 3]]).all()
+    assert torch.isfinite(got["d_b"]).all() and torch.isfinite(got["d_x"]).all()
