@@ -244,6 +244,14 @@ DEV bool boundary(const Seqs& q, int32_t t, int32_t T) {
   return q.begin(q.of(t)) == t && q.of(t) > 0;
 }
 
+// 2^x h + e, of a whole segment: growing states may have a factor past float32's range and still be zero or small, so from 2^126 on
+// it is taken in two halves (beyond 2^254 only denormal states would stay finite; theirs is taken as 2^254)
+DEV float through(float x, float h, float e) {
+  const bool large = x > 126.0f;
+  const float f = hw_exp2(large ? fminf(0.5f * x, 127.0f) : x);
+  return fmaf(f, large ? f * h : h, e);
+}
+
 // A state carried over `count` (at most K of them here) segments from segment s on, in steps of `dir`: the loads of all before
 // the first is used
 constexpr int BATCH = 8;
@@ -261,7 +269,7 @@ DEV void over_segments(const SsmArgs& p, const Where& w, int32_t s, int32_t coun
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int n = 0; n < NS; ++n) h[n] = k < count ? fmaf(hw_exp2(A2[n] * total[k]), h[n], e[k][n]) : h[n];
+    for (int n = 0; n < NS; ++n) h[n] = k < count ? through(A2[n] * total[k], h[n], e[k][n]) : h[n];
 }
 
 // ENDS: what each segment but the last leaves (from its last sequence's start, if one begins in it).  Otherwise the walk itself.

@@ -359,3 +359,36 @@ def test_one_channels_infinite_state_leaves_the_others_sums():
     got = k.backward(k.forward(want_carry=True)[2])
     assert torch.isposinf(got["d_c"][..., 1]).all() and torch.isfinite(got["d_c"][..., [0, 2, 3]]).all()
     assert torch.isfinite(got["d_b"]).all() and torch.isfinite(got["d_x"]).all()
+
+
+@pytest.mark.parametrize("T,quiet", [(1003, 990), (4003, 3900)])
+def test_growth_past_float32_in_a_quiet_row(T, quiet):
+    # rates of 1 and steps of log 2: 2^T over the row.  x is zero up to step `quiet`, so the states are, and stay below 2^115 after it; the
+    # steps before the last are cut into segments, each of which would multiply a zero by an infinity
+    k = Case(1, T, 40, 3, F32, 75, state=False)
+    k.A = torch.ones_like(k.A)
+    k.dt, k.dt_bias, k.x = torch.zeros_like(k.dt), torch.zeros_like(k.dt_bias), k.x.clone()
+    k.x[:, :quiet] = 0
+    y, last, carry = k.forward(want_carry=True)
+    want, wl = plain.ssm(*[t.detach() if t is not None else None for t in k.leaves()])
+    assert not y[:, :quiet].any() and torch.isfinite(y).all()
+    # each of the steps after it adds 16 u of the largest state so far (as above), and the state doubles: 2 x 16 u of its magnitudes
+    magnitudes = plain.ssm(*[t.detach().abs() if t is not None and i not in (1, 2, 7) else t if t is None else t.detach() for i, t in enumerate(k.leaves())])[1]
+    close(last, wl[:, 0], 16 * U32 * (T - quiet) * magnitudes[:, 0], "h_last")
+    # the other way: only the first steps have a gradient, so nothing flows back to them
+    k.dy = k.dy.clone()
+    k.dy[:, T - quiet:] = 0
+    got = k.backward(carry)
+    assert all(torch.isfinite(t).all() for t in got.values())
+    assert not got["d_x"][:, T - quiet:].any() and got["d_x"][:, :T - quiet].any()
+
+
+def test_growth_past_float32_of_a_small_state():
+    # h = 2^-100 grows by 2^150 over a row of several segments: 2^50, though the factor is infinite
+    T = 2000
+    k = Case(1, T, 64, 4, F32, 76)
+    k.A, k.dt, k.dt_bias = torch.full_like(k.A, 150 / T), torch.zeros_like(k.dt), torch.zeros_like(k.dt_bias)
+    k.x, k.h0 = torch.zeros_like(k.x), torch.full_like(k.h0, 2.0 ** -100)
+    y, last, _ = k.forward()
+    # log 2 and A are off by 3 u together, so the exponent 104 = 150 log 2 by 312 u; each of its steps adds 4 u
+    close(last, torch.full((1, 64, 4), 2.0 ** 50, dtype=torch.float64), 2.0 ** 50 * U32 * (312 + 4 * T), "h_last")
