@@ -154,8 +154,9 @@ pararnn_status pararnn_block_gated_linear_vjp(int dtype, int act, int64_t R, int
  * bits = 32: m, v float32.  bits = 8: a byte each, with a float32 scale s for each block of PARARNN_BLOCK_ADAMW_BLOCK elements
  * of m and of v, the smallest power of two of at least 2^-80 with max |value| <= 1.875 s.  A code's lowest three bits are f, the
  * bits above it e (m: four and a sign above them, bias 15; v: five, bias 31): the magnitude is s (1 + f/8) 2^(e-bias), for e = 0
- * s f/8 2^(1-bias).  A new moment is rounded up or down at random, with probabilities that keep its mean (to nearest, slow
- * averages would stand still), by 16 bits of a hash of the seed, the step and the element's place in the state.  A block
+ * s f/8 2^(1-bias).  A new moment is rounded up or down at random, with probabilities that keep its mean to 2^-16 of a step (to
+ * nearest, slow averages would stand still): up where its place between two codes and a multiple of 2^-16 below one, 16 bits of a hash of
+ * the seed, the step and the element's place in the state, add up to one or more (m) or to more than one (v).  A block
  * with a NaN or an infinity has s = NaN, and its values are NaN from then on.
  * The step and, if wanted, lr and grad_scale may be read from device memory, so that a captured graph follows them.
  * The same tensor must not be given twice, nor overlapping ones.

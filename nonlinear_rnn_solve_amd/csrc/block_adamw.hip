@@ -56,7 +56,8 @@ template <int BIAS> DEV float decode(uint32_t code, float scale) {
   if constexpr (BIAS == 15) x = __uint_as_float(__float_as_uint(x) | (code & 128) << 24);
   return x;
 }
-// of |x| <= 1.875 2^e, rounded up where its place between two codes and `number` / 2^20 add up to one or more
+// of |x| <= 1.875 2^e, rounded up where its place between two codes and `number` / 2^20 add up to one or more (a number less by one:
+// to more than one)
 template <int BIAS> DEV uint32_t encode(float x, int e, uint32_t number) {
   const float y = ldexpf(fabsf(x), -e);
   const uint32_t normal = ((__float_as_uint(y) + number) >> 20) - (127 - BIAS) * 8;
@@ -176,7 +177,8 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
         const uint64_t e = static_cast<uint64_t>(place) + i;
         const uint32_t h = mix(static_cast<uint32_t>(e) ^ mix(key ^ static_cast<uint32_t>(e >> 32)));
         cm |= encode<15>(nm[i], em, (h & 0xffff) << 4) << (8 * i);
-        // more than one, for v: a tie goes down, so that no 1/2^20 of all second moments grows where nothing is to be added
+        // more than one, for v: a tie goes down, its chance is 2^-16 lower than its place.  Elementary forms that scale by torch's ldexp are
+        // short of their ties where that is no power of two on this GPU (131071.99 for 2^17), and v's codes are compared with theirs
         const uint32_t up = (h >> 16) << 4;
         cv |= encode<31>(nv[i], ev, up ? up - 1 : 0) << (8 * i);
       }

@@ -322,3 +322,25 @@ def test_infinite_parameters_stay(decay):
     block.adamw_step([p], [torch.tensor([0.5, 0.0, 0.0], device="cuda")], m, v, 1, lr=0.5, weight_decay=decay)
     assert p[:2].tolist() == [float("inf"), float("-inf")]
     close(p[2:], torch.tensor([1.0 - 0.5 * decay], dtype=torch.float64), U32, "param")        # one rounding below 1, and decay's own
+
+
+def test_rounding_of_ties():
+    # 17/16 is halfway between two codes: m goes up where the element's number is 2^19 / 2^20 or more, v where it is more.  One in 2^16 is just that
+    def mix(x):
+        x = (x ^ (x >> 16)) * 0x7FEB352D & 0xFFFFFFFF
+        x = (x ^ (x >> 15)) * 0x846CA68B & 0xFFFFFFFF
+        return x ^ (x >> 16)
+
+    n, seed, step = 1 << 21, 7, 3
+    h = mix(torch.arange(n) ^ mix(mix(torch.tensor(seed) ^ mix(torch.tensor(step)))))
+    for power, name in ((1, "m"), (2, "v")):
+        g = torch.full((n,), float(torch.tensor(17 / 16, dtype=torch.float64) ** (1 / power)), device="cuda")
+        assert float(g[0] ** power) == 17 / 16
+        p = [torch.zeros(n, device="cuda")]
+        m, v = (torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2))
+        ms, vs = (torch.zeros(n // 256, device="cuda") for _ in range(2))
+        block.adamw_step(p, [g], m, v, step, betas=(0.0, 0.0), m_scale=ms, v_scale=vs, seed=seed)
+        number = (h & 0xFFFF if name == "m" else h >> 16) << 4
+        assert int((number == 1 << 19).sum()) > 0
+        up = number >= 1 << 19 if name == "m" else number > 1 << 19
+        assert torch.equal(f64(block.adamw_moments(m, v, ms, vs)[name == "v"]), torch.where(up, 9 / 8, 1.0).double()), name
