@@ -35,6 +35,8 @@ template <int ACT> DEV float slope(float g) {
     const float s = sigmoid(g);
     return silu_slope(g, s);
   }
+  // beyond 16 the sigmoid is 0 or 1 and the slope too, where g^3 could still pass float32's range (and 0 times infinity follow)
+  g = fabsf(g) > 16.0f ? copysignf(16.0f, g) : g;
   const float s = sigmoid(1.5957691216057308f * fmaf(0.044715f * g, g * g, g));
   return s * fmaf(g * (1.0f - s), 1.5957691216057308f * fmaf(3 * 0.044715f * g, g, 1.0f), 1.0f);
 }

@@ -323,3 +323,15 @@ def test_float32_at_its_lowest_value():
     pre = block.gated_linear(x, w, w, want_pre=True)[1]
     want = f64(x) @ f64(w).t()
     close(pre[:, :2], want, 4 * U32 * (f64(x).abs() @ f64(w).abs().t()), "gate")
+
+
+@pytest.mark.parametrize("activation", ["silu", "gelu"])
+@pytest.mark.parametrize("far", [17.0, 100.0, 1e15, 1e20, 3e38])
+def test_gradients_of_gates_far_out(activation, far):
+    # h = act(x) (x 2^-20): 0 for negative x, x^2 2^-20 for positive, whose derivative is x 2^-19 (silu at 17: 1 + 17 e^-17 within 1e-6)
+    x = torch.tensor([[far], [-far]], device="cuda")
+    one, small = torch.ones(1, 1, device="cuda"), torch.full((1, 1), 2.0 ** -20, device="cuda")
+    pre = block.gated_linear(x, one, small, activation, want_pre=True)[1]
+    got = block.gated_linear_vjp(x, one, small, pre, torch.ones(2, 1, device="cuda"), activation, want_params=False)["d_x"]
+    want = torch.tensor([[f64(x)[0, 0] * 2.0 ** -19], [0.0]], dtype=torch.float64)
+    close(got, want, 1e-5 * (want + 17 * 2.0 ** -19), "d_x")
