@@ -126,7 +126,8 @@ pararnn_status pararnn_block_selective_scan_vjp(const pararnn_block_ssm* prob, c
  * g Phi(g) in its tanh form.  x [R][D], w_gate, w_up [F][D], h [R][F] of dtype, with row strides.
  *   pre  [R][2F] float32, dense: g and u of each row side by side, for the gradient; or NULL
  * Bfloat16 products are exact and summed in float32.  Float32 products have float32's accuracy; an infinity among float32 values
- * makes the results it enters NaN.
+ * makes the results it enters infinite or NaN, which of the two depends on the sizes (up to 64 rows the forward pass multiplies in
+ * float32, otherwise a value is split into bfloat16).
  * UNSUPPORTED: R, D or F of 2^31 - 512 or more.
  * ---------------------------------------------------------------------------------------------- */
 typedef enum { PARARNN_BLOCK_SILU = 0, PARARNN_BLOCK_GELU = 1 } pararnn_block_act;

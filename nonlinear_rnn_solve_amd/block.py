@@ -112,7 +112,7 @@ def gated_linear(x, w_gate, w_up, activation="silu", want_pre=False, out=None):
 
     x: [..., D], rows of any one stride; w_gate, w_up: [F, D] in x's type (two halves of one tensor, for instance);
     activation: "silu" or "gelu" (its tanh form).  Products are summed in float32 (an infinity among float32 values makes the
-    results it enters NaN).
+    results it enters infinite or NaN, by the sizes).
     Returns (h, pre): h [..., F] in x's type; pre, float32 [rows, 2 F], what gated_linear_vjp needs, or None without
     want_pre.  out: a tensor for h.
     """

@@ -102,7 +102,7 @@ template <typename T> DEV void put_plain(const GemmArgs& p, int64_t m, int64_t n
 // are 2^-24 of a term each at most, 2^-24 together in what was measured, and without a bias.  (Cut off and not rounded the parts have the
 // value's sign and twice the size: what was left out reached 2^-21 and shrank every term, by 0.7 2^-24 on average.)  That is float32's
 // accuracy at 2.7 times its rate: 6 instructions of 32 cycles in place of 8 of 64.  (An infinity less itself is a NaN: a
-// float32 infinity makes its row's or column's results NaN.)
+// float32 infinity makes its row's or column's results NaN here, infinite where few rows are multiplied in float32.)
 template <typename T> struct Parts {
   static constexpr int PL = sizeof(T) == 4 ? 3 : 1;             // numbers that make one
   static constexpr int CPR = sizeof(T) == 4 ? 4 : 8;            // 16-byte pieces of a row in shared memory

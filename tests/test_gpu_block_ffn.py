@@ -335,3 +335,20 @@ def test_gradients_of_gates_far_out(activation, far):
     got = block.gated_linear_vjp(x, one, small, pre, torch.ones(2, 1, device="cuda"), activation, want_params=False)["d_x"]
     want = torch.tensor([[f64(x)[0, 0] * 2.0 ** -19], [0.0]], dtype=torch.float64)
     close(got, want, 1e-5 * (want + 17 * 2.0 ** -19), "d_x")
+
+
+@pytest.mark.parametrize("R", [32, 64, 65, 150])
+def test_nan_and_infinity_stay_in_their_rows_in_float32(R):
+    # infinite or NaN, by the kernel that the rows take; never finite, never beyond the row
+    x, wg, wu, dh = make(R, 96, 140, F32, seed=22)
+    clean, pre = block.gated_linear(x, wg, wu, want_pre=True)
+    d_clean = block.gated_linear_vjp(x, wg, wu, pre, dh)["d_x"]
+    x = x.clone()
+    x[R - 1, 5], x[7, 95] = float("nan"), float("inf")
+    h, pre = block.gated_linear(x, wg, wu, want_pre=True)
+    rows = [r for r in range(R) if r not in (7, R - 1)]
+    assert torch.equal(h[rows], clean[rows]) and torch.isnan(h[R - 1]).all()
+    assert not torch.isfinite(pre[7]).any()
+    got = block.gated_linear_vjp(x, wg, wu, pre, dh)
+    assert torch.equal(got["d_x"][rows], d_clean[rows])
+    assert not torch.isfinite(got["d_w_up"][:, 95]).any() and torch.isnan(got["d_w_up"][:, 5]).all()
