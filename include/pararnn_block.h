@@ -70,7 +70,7 @@ pararnn_status pararnn_block_causal_conv_vjp(const pararnn_block_conv* prob, con
  *     dt = softplus(delta_t[d] + dt_bias[d]),    h_t[d,n] = exp(dt A[d,n]) h_{t-1}[d,n] + dt x_t[d] B_t[g,n]
  *     y_t[d] = (sum_n C_t[g,n] h_t[d,n] + skip[d] x_t[d]) z_t[d] sig(z_t[d])
  * The D channels form G groups of D / G consecutive ones, which share B and C.  N <= PARARNN_BLOCK_MAX_STATES (else
- * UNSUPPORTED); so are a T of 2^31 - 16 or more, strides over t of PARARNN_BLOCK_SSM_MAX_STEP or more, and a launch of 2^32
+ * UNSUPPORTED); so are a T of 2^31 - 16 or more, strides over t of PARARNN_BLOCK_SSM_MAX_STEP or more (T > 1), and a launch of 2^32
  * threads.  A's sign is not checked: positive rates grow.  A rate of -infinity is a state that forgets at every step; its gradients with
  * respect to delta and dt_bias are NaN (0 times infinity), all others are finite.
  * ---------------------------------------------------------------------------------------------- */

@@ -1033,10 +1033,12 @@ static bool problem_ok(const pararnn_block_ssm* q) {
     if (!plane_ok(q->B, (*s)[0]) || !plane_ok(q->T, (*s)[1]) || !plane_ok(q->G, (*s)[2])) return false;
   return true;
 }
+// A step's stride as the kernels take it: that of a single step means nothing, and is any number.
+static int64_t step_of(const pararnn_block_ssm* q, int64_t stride) { return q->T > 1 ? stride : 0; }
 // a step's stride that does not fit the offsets inside a tile
-static bool far(int64_t stride) { return stride >= PARARNN_BLOCK_SSM_MAX_STEP; }
+static bool far(const pararnn_block_ssm* q, int64_t stride) { return step_of(q, stride) >= PARARNN_BLOCK_SSM_MAX_STEP; }
 static bool supported(const pararnn_block_ssm* q, const Split& s, int threads) {
-  if (far(q->sx[1]) || far(q->sdelta[1]) || (q->z && far(q->sz[1])) || far(q->sb[1]) || far(q->sc[1])) return false;
+  if (far(q, q->sx[1]) || far(q, q->sdelta[1]) || (q->z && far(q, q->sz[1])) || far(q, q->sb[1]) || far(q, q->sc[1])) return false;
   if (q->N > PARARNN_BLOCK_MAX_STATES || q->T > INT32_MAX - CT || q->D > INT32_MAX / 64) return false;
   if (s.ctiles * q->G > INT32_MAX || q->B > INT32_MAX) return false;
   return s.rows == 0 || (s.S <= INT64_C(0xffffffff) / s.rows && grid_ok(s.rows * s.S, threads));
@@ -1046,6 +1048,7 @@ static SsmArgs ssm_args(const pararnn_block_ssm* q, const Split& s) {
   p.x = q->x, p.delta = q->delta, p.z = q->z, p.b = q->b, p.c = q->c;
   for (int k = 0; k < 2; ++k) p.sx[k] = q->sx[k], p.sdelta[k] = q->sdelta[k], p.sz[k] = q->sz[k];
   for (int k = 0; k < 3; ++k) p.sb[k] = q->sb[k], p.sc[k] = q->sc[k];
+  for (int64_t* t : {&p.sx[1], &p.sdelta[1], &p.sz[1], &p.sb[1], &p.sc[1]}) *t = step_of(q, *t);
   p.A = q->A, p.skip = q->skip, p.dt_bias = q->dt_bias, p.h0 = q->h0;
   p.seqs = {q->cu_seqlens, q->cu_seqlens ? q->n_seqs : 1, q->T};
   p.B = q->B, p.D = q->D;
@@ -1107,7 +1110,7 @@ extern "C" pararnn_status pararnn_block_selective_scan(const pararnn_block_ssm* 
   if (!ptr_ok(y, dtype_size(q->dtype), any && q->T > 0) || !ptr_ok(h_last, 4, false) || !ptr_ok(carry, 4, false))
     return PARARNN_ERR_INVALID_ARG;
   const Split s = forward_split(q->B, q->T, q->D, q->G);
-  if (far(sy[1]) || !supported(q, s, waves_of(q->N) * WAVE)) return PARARNN_ERR_UNSUPPORTED;
+  if (far(q, sy[1]) || !supported(q, s, waves_of(q->N) * WAVE)) return PARARNN_ERR_UNSUPPORTED;
   const Room r = room(q->B, q->T, q->D, q->N, q->G, false);
   if (!ws_ok(ws, ws_bytes, static_cast<size_t>(r.total()) * sizeof(float))) return PARARNN_ERR_WORKSPACE;
   if (!any) return PARARNN_OK;
@@ -1121,7 +1124,7 @@ extern "C" pararnn_status pararnn_block_selective_scan(const pararnn_block_ssm* 
     return launched();
   }
   p.y = y;
-  p.sy[0] = sy[0], p.sy[1] = sy[1];
+  p.sy[0] = sy[0], p.sy[1] = step_of(q, sy[1]);
   p.h_last = h_last, p.carry = carry;
   p.in_place = h_last && h_last == q->h0;
   float* f = static_cast<float*>(ws);
@@ -1149,7 +1152,8 @@ extern "C" pararnn_status pararnn_block_selective_scan_vjp(const pararnn_block_s
 
   const Split s = gradient_split(q->B, q->T, q->D, q->G);
   const int64_t values = q->B * q->T * q->G * 2 * q->N, cols = q->D * (q->N + 2);
-  if (far(grad->sdy[1]) || far(grad->sdx[1]) || far(grad->sddelta[1]) || (q->z && far(grad->sdz[1]))) return PARARNN_ERR_UNSUPPORTED;
+  if (far(q, grad->sdy[1]) || far(q, grad->sdx[1]) || far(q, grad->sddelta[1]) || (q->z && far(q, grad->sdz[1])))
+    return PARARNN_ERR_UNSUPPORTED;
   if (!supported(q, s, waves_of(q->N) * WAVE) || !grid_ok(ceil_div(values, 256), 256) || !grid_ok(ceil_div(cols, 64), 256))
     return PARARNN_ERR_UNSUPPORTED;
   const Room r = room(q->B, q->T, q->D, q->N, q->G, true);
@@ -1170,6 +1174,7 @@ extern "C" pararnn_status pararnn_block_selective_scan_vjp(const pararnn_block_s
   g.dx = grad->d_x, g.ddelta = grad->d_delta, g.dz = grad->d_z;
   for (int k = 0; k < 2; ++k)
     g.sdy[k] = grad->sdy[k], g.sdx[k] = grad->sdx[k], g.sddelta[k] = grad->sddelta[k], g.sdz[k] = grad->sdz[k];
+  for (int64_t* t : {&g.sdy[1], &g.sdx[1], &g.sddelta[1], &g.sdz[1]}) *t = step_of(q, *t);
   if (steps) {
     const pararnn_status st1 = q->dtype == PARARNN_BF16 ? by_states<Backward, bf16>(q->N, g, s, st)
                                                         : by_states<Backward, float>(q->N, g, s, st);

@@ -219,3 +219,12 @@ def test_plain_forms_against_torch_and_differences():
     s = torch.log(torch.tensor(2.0, dtype=torch.float64))
     assert torch.allclose(y[0, :, 0], torch.stack([s * (torch.exp(-2 * s) ** torch.arange(k + 1)).sum() for k in range(5)]))
     assert plain.values(15)[127] == 1.875 and plain.values(31)[255] == 1.875 and plain.values(15)[129] == -2.0 ** -17 and plain.values(31)[1] == 2.0 ** -33
+
+
+def test_ssm_steps_too_far_apart(lib):
+    # 2^24 elements between two steps; between one and none nothing is (without a GPU the launch itself then fails)
+    sy = struct.pack("@2q", 1 << 26, 1 << 24)
+    run = lambda p: lib.pararnn_block_selective_scan(p, P, sy, None, None, WS, BIG, None)  # noqa: E731
+    assert run(ssm(B=1, T=2)) == -2 and run(ssm(B=1, T=300, st=1 << 24)) == -2
+    if not torch.cuda.is_available():
+        assert run(ssm(B=1, T=1)) == run(ssm(B=1, T=1, st=1 << 24, st3=1 << 25)) == -4

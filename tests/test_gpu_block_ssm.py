@@ -392,3 +392,21 @@ def test_growth_past_float32_of_a_small_state():
     y, last, _ = k.forward()
     # log 2 and A are off by 3 u together, so the exponent 104 = 150 log 2 by 312 u; each of its steps adds 4 u
     close(last, torch.full((1, 64, 4), 2.0 ** 50, dtype=torch.float64), 2.0 ** 50 * U32 * (312 + 4 * T), "h_last")
+
+
+def test_a_single_steps_stride_means_nothing():
+    # [B, 1, D] planes whose (unused) step is 2^24 elements and more, forward and backward, outputs too
+    k = Case(3, 1, 8, 4, F32, 77)
+    y, last, carry = k.forward(want_carry=True)
+    want = k.backward(carry)
+
+    def far(t):
+        s = torch.empty(t.numel(), device="cuda")
+        v = torch.as_strided(s, t.shape, (t.shape[2], 1 << 24, 1))
+        return v.copy_(t)
+
+    k.x, k.dt, k.z, k.b, k.c, k.dy = (far(t) for t in (k.x, k.dt, k.z, k.b, k.c, k.dy))
+    got_y, got_last, got_carry = k.forward(want_carry=True, out=far(torch.zeros_like(y)))
+    assert torch.equal(got_y, y) and torch.equal(got_last, last) and torch.equal(got_carry, carry)
+    got = k.backward(carry, out=[far(torch.zeros_like(want[n])) for n in ("d_x", "d_dt", "d_z", "d_b", "d_c")])
+    assert all(torch.equal(got[n], want[n]) for n in want)
