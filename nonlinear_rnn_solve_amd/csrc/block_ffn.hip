@@ -264,7 +264,7 @@ template <typename T> __global__ __launch_bounds__(256) void k_join(const GemmAr
 // eight rows of tiles.
 constexpr int kStages = 2, kStageBytes = 512 * 128, kLoads = 8;   // loads of a thread for a stage
 DEV void load_to_lds(const void* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
 }
 // all loads have landed, all reads of the past stage are done, in every wave
 DEV void stage_ready() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
