@@ -712,7 +712,7 @@ template <typename T, bool GATED, int ACT> static bool gemm(GemmArgs p, float* s
   if constexpr (sizeof(T) == 2) if (large(p.M, p.N, GATED) && p.K > 0 && p.K * static_cast<int64_t>(e) % kKBytes == 0 &&
       aligned16(p.a, p.sa, e) && aligned16(p.b0, p.sb0, e) && (!GATED || aligned16(p.b1, p.sb1, e))) {
     const int64_t mt = ceil_div(p.M, 256), nt = ceil_div(p.N, GATED ? 128 : 256);
-    if (!grid_ok(mt * nt, 256)) return false;
+    if (!grid_ok(mt * nt, 512)) return false;
     k_gemm_large<GATED, ACT><<<dim3(static_cast<uint32_t>(mt * nt)), dim3(512), 0, st>>>(
         p, static_cast<uint32_t>(mt), static_cast<uint32_t>(nt));
     return true;

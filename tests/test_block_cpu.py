@@ -228,3 +228,11 @@ def test_ssm_steps_too_far_apart(lib):
     assert run(ssm(B=1, T=2)) == -2 and run(ssm(B=1, T=300, st=1 << 24)) == -2
     if not torch.cuda.is_available():
         assert run(ssm(B=1, T=1)) == run(ssm(B=1, T=1, st=1 << 24, st3=1 << 25)) == -4
+
+
+def test_gated_linear_launch_limit(lib):
+    # 4096 by 3000 large tiles are 2^32.55 threads in workgroups of 512; 4096 by 2000 are 2^31.97 (without a GPU their launch then fails)
+    run = lambda F: lib.pararnn_block_gated_linear(1, 0, 1 << 20, 64, F, P, 64, P, 64, P, 64, P, F, None, None, 0, None)  # noqa: E731
+    assert run(128 * 3000) == -2
+    if not torch.cuda.is_available():
+        assert run(128 * 2000) == -4
