@@ -8,7 +8,7 @@ ValueError, statuses of the C ABI PararnnError; big planes are float32 or bfloat
 as they like in the others; float32 arguments (states, parameters) are contiguous and of the stated shape, dimensions of one
 entry aside, or flat; results are detached from autograd (examples/selective_lm.py wraps the operators in autograd functions) and a
 tensor given to be written counts as modified in place; it shares no memory with an input or another output unless its operator
-says so.  Nothing here synchronises, so calls can be captured in a HIP graph.
+says so (ValueError where both are dense and overlap or begin at the same place; interleaved views are not told apart).  Nothing here synchronises, so calls can be captured in a HIP graph.
 """
 from __future__ import annotations
 

@@ -37,13 +37,26 @@ void copy_strides(int64_t* to, const Tensor& t, int n) {
 }
 float* floats_of(const Tensor& t) { return static_cast<float*>(t.data_ptr()); }
 Maybe given_at(const std::optional<std::vector<Maybe>>& out, size_t k) { return out ? (*out)[k] : Maybe(); }
-// a caller's output takes no input's place (slices of one tensor interleave, so only the same beginning is told from them)
-void apart(const Maybe& out, const char* name, std::initializer_list<std::pair<const Tensor*, const char*>> others) {
-  if (!out || !out->numel()) return;
-  for (const auto& [t, what] : others)
-    if (t && t->numel() && t->data_ptr() == out->data_ptr()) refuse(std::string(name) + " must not share memory with " + what);
-}
 const Tensor* maybe(const Maybe& t) { return t ? &*t : nullptr; }
+// Whether two tensors are seen to share memory: they begin at the same place, or both fill theirs without gaps and the two overlap (slices
+// of one tensor interleave, so of tensors with gaps only the same beginning tells).
+bool meet(const Tensor& a, const Tensor& b) {
+  if (!a.numel() || !b.numel()) return false;
+  const char *pa = static_cast<const char*>(a.data_ptr()), *pb = static_cast<const char*>(b.data_ptr());
+  if (pa == pb) return true;
+  return pa < pb + b.nbytes() && pb < pa + a.nbytes() && a.is_non_overlapping_and_dense() && b.is_non_overlapping_and_dense();
+}
+using Named = std::pair<const Tensor*, const char*>;
+// a caller's output takes no input's place, nor another output's
+void apart(const Maybe& out, const char* name, std::initializer_list<Named> others) {
+  if (!out) return;
+  for (const auto& [t, what] : others)
+    if (t && meet(*out, *t)) refuse(std::string(name) + " must not share memory with " + what);
+}
+// a state that leaves may be the one that entered, but no part of it
+void apart_or_same(const Maybe& last, const char* name, const Maybe& state, const char* what) {
+  if (last && state && last->data_ptr() != state->data_ptr()) apart(last, name, {{&*state, what}});
+}
 
 // ---------------------------------------------------------------- causal convolution
 struct Conv {
@@ -76,7 +89,9 @@ std::tuple<Tensor, Tensor> causal_conv(const Tensor& x, const Tensor& weight, co
   const Conv c(x, weight, bias, state, cu, silu);
   const Call call(x.device());
   const Tensor y = output(out, "out", x);
-  apart(out, "out", {{&x, "x"}});
+  apart(out, "out", {{&x, "x"}, {&weight, "weight"}, {maybe(bias), "bias"}, {maybe(state), "state"}, {maybe(cu), "cu_seqlens"}});
+  apart(last, "last", {{maybe(out), "out"}, {&x, "x"}, {&weight, "weight"}, {maybe(bias), "bias"}, {maybe(cu), "cu_seqlens"}});
+  apart_or_same(last, "last", state, "a part of state");
   const Tensor left = last ? *last : new_floats(c.shape, x);
   float* pl = floats(left, "last", c.shape, x.device());
   const int64_t sy[2] = {y.stride(0), y.stride(1)};
@@ -92,7 +107,8 @@ py::dict causal_conv_vjp(const Tensor& x, const Tensor& weight, const Tensor& dy
   const Call call(x.device());
   plane(dy, "dy", x);
   const Tensor dx = output(out, "out", x);
-  apart(out, "out", {{&x, "x"}, {&dy, "dy"}});
+  apart(out, "out", {{&x, "x"}, {&dy, "dy"}, {&weight, "weight"}, {maybe(bias), "bias"}, {maybe(state), "state"}, {maybe(d_last), "d_last"},
+                     {maybe(cu), "cu_seqlens"}});
   pararnn_block_conv_grad g{};
   g.dy = dy.data_ptr();
   g.d_last = floats(d_last, "d_last", c.shape, x.device());
@@ -175,7 +191,11 @@ std::tuple<Tensor, Tensor, Maybe> selective_scan(const Tensor& x, const Tensor& 
   const Ssm s(x, dt, A, b, c, skip, z, dt_bias, h0, cu);
   const Call call(x.device());
   const Tensor y = output(out, "out", x);
-  apart(out, "out", {{&x, "x"}, {&dt, "dt"}, {maybe(z), "z"}, {&b, "b"}, {&c, "c"}});
+  for (const auto& [t, name] : {std::pair<const Maybe&, const char*>{out, "out"}, {h_last, "h_last"}})
+    apart(t, name, {{&x, "x"}, {&dt, "dt"}, {maybe(z), "z"}, {&b, "b"}, {&c, "c"}, {&A, "A"}, {maybe(skip), "skip"},
+                    {maybe(dt_bias), "dt_bias"}, {maybe(cu), "cu_seqlens"}});
+  apart(out, "out", {{maybe(h0), "h0"}, {maybe(h_last), "h_last"}});
+  apart_or_same(h_last, "h_last", h0, "a part of h0");
   const Tensor last = h_last ? *h_last : new_floats(s.shape, x);
   float* pl = floats(last, "h_last", s.shape, x.device());
   Maybe carry;
@@ -212,7 +232,9 @@ py::dict selective_scan_vjp(const Tensor& x, const Tensor& dt, const Tensor& A, 
   const Tensor dx = output(given_at(out, 0), "out", x), dd = output(given_at(out, 1), "out", x);
   const Tensor db = shared_output(given_at(out, 3), "out", x, b), dc = shared_output(given_at(out, 4), "out", x, b);
   for (size_t k = 0; out && k < 5; ++k) {
-    apart((*out)[k], "out", {{&x, "x"}, {&dt, "dt"}, {maybe(z), "z"}, {&b, "b"}, {&c, "c"}, {&dy, "dy"}});
+    apart((*out)[k], "out", {{&x, "x"}, {&dt, "dt"}, {maybe(z), "z"}, {&b, "b"}, {&c, "c"}, {&dy, "dy"}, {&A, "A"}, {maybe(skip), "skip"},
+                             {maybe(dt_bias), "dt_bias"}, {maybe(h0), "h0"}, {maybe(d_last), "d_last"}, {maybe(carry), "carry"},
+                             {maybe(cu), "cu_seqlens"}});
     for (size_t j = 0; j < k; ++j) apart((*out)[k], "out", {{maybe((*out)[j]), "another of out"}});
   }
   pararnn_block_ssm_grad g{};
@@ -326,7 +348,7 @@ py::dict gated_linear_vjp(const Tensor& x, const Tensor& w_gate, const Tensor& w
     res["d_w_up"] = du = output(given_at(w_out, 1), "w_out", w_up);
   }
   for (const Maybe& t : {out, given_at(w_out, 0), given_at(w_out, 1)})
-    apart(t, "an output", {{&x, "x"}, {&w_gate, "w_gate"}, {&w_up, "w_up"}, {&dh, "dh"}});
+    apart(t, "an output", {{&x, "x"}, {&w_gate, "w_gate"}, {&w_up, "w_up"}, {&dh, "dh"}, {maybe(pre), "pre"}});
   apart(given_at(w_out, 1), "w_out", {{maybe(given_at(w_out, 0)), "another of w_out"}, {maybe(out), "out"}});
   apart(given_at(w_out, 0), "w_out", {{maybe(out), "out"}});
   const Tensor ws = call.workspace(pararnn_block_gated_linear_workspace_bytes(l.dtype, l.R, l.D, l.F, 1));

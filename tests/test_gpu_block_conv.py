@@ -248,3 +248,27 @@ def test_outputs_in_an_inputs_place_are_refused():
     for t in (x, dy):
         with pytest.raises(ValueError, match="share memory"):
             block.causal_conv_vjp(x, w, dy, out=t)
+
+
+def test_outputs_that_overlap_something_are_refused():
+    # parts of dense tensors, and a state that leaves into a part of the one that entered; the state itself is allowed
+    x, w, b = torch.randn(2, 9, 8, device="cuda"), torch.randn(8, 4, device="cuda"), torch.randn(8, device="cuda")
+    flat = torch.randn(400, device="cuda")
+    state, shifted = flat[:48].view(2, 3, 8), flat[24:72].view(2, 3, 8)
+    beside = flat[48:96].view(2, 3, 8)
+    inside = flat[100:244].view(2, 9, 8)
+    for kw in (dict(state=state, last=shifted), dict(last=x.view(-1)[:48].view(2, 3, 8)), dict(last=x.view(-1)[5:53].view(2, 3, 8)),
+               dict(out=inside, last=flat[200:248].view(2, 3, 8)), dict(out=flat[40:184].view(2, 9, 8), state=state)):
+        with pytest.raises(ValueError, match="share memory"):
+            block.causal_conv(x, w, b, **kw)
+    with pytest.raises(ValueError, match="share memory"):
+        block.causal_conv_vjp(flat[100:244].view(2, 9, 8), w, x, b, out=flat[150:294].view(2, 9, 8))
+    want = block.causal_conv(x, w, b, state=state.clone())[1]
+    block.causal_conv(x, w, b, state=state, last=beside)
+    assert torch.equal(beside, want)
+    block.causal_conv(x, w, b, state=state, last=state)
+    assert torch.equal(state, want)
+    # slices of one tensor interleave
+    both = torch.randn(2, 9, 16, device="cuda")
+    y, _ = block.causal_conv(both[..., :8], w, b, out=both[..., 8:])
+    assert torch.equal(y, block.causal_conv(both[..., :8].clone(), w, b)[0])

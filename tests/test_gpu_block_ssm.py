@@ -410,3 +410,25 @@ def test_a_single_steps_stride_means_nothing():
     assert torch.equal(got_y, y) and torch.equal(got_last, last) and torch.equal(got_carry, carry)
     got = k.backward(carry, out=[far(torch.zeros_like(want[n])) for n in ("d_x", "d_dt", "d_z", "d_b", "d_c")])
     assert all(torch.equal(got[n], want[n]) for n in want)
+
+
+def test_outputs_that_overlap_something_are_refused():
+    k = Case(2, 20, 8, 4, F32, 78)
+    flat = torch.randn(1000, device="cuda")
+    k.h0 = flat[:64].view(2, 8, 4)
+    for kw in (dict(h_last=flat[32:96].view(2, 8, 4)), dict(h_last=flat[200:264].view(2, 8, 4), out=flat[240:560].view(2, 20, 8)),
+               dict(out=flat[60:380].view(2, 20, 8))):
+        with pytest.raises(ValueError, match="share memory"):
+            k.forward(**kw)
+    k.skip = flat[600:608]
+    with pytest.raises(ValueError, match="share memory"):
+        k.forward(h_last=flat[590:654].view(2, 8, 4))
+    carry = k.forward(want_carry=True)[2]
+    for out in ([None, flat[:320].view(2, 20, 8), None, None, None], [flat[500:820].view(2, 20, 8), None, None, None, None]):
+        with pytest.raises(ValueError, match="share memory"):
+            k.backward(carry, out=out)
+    want = k.forward()[1]
+    _, last, _ = k.forward(h_last=flat[64:128].view(2, 8, 4))
+    assert torch.equal(last, want)
+    _, last, _ = k.forward(h_last=k.h0)
+    assert torch.equal(k.h0, want)
