@@ -55,8 +55,7 @@ struct SsmGradArgs {
   int64_t sdy[2], sdx[2], sddelta[2], sdz[2];
   float *d_h0;
   float *part_bc;               // [G ctiles][B][T][2][N]: a channel tile's sums for d_b and d_c
-  float *part_A;                // [S B][N][D]
-  float *part_d;                // [S B][2][D]: for d_skip, d_dt_bias
+  float *part_A;                // [S B][N + 2][D]: for d_A, then d_skip and d_dt_bias
 };
 
 // the workgroup's channels, row and segment
