@@ -13,6 +13,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from nonlinear_rnn_solve_amd import lm  # noqa: E402
@@ -29,6 +30,7 @@ class GatedScan(torch.autograd.Function):
         return h, h_last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh, d_last):
         proj, lam, h0, cu, carry = ctx.saved_tensors
         d_proj = torch.empty_like(proj)
@@ -47,6 +49,7 @@ class LayerNorm(torch.autograd.Function):
         return y, s
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, ds):
         s, weight, stats = ctx.saved_tensors
         g = lm.layer_norm_vjp(dy.contiguous(), s, weight, stats, d_sum=ds.contiguous())
@@ -63,6 +66,7 @@ class TokenLogprobs(torch.autograd.Function):
         return t.logp, t.entropy
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g, ge):
         logits, targets, lse, entropy = ctx.saved_tensors
         return lm.token_logprobs_vjp(logits, targets, lse, entropy, g.contiguous(), ge.contiguous(), out=logits.detach()), None

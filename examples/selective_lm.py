@@ -14,6 +14,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
@@ -28,6 +29,7 @@ class CausalConv(torch.autograd.Function):
         return block.causal_conv(x, weight, bias, state=state, cu_seqlens=cu)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, d_last):
         x, weight, bias, state, cu = ctx.saved_tensors
         g = block.causal_conv_vjp(x, weight, dy.contiguous(), bias, state=state, d_last=d_last.contiguous(), cu_seqlens=cu,
@@ -49,6 +51,7 @@ class SelectiveScan(torch.autograd.Function):
         return y, h_last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, d_last):
         x, dt, A, low, skip, z, dt_bias, h0, cu, carry = ctx.saved_tensors
         n, rank = A.shape[1], ctx.rank
@@ -67,6 +70,7 @@ class GatedLinear(torch.autograd.Function):
         return h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh):
         x, w_gate, w_up, pre = ctx.saved_tensors
         g = block.gated_linear_vjp(x, w_gate, w_up, pre, dh.contiguous())

@@ -90,3 +90,23 @@ def test_packed_documents_do_not_meet():
             assert float((logits[:, a:b] - alone).abs().max()) <= 1e-4
             for (c, h), (c1, h1) in zip(states, last):
                 assert float((c[:, j] - c1).abs().max()) <= 1e-4 and float((h[:, j] - h1).abs().max()) <= 1e-4
+
+
+def test_second_derivatives_are_refused():
+    # the gradients' operators have none: a gradient of a gradient must not come out without their part
+    g = torch.Generator().manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=g).cuda().requires_grad_()  # noqa: E731
+    x, low, w = r(2, 5, 8), r(2, 5, 3 + 2 * 4), r(8, 4)
+    calls = {
+        "conv": (selective_lm.CausalConv.apply(x, w, r(8), None, None), x),
+        "scan": (selective_lm.SelectiveScan.apply(x, r(2, 5, 8), -w.exp(), low, 3, r(8), r(2, 5, 8), r(8), None, None), x),
+        "product": (selective_lm.GatedLinear.apply(x, r(16, 8), r(16, 8)), x),
+        "norm": (selective_lm.LayerNorm.apply(x, r(2, 5, 8), r(8), r(8)), x),
+        "logprobs": (selective_lm.TokenLogprobs.apply(low, torch.zeros(2, 5, dtype=torch.int64, device="cuda")), low),
+    }
+    for name, (out, leaf) in calls.items():
+        loss = sum(t.square().sum() for t in (out if isinstance(out, tuple) else (out,)))
+        (first,) = torch.autograd.grad(loss, leaf, create_graph=True)
+        assert torch.isfinite(first).all(), name
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            first.sum().backward()
