@@ -158,7 +158,7 @@ pararnn_status pararnn_block_gated_linear_vjp(int dtype, int act, int64_t R, int
  * s f/8 2^(1-bias).  A new moment is rounded up or down at random, with probabilities that keep its mean to 2^-16 of a step (to
  * nearest, slow averages would stand still): up where its place between two codes and a multiple of 2^-16 below one, 16 bits of a hash of
  * the seed, the step and the element's place in the state, add up to one or more (m) or to more than one (v).  A block
- * with a NaN or an infinity has s = NaN, and its values are NaN from then on.
+ * with a NaN, an infinity or a magnitude above 1.875 2^127 has s = NaN, and its values are NaN from then on.
  * The step and, if wanted, lr and grad_scale may be read from device memory, so that a captured graph follows them.
  * The same tensor must not be given twice, nor overlapping ones.
  * ---------------------------------------------------------------------------------------------- */

@@ -71,7 +71,7 @@ DEV int scale_exponent(float most) {
   const int e = static_cast<int>(u >> 23) - 127 + ((u & 0x7fffffu) > 0x700000u);
   return e > -80 ? e : -80;
 }
-DEV float power_of_two(int e) { return e > 127 ? __builtin_huge_valf() : __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+DEV float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 template <typename W> using Loose = W __attribute__((aligned(1)));
 DEV uint32_t load_codes(const void* p, int64_t at) {
@@ -171,6 +171,7 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamwArgs a) {
       }
       bad = __builtin_amdgcn_ballot_w64(bad) != 0;
       const int em = scale_exponent(wave_max(mm)), ev = scale_exponent(wave_max(mv));
+      bad = bad || em > 127 || ev > 127;   // no float holds 2^128
       uint32_t cm = 0, cv = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {

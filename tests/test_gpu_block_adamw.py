@@ -344,3 +344,19 @@ def test_rounding_of_ties():
         assert int((number == 1 << 19).sum()) > 0
         up = number >= 1 << 19 if name == "m" else number > 1 << 19
         assert torch.equal(f64(block.adamw_moments(m, v, ms, vs)[name == "v"]), torch.where(up, 9 / 8, 1.0).double()), name
+
+
+def test_moments_that_no_scale_holds():
+    # v = 3.3e38 asks for a scale of 2^128: NaN, as for an infinity, and not an infinity beside NaNs; 3.1e38 has 2^127
+    for big, held in ((3.3e38 ** 0.5, False), (3.1e38 ** 0.5, True)):
+        p, g = torch.zeros(512, device="cuda"), torch.zeros(512, device="cuda")
+        g[3] = big
+        m, v = (torch.zeros(512, dtype=torch.uint8, device="cuda") for _ in range(2))
+        ms, vs = (torch.zeros(2, device="cuda") for _ in range(2))
+        block.adamw_step([p], [g], m, v, 1, betas=(0.9, 0.0), m_scale=ms, v_scale=vs)
+        av = block.adamw_moments(m, v, ms, vs)[1]
+        assert not av[256:].any()
+        if held:
+            assert float(vs[0]) == 2.0 ** 127 and abs(float(av[3]) - 3.1e38) <= 2.0 ** 124 and not av[4:].any()
+        else:
+            assert torch.isnan(vs[0]) and torch.isnan(av[:256]).all()
