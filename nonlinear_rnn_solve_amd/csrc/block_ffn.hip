@@ -258,7 +258,8 @@ template <typename T> __global__ __launch_bounds__(256) void k_join(const GemmAr
 // sixteen rows fill 256 bytes twice over where they are exchanged by a row's number, once by half of it) is made by which piece each
 // lane asks for.  Reads and loads are issued between the products, each of which keeps the matrix unit busy for eight instructions'
 // time.  Eight waves against four of 128 by 128 (one a SIMD, so that a wait is a stall), forward with pre: R = D = F = 2048 54 and 61 us,
-// R = 4096, D = 1024, F = 4096 80 and 90, R = 8192, D = 4096, F = 8192 (1.1 TFLOP) 1018 and 1007, gradient 2126 and 2186.
+// R = 4096, D = 1024, F = 4096 80 and 90, R = 8192, D = 4096, F = 8192 (1.1 TFLOP) 1018 and 1007, gradient 2126 and 2186 (with
+// one bfloat16 for each of dg and du; with two it is 3820: 1675 us for each of its products, 1.31 PFLOP/s, 77% of the matrix units' time).
 // Rows past the end are read as the last and left out of the result.  k is a multiple of the stage, everything 16-byte
 // aligned.  Neighbouring tiles share rows and columns: each of the eight L2 caches gets a run of tiles of its own, in bands of
 // eight rows of tiles.
@@ -682,9 +683,9 @@ constexpr int64_t kCus = 256, kMostParts = 8;
 static bool large(int64_t M, int64_t N, bool gated) { return ceil_div(M, 256) * ceil_div(N, gated ? 128 : 256) >= kCus / 2; }
 static bool aligned16(const void* p, int64_t stride, size_t e) { return aligned(p, 16) && stride * static_cast<int64_t>(e) % 16 == 0; }
 // Columns of a workgroup of k_gemm: 128 where those workgroups are twice the chip's units, or once for two products in bfloat16.
-// 128 and 64, float32: 387 (gradient, R = 1001, D = 1025, F = 2731) 124 and 116 us, 512 (R = 700, D = 1024, F = 4096) 86 and 97;
-// forward 344 (the first) 98 and 96, 512 (R = 1024) 106 and 118; bfloat16 forward 344 (the first) 34 and 40, 384 30 and 33.
-// (bfloat16 gradients of so many are in the large tiles: 256, R = 1500, D = 1000, F = 2000, took 57 us with 128 columns, 44 with 64.)
+// Whole calls with 128 and 64, float32: gradient of 387 (R = 1001, D = 1025, F = 2731) 235 and 216 us, 512 (R = 700, D = 1024, F = 4096)
+// 196 and 208; forward with pre 344 (the first) 85 and 89, 512 (R = 1024) 103 and 116; bfloat16 344 (the first) 32 and 37, 384 27 and 30.
+// (bfloat16 gradients of so many are in the large tiles: 256, R = 1500, D = 1000, F = 2000, took 138 us with 128 columns, 125 with 64.)
 static int columns_of(size_t e, int64_t M, int64_t N, bool gated) {
   if (e == 2 && !gated) return 64;
   return ceil_div(M, 128) * ceil_div(N, gated ? 64 : 128) >= (e == 2 ? kCus : 2 * kCus) ? 128 : 64;
@@ -775,7 +776,8 @@ static bool sizes_ok(int64_t R, int64_t D, int64_t F) {
          (R > kMost || D > kMost || F > kMost || (sizes_fit(R, D, 4) && sizes_fit(R, F, 4) && sizes_fit(F, D, 4)));
 }
 // Row stride of n elements in the workspace: not a large power of two, which would put the rows of a tile behind each other in few
-// of the memory's channels (the two gradient products of R = 8192, D = 4096, F = 8192: 970 -> 882 us each).
+// of the memory's channels (the two gradient products of R = 8192, D = 4096, F = 8192, with one bfloat16 for
+// each of dg and du: 970 -> 882 us each).
 static int64_t spread(int64_t n, size_t e) { return n * static_cast<int64_t>(e) % 4096 ? n : n + kPad; }
 // elements of the gradient's workspace: d_pre [R][planes][F2], d_pre^T [2 F][planes][Rp], x^T [D][Rp], weights^T [D][F2], with row
 // strides Fs, Rs, Xs and Ws, and float32 sums of parts of k

@@ -18,9 +18,10 @@ namespace lm {
 // the sums.  B and C are then held one value a lane, replicated over the wave's four rows of 16 lanes, and reach the
 // products by the row broadcast of their operand (no instruction, no access of its own).
 //
-// Bound by vector instructions (32 of a wave's cycles a step and state, half of them the exponential): B = 2, T = 4096, D = 4096,
-// N = 16, bf16 with z: 114 us for the segments' ends and 168 for the walk (268 MB; the planes alone 53 at a large copy's rate); the
-// gradient 110 and 540 to 590 (470 MB, 92).
+// Bound by vector instructions: one exponential and four multiplications alone take 8.3 ns of a SIMD a wave's step and state (3.7 of
+// them the exponential), the walk 20.  The rest is a step's reads and writes of shared memory, softplus, SiLU, conversions, and scalar
+// registers kept in vector lanes (62 of them at N = 16, 73 in the gradient).  B = 2, T = 4096, D = 4096, N = 16, bf16 with z: 114 us for
+// the segments' ends and 168 for the walk (268 MB; the planes alone 53 at a large copy's rate); the gradient 108 and 550 (470 MB, 92).
 //
 // Few rows and channels leave the chip empty, so long rows are cut into segments of whole tiles.  One launch finds what each
 // segment leaves from a zero state and the sum of its dt (the decay over the segment is exp(A sum)), the next walks the
